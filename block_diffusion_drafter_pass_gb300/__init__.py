@@ -32,6 +32,7 @@ EXPORTED = (
     "dflash_block_sched_set_cost", "dflash_block_sched_expected_tau", "dflash_block_sched_choose",
     "dflash_debug_wait_timeout", "dflash_target_feature_layers", "dflash_target_create", "dflash_target_forward",
     "dflash_debug_read_kv_q8", "dflash_set_conv",
+    "dflash_kv_append", "dflash_paged_attn", "dflash_shared_prefix_attn", "dflash_paged_attn_workspace",
 )
 SAMPLE_WIDTH = 32   # DFLASH_SAMPLE_WIDTH
 
@@ -76,6 +77,16 @@ class dflash_weights(ctypes.Structure):
         ("layers", ctypes.POINTER(dflash_layer_weights))]
 
 
+DFLASH_BF16, DFLASH_FP16 = 0, 1   # dflash_paged_batch.dtype
+KV_PAGE = 64                      # tokens per page
+
+
+class dflash_paged_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "n_heads", "n_kv_heads", "head_dim", "n_seq", "n_tokens", "n_pages",
+                                            "table_pages")] + [("table_stride", ctypes.c_longlong)] + [
+        (n, ctypes.c_void_p) for n in ("pool", "page_table", "q_start", "kv_len", "status")]
+
+
 _lib = None
 
 
@@ -87,7 +98,8 @@ def load_library() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise DFlashError(DFLASH_ECUDA, f"{LIB_PATH} is missing; build it with __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
-    P, I, VP = ctypes.POINTER, ctypes.c_int, ctypes.c_void_p
+    P, I, VP, LL, F = ctypes.POINTER, ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_float
+    batch = P(dflash_paged_batch)
     i32p = P(ctypes.c_int32)
     sigs = {
         "dflash_create": ([P(dflash_config), P(dflash_weights), P(VP)], I),
@@ -123,6 +135,10 @@ def load_library() -> ctypes.CDLL:
         "dflash_target_feature_layers": ([I, I, i32p], I),
         "dflash_target_create": ([P(dflash_config), P(dflash_weights), i32p, P(VP)], I),
         "dflash_target_forward": ([VP, i32p, I, VP, I, I, VP, VP, VP], I),
+        "dflash_kv_append": ([batch, VP, LL, VP, LL, VP, LL, VP, LL, VP, F, VP], I),
+        "dflash_paged_attn_workspace": ([batch, P(ctypes.c_size_t)], I),
+        "dflash_paged_attn": ([batch, VP, LL, VP, LL, I, I, I, F, VP, ctypes.c_size_t, VP], I),
+        "dflash_shared_prefix_attn": ([batch, VP, I, VP, LL, VP, LL, I, F, VP, ctypes.c_size_t, VP], I),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -188,6 +204,175 @@ def dflash_gemm_noalloc(W, X, Y=None, splits: int = 0, stream=None):
         Y = torch.empty(M, N, dtype=torch.float32, device=W.device)
     _check(load_library().dflash_gemm_noalloc(_ptr(W), _ptr(X), _ptr(Y), N, M, K, splits, _stream(stream)))
     return Y
+
+
+# --- operators over a caller's page pool --------------------------------------
+
+def kv_pool(n_pages: int, n_kv_heads: int, head_dim: int, dtype=None, device="cuda"):
+    """A zeroed page pool [n_pages, 2, n_kv_heads, 64 * head_dim]: per page the
+    keys [n_kv][64][d], then the values transposed [n_kv][d][64]."""
+    import torch
+    return torch.zeros(n_pages, 2, n_kv_heads, KV_PAGE * head_dim, dtype=dtype or torch.bfloat16, device=device)
+
+
+def kv_pool_views(pool, head_dim: int):
+    """(keys [n_pages, n_kv, 64, d], values [n_pages, n_kv, d, 64]) of a pool, sharing its memory."""
+    n, _, h, _ = pool.shape
+    return pool[:, 0].view(n, h, KV_PAGE, head_dim), pool[:, 1].view(n, h, head_dim, KV_PAGE)
+
+
+def _refuse(message: str):
+    raise DFlashError(DFLASH_EINVAL, message)
+
+
+def _rows_arg(name, t, pool, shape=None):
+    """A token buffer [T, heads, d] of the pool's type and device whose head
+    rows are contiguous; its stride between tokens."""
+    if t.dtype != pool.dtype or t.device != pool.device or t.dim() != 3:
+        _refuse(f"{name} must be a [tokens, heads, d] tensor of the pool's dtype and device")
+    T, h, d = t.shape
+    if shape is not None and t.shape != shape:
+        _refuse(f"{name} must have shape {tuple(shape)}")
+    s = t.stride()
+    if T and h and d and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+        _refuse(f"{name}: the heads of a token must be contiguous")
+    return s[0] if T > 1 else h * d   # one token: no stride is used
+
+
+def _i32_arg(name, t, device, shape):
+    import torch
+    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+        _refuse(f"{name} must be a contiguous int32 tensor {shape} on the pool's device")
+    return t.data_ptr()
+
+
+def _paged_batch(pool, n_heads, head_dim, n_tokens, q_start, kv_len, page_table, status):
+    import torch
+    if not pool.is_cuda or pool.dim() != 4 or pool.shape[1] != 2 or not pool.is_contiguous():
+        _refuse("the pool must be a contiguous CUDA tensor [n_pages, 2, n_kv_heads, 64 * head_dim]")
+    if pool.dtype not in (torch.bfloat16, torch.float16):
+        _refuse("the pool must be bfloat16 or float16")
+    if pool.shape[3] != KV_PAGE * head_dim:
+        _refuse("the pool's last dimension must be 64 * head_dim")
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != pool.device:
+        _refuse("page_table must be an int32 tensor [n_seq, pages] on the pool's device")
+    n_seq, pages = page_table.shape
+    if pages > 1 and page_table.stride(1) != 1:
+        _refuse("the rows of page_table must be contiguous")
+    stride = page_table.stride(0) if n_seq > 1 else pages
+    if stride < pages:
+        _refuse("the rows of page_table must not overlap")
+    if pages == 0:   # no cache at all: nothing to read, and no row to point at
+        _refuse("page_table needs at least one column")
+    return dflash_paged_batch(
+        DFLASH_FP16 if pool.dtype == torch.float16 else DFLASH_BF16, n_heads, pool.shape[2], head_dim, n_seq, n_tokens,
+        pool.shape[0], pages, stride, _ptr(pool), _ptr(page_table),
+        _i32_arg("q_start", q_start, pool.device, (n_seq + 1,)), _i32_arg("kv_len", kv_len, pool.device, (n_seq,)),
+        0 if status is None else _i32_arg("status", status, pool.device, (1,)))
+
+
+class _on:
+    """The device and stream that a call runs on: results and workspaces are
+    allocated there, so the caching allocator orders their reuse with it."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.cm = []
+        if torch.cuda.current_device() != device.index:
+            self.cm.append(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.cm.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.cm:
+            c.__enter__()
+        import torch
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.cm):
+            c.__exit__(*exc)
+
+
+def dflash_kv_append(pool, k, v, q_start, kv_len, page_table, *, q=None, q_out=None, positions=None,
+                     rope_base: float = 0.0, status=None, stream=None):
+    """Append the new tokens' k and v [T, n_kv, d] to their pages (k rotated at
+    base rope_base; 0: not rotated) and rotate q [T, n_heads, d] beside them.
+    q_start [n_seq + 1], kv_len [n_seq] (the new tokens counted) and page_table
+    [n_seq, pages] are int32 device tensors. Returns the rotated queries
+    (q_out, which may be q itself), or None without q."""
+    import torch
+    T, n_kv, d = k.shape if k.dim() == 3 else _refuse("k must be [tokens, n_kv_heads, d]")
+    ks, vs = _rows_arg("k", k, pool), _rows_arg("v", v, pool, k.shape)
+    n_heads = n_kv if q is None else q.shape[1] if q.dim() == 3 else _refuse("q must be [tokens, heads, d]")
+    b = _paged_batch(pool, n_heads, d, T, q_start, kv_len, page_table, status)
+    if n_kv != pool.shape[2]:
+        _refuse("k and the pool have different numbers of heads")
+    if q is None and q_out is not None:
+        _refuse("q_out without q")
+    qs = 0 if q is None else _rows_arg("q", q, pool, (T, n_heads, d))
+    pos = 0 if positions is None else _i32_arg("positions", positions, pool.device, (T,))
+    with _on(pool.device, stream) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty(T, n_heads, d, dtype=q.dtype, device=q.device)
+        qos = 0 if q is None else _rows_arg("q_out", q_out, pool, (T, n_heads, d))
+        _check(load_library().dflash_kv_append(ctypes.byref(b), _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, _ptr(q_out), qos,
+                                               pos, float(rope_base), s))
+    return q_out
+
+
+def _attend(call, q, pool, q_start, kv_len, page_table, scale, out, status, stream):
+    import torch
+    if q.dim() != 3:
+        _refuse("q must be [tokens, heads, d]")
+    T, n_heads, d = q.shape
+    qs = _rows_arg("q", q, pool)
+    b = _paged_batch(pool, n_heads, d, T, q_start, kv_len, page_table, status)
+    if scale is None:
+        scale = d ** -0.5
+    lib = load_library()
+    with _on(pool.device, stream) as s:
+        need = ctypes.c_size_t()
+        _check(lib.dflash_paged_attn_workspace(ctypes.byref(b), ctypes.byref(need)))
+        ws = torch.empty(need.value, dtype=torch.uint8, device=pool.device)
+        if out is None:
+            out = torch.empty(T, n_heads, d, dtype=q.dtype, device=q.device)
+        os_ = _rows_arg("out", out, pool, q.shape)
+        _check(call(lib, b, _ptr(q), qs, _ptr(out), os_, float(scale), _ptr(ws), need.value, s))
+    return out
+
+
+def dflash_paged_attn(q, pool, q_start, kv_len, page_table, *, window: int = 0, sinks: int = 0, causal: bool = True,
+                      scale: Optional[float] = None, out=None, status=None, stream=None):
+    """Attention of the new tokens q [T, n_heads, d] over their sequences'
+    caches (their own keys and values appended before) -> [T, n_heads, d].
+    window > 0: keys after position - window and the first `sinks` ones only.
+    scale defaults to d ** -0.5. Rows of no sequence are left as they are (a
+    fresh `out` is not initialised)."""
+    def call(lib, b, qp, qs, op, os_, sc, ws, wb, s):
+        return lib.dflash_paged_attn(ctypes.byref(b), qp, qs, op, os_, int(window), int(sinks), 1 if causal else 0, sc,
+                                     ws, wb, s)
+    return _attend(call, q, pool, q_start, kv_len, page_table, scale, out, status, stream)
+
+
+def dflash_shared_prefix_attn(q, pool, q_start, kv_len, page_table, prefix_table, prefix_len: int, *,
+                              causal: bool = True, scale: Optional[float] = None, out=None, status=None, stream=None):
+    """Attention of a batch whose sequences share their first prefix_len tokens
+    (pages prefix_table, int32 on the device, in the same pool): every token
+    sees the prefix and then its own cache (kv_len and page_table count the
+    tokens behind the prefix). The prefix is read once for the whole batch."""
+    prefix_len = int(prefix_len)
+    need = (max(prefix_len, 0) + KV_PAGE - 1) // KV_PAGE
+    if prefix_table.dim() != 1 or prefix_table.shape[0] < need:
+        _refuse("prefix_table must be one row of at least ceil(prefix_len / 64) page ids")
+    table = _i32_arg("prefix_table", prefix_table, pool.device, tuple(prefix_table.shape))
+
+    def call(lib, b, qp, qs, op, os_, sc, ws, wb, s):
+        return lib.dflash_shared_prefix_attn(ctypes.byref(b), table, prefix_len, qp, qs, op, os_, 1 if causal else 0, sc,
+                                             ws, wb, s)
+    return _attend(call, q, pool, q_start, kv_len, page_table, scale, out, status, stream)
 
 
 class BlockScheduler:

@@ -192,7 +192,7 @@ int gemm_act_rows(int M, int N, int K, int num_sms);
 
 // Row-major [rows, cols] bf16 TMA descriptor (box 64 x box_rows, 128B swizzle).
 bool encode_matrix_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
-// Message returned by dflash_last_error(NULL).
+// Message returned by dflash_last_error(NULL): a string literal (kept by address).
 void set_unattached_error(const char* msg);
 
 // ----------------------------------------------------------------------------

@@ -1,0 +1,119 @@
+// paged.cuh - what the operators over caller-owned page pools share: the
+// device view of a batch, the token types, and the token -> (sequence,
+// position) map.
+//
+// Page layout (one page = 64 tokens, as the contexts' own pools): keys
+// [n_kv][64][d], then values transposed [n_kv][d][64], 16-bit elements; a
+// pool is n_pages of them. Sequence i owns the new tokens q_start[i] ..
+// q_start[i+1]-1 of the token buffers, and its cache holds kv_len[i] tokens,
+// those new ones last: new token j sits at position kv_len - q_len + j, slot
+// position % 64 of page page_table[i][position / 64].
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dflash.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace dfl {
+
+constexpr int kPagedMaxSeqs = 1024;      // sequences of one call (their bounds are held in shared memory)
+constexpr int kPagedMaxTable = 1 << 24;  // pages of one sequence: positions stay below 2^30
+
+// The batch as the kernels read it. All arrays are on the device.
+struct PagedView {
+  int n_heads, n_kv, group;   // query heads, kv heads, query heads per kv head
+  int n_seq, n_tokens, n_pages;
+  int table_pages;            // entries of one page-table row
+  long long table_stride;
+  const int32_t* page_table;
+  const int32_t* q_start;     // [n_seq + 1]
+  const int32_t* kv_len;      // [n_seq]
+  uint16_t* pool;
+  int32_t* status;
+};
+
+// Checks what the host can see of a batch; the message of the first fault, or null.
+const char* paged_check(const dflash_paged_batch* b);
+PagedView paged_view(const dflash_paged_batch& b);
+inline bool misaligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15; }
+// A row stride, in elements, that rows of `width` elements with 16-byte loads allow.
+inline bool bad_stride(long long s, long long width) { return s < width || s % 8 || s > (1ll << 36); }
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (F16) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  } else {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (F16) asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The bounds of the sequences' new tokens, read into shared memory as
+// non-decreasing numbers within [0, n_tokens]: what a caller's broken array
+// says otherwise is bent to that (and latched), so no index derived from it
+// leaves a buffer. All threads of the block call it; ends with a barrier.
+// s_part holds one int per warp.
+__device__ __forceinline__ void load_q_start(const PagedView& b, int* s_q, int* s_part) {
+  const int n = b.n_seq + 1, tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  int carry = 0;
+  bool bent = false;
+  for (int base = 0; base < n; base += nthr) {
+    const int i = base + tid;
+    const int raw = i < n ? b.q_start[i] : 0;
+    int v = min(max(raw, 0), b.n_tokens);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, y);
+    }
+    if (lane == 31) s_part[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) v = max(v, s_part[w]);
+    v = max(v, carry);
+    int all = carry;
+    for (int w = 0; w < (nthr >> 5); ++w) all = max(all, s_part[w]);
+    carry = all;
+    if (i < n) {
+      s_q[i] = v;
+      bent |= v != raw;
+    }
+    __syncthreads();
+  }
+  if (bent) latch_status(b.status, kDevBounds);
+}
+
+// The sequence whose new tokens hold token t: the last i in [0, n_seq) with
+// s_q[i] <= t (sequences without new tokens share their start with the next
+// one and are passed over). t in [s_q[0], s_q[n_seq]).
+__device__ __forceinline__ int seq_of_token(const int* s_q, int n_seq, int t) {
+  int lo = 0, hi = n_seq - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_q[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Cached tokens of sequence i, bent to what its page-table row can hold.
+__device__ __forceinline__ int cached_tokens(const PagedView& b, int i) {
+  const int raw = b.kv_len[i];
+  const int v = min(max(raw, 0), b.table_pages * kPage);
+  if (v != raw) latch_status(b.status, kDevBounds);
+  return v;
+}
+
+}  // namespace dfl

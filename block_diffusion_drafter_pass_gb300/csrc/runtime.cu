@@ -14,6 +14,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <map>
@@ -33,6 +34,14 @@ namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::string g_create_error = "no error";
+// The message of a context-free entry point that failed after the last failed
+// create (string literals only, so calls of several threads may fail at once).
+std::atomic<const char*> g_literal_error{nullptr};
+
+void set_create_error(const std::string& msg) {
+  g_create_error = msg;
+  g_literal_error = nullptr;
+}
 
 bool load_encode() {
   if (g_encode) return true;
@@ -77,7 +86,7 @@ namespace dfl {
 bool encode_matrix_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   return load_encode() && encode_2d(m, ptr, rows, cols, box_rows);
 }
-void set_unattached_error(const char* msg) { g_create_error = msg; }
+void set_unattached_error(const char* msg) { g_literal_error = msg; }
 }  // namespace dfl
 
 struct dflash_ctx {
@@ -194,7 +203,7 @@ struct ApiRange {
 
 dflash_status fail(dflash_ctx* c, dflash_status s, const std::string& msg) {
   if (c) c->err = msg;
-  else g_create_error = msg;
+  else set_create_error(msg);
   return s;
 }
 
@@ -363,7 +372,11 @@ dflash_status check_seqs(dflash_ctx* ctx, const int32_t* seq_ids, int n_seq, Seq
 
 extern "C" {
 
-const char* dflash_last_error(const dflash_ctx* ctx) { return ctx ? ctx->err.c_str() : g_create_error.c_str(); }
+const char* dflash_last_error(const dflash_ctx* ctx) {
+  if (ctx) return ctx->err.c_str();
+  const char* literal = g_literal_error;
+  return literal ? literal : g_create_error.c_str();
+}
 
 dflash_status dflash_destroy(dflash_ctx* ctx) {
   if (!ctx) return DFLASH_EINVAL;
@@ -461,7 +474,7 @@ dflash_status create_impl(const dflash_config* cfg_in, const dflash_weights* w, 
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&ctx->num_sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) {
-    g_create_error = std::string("no CUDA device: ") + cudaGetErrorString(e);
+    set_create_error(std::string("no CUDA device: ") + cudaGetErrorString(e));
     delete ctx;
     return DFLASH_ECUDA;
   }
@@ -474,7 +487,7 @@ dflash_status create_impl(const dflash_config* cfg_in, const dflash_weights* w, 
   ctx->items_cap = 4 * ctx->num_sms + c.max_batch * nkv + 64;
 
   auto bad = [&](cudaError_t err, const char* what) {
-    g_create_error = std::string(what) + ": " + cudaGetErrorString(err);
+    set_create_error(std::string(what) + ": " + cudaGetErrorString(err));
     dflash_destroy(ctx);
     return err == cudaErrorMemoryAllocation ? DFLASH_ENOMEM : DFLASH_ECUDA;
   };
@@ -562,7 +575,7 @@ dflash_status create_impl(const dflash_config* cfg_in, const dflash_weights* w, 
          encode_2d(&ctx->m_wd[l], L.w_down, H, F, wb);
   }
   if (!ok) {
-    g_create_error = "cuTensorMapEncodeTiled rejected a weight layout";
+    set_create_error("cuTensorMapEncodeTiled rejected a weight layout");
     dflash_destroy(ctx);
     return DFLASH_EINVAL;
   }

@@ -35,6 +35,7 @@
 #ifndef DFLASH_H
 #define DFLASH_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -394,6 +395,101 @@ typedef struct {
  * rank not a multiple of 8 in [8, 128], hidden not a multiple of 128, a NULL
  * or misaligned pointer), ENOMEM, ECUDA. */
 dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, int rank, void* stream);
+
+/* ---- operators over a caller's page pool ----
+ * Stateless forms of what a context does inside its passes, for callers that
+ * keep their own cache (a target model with windowed layers, a server that
+ * shares prompts between requests). The caller owns the pool, the page tables
+ * and the lengths; all of them are read on the device when the kernels run, so
+ * a captured call replays with the tables and lengths of that moment.
+ *
+ * A pool is n_pages pages of 64 tokens, each the keys [n_kv_heads][64][d] and
+ * then the values transposed [n_kv_heads][d][64] (the layout of the contexts'
+ * own pools). A batch is n_seq sequences; sequence i has the new tokens
+ * q_start[i] .. q_start[i+1]-1 of the token buffers (q, k, v, out) and a cache
+ * of kv_len[i] tokens with those new ones last: new token j is at position
+ * kv_len[i] - (q_start[i+1] - q_start[i]) + j, and position p lies in slot
+ * p % 64 of page page_table[i][p / 64]. A sequence may have no new tokens.
+ * Rows of the token buffers before q_start[0] and from q_start[n_seq] on are
+ * left as they are. Head rows are contiguous; the stride between tokens is the
+ * caller's (a column range of a wider matrix will do).
+ *
+ * Broken device arrays end in no access out of range: q_start is bent to
+ * non-decreasing numbers within [0, n_tokens], kv_len to [0, 64*table_pages],
+ * and tokens whose page id is outside [0, n_pages) are not written and not
+ * seen. Each of these sets bit 2 (EDEVICE's) of *status, which the caller
+ * clears. Slots past a length may hold any bits. */
+enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1 };
+
+typedef struct {
+  int dtype;                 /* of pool and token buffers: DFLASH_BF16 or DFLASH_FP16 */
+  int n_heads;               /* query heads; head h reads kv head h / (n_heads / n_kv_heads) */
+  int n_kv_heads;            /* divides n_heads, at most 128 query heads each       */
+  int head_dim;              /* d: 64 or 128                                        */
+  int n_seq;                 /* 0..1024                                             */
+  int n_tokens;              /* rows of the token buffers, 0..2^24                  */
+  int n_pages;
+  int table_pages;           /* entries of a page-table row: 1..2^24                */
+  long long table_stride;    /* elements between page-table rows, >= table_pages    */
+  void* pool;                /* device, 16-byte aligned                             */
+  const int32_t* page_table; /* device [n_seq][table_stride]                        */
+  const int32_t* q_start;    /* device [n_seq + 1]                                  */
+  const int32_t* kv_len;     /* device [n_seq]                                      */
+  int32_t* status;           /* device [1], or NULL                                 */
+} dflash_paged_batch;
+
+/* Write the new tokens' keys and values into their pages, the keys rotated on
+ * the way (rotate-half pairing (i, i + d/2), angle position * rope_base^(-2i/d),
+ * exact to fp32 at any int32 position), and rotate the queries beside them.
+ *  k, v       device [n_tokens][n_kv_heads][d], strides in elements between
+ *             tokens (multiples of 8), 16-byte aligned
+ *  q, q_out   device [n_tokens][n_heads][d], or both NULL; q_out may be q
+ *  positions  device [n_tokens] rotation positions, or NULL: the cache
+ *             positions (callers behind a shared prefix add its length)
+ *  rope_base  in (1, 1e12], or 0: nothing is rotated (q is copied)
+ * Slots written by one call must be distinct: a page that two sequences of the
+ * batch both append to gets either one's values. A token before its cache
+ * (kv_len below the number of new tokens) is skipped, its queries too, and
+ * sets the status. Errors: EINVAL, ECUDA. */
+dflash_status dflash_kv_append(const dflash_paged_batch* b, const void* k, long long k_stride, const void* v,
+                               long long v_stride, const void* q, long long q_stride, void* q_out,
+                               long long q_out_stride, const int32_t* positions, float rope_base, void* stream);
+
+/* Device bytes that the two attention calls below need as workspace for this
+ * batch's shape (it depends on n_heads, n_kv_heads, head_dim, n_tokens and the
+ * device only). Its contents need no preparation and mean nothing afterwards;
+ * calls that may run at the same time need one each. Errors: EINVAL, ECUDA. */
+dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b, size_t* bytes);
+
+/* Attention of every new token over its sequence's cache (the new tokens'
+ * keys and values appended before): softmax over the visible keys of
+ * scale * q.k in fp32, times the values.
+ *  q, out   device [n_tokens][n_heads][d], strides in elements between tokens
+ *           (multiples of 8), 16-byte aligned; out must not overlap q
+ *  causal   1: the token at position p sees keys 0..p; 0: the whole cache
+ *  window   > 0: of those, only keys after p - window and the first `sinks`
+ *           keys; 0: all (sinks is then ignored)
+ *  scale    positive and finite
+ *  workspace  device, 16-byte aligned, at least dflash_paged_attn_workspace
+ * A token that sees no key gets zeros. Keys and values it does not see have no
+ * influence on it, infinities and NaN included (non-finite values in hidden
+ * places of a page cost time).
+ * Errors: EINVAL (also a workspace that is too small), ECUDA. */
+dflash_status dflash_paged_attn(const dflash_paged_batch* b, const void* q, long long q_stride, void* out,
+                                long long out_stride, int window, int sinks, int causal, float scale, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* The same for a batch whose sequences share their first prefix_len tokens,
+ * held once in the pool: every token sees the whole prefix and then its own
+ * cache (causal as above, in which the first own position is 0; a token that
+ * lies before its own cache sees prefix keys up to its place only). Prefix
+ * keys and values are read once for all tokens, not once for each sequence.
+ *  prefix_table  device [ceil(prefix_len / 64)] page ids
+ *  prefix_len    0..2^30 (0: dflash_paged_attn without a window)
+ * Errors: EINVAL, ECUDA. */
+dflash_status dflash_shared_prefix_attn(const dflash_paged_batch* b, const int32_t* prefix_table, int prefix_len,
+                                        const void* q, long long q_stride, void* out, long long out_stride, int causal,
+                                        float scale, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- inspection hooks (used by the parity tests; they synchronise) ---- */
 
