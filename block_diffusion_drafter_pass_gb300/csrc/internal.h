@@ -192,6 +192,10 @@ int gemm_act_rows(int M, int N, int K, int num_sms);
 
 // Row-major [rows, cols] bf16 TMA descriptor (box 64 x box_rows, 128B swizzle).
 bool encode_matrix_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// 16-bit elements in three dimensions (strides in bytes, of dimensions 1 and
+// 2; inner box 64 elements, 128B swizzle); places out of range read as zeros.
+bool encode_box_3d(CUtensorMap* m, const void* ptr, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                   const uint32_t (&box)[3]);
 // Message returned by dflash_last_error(NULL): a string literal (kept by address).
 void set_unattached_error(const char* msg);
 

@@ -10,8 +10,32 @@
 // prefix is seen whole (up to P + p when a cache holds fewer tokens than the
 // block has). A row that sees nothing is zero.
 //
-// One warp per (token, head), page by page with the running maximum and sum of
-// the softmax.
+// Work. The rows of a kv head (group query heads of each token) are cut into
+// tiles of up to 2 x 128 rows: a tile's tokens are one sequence's, or behind a
+// shared prefix neighbours of any sequences, so that the prefix is read once
+// for all of them. A tile walks steps of 128 keys (two pages): of its own
+// cache the pages that some row sees (first tokens, then the window); behind a
+// prefix the prefix and then the cache of each of its sequences in turn, where
+// the other sequences' rows see nothing. All steps of all (tile, kv head) in
+// one line are dealt to the CTAs in equal runs, so long rows are split over
+// the keys as far as needed and no CTA waits for a longer one; a tile that
+// ends in another CTA leaves unnormalised partials (O, maximum, sum), which
+// paged_combine_kernel joins. Every CTA finds its run from the lengths on the
+// device, so a captured launch follows them.
+//
+// Per CTA: warp 0 brings the queries, and keys and values into a ring of step
+// halves (128 keys, or their values transposed), by TMA; warp 1 issues
+// tcgen05.mma from one thread; two groups of four warps run the softmax of two
+// streams, each with its own S/P and O in tensor memory. A tile of more
+// than 128 rows gives each stream 128 rows and both read the same keys
+// ("pair": a key tile is loaded once for 256 rows, which is what a product of
+// this shape needs to stay off the L2's limit); a smaller tile gives both
+// streams the same rows and every other step ("alternate": a split over the
+// keys inside the CTA, joined in its epilogue). Either way one stream's
+// products run while the other's softmax does.
+#include <cuda.h>
+
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -21,60 +45,928 @@
 namespace dfl {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384;         // producer, MMA, two idle warps, 2 x 4 softmax warps
+constexpr int kSoftWarp0 = 4;
+// The block is launched at 168 registers a thread; the first warpgroup drops
+// to 88 and the two softmax warpgroups rise to 208: the same sum.
+constexpr uint32_t kRegsFew = 88, kRegsMany = 208;
+static_assert(128 * kRegsFew + 256 * kRegsMany == kThreads * 168, "register split");
+constexpr int kStepKeys = 2 * kPage;
+constexpr int kRows = 128;            // rows of a stream: the MMA's M
+// The producer is at most the ring's 8 halves of values and 2 steps of keys
+// ahead of the softmax (a step's values are not overwritten before its P).
+constexpr int kStepRing = 16;
+constexpr int kNoEnd = 1 << 30;       // above every position
+constexpr float kRescaleLog2 = 8.f;   // rescale O when a row's maximum grows by more than 2^8
 
 struct PagedAttnArgs {
   PagedView b;
   const int32_t* prefix_table;
   int prefix_len;
+  int shared;                  // tiles span sequences, behind prefix_len shared tokens
   const uint16_t* q;
   long long q_stride;
   uint16_t* out;
   long long out_stride;
   int window, sinks, causal;
   float scale_log2;
+  int stream_tokens;           // tokens of one stream's 128 rows
+  int tile_tokens;             // tokens of a tile: one or two streams
+  // partials: two slots per CTA (0: a tile begun by an earlier CTA, 1: a tile
+  // that a later CTA ends), rows_cap rows each
+  int rows_cap;
+  float* part_o;               // [cta][2][rows_cap][d]
+  float2* part_ml;             // [cta][2][rows_cap] maximum (log2 units), sum
+  int4* split;                 // [cta] tile begun here and ended elsewhere: first token, tokens, kv head, CTAs (0: none)
 };
 
+struct PagedMaps {
+  CUtensorMap k, v, q;
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kBox = kRows * 128;                  // 128 rows of 64 elements, swizzled
+  static constexpr int kHalf = (D / 64) * kBox;             // a step's keys, or its values
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kQBytes = 2 * kHalf;                 // queries of both streams
+  static constexpr int kIntOff = kQBytes + kSlots * kHalf;
+  static constexpr int kInts = 3 * (kPagedMaxSeqs + 1);     // q_start, kv_len, tile or step bases
+  static constexpr int kSmem = kIntOff + kInts * 4 + 1024;
+  static_assert(kSmem <= 227 * 1024 - 4096, "static shared variables need the rest");
+  // TMEM columns: S of the streams (P over its first 64), then their O
+  static constexpr uint32_t kOCol = 2 * kStepKeys;
+  static constexpr uint32_t kTmemCols = 512;
+};
+
+// The sequences' metadata in shared memory (bent into range when loaded).
+struct Meta {
+  const int* q;      // [n_seq + 1]
+  const int* len;    // [n_seq]
+  const int* base;   // [n_seq + 1] own cache: tiles before a sequence; shared: own-cache steps before it
+};
+
+struct Tile {
+  int t0, ntok;         // tokens
+  int seq0, seq1;       // sequences of the first and last token
+  int n;                // steps, at least 1 (a tile that sees nothing has a step without a visible key)
+  int head_steps;       // own cache: steps over the first tokens; shared: over the prefix
+  int window_step;      // own cache: the step index after those
+};
+
+__device__ __forceinline__ int steps_of(int keys) { return keys > 0 ? (keys + kStepKeys - 1) / kStepKeys : 0; }
+
+__device__ __forceinline__ Tile tile_at(const PagedAttnArgs& a, const Meta& m, int tile) {
+  Tile r;
+  if (a.shared) {
+    r.t0 = m.q[0] + tile * a.tile_tokens;
+    r.ntok = min(a.tile_tokens, m.q[a.b.n_seq] - r.t0);
+    const int last = r.t0 + r.ntok - 1;
+    r.seq0 = seq_of_token(m.q, a.b.n_seq, r.t0);
+    r.seq1 = seq_of_token(m.q, a.b.n_seq, last);
+    r.head_steps = steps_of(a.prefix_len);
+    r.window_step = 0;
+    // the last sequence may go on behind the tile: its keys up to the tile's last row
+    const int end = a.causal ? m.len[r.seq1] - (m.q[r.seq1 + 1] - 1 - last) : m.len[r.seq1];
+    r.n = max(1, r.head_steps + m.base[r.seq1] - m.base[r.seq0] + steps_of(end));
+    return r;
+  }
+  int lo = 0, hi = a.b.n_seq - 1;   // the last sequence whose tiles start at or before this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (m.base[mid] <= tile) lo = mid;
+    else hi = mid - 1;
+  }
+  r.seq0 = r.seq1 = lo;
+  r.t0 = m.q[lo] + (tile - m.base[lo]) * a.tile_tokens;
+  r.ntok = min(a.tile_tokens, m.q[lo + 1] - r.t0);
+  const int pos0 = m.len[lo] - (m.q[lo + 1] - r.t0);
+  const int end = a.causal ? pos0 + r.ntok : m.len[lo];
+  const int w1 = steps_of(end);
+  const int w0 = a.window > 0 ? min(max(0, pos0 - a.window + 1) / kStepKeys, w1) : 0;
+  r.head_steps = min(steps_of(a.sinks), w0);
+  r.window_step = w0;
+  r.n = max(1, r.head_steps + w1 - w0);
+  return r;
+}
+
+// One step: 128 keys from `base` of a sequence's cache (seq >= 0) or of the
+// prefix (seq = -1), of which those below `end` exist.
+struct Step {
+  int seq, base, end;
+};
+
+// The steps of a tile in order, from any of them on.
+struct StepWalk {
+  Step s;
+  int left;   // steps left in this run of keys
+  __device__ __forceinline__ void start(const PagedAttnArgs& a, const Meta& m, const Tile& t, int j) {
+    if (a.shared) {
+      if (j < t.head_steps) {
+        s = Step{-1, j * kStepKeys, a.prefix_len};
+        left = t.head_steps - j;
+        return;
+      }
+      const int want = m.base[t.seq0] + j - t.head_steps;
+      int lo = t.seq0, hi = t.seq1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (m.base[mid] <= want) lo = mid;
+        else hi = mid - 1;
+      }
+      s = Step{lo, (want - m.base[lo]) * kStepKeys, m.len[lo]};
+      left = lo < t.seq1 ? m.base[lo + 1] - want : INT32_MAX;
+      return;
+    }
+    const bool head = j < t.head_steps;
+    s = Step{t.seq0, (head ? j : t.window_step + j - t.head_steps) * kStepKeys, m.len[t.seq0]};
+    left = head ? t.head_steps - j : INT32_MAX;
+  }
+  __device__ __forceinline__ void next(const PagedAttnArgs& a, const Meta& m, const Tile& t) {
+    s.base += kStepKeys;
+    if (--left > 0) return;
+    if (!a.shared) {
+      s.base = t.window_step * kStepKeys;
+      left = INT32_MAX;
+      return;
+    }
+    int i = s.seq < 0 ? t.seq0 : s.seq + 1;
+    while (i < t.seq1 && m.base[i + 1] == m.base[i]) ++i;
+    s = Step{i, 0, m.len[i]};
+    left = i < t.seq1 ? m.base[i + 1] - m.base[i] : INT32_MAX;
+  }
+};
+
+// Whether some row of the tokens [ta, tb) of a tile sees a key of the step.
+__device__ __forceinline__ bool step_counts(const PagedAttnArgs& a, const Meta& m, const Step& s, int ta, int tb) {
+  if (s.seq < 0) return true;
+  const int q0 = m.q[s.seq], q1 = m.q[s.seq + 1];
+  const int first = max(ta, q0), last = min(tb, q1) - 1;
+  if (first > last) return false;
+  const int shift = m.len[s.seq] - q1;   // position of token t: t + shift
+  if (a.causal && s.base > last + shift) return false;
+  if (a.window > 0 && s.base + kStepKeys - 1 < first + shift - a.window + 1 && s.base >= a.sinks) return false;
+  return true;
+}
+
+// The row of one softmax thread: what it sees of its sequence's cache, and (of
+// a shared prefix) prefix_len more.
+struct Row {
+  int token, seq;   // token < 0: no row
+  int lo, hi;
+};
+
+__device__ __forceinline__ Row row_at(const PagedAttnArgs& a, const Meta& m, const Tile& t, int stream, int r) {
+  Row x;
+  const int j = r / a.b.group, token = t.t0 + stream * a.stream_tokens + j;
+  x.token = j < a.stream_tokens && token < t.t0 + t.ntok ? token : -1;
+  x.seq = t.seq0 == t.seq1 || x.token < 0 ? t.seq0 : seq_of_token(m.q, a.b.n_seq, x.token);
+  const int pos = m.len[x.seq] - m.q[x.seq + 1] + x.token;
+  x.lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+  x.hi = a.causal ? pos : kNoEnd;
+  return x;
+}
+
+// Its span of a step's run of keys (empty: hi < 0).
+__device__ __forceinline__ RowSpan span_of(const PagedAttnArgs& a, const Row& x, const Step& s) {
+  if (x.token < 0 || (s.seq >= 0 && s.seq != x.seq)) return RowSpan{0, -1, 0};
+  if (s.seq < 0) return RowSpan{0, x.hi + a.prefix_len, 0};
+  return RowSpan{x.lo, x.hi, a.sinks};
+}
+
+__device__ __forceinline__ const int32_t* table_of(const PagedAttnArgs& a, int seq) {
+  return seq < 0 ? a.prefix_table : a.b.page_table + seq * a.b.table_stride;
+}
+
+// An item: steps [j, j + nj) of one tile and kv head. Every role walks the
+// CTA's items in the same order; each warp keeps its own in shared memory.
+struct Item {
+  Tile t;
+  int tile, head, j, nj;
+  int pair;         // each stream has its own 128 rows (else: the same rows, every other step)
+  long long todo;   // steps of the CTA from this item on
+};
+
+__device__ __forceinline__ void set_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
+  it.t = tile_at(a, m, it.tile);
+  it.pair = it.t.ntok > a.stream_tokens;
+}
+
+__device__ __forceinline__ bool first_item(const PagedAttnArgs& a, const Meta& m, Item& it, const int* begin,
+                                           long long steps) {
+  if (steps <= 0) return false;
+  it.todo = steps;
+  it.tile = begin[0];
+  it.head = begin[1];
+  it.j = begin[2];
+  set_item(a, m, it);
+  it.nj = static_cast<int>(min(steps, static_cast<long long>(it.t.n - it.j)));
+  return true;
+}
+
+__device__ __forceinline__ bool next_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
+  it.todo -= it.nj;
+  if (it.todo <= 0) return false;
+  it.j = 0;
+  if (++it.head == a.b.n_kv) {
+    it.head = 0;
+    ++it.tile;
+    set_item(a, m, it);
+  }
+  it.nj = static_cast<int>(min(it.todo, static_cast<long long>(it.t.n)));
+  return true;
+}
+
+// Row of a partial: [cta][slot][rows_cap], slot 1 for a tile that begins here.
+__device__ __forceinline__ size_t partial_row(const PagedAttnArgs& a, const Item& it, int stream, int r) {
+  return (static_cast<size_t>(blockIdx.x) * 2 + (it.j == 0 ? 1 : 0)) * a.rows_cap + (it.pair ? stream * kRows : 0) + r;
+}
+
+__device__ __forceinline__ uint16_t* out_row(const PagedAttnArgs& a, int token, int kvh, int g, int d) {
+  return a.out + token * a.out_stride + static_cast<long long>(kvh * a.b.group + g) * d;
+}
+
+// One row of an item again, read key by key by one warp, and written over what
+// the products gave: they met a non-finite value, which may have come from a
+// place that the row does not see (0 times infinity or NaN).
 template <int D, bool F16>
-__global__ void __launch_bounds__(kWarps * 32) paged_rows_kernel(const __grid_constant__ PagedAttnArgs a) {
-  __shared__ int s_q[kPagedMaxSeqs + 1];
-  __shared__ int s_part[kWarps];
+__device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Meta& m, const Item& it, int stream, int r) {
+  const int lane = threadIdx.x & 31, rows_of = it.pair ? stream : 0;
+  const Row x = row_at(a, m, it.t, rows_of, r);
+  const int g = r % a.b.group;
+  const uint16_t* q = a.q + x.token * a.q_stride + static_cast<long long>(it.head * a.b.group + g) * D;
+  const size_t page_elems = static_cast<size_t>(2) * a.b.n_kv * kPage * D;
+  RowState<D> st;
+  st.clear();
+  StepWalk w;
+  w.start(a, m, it.t, it.j);
+  for (int j = 0; j < it.nj; ++j, w.next(a, m, it.t)) {
+    const RowSpan sp = span_of(a, x, w.s);
+    for (int u = 0; u < 2; ++u) {
+      const int key0 = w.s.base + u * kPage;
+      const unsigned long long vis = sp.hi >= 0 ? row_sees(sp, key0, w.s.end) : 0ull;
+      if (vis == 0) continue;
+      const int page = table_of(a, w.s.seq)[key0 / kPage];
+      if (page < 0 || page >= a.b.n_pages) continue;
+      const uint16_t* kp = a.b.pool + page * page_elems + static_cast<size_t>(it.head) * kPage * D;
+      row_page<D, F16>(st, q, kp, kp + static_cast<size_t>(a.b.n_kv) * kPage * D, a.scale_log2, vis, lane);
+    }
+  }
+  if (it.nj == it.t.n) {
+    const float f = st.l > 0.f || st.l != st.l ? 1.f / st.l : 0.f;
+    uint16_t* o = out_row(a, x.token, it.head, g, D) + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+      *reinterpret_cast<uint32_t*>(o + e) = pack2<F16>(st.acc[e] * f, st.acc[e + 1] * f);
+  } else {
+    const size_t pr = partial_row(a, it, stream, r);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) a.part_o[pr * D + lane * (D / 32) + e] = st.acc[e];
+    if (lane == 0) a.part_ml[pr] = make_float2(st.m, st.l);
+  }
+}
+
+// Sum over the threads before this one; `total` over all. One int64 per warp in s_part.
+__device__ __forceinline__ long long block_scan(long long v, long long* s_part, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();   // the previous use of s_part is read
+  if (lane == 31) s_part[warp] = x;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += s_part[w];
+    total += s_part[w];
+  }
+  return before + x - v;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs a) {
+  using C = Cfg<D>;
+  constexpr int S = C::kSlots;
+  // fp16 has no weights below 2^-24: a row's largest is put at 2^7 (and may
+  // stand at 2^15 before O is rescaled), so that weights 2^-31 of it still count
+  constexpr float kBias = F16 ? 7.f : 0.f;
+  constexpr uint32_t kIdescS = F16 ? idesc_f16_f32(kRows, kStepKeys) : idesc_bf16_f32(kRows, kStepKeys);
+  constexpr uint32_t kIdescO = F16 ? idesc_f16_f32(kRows, D) : idesc_bf16_f32(kRows, D);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int* s_ints = reinterpret_cast<int*>(smem + C::kIntOff);
+  int *s_q = s_ints, *s_len = s_ints + kPagedMaxSeqs + 1, *s_base = s_ints + 2 * (kPagedMaxSeqs + 1);
+  __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
+  __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) uint64_t x_ml, x_bad;   // the two softmax groups at an alternating tile's end
+  __shared__ float2 s_ml[2][kRows];
+  __shared__ uint8_t s_bad[kRows];
+  __shared__ uint8_t s_gone[kStepRing];   // of the CTA's recent steps: bit u, page u has no place in the pool
+  __shared__ long long s_part[kThreads / 32];
+  __shared__ int s_begin[3];
+  __shared__ Item s_item[kThreads / 32];
+  __shared__ int s_go[kThreads / 32];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_seq = a.b.n_seq, n_kv = a.b.n_kv, G = a.b.group;
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
+    mbar_init(&mma_done, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&pv_done[s], 1);
+    }
+    mbar_init(&x_ml, 8);
+    mbar_init(&x_bad, 8);
+    abort_flag = 0;
+    s_begin[0] = -1;
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+    tma_prefetch_desc(&maps.q);
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, C::kTmemCols);
   grid_dep_wait();
   grid_dep_launch();
-  load_q_start(a.b, s_q, s_part);
-  const int lane = threadIdx.x & 31, h = blockIdx.x * kWarps + (threadIdx.x >> 5), t = blockIdx.y;
-  if (h >= a.b.n_heads || t < s_q[0] || t >= s_q[a.b.n_seq]) return;
-  const int i = seq_of_token(s_q, a.b.n_seq, t);
-  const int len = cached_tokens(a.b, i);
-  const int pos = len - (s_q[i + 1] - s_q[i]) + (t - s_q[i]);
-  const int kvh = h / a.b.group;
-  const uint16_t* q = a.q + t * a.q_stride + h * D;
-  const size_t page_elems = static_cast<size_t>(2) * a.b.n_kv * kPage * D;
-  RowState<D> r;
-  r.clear();
-  auto walk = [&](const int32_t* table, const RowSpan& span, int end) {
-    const int pages = (min(end, span.hi == INT32_MAX ? end : span.hi + 1) + kPage - 1) / kPage;
-    for (int g = 0; g < pages; ++g) {
-      const unsigned long long vis = row_sees(span, g * kPage, end);
-      if (vis == 0) continue;
-      const int page = table[g];
-      if (page < 0 || page >= a.b.n_pages) {
-        if (lane == 0) latch_status(a.b.status, kDevBounds);
-        continue;
-      }
-      const uint16_t* kp = a.b.pool + page * page_elems + static_cast<size_t>(kvh) * kPage * D;
-      row_page<D, F16>(r, q, kp, kp + static_cast<size_t>(a.b.n_kv) * kPage * D, a.scale_log2, vis, lane);
+
+  // ---- the batch's shape, and this CTA's run of steps ----
+  load_q_start(a.b, s_q, reinterpret_cast<int*>(s_part));
+  long long total = 0;
+  for (int i0 = 0; i0 < n_seq; i0 += kThreads) {
+    const int i = i0 + tid;
+    int v = 0;
+    if (i < n_seq) {
+      const int nq = s_q[i + 1] - s_q[i], len = cached_tokens(a.b, i);
+      s_len[i] = len;
+      if (a.shared) v = nq > 0 ? steps_of(len) : 0;
+      else v = (nq + a.tile_tokens - 1) / a.tile_tokens;
     }
+    long long part;
+    const long long before = total + block_scan(v, s_part, part);
+    if (i < n_seq) s_base[i] = static_cast<int>(before);
+    total += part;
+  }
+  if (tid == 0) s_base[n_seq] = static_cast<int>(total);
+  __syncthreads();
+  const Meta m{s_q, s_len, s_base};
+  const int n_tiles = a.shared ? (s_q[n_seq] - s_q[0] + a.tile_tokens - 1) / a.tile_tokens : static_cast<int>(total);
+  const int per = (n_tiles + kThreads - 1) / kThreads;
+  const int tile_a = min(tid * per, n_tiles), tile_b = min(tile_a + per, n_tiles);
+  long long mine = 0;
+  for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(tile_at(a, m, t).n) * n_kv;
+  long long all;
+  const long long before = block_scan(mine, s_part, all);
+  const long long ctas = min(static_cast<long long>(gridDim.x), all);
+  const bool works = blockIdx.x < ctas;
+  const long long x0 = works ? all * blockIdx.x / ctas : 0;
+  const long long x1 = works ? all * (blockIdx.x + 1) / ctas : 0;
+  if (works && x0 >= before && x0 < before + mine) {
+    long long rem = x0 - before;
+    for (int t = tile_a; t < tile_b; ++t) {
+      const int n = tile_at(a, m, t).n;
+      if (rem < static_cast<long long>(n) * n_kv) {
+        s_begin[0] = t;
+        s_begin[1] = static_cast<int>(rem / n);
+        s_begin[2] = static_cast<int>(rem % n);
+        break;
+      }
+      rem -= static_cast<long long>(n) * n_kv;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  Item& it = s_item[warp];   // written by lane 0
+  auto first = [&]() { return first_item(a, m, it, s_begin, x1 - x0); };
+  auto next = [&]() { return next_item(a, m, it); };
+  auto give_up = [&]() {
+    abort_flag = 1;
+    latch_status(a.b.status, kDevTimeout);
   };
-  if (a.prefix_len > 0)
-    walk(a.prefix_table, RowSpan{0, a.causal ? a.prefix_len + pos : INT32_MAX, 0}, a.prefix_len);
-  walk(a.b.page_table + i * a.b.table_stride,
-       RowSpan{a.window > 0 ? max(0, pos - a.window + 1) : 0, a.causal ? pos : INT32_MAX, a.sinks}, len);
-  const float inv = r.l > 0.f || r.l != r.l ? 1.f / r.l : 0.f;
-  uint16_t* o = a.out + t * a.out_stride + h * D + lane * (D / 32);
+  // Order of the ring's halves in an item: the keys of the first `lead` steps,
+  // then the values of step j and the keys of step j + lead in turn - the
+  // order in which the products are issued.
+
+  if (warp < kSoftWarp0) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew) : "memory");
+  if (warp == 0) {
+    // ---------------- queries, keys and values ----------------
+    if (lane == 0) {
+      int c = 0, steps = 0;   // ring halves, steps whose keys were brought
+      bool dead = false;
+      int4 split = make_int4(0, 0, 0, 0);
+      long long at = x0;   // place of the item's first step in the line of all steps
+      // The queries of an item can come when the products S of the item before
+      // are done; its first keys and values need not wait for that, so the
+      // queries are brought in from the ring's waits.
+      int nq = 0;          // items whose queries are on their way
+      int q_pair = 0, q_head = 0, q_t0 = 0;   // the item whose queries are due
+      bool q_due = false;
+      auto bring_q = [&]() {
+        const int n = q_pair ? 2 : 1;
+        mbar_arrive_expect_tx(&q_full, n * (D / 64) * a.stream_tokens * G * 128);
+        for (int s = 0; s < n; ++s)
 #pragma unroll
-  for (int e = 0; e < D / 32; e += 2)
-    *reinterpret_cast<uint32_t*>(o + e) = pack2<F16>(r.acc[e] * inv, r.acc[e + 1] * inv);
+          for (int bx = 0; bx < D / 64; ++bx)
+            tma_load_3d(smem + s * C::kHalf + bx * C::kBox, &maps.q, &q_full, bx * 64, q_head * G,
+                        q_t0 + s * a.stream_tokens);
+        ++nq;
+        q_due = false;
+      };
+      auto q_now = [&]() {
+        if (!q_due || dead) return;
+        if (!mbar_wait(&q_empty, (nq & 1) ^ 1, &abort_flag)) {
+          give_up();
+          dead = true;
+          return;
+        }
+        bring_q();
+      };
+      for (bool go = first(); go && !dead; go = next()) {
+        q_now();
+        q_pair = it.pair;
+        q_head = it.head;
+        q_t0 = it.t.t0;
+        q_due = true;
+        const int lead = it.pair ? 1 : 2;
+        StepWalk wk, wv;
+        wk.start(a, m, it.t, it.j);
+        wv = wk;
+        auto put = [&](const Step& s, bool keys) {
+          const int slot = c % S;
+          const unsigned long long w0 = global_ns();
+          while (true) {
+            if (q_due && mbar_test_wait(&q_empty, (nq & 1) ^ 1)) bring_q();
+            if (mbar_try_wait(&kv_empty[slot], ((c / S) & 1) ^ 1)) break;
+            if (abort_flag || global_ns() - w0 > kWaitLimitNs) {
+              give_up();
+              dead = true;
+              return;
+            }
+          }
+          uint8_t* dst = smem + C::kQBytes + slot * C::kHalf;
+          const int32_t* table = table_of(a, s.seq);
+          // a page past the sequence's end, or none of the pool's, reads as
+          // zeros: from behind the pool's last page
+          int page[2], gone = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int key0 = s.base + u * kPage;
+            page[u] = a.b.n_pages;
+            if (key0 < s.end) {
+              page[u] = table[key0 / kPage];
+              if (page[u] < 0 || page[u] >= a.b.n_pages) {
+                latch_status(a.b.status, kDevBounds);
+                page[u] = a.b.n_pages;
+                gone |= 1 << u;
+              }
+            }
+          }
+          if (keys) s_gone[steps++ % kStepRing] = gone;   // read behind this half's barrier and the product's
+          mbar_arrive_expect_tx(&kv_full[slot], C::kHalf);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (keys) {
+#pragma unroll
+              for (int bx = 0; bx < D / 64; ++bx)
+                tma_load_3d(dst + bx * C::kBox + u * (C::kBox / 2), &maps.k, &kv_full[slot], bx * 64, it.head * kPage,
+                            page[u]);
+            } else {
+              tma_load_3d(dst + u * (C::kHalf / 2), &maps.v, &kv_full[slot], 0, it.head * D, page[u]);
+            }
+          }
+          ++c;
+        };
+        for (int j = 0; j < min(lead, it.nj) && !dead; ++j, wk.next(a, m, it.t)) put(wk.s, true);
+        for (int j = 0; j < it.nj && !dead; ++j) {
+          put(wv.s, false);
+          wv.next(a, m, it.t);
+          if (j + lead < it.nj && !dead) {
+            put(wk.s, true);
+            wk.next(a, m, it.t);
+          }
+        }
+        if (it.j == 0 && it.nj < it.t.n) {
+          const long long last = at + it.t.n - 1;   // in CTA c with all * c / ctas <= last
+          split = make_int4(it.t.t0, it.t.ntok, it.head,
+                            static_cast<int>(((last + 1) * ctas - 1) / all) - static_cast<int>(blockIdx.x) + 1);
+        }
+        at += it.nj;
+      }
+      q_now();
+      a.split[blockIdx.x] = split;
+      // copies still in flight complete before shared memory is released
+      for (int j = max(0, c - S); j < c; ++j) mbar_wait(&kv_full[j % S], (j / S) & 1);
+      if (nq > 0) mbar_wait(&q_full, (nq - 1) & 1);
+    }
+  } else if (warp == 1) {
+    // ---------------- products ----------------
+    if (lane == 0) {
+      const uint32_t q_base = smem_u32(smem), ring = q_base + C::kQBytes;
+      int c = 0, k = 0;    // ring halves, items
+      uint32_t p_par = 0;  // bit s: parity of stream s's next P
+      bool dead = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (dead || !mbar_wait(bar, parity, &abort_flag)) {
+          if (!dead) give_up();
+          dead = true;
+        }
+        tc_fence_after();
+      };
+      auto issue_s = [&](int s, int half, bool pair) {   // S = Q K^T
+        const uint32_t qb = q_base + (pair ? s * C::kHalf : 0), kb = ring + (half % S) * C::kHalf;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kBox + (kk & 3) * 32;
+          tc_mma_bf16(tmem + s * kStepKeys, sdesc_kmajor_sw128(qb + off), sdesc_kmajor_sw128(kb + off), kIdescS, kk > 0);
+        }
+        tc_commit(&s_full[s]);
+      };
+      auto issue_pv = [&](int s, int half, bool add) {   // O (+)= P V
+        const uint32_t vb = ring + (half % S) * C::kHalf;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16_ts(tmem + C::kOCol + s * D, tmem + s * kStepKeys + u * 32 + kk * 8,
+                           sdesc_kmajor_sw128(vb + u * (C::kHalf / 2) + kk * 32), kIdescO, (add || u + kk > 0) ? 1u : 0u);
+        tc_commit(&pv_done[s]);
+      };
+      auto full = [&](int half) { wait(&kv_full[half % S], (half / S) & 1); };
+      auto free_half = [&](int half) { tc_commit(&kv_empty[half % S]); };
+      for (bool go = first(); go && !dead; go = next(), ++k) {
+        wait(&q_full, k & 1);
+        if (dead) break;
+        uint32_t add = 0;    // bit s: stream s's O holds products of this item
+        if (it.pair) {
+          const int mid = it.t.t0 + a.stream_tokens, end = it.t.t0 + it.t.ntok;
+          StepWalk w;
+          w.start(a, m, it.t, it.j);
+          auto wanted = [&]() {   // bit s: stream s has a row that sees keys of the step
+            return (step_counts(a, m, w.s, it.t.t0, mid) ? 1u : 0u) | (step_counts(a, m, w.s, mid, end) ? 2u : 0u);
+          };
+          uint32_t now = wanted();
+          full(c);
+          if (dead) break;
+          for (int s = 0; s < 2; ++s)
+            if (now >> s & 1) issue_s(s, c, true);
+          free_half(c++);
+          if (it.nj == 1) tc_commit(&q_empty);
+          for (int j = 0; j < it.nj && !dead; ++j) {
+            const bool more = j + 1 < it.nj;
+            uint32_t then = 0;
+            if (more) {
+              w.next(a, m, it.t);
+              then = wanted();
+            }
+            bool vr = false, kr = false;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (now >> s & 1) {
+                if (!vr) full(c);
+                vr = true;
+                wait(&p_full[s], p_par >> s & 1);
+                if (dead) break;
+                issue_pv(s, c, add >> s & 1);
+                add |= 1u << s;
+                p_par ^= 1u << s;
+              }
+              if (then >> s & 1) {
+                if (!kr) full(c + 1);
+                kr = true;
+                if (dead) break;
+                issue_s(s, c + 1, true);
+              }
+            }
+            // a half that no stream needed is still waited for before it goes back
+            if (!dead && !vr) full(c);
+            if (!dead && more && !kr) full(c + 1);
+            if (dead) break;
+            free_half(c++);
+            if (more) {
+              free_half(c++);
+              if (j + 2 == it.nj) tc_commit(&q_empty);
+            }
+            now = then;
+          }
+        } else {
+          for (int j = 0; j < min(2, it.nj) && !dead; ++j) {
+            full(c);
+            if (dead) break;
+            issue_s(j, c, false);
+            free_half(c++);
+          }
+          if (it.nj <= 2 && !dead) tc_commit(&q_empty);
+          for (int j = 0; j < it.nj && !dead; ++j) {
+            const int s = j & 1;
+            full(c);
+            wait(&p_full[s], p_par >> s & 1);
+            if (dead) break;
+            issue_pv(s, c, add >> s & 1);
+            add |= 1u << s;
+            p_par ^= 1u << s;
+            free_half(c++);
+            if (j + 2 < it.nj) {
+              full(c);
+              if (dead) break;
+              issue_s(s, c, false);
+              free_half(c++);
+              if (j + 3 == it.nj) tc_commit(&q_empty);
+            }
+          }
+        }
+      }
+      // every issued product completes before TMEM and shared memory are released
+      tc_commit(&mma_done);
+      mbar_wait(&mma_done, 0);
+    }
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany) : "memory");
+    // ---------------- softmax and output ----------------
+    const int stream = warp >= kSoftWarp0 + 4 ? 1 : 0;
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_tmem = lane_tmem + stream * kStepKeys;
+    const uint32_t o_tmem = lane_tmem + C::kOCol + stream * D;
+    const float sl2 = a.scale_log2;
+    int ns = 0;         // S tiles taken by this stream
+    int nx = 0;         // alternating tiles ended
+    int items = 0;
+    int step0 = 0;      // steps of the CTA's items before this one
+    bool dead = false;
+    // waits taken by all 32 lanes together, so the warp-collective TMEM
+    // accesses after them never diverge (also when a wait runs out)
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag))) {
+        give_up();
+        dead = true;
+      }
+      tc_fence_after();
+    };
+    auto warp_arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    while (true) {
+      __syncwarp();
+      if (lane == 0) s_go[warp] = items == 0 ? first() : next();
+      __syncwarp();
+      if (!s_go[warp] || dead) break;
+      ++items;
+      const Row row = row_at(a, m, it.t, it.pair ? stream : 0, r);
+      const int ta = it.t.t0 + (stream ? a.stream_tokens : 0);
+      const int tb = min(ta + a.stream_tokens, it.t.t0 + it.t.ntok);
+      float mref = -INFINITY, l = 0.f;   // the row's reference maximum (log2 units, less the bias), sum
+      int done = 0;                      // steps of this item that this stream took
+      StepWalk w;
+      w.start(a, m, it.t, it.j);
+      for (int j = 0; j < it.nj; ++j, w.next(a, m, it.t)) {
+        if (it.pair ? !step_counts(a, m, w.s, ta, tb) : ((j & 1) != stream)) continue;
+        warp_wait(&s_full[stream], ns & 1);
+        if (dead) break;
+        // columns [0, c_hi) less those in [c_sink, c_lo) are seen
+        const RowSpan sp = span_of(a, row, w.s);
+        const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
+        const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
+        const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
+        uint32_t pk[32];
+        if (__all_sync(0xffffffffu, none)) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = 0u;
+          tmem_st_u32(s_tmem, pk);
+          tmem_st_u32(s_tmem + 32, pk);
+        } else {
+          // a half of the scores at a time: the second for its maximum, the
+          // first for its maximum and weights, the second again. P replaces
+          // scores of the first half, which are in registers by then.
+          const int gone = s_gone[(step0 + j) % kStepRing];
+          const bool plain =
+              __all_sync(0xffffffffu, c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys)) && gone == 0;
+          float sv[64];
+          auto load = [&](int c0) {
+            tmem_ld64(s_tmem + c0, sv);
+            if (!plain) {
+              const int end = gone >> (c0 / 64) & 1 ? 0 : c_hi - c0;
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                sv[c] = c < end && (c >= c_lo - c0 || c < c_sink - c0) ? sv[c] : -INFINITY;
+            }
+          };
+          load(64);
+          const float mx1 = row_max(sv);
+          load(0);
+          const float mx = fmaxf(row_max(sv), mx1) * sl2 - kBias;
+          if (__any_sync(0xffffffffu, mx > mref + kRescaleLog2)) {
+            const float nm = fmaxf(mref, mx);
+            const float alpha = nm == -INFINITY ? 1.f : ex2(mref - nm);
+            l *= alpha;
+            mref = nm;
+            if (done > 0) {   // O holds the stream's products so far: wait for them, then rescale
+              warp_wait(&pv_done[stream], (ns - 1) & 1);
+              if (!dead) {
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                  float o[32];
+                  tmem_ld32(o_tmem + c0, o);
+#pragma unroll
+                  for (int c = 0; c < 32; ++c) o[c] *= alpha;
+                  tmem_st32(o_tmem + c0, o);
+                }
+                tmem_wait_st();
+              }
+            }
+          }
+          const float neg = mref == -INFINITY ? 0.f : -mref;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          auto weights = [&](uint32_t p_tmem) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float p0 = ex2(fmaf(sv[2 * c], sl2, neg));
+              const float p1 = ex2(fmaf(sv[2 * c + 1], sl2, neg));
+              sum[c & 3] += p0 + p1;
+              pk[c] = pack2<F16>(p0, p1);
+            }
+            tmem_st_u32(p_tmem, pk);
+          };
+          weights(s_tmem);
+          load(64);
+          weights(s_tmem + 32);
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        tmem_wait_st();
+        warp_arrive(&p_full[stream]);
+        ++done;
+        ++ns;
+        if (dead) break;
+      }
+      if (dead) break;
+      step0 += it.nj;
+      if (done > 0) {
+        warp_wait(&pv_done[stream], (ns - 1) & 1);
+        if (dead) break;
+      }
+
+      const bool whole = it.nj == it.t.n;
+      const bool live = row.token >= 0;
+      const size_t prow = partial_row(a, it, stream, r);
+      uint16_t* out = out_row(a, row.token, it.head, r % G, D);
+      float* part = a.part_o + prow * D;
+      auto store32 = [&](int c0, const float (&o)[32]) {
+        if (whole) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            *reinterpret_cast<uint4*>(out + c0 + c) =
+                make_uint4(pack2<F16>(o[c], o[c + 1]), pack2<F16>(o[c + 2], o[c + 3]), pack2<F16>(o[c + 4], o[c + 5]),
+                           pack2<F16>(o[c + 6], o[c + 7]));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            *reinterpret_cast<float4*>(part + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+        }
+      };
+      float check = 0.f;   // NaN once a stored value is not finite
+      if (it.pair) {
+        const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          if (done > 0) tmem_ld32(o_tmem + c0, o);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            o[c] = done > 0 && l != 0.f ? o[c] * f : 0.f;
+            check = fmaf(o[c], 0.f, check);
+          }
+          if (live) store32(c0, o);
+        }
+        if (live && !whole) a.part_ml[prow] = make_float2(mref, l);
+      } else {
+        // both streams hold a part of every row's sum: each group joins half of the columns
+        if (stream == 0) s_bad[r] = 0;
+        s_ml[stream][r] = make_float2(mref, l);
+        warp_arrive(&x_ml);
+        warp_wait(&x_ml, nx & 1);
+        if (dead) break;
+        const float2 m0 = s_ml[0][r], m1 = s_ml[1][r];
+        const float top = fmaxf(m0.x, m1.x);
+        float w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - top), w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - top);
+        const float lj = m0.y * w0 + m1.y * w1;
+        if (whole) {
+          const float f = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
+          w0 *= f;
+          w1 *= f;
+        }
+        const bool has1 = it.nj > 1;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 2; c0 += 32) {
+          const int col = stream * (D / 2) + c0;
+          float o0[32], o1[32];
+          tmem_ld32(lane_tmem + C::kOCol + col, o0);
+          if (has1) tmem_ld32(lane_tmem + C::kOCol + D + col, o1);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float o = m0.y != 0.f ? o0[c] * w0 : 0.f;
+            if (has1 && m1.y != 0.f) o = fmaf(o1[c], w1, o);
+            o0[c] = o;
+            check = fmaf(o, 0.f, check);
+          }
+          if (live) store32(col, o0);
+        }
+        if (live && check != 0.f) s_bad[r] = 1;
+        if (live && !whole && stream == 0) a.part_ml[prow] = make_float2(top, lj);
+        // also: both groups have read both O before either's next P lets O be overwritten
+        warp_arrive(&x_bad);
+        warp_wait(&x_bad, nx & 1);
+        if (dead) break;
+        ++nx;
+        check = stream == 0 && s_bad[r] ? 1.f : 0.f;
+      }
+      // rows that met a non-finite value: again, from what they see
+      for (uint32_t bad = __ballot_sync(0xffffffffu, live && check != 0.f); bad; bad &= bad - 1)
+        redo_row<D, F16>(a, m, it, stream, quarter * 32 + __ffs(bad) - 1);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Join the pieces of the tile that CTA blockIdx.x of the main kernel began and
+// did not end: piece 0 in its slot 1, the others in slot 0 of the CTAs after
+// it. One warp per row; lanes hold the pieces' maxima and sums, 32 pieces at a
+// time, then every piece's row is read as one coalesced load.
+constexpr int kCombineWarps = 8;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int kPer = D / 32;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int4 sp = a.split[blockIdx.x];   // first token, tokens, kv head, pieces
+  if (sp.w == 0) return;
+  const int lane = threadIdx.x & 31, G = a.b.group, stream_rows = a.stream_tokens * G;
+  const int rows = sp.y * G;
+  for (int i = blockIdx.y * kCombineWarps + (threadIdx.x >> 5); i < rows; i += gridDim.y * kCombineWarps) {
+    const int row = i < stream_rows ? i : kRows + i - stream_rows;
+    auto at = [&](int p) {
+      return ((static_cast<size_t>(blockIdx.x) + p) * 2 + (p == 0 ? 1 : 0)) * a.rows_cap + row;
+    };
+    float top = -INFINITY;
+    for (int p = lane; p < sp.w; p += 32) top = fmaxf(top, a.part_ml[at(p)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f, acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int p0 = 0; p0 < sp.w; p0 += 32) {
+      const float2 ml = p0 + lane < sp.w ? a.part_ml[at(p0 + lane)] : make_float2(-INFINITY, 0.f);
+      const float wl = exp2f(ml.x - ref);
+      l += wl * ml.y;
+      const int n = min(32, sp.w - p0);
+#pragma unroll 8
+      for (int p = 0; p < n; ++p) {
+        const float w = __shfl_sync(0xffffffffu, wl, p);
+        const float* src = a.part_o + at(p0 + p) * D + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src + e);
+          acc[e] = fmaf(w, v.x, acc[e]);
+          acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int j = i / G;
+    uint16_t* out = a.out + (sp.x + j) * a.out_stride + static_cast<long long>(sp.z * G + i - j * G) * D + lane * kPer;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2)
+      *reinterpret_cast<uint32_t*>(out + e) = pack2<F16>(acc[e] * f, acc[e + 1] * f);
+  }
 }
 
 const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_stride, const void* out,
@@ -90,24 +982,77 @@ const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_s
   return nullptr;
 }
 
+// The tile's shape and the workspace's layout for a batch.
+struct Plan {
+  int ctas, stream_tokens, tile_tokens, rows_cap;
+  size_t o_off, ml_off, bytes;   // the split records come first
+};
+
+bool make_plan(const dflash_paged_batch& b, Plan& p) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p.ctas, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return false;
+  const int group = b.n_heads / b.n_kv_heads;
+  p.stream_tokens = kRows / group;
+  p.tile_tokens = 2 * p.stream_tokens;
+  p.rows_cap = b.n_tokens > p.stream_tokens ? 2 * kRows : std::min(kRows, b.n_tokens * group);
+  auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
+  p.ml_off = up(sizeof(int4) * p.ctas);
+  p.o_off = p.ml_off + up(sizeof(float2) * 2 * p.ctas * p.rows_cap);
+  p.bytes = p.o_off + sizeof(float) * 2 * p.ctas * p.rows_cap * b.head_dim;
+  return true;
+}
+
+template <int D, bool F16>
+cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p, cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(paged_attn_kernel<D, F16>, dim3(p.ctas), dim3(kThreads), Cfg<D>::kSmem, s, maps, a);
+  if (e != cudaSuccess) return e;
+  const int rows = std::min(8, (p.rows_cap + kCombineWarps - 1) / kCombineWarps);
+  return launch_pdl(paged_combine_kernel<D, F16>, dim3(p.ctas, rows), dim3(kCombineWarps * 32), 0, s, a);
+}
+
+dflash_status refuse(const char* why) {
+  set_unattached_error(why);
+  return DFLASH_EINVAL;
+}
+
+dflash_status fail_cuda(const char* why) {
+  set_unattached_error(why);
+  return DFLASH_ECUDA;
+}
+
 dflash_status run(const dflash_paged_batch& b, PagedAttnArgs& a, void* workspace, size_t workspace_bytes, void* stream) {
-  (void)workspace;
-  (void)workspace_bytes;
+  Plan p;
+  if (!make_plan(b, p)) return fail_cuda("paged attention: no CUDA device");
+  if (!workspace || misaligned16(workspace) || workspace_bytes < p.bytes)
+    return refuse("the workspace is null, not 16-byte aligned or smaller than dflash_paged_attn_workspace says");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.stream_tokens = p.stream_tokens;
+  a.tile_tokens = p.tile_tokens;
+  a.rows_cap = p.rows_cap;
+  a.split = reinterpret_cast<int4*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
+  a.part_o = reinterpret_cast<float*>(ws + p.o_off);
+  const uint64_t d = b.head_dim, n_kv = b.n_kv_heads, pages = b.n_pages;
+  const uint64_t page_bytes = 2 * n_kv * kPage * d * 2;
+  PagedMaps maps;
+  // keys: rows of d elements, a page's rows head after head; values: rows of
+  // the page's 64 slots; queries: [token][head][d]
+  if (!encode_box_3d(&maps.k, b.pool, {d, kPage * n_kv, pages}, {d * 2, page_bytes}, {64, kPage, 1}) ||
+      !encode_box_3d(&maps.v, static_cast<uint8_t*>(b.pool) + page_bytes / 2, {kPage, d * n_kv, pages},
+                     {kPage * 2, page_bytes}, {64, static_cast<uint32_t>(d), 1}) ||
+      !encode_box_3d(&maps.q, a.q, {d, static_cast<uint64_t>(b.n_heads), static_cast<uint64_t>(b.n_tokens)},
+                     {d * 2, static_cast<uint64_t>(a.q_stride) * 2},
+                     {64, static_cast<uint32_t>(a.b.group), static_cast<uint32_t>(p.stream_tokens)}))
+    return fail_cuda("paged attention: cannot describe the pool or the queries for TMA");
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid((b.n_heads + kWarps - 1) / kWarps, b.n_tokens);
   cudaError_t e;
-  if (b.head_dim == 128) {
-    e = b.dtype == DFLASH_FP16 ? launch_pdl(paged_rows_kernel<128, true>, grid, dim3(kWarps * 32), 0, s, a)
-                               : launch_pdl(paged_rows_kernel<128, false>, grid, dim3(kWarps * 32), 0, s, a);
-  } else {
-    e = b.dtype == DFLASH_FP16 ? launch_pdl(paged_rows_kernel<64, true>, grid, dim3(kWarps * 32), 0, s, a)
-                               : launch_pdl(paged_rows_kernel<64, false>, grid, dim3(kWarps * 32), 0, s, a);
-  }
-  if (e != cudaSuccess) {
-    set_unattached_error("paged attention: kernel launch failed");
-    return DFLASH_ECUDA;
-  }
-  return DFLASH_OK;
+  if (b.head_dim == 128) e = b.dtype == DFLASH_FP16 ? launch<128, true>(maps, a, p, s) : launch<128, false>(maps, a, p, s);
+  else e = b.dtype == DFLASH_FP16 ? launch<64, true>(maps, a, p, s) : launch<64, false>(maps, a, p, s);
+  return e == cudaSuccess ? DFLASH_OK : fail_cuda("paged attention: kernel launch failed");
 }
 
 PagedAttnArgs attn_args(const dflash_paged_batch& b, const void* q, long long q_stride, void* out, long long out_stride,
@@ -124,11 +1069,6 @@ PagedAttnArgs attn_args(const dflash_paged_batch& b, const void* q, long long q_
   return a;
 }
 
-dflash_status refuse(const char* why) {
-  set_unattached_error(why);
-  return DFLASH_EINVAL;
-}
-
 }  // namespace
 }  // namespace dfl
 
@@ -138,6 +1078,10 @@ extern "C" dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b
   if (!bytes) return refuse("null pointer");
   *bytes = 0;
   if (const char* why = paged_check(b)) return refuse(why);
+  if (b->n_seq == 0 || b->n_tokens == 0) return DFLASH_OK;
+  Plan p;
+  if (!make_plan(*b, p)) return fail_cuda("paged attention: no CUDA device");
+  *bytes = p.bytes;
   return DFLASH_OK;
 }
 
@@ -148,8 +1092,9 @@ extern "C" dflash_status dflash_paged_attn(const dflash_paged_batch* b, const vo
   if (window < 0 || sinks < 0) return refuse("window and sinks must not be negative");
   if (b->n_seq == 0 || b->n_tokens == 0) return DFLASH_OK;
   PagedAttnArgs a = attn_args(*b, q, q_stride, out, out_stride, causal, scale);
-  a.window = window;
-  a.sinks = window > 0 ? sinks : 0;
+  // positions stay below 2^30, so wider spans see the same
+  a.window = std::min(window, 1 << 30);
+  a.sinks = window > 0 ? std::min(sinks, 1 << 30) : 0;
   return run(*b, a, workspace, workspace_bytes, stream);
 }
 
@@ -164,5 +1109,6 @@ extern "C" dflash_status dflash_shared_prefix_attn(const dflash_paged_batch* b, 
   PagedAttnArgs a = attn_args(*b, q, q_stride, out, out_stride, causal, scale);
   a.prefix_table = prefix_table;
   a.prefix_len = prefix_len;
+  a.shared = 1;
   return run(*b, a, workspace, workspace_bytes, stream);
 }

@@ -86,6 +86,15 @@ namespace dfl {
 bool encode_matrix_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows) {
   return load_encode() && encode_2d(m, ptr, rows, cols, box_rows);
 }
+bool encode_box_3d(CUtensorMap* m, const void* ptr, const uint64_t (&dims)[3], const uint64_t (&strides)[2],
+                   const uint32_t (&box)[3]) {
+  if (!load_encode()) return false;
+  const cuuint64_t gd[3] = {dims[0], dims[1], dims[2]}, gs[2] = {strides[0], strides[1]};
+  const cuuint32_t bx[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), gd, gs, bx, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 void set_unattached_error(const char* msg) { g_literal_error = msg; }
 }  // namespace dfl
 
