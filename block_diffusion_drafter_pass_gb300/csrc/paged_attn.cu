@@ -24,9 +24,10 @@
 // device, so a captured launch follows them.
 //
 // Per CTA: warp 0 brings the queries, and keys and values into a ring of step
-// halves (128 keys, or their values transposed), by TMA; warp 1 issues
-// tcgen05.mma from one thread; two groups of four warps run the softmax of two
-// streams, each with its own S/P and O in tensor memory. A tile of more
+// halves (128 keys, or their values transposed), by TMA; two streams, each
+// with its own S/P and O in tensor memory, have one warp that issues their
+// tcgen05.mma from one thread (one for both left the tensor cores waiting for
+// its bookkeeping: 390 us on the windowed prefill) and four softmax warps. A tile of more
 // than 128 rows gives each stream 128 rows and both read the same keys
 // ("pair": a key tile is loaded once for 256 rows, which is what a product of
 // this shape needs to stay off the L2's limit); a smaller tile gives both
@@ -45,17 +46,15 @@
 namespace dfl {
 namespace {
 
-constexpr int kThreads = 384;         // producer, MMA, two idle warps, 2 x 4 softmax warps
-constexpr int kSoftWarp0 = 4;
-// The block is launched at 168 registers a thread; the first warpgroup drops
-// to 88 and the two softmax warpgroups rise to 208: the same sum.
-constexpr uint32_t kRegsFew = 88, kRegsMany = 208;
-static_assert(128 * kRegsFew + 256 * kRegsMany == kThreads * 168, "register split");
+constexpr int kThreads = 352;         // producer, 2 x MMA, 2 x 4 softmax warps
+constexpr int kSoftWarp0 = 3;
 constexpr int kStepKeys = 2 * kPage;
 constexpr int kRows = 128;            // rows of a stream: the MMA's M
 // The producer is at most the ring's 8 halves of values and 2 steps of keys
 // ahead of the softmax (a step's values are not overwritten before its P).
 constexpr int kStepRing = 16;
+constexpr int kIdsAhead = 4, kIdRing = 16;   // steps
+constexpr int kItemSteps = 2;         // what an item costs beside its steps, in steps (dealing only)
 constexpr int kNoEnd = 1 << 30;       // above every position
 constexpr float kRescaleLog2 = 8.f;   // rescale O when a row's maximum grows by more than 2^8
 
@@ -98,6 +97,21 @@ struct Cfg {
   static constexpr uint32_t kOCol = 2 * kStepKeys;
   static constexpr uint32_t kTmemCols = 512;
 };
+
+// A shared-memory descriptor (sdesc_kmajor_sw128) in two halves: the upper one
+// is the same for every tile, and addresses step within the lower one.
+__device__ __forceinline__ uint32_t sdesc_low(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint64_t sdesc_of(uint32_t low) {
+  constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (static_cast<uint64_t>(kHigh) << 32) | low;
+}
+
+// 2^x, not moved by the compiler.
+__device__ __forceinline__ float ex2_here(float x) {
+  float y;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // The sequences' metadata in shared memory (bent into range when loaded).
 struct Meta {
@@ -240,41 +254,53 @@ __device__ __forceinline__ const int32_t* table_of(const PagedAttnArgs& a, int s
 
 // An item: steps [j, j + nj) of one tile and kv head. Every role walks the
 // CTA's items in the same order; each warp keeps its own in shared memory.
+// In the line that is dealt to the CTAs a tile and head takes kItemSteps
+// places for what it costs at its begin and end, then one for each step; a run
+// that ends within those leaves the item to the next CTA.
 struct Item {
   Tile t;
   int tile, head, j, nj;
   int pair;         // each stream has its own 128 rows (else: the same rows, every other step)
-  long long todo;   // steps of the CTA from this item on
+  int place;        // the run's place within this tile and head
+  long long todo;   // places of the CTA from this item on
 };
+
+__device__ __forceinline__ int places_of(int steps) { return steps + kItemSteps; }
 
 __device__ __forceinline__ void set_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
   it.t = tile_at(a, m, it.tile);
   it.pair = it.t.ntok > a.stream_tokens;
 }
 
+// The item at the run's place; false when the run ends before its steps.
+__device__ __forceinline__ bool cut_item(Item& it) {
+  const int take = static_cast<int>(min(it.todo, static_cast<long long>(places_of(it.t.n) - it.place)));
+  it.j = max(it.place - kItemSteps, 0);
+  it.nj = it.place + take - kItemSteps - it.j;
+  it.todo -= take;
+  return it.nj > 0;
+}
+
 __device__ __forceinline__ bool first_item(const PagedAttnArgs& a, const Meta& m, Item& it, const int* begin,
-                                           long long steps) {
-  if (steps <= 0) return false;
-  it.todo = steps;
+                                           long long places) {
+  if (places <= 0) return false;
+  it.todo = places;
   it.tile = begin[0];
   it.head = begin[1];
-  it.j = begin[2];
+  it.place = begin[2];
   set_item(a, m, it);
-  it.nj = static_cast<int>(min(steps, static_cast<long long>(it.t.n - it.j)));
-  return true;
+  return cut_item(it);
 }
 
 __device__ __forceinline__ bool next_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
-  it.todo -= it.nj;
   if (it.todo <= 0) return false;
-  it.j = 0;
+  it.place = 0;
   if (++it.head == a.b.n_kv) {
     it.head = 0;
     ++it.tile;
     set_item(a, m, it);
   }
-  it.nj = static_cast<int>(min(it.todo, static_cast<long long>(it.t.n)));
-  return true;
+  return cut_item(it);
 }
 
 // Row of a partial: [cta][slot][rows_cap], slot 1 for a tile that begins here.
@@ -364,11 +390,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *s_q = s_ints, *s_len = s_ints + kPagedMaxSeqs + 1, *s_base = s_ints + 2 * (kPagedMaxSeqs + 1);
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], pv_done[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2];
   __shared__ __align__(8) uint64_t x_ml, x_bad;   // the two softmax groups at an alternating tile's end
   __shared__ float2 s_ml[2][kRows];
   __shared__ uint8_t s_bad[kRows];
-  __shared__ uint8_t s_gone[kStepRing];   // of the CTA's recent steps: bit u, page u has no place in the pool
+  __shared__ int s_page[kIdRing][2];
+  // of the CTA's recent steps: bit u, page u is not there; bit 2 + s, stream s
+  // of a pair takes the step
+  __shared__ uint8_t s_step[kStepRing];
   __shared__ long long s_part[kThreads / 32];
   __shared__ int s_begin[3];
   __shared__ Item s_item[kThreads / 32];
@@ -381,15 +410,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(&kv_full[s], 1);
-      mbar_init(&kv_empty[s], 1);
+      mbar_init(&kv_empty[s], 2);   // both streams
     }
     mbar_init(&q_full, 1);
-    mbar_init(&q_empty, 1);
-    mbar_init(&mma_done, 1);
+    mbar_init(&q_empty, 2);
+    mbar_init(&mma_done, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);
-      mbar_init(&pv_done[s], 1);
+      mbar_init(&o_done[s], 1);
     }
     mbar_init(&x_ml, 8);
     mbar_init(&x_bad, 8);
@@ -428,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (n_tiles + kThreads - 1) / kThreads;
   const int tile_a = min(tid * per, n_tiles), tile_b = min(tile_a + per, n_tiles);
   long long mine = 0;
-  for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(tile_at(a, m, t).n) * n_kv;
+  for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(places_of(tile_at(a, m, t).n)) * n_kv;
   long long all;
   const long long before = block_scan(mine, s_part, all);
   const long long ctas = min(static_cast<long long>(gridDim.x), all);
@@ -438,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (works && x0 >= before && x0 < before + mine) {
     long long rem = x0 - before;
     for (int t = tile_a; t < tile_b; ++t) {
-      const int n = tile_at(a, m, t).n;
+      const int n = places_of(tile_at(a, m, t).n);
       if (rem < static_cast<long long>(n) * n_kv) {
         s_begin[0] = t;
         s_begin[1] = static_cast<int>(rem / n);
@@ -460,19 +489,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 1;
     latch_status(a.b.status, kDevTimeout);
   };
-  // Order of the ring's halves in an item: the keys of the first `lead` steps,
-  // then the values of step j and the keys of step j + lead in turn - the
-  // order in which the products are issued.
+  // An item goes in rounds j = -lead .. nj-1: round j multiplies P of step j
+  // with its values and issues the scores of step j + lead, so the ring holds,
+  // in turn, the values of step j and the keys of step j + lead. lead is 1 for
+  // a pair (both streams take every step) and 2 for an alternating tile
+  // (stream s takes the steps of parity s).
+  // The loops here are kept rolled where they can be: an item's path is walked
+  // a few times by each warp, so code that does not stay in the instruction
+  // caches costs more than the loops (unrolled over all 128 scores, the first
+  // and last steps of an item took 3 to 7 us each instead of 1).
 
-  if (warp < kSoftWarp0) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew) : "memory");
   if (warp == 0) {
     // ---------------- queries, keys and values ----------------
     if (lane == 0) {
       int c = 0, steps = 0;   // ring halves, steps whose keys were brought
       bool dead = false;
       int4 split = make_int4(0, 0, 0, 0);
-      long long at = x0;   // place of the item's first step in the line of all steps
       // The queries of an item can come when the products S of the item before
       // are done; its first keys and values need not wait for that, so the
       // queries are brought in from the ring's waits.
@@ -506,40 +538,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_t0 = it.t.t0;
         q_due = true;
         const int lead = it.pair ? 1 : 2;
-        StepWalk wk, wv;
-        wk.start(a, m, it.t, it.j);
-        wv = wk;
-        auto put = [&](const Step& s, bool keys) {
+        // Page ids are copied kIdsAhead steps before their keys are due, so no
+        // load waits for one.
+        StepWalk wf, wk;   // of the ids, of the keys
+        wf.start(a, m, it.t, it.j);
+        wk = wf;
+        const int step0 = steps;
+        int nf = 0;        // steps of this item whose ids are on their way
+        auto fetch_ids = [&]() {
+          if (nf < it.nj) {
+            const int32_t* table = table_of(a, wf.s.seq);
+            int* dst = s_page[(step0 + nf) % kIdRing];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int key0 = wf.s.base + u * kPage;
+              if (key0 < wf.s.end) copy_async4(dst + u, table + key0 / kPage);
+              else dst[u] = -1;
+            }
+            wf.next(a, m, it.t);
+            ++nf;
+          }
+          copy_async_commit();
+        };
+        for (int i = 0; i < kIdsAhead; ++i) fetch_ids();
+#pragma unroll 1
+        for (int i = -2 * lead; i < 2 * it.nj; ++i) {   // round i >> 1: values, then keys
+          const bool keys = i & 1;
+          const int j = (i >> 1) + (keys ? lead : 0);
+          if (j < 0 || j >= it.nj) continue;
+          if (keys) {
+            fetch_ids();
+            copy_async_wait<kIdsAhead>();
+          }
           const int slot = c % S;
-          const unsigned long long w0 = global_ns();
+          const unsigned long long t_wait = global_ns();
           while (true) {
             if (q_due && mbar_test_wait(&q_empty, (nq & 1) ^ 1)) bring_q();
             if (mbar_try_wait(&kv_empty[slot], ((c / S) & 1) ^ 1)) break;
-            if (abort_flag || global_ns() - w0 > kWaitLimitNs) {
+            if (abort_flag || global_ns() - t_wait > kWaitLimitNs) {
               give_up();
               dead = true;
-              return;
+              break;
             }
           }
+          if (dead) break;
           uint8_t* dst = smem + C::kQBytes + slot * C::kHalf;
-          const int32_t* table = table_of(a, s.seq);
           // a page past the sequence's end, or none of the pool's, reads as
           // zeros: from behind the pool's last page
           int page[2], gone = 0;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int key0 = s.base + u * kPage;
+            page[u] = s_page[(step0 + j) % kIdRing][u];
+            if (page[u] >= 0 && page[u] < a.b.n_pages) continue;
             page[u] = a.b.n_pages;
-            if (key0 < s.end) {
-              page[u] = table[key0 / kPage];
-              if (page[u] < 0 || page[u] >= a.b.n_pages) {
-                latch_status(a.b.status, kDevBounds);
-                page[u] = a.b.n_pages;
-                gone |= 1 << u;
-              }
-            }
+            gone |= 1 << u;
           }
-          if (keys) s_gone[steps++ % kStepRing] = gone;   // read behind this half's barrier and the product's
+          if (keys) {
+            if (gone && wk.s.base + (gone == 2 ? kPage : 0) < wk.s.end) latch_status(a.b.status, kDevBounds);
+            int flags = gone;
+            if (it.pair) {
+              const int mid = it.t.t0 + a.stream_tokens;
+              flags |= (step_counts(a, m, wk.s, it.t.t0, mid) ? 4 : 0) |
+                       (step_counts(a, m, wk.s, mid, it.t.t0 + it.t.ntok) ? 8 : 0);
+            }
+            wk.next(a, m, it.t);
+            s_step[steps++ % kStepRing] = static_cast<uint8_t>(flags);   // read behind this half's barrier and the product's
+          }
           mbar_arrive_expect_tx(&kv_full[slot], C::kHalf);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -553,22 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           ++c;
-        };
-        for (int j = 0; j < min(lead, it.nj) && !dead; ++j, wk.next(a, m, it.t)) put(wk.s, true);
-        for (int j = 0; j < it.nj && !dead; ++j) {
-          put(wv.s, false);
-          wv.next(a, m, it.t);
-          if (j + lead < it.nj && !dead) {
-            put(wk.s, true);
-            wk.next(a, m, it.t);
-          }
         }
-        if (it.j == 0 && it.nj < it.t.n) {
-          const long long last = at + it.t.n - 1;   // in CTA c with all * c / ctas <= last
+        if (it.j == 0 && it.nj < it.t.n) {   // the run ends here: the tile's last place is in CTA c with all * c / ctas <= it
+          const long long last = x1 + it.t.n - it.nj - 1;
           split = make_int4(it.t.t0, it.t.ntok, it.head,
                             static_cast<int>(((last + 1) * ctas - 1) / all) - static_cast<int>(blockIdx.x) + 1);
         }
-        at += it.nj;
       }
       q_now();
       a.split[blockIdx.x] = split;
@@ -576,12 +630,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = max(0, c - S); j < c; ++j) mbar_wait(&kv_full[j % S], (j / S) & 1);
       if (nq > 0) mbar_wait(&q_full, (nq - 1) & 1);
     }
-  } else if (warp == 1) {
-    // ---------------- products ----------------
+  } else if (warp < kSoftWarp0) {
+    // ---------------- products of one stream ----------------
+    // In each round the product of the step's weights with its values and the
+    // scores of the step `lead` later, where the stream takes them. Each stream
+    // waits for every half and arrives for it, its own or not: a stream that
+    // passed over halves could meet a barrier a whole turn of the ring away.
     if (lane == 0) {
+      const int s = warp - 1;
       const uint32_t q_base = smem_u32(smem), ring = q_base + C::kQBytes;
-      int c = 0, k = 0;    // ring halves, items
-      uint32_t p_par = 0;  // bit s: parity of stream s's next P
+      int c = 0, steps = 0, k = 0, np = 0;   // ring halves, steps with scores, items, P tiles taken
       bool dead = false;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         if (dead || !mbar_wait(bar, parity, &abort_flag)) {
@@ -590,116 +648,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
       };
-      auto issue_s = [&](int s, int half, bool pair) {   // S = Q K^T
-        const uint32_t qb = q_base + (pair ? s * C::kHalf : 0), kb = ring + (half % S) * C::kHalf;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * C::kBox + (kk & 3) * 32;
-          tc_mma_bf16(tmem + s * kStepKeys, sdesc_kmajor_sw128(qb + off), sdesc_kmajor_sw128(kb + off), kIdescS, kk > 0);
-        }
-        tc_commit(&s_full[s]);
-      };
-      auto issue_pv = [&](int s, int half, bool add) {   // O (+)= P V
-        const uint32_t vb = ring + (half % S) * C::kHalf;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_bf16_ts(tmem + C::kOCol + s * D, tmem + s * kStepKeys + u * 32 + kk * 8,
-                           sdesc_kmajor_sw128(vb + u * (C::kHalf / 2) + kk * 32), kIdescO, (add || u + kk > 0) ? 1u : 0u);
-        tc_commit(&pv_done[s]);
-      };
-      auto full = [&](int half) { wait(&kv_full[half % S], (half / S) & 1); };
-      auto free_half = [&](int half) { tc_commit(&kv_empty[half % S]); };
       for (bool go = first(); go && !dead; go = next(), ++k) {
+        const int pair = it.pair, nj = it.nj, lead = pair ? 1 : 2;
         wait(&q_full, k & 1);
         if (dead) break;
-        uint32_t add = 0;    // bit s: stream s's O holds products of this item
-        if (it.pair) {
-          const int mid = it.t.t0 + a.stream_tokens, end = it.t.t0 + it.t.ntok;
-          StepWalk w;
-          w.start(a, m, it.t, it.j);
-          auto wanted = [&]() {   // bit s: stream s has a row that sees keys of the step
-            return (step_counts(a, m, w.s, it.t.t0, mid) ? 1u : 0u) | (step_counts(a, m, w.s, mid, end) ? 2u : 0u);
-          };
-          uint32_t now = wanted();
-          full(c);
-          if (dead) break;
-          for (int s = 0; s < 2; ++s)
-            if (now >> s & 1) issue_s(s, c, true);
-          free_half(c++);
-          if (it.nj == 1) tc_commit(&q_empty);
-          for (int j = 0; j < it.nj && !dead; ++j) {
-            const bool more = j + 1 < it.nj;
-            uint32_t then = 0;
-            if (more) {
-              w.next(a, m, it.t);
-              then = wanted();
-            }
-            bool vr = false, kr = false;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (now >> s & 1) {
-                if (!vr) full(c);
-                vr = true;
-                wait(&p_full[s], p_par >> s & 1);
-                if (dead) break;
-                issue_pv(s, c, add >> s & 1);
-                add |= 1u << s;
-                p_par ^= 1u << s;
-              }
-              if (then >> s & 1) {
-                if (!kr) full(c + 1);
-                kr = true;
-                if (dead) break;
-                issue_s(s, c + 1, true);
-              }
-            }
-            // a half that no stream needed is still waited for before it goes back
-            if (!dead && !vr) full(c);
-            if (!dead && more && !kr) full(c + 1);
-            if (dead) break;
-            free_half(c++);
-            if (more) {
-              free_half(c++);
-              if (j + 2 == it.nj) tc_commit(&q_empty);
-            }
-            now = then;
-          }
-        } else {
-          for (int j = 0; j < min(2, it.nj) && !dead; ++j) {
-            full(c);
-            if (dead) break;
-            issue_s(j, c, false);
-            free_half(c++);
-          }
-          if (it.nj <= 2 && !dead) tc_commit(&q_empty);
-          for (int j = 0; j < it.nj && !dead; ++j) {
-            const int s = j & 1;
-            full(c);
-            wait(&p_full[s], p_par >> s & 1);
-            if (dead) break;
-            issue_pv(s, c, add >> s & 1);
-            add |= 1u << s;
-            p_par ^= 1u << s;
-            free_half(c++);
-            if (j + 2 < it.nj) {
-              full(c);
+        bool add = false;
+        uint32_t takes = 0;   // bit i: the stream takes step j + i
+#pragma unroll 1
+        for (int j = -lead; j < nj && !dead; ++j) {
+          if (j >= 0) {   // O (+)= P V
+            const int slot = c % S;
+            wait(&kv_full[slot], (c / S) & 1);
+            if (takes & 1) {
+              wait(&p_full[s], np & 1);
               if (dead) break;
-              issue_s(s, c, false);
-              free_half(c++);
-              if (j + 3 == it.nj) tc_commit(&q_empty);
+              const uint32_t vb = sdesc_low(ring + slot * C::kHalf);
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_bf16_ts(tmem + C::kOCol + s * D, tmem + s * kStepKeys + kk * 8,
+                               sdesc_of(vb + (((kk >> 2) * (C::kHalf / 2) + (kk & 3) * 32) >> 4)), kIdescO,
+                               (add || kk > 0) ? 1u : 0u);
+              tc_commit(&kv_empty[slot]);
+              add = true;
+              ++np;
+            } else {
+              if (dead) break;
+              mbar_arrive(&kv_empty[slot]);
             }
+            ++c;
           }
+          if (j + lead < nj) {   // S = Q K^T
+            const int slot = c % S;
+            wait(&kv_full[slot], (c / S) & 1);
+            if (dead) break;
+            const bool take = pair ? s_step[steps % kStepRing] >> (2 + s) & 1 : ((j + lead) & 1) == s;
+            if (take) {
+              const uint32_t qb = sdesc_low(q_base + (pair ? s * C::kHalf : 0)), kb = sdesc_low(ring + slot * C::kHalf);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+                tc_mma_bf16(tmem + s * kStepKeys, sdesc_of(qb + off), sdesc_of(kb + off), kIdescS, kk > 0);
+              }
+              tc_commit(&s_full[s]);
+              tc_commit(&kv_empty[slot]);
+              takes |= 1u << lead;
+            } else {
+              mbar_arrive(&kv_empty[slot]);
+            }
+            ++c;
+            ++steps;
+            if (j + lead + 1 == nj) tc_commit(&q_empty);   // the item's queries are not needed any more
+          }
+          takes >>= 1;
         }
+        if (dead) break;
+        if (add) tc_commit(&o_done[s]);   // only then does the softmax wait for it
       }
       // every issued product completes before TMEM and shared memory are released
       tc_commit(&mma_done);
       mbar_wait(&mma_done, 0);
     }
-  }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany) : "memory");
     // ---------------- softmax and output ----------------
     const int stream = warp >= kSoftWarp0 + 4 ? 1 : 0;
     const int quarter = warp & 3, r = quarter * 32 + lane;
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     int ns = 0;         // S tiles taken by this stream
     int nx = 0;         // alternating tiles ended
-    int items = 0;
+    int items = 0, outs = 0;   // items, those of them with products of this stream
     int step0 = 0;      // steps of the CTA's items before this one
     bool dead = false;
     // waits taken by all 32 lanes together, so the warp-collective TMEM
@@ -748,68 +757,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
         const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
         const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
-        uint32_t pk[32];
         if (__all_sync(0xffffffffu, none)) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = 0u;
-          tmem_st_u32(s_tmem, pk);
-          tmem_st_u32(s_tmem + 32, pk);
+          const uint32_t zero[16] = {};
+#pragma unroll 1
+          for (int c0 = 0; c0 < kStepKeys / 2; c0 += 16) tmem_st_u16(s_tmem + c0, zero);
         } else {
-          // a half of the scores at a time: the second for its maximum, the
-          // first for its maximum and weights, the second again. P replaces
-          // scores of the first half, which are in registers by then.
-          const int gone = s_gone[(step0 + j) % kStepRing];
+          const int gone = s_step[(step0 + j) % kStepRing] & 3;
           const bool plain =
               __all_sync(0xffffffffu, c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys)) && gone == 0;
+          // a half of the scores (one page) at a time: for the maximum, and
+          // again for the weights
           float sv[64];
-          auto load = [&](int c0) {
-            tmem_ld64(s_tmem + c0, sv);
+          auto load = [&](int u) {
+            tmem_ld64(s_tmem + u * kPage, sv);
             if (!plain) {
-              const int end = gone >> (c0 / 64) & 1 ? 0 : c_hi - c0;
+              const int c0 = u * kPage;
+              unsigned long long vis = slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
+              if (gone >> u & 1) vis = 0;
+              const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
 #pragma unroll
-              for (int c = 0; c < 64; ++c)
-                sv[c] = c < end && (c >= c_lo - c0 || c < c_sink - c0) ? sv[c] : -INFINITY;
+              for (int c = 0; c < 32; ++c) {
+                sv[c] = v0 >> c & 1 ? sv[c] : -INFINITY;
+                sv[32 + c] = v1 >> c & 1 ? sv[32 + c] : -INFINITY;
+              }
             }
           };
-          load(64);
-          const float mx1 = row_max(sv);
-          load(0);
-          const float mx = fmaxf(row_max(sv), mx1) * sl2 - kBias;
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            load(u);
+            mx = fmaxf(mx, row_max(sv));
+          }
+          mx = mx * sl2 - kBias;
           if (__any_sync(0xffffffffu, mx > mref + kRescaleLog2)) {
             const float nm = fmaxf(mref, mx);
             const float alpha = nm == -INFINITY ? 1.f : ex2(mref - nm);
             l *= alpha;
             mref = nm;
-            if (done > 0) {   // O holds the stream's products so far: wait for them, then rescale
-              warp_wait(&pv_done[stream], (ns - 1) & 1);
-              if (!dead) {
+            if (done > 0) {
+              // O holds the stream's products so far: they were issued before
+              // the product whose scores these are, and end in that order
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                  float o[32];
-                  tmem_ld32(o_tmem + c0, o);
+              for (int c0 = 0; c0 < D; c0 += 32) {
+                float o[32];
+                tmem_ld32(o_tmem + c0, o);
 #pragma unroll
-                  for (int c = 0; c < 32; ++c) o[c] *= alpha;
-                  tmem_st32(o_tmem + c0, o);
-                }
-                tmem_wait_st();
+                for (int c = 0; c < 32; ++c) o[c] *= alpha;
+                tmem_st32(o_tmem + c0, o);
               }
+              tmem_wait_st();
             }
           }
           const float neg = mref == -INFINITY ? 0.f : -mref;
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          auto weights = [&](uint32_t p_tmem) {
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
+            load(u);
+            uint32_t pk[32];
+            // exponentials, then packing, then sums: the three in turn for each
+            // pair cost 5.7 instead of 5.2 cycles a value (two warps a scheduler)
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float p0 = ex2(fmaf(sv[2 * c], sl2, neg));
-              const float p1 = ex2(fmaf(sv[2 * c + 1], sl2, neg));
-              sum[c & 3] += p0 + p1;
-              pk[c] = pack2<F16>(p0, p1);
-            }
-            tmem_st_u32(p_tmem, pk);
-          };
-          weights(s_tmem);
-          load(64);
-          weights(s_tmem + 32);
+            for (int c = 0; c < 64; ++c) sv[c] = ex2_here(fmaf(sv[c], sl2, neg));
+#pragma unroll
+            for (int c = 0; c < 32; ++c) pk[c] = pack2<F16>(sv[2 * c], sv[2 * c + 1]);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) sum[c & 3] += sv[c];
+            tmem_st_u32(s_tmem + u * (kPage / 2), pk);
+          }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
         tmem_wait_st();
@@ -820,78 +834,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (dead) break;
       step0 += it.nj;
-      if (done > 0) {
-        warp_wait(&pv_done[stream], (ns - 1) & 1);
-        if (dead) break;
-      }
+      if (done > 0) warp_wait(&o_done[stream], outs++ & 1);
+      if (dead) break;
 
       const bool whole = it.nj == it.t.n;
       const bool live = row.token >= 0;
       const size_t prow = partial_row(a, it, stream, r);
       uint16_t* out = out_row(a, row.token, it.head, r % G, D);
       float* part = a.part_o + prow * D;
-      auto store32 = [&](int c0, const float (&o)[32]) {
-        if (whole) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 8)
-            *reinterpret_cast<uint4*>(out + c0 + c) =
-                make_uint4(pack2<F16>(o[c], o[c + 1]), pack2<F16>(o[c + 2], o[c + 3]), pack2<F16>(o[c + 4], o[c + 5]),
-                           pack2<F16>(o[c + 6], o[c + 7]));
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<float4*>(part + c0 + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-        }
-      };
-      float check = 0.f;   // NaN once a stored value is not finite
-      if (it.pair) {
-        const float f = whole ? (l > 0.f || l != l ? 1.f / l : 0.f) : 1.f;
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          float o[32];
-          if (done > 0) tmem_ld32(o_tmem + c0, o);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            o[c] = done > 0 && l != 0.f ? o[c] * f : 0.f;
-            check = fmaf(o[c], 0.f, check);
-          }
-          if (live) store32(c0, o);
-        }
-        if (live && !whole) a.part_ml[prow] = make_float2(mref, l);
-      } else {
-        // both streams hold a part of every row's sum: each group joins half of the columns
+      // A pair's stream has its rows' whole sums in its O. Of an alternating
+      // tile both streams hold a part of every row's: the groups exchange
+      // maxima and sums, and each joins half of the columns.
+      float w0 = 1.f, w1 = 0.f, top = mref, lj = l;   // out = w0 * O of stream s0 + w1 * O of stream 1
+      int col = 0, col_end = D, s0 = stream;
+      bool use0 = done > 0 && l != 0.f, use1 = false;   // a stream without a visible key has no O to read
+      if (!it.pair) {
         if (stream == 0) s_bad[r] = 0;
         s_ml[stream][r] = make_float2(mref, l);
         warp_arrive(&x_ml);
         warp_wait(&x_ml, nx & 1);
         if (dead) break;
         const float2 m0 = s_ml[0][r], m1 = s_ml[1][r];
-        const float top = fmaxf(m0.x, m1.x);
-        float w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - top), w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - top);
-        const float lj = m0.y * w0 + m1.y * w1;
-        if (whole) {
-          const float f = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
-          w0 *= f;
-          w1 *= f;
-        }
-        const bool has1 = it.nj > 1;
+        top = fmaxf(m0.x, m1.x);
+        w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - top);
+        w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - top);
+        lj = m0.y * w0 + m1.y * w1;
+        use0 = m0.y != 0.f;
+        use1 = m1.y != 0.f;
+        s0 = 0;
+        col = stream * (D / 2);
+        col_end = col + D / 2;
+      }
+      if (whole) {
+        const float f = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
+        w0 *= f;
+        w1 *= f;
+      }
+      const bool any0 = __any_sync(0xffffffffu, use0), any1 = __any_sync(0xffffffffu, use1);
+      float check = 0.f;   // NaN once a stored value is not finite
 #pragma unroll 1
-        for (int c0 = 0; c0 < D / 2; c0 += 32) {
-          const int col = stream * (D / 2) + c0;
-          float o0[32], o1[32];
-          tmem_ld32(lane_tmem + C::kOCol + col, o0);
-          if (has1) tmem_ld32(lane_tmem + C::kOCol + D + col, o1);
+      for (; col < col_end; col += 32) {
+        float o[32];
+        if (any0) tmem_ld32(lane_tmem + C::kOCol + s0 * D + col, o);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float o = m0.y != 0.f ? o0[c] * w0 : 0.f;
-            if (has1 && m1.y != 0.f) o = fmaf(o1[c], w1, o);
-            o0[c] = o;
-            check = fmaf(o, 0.f, check);
-          }
-          if (live) store32(col, o0);
+        for (int c = 0; c < 32; ++c) o[c] = use0 ? o[c] * w0 : 0.f;
+        if (any1) {
+          float o1[32];
+          tmem_ld32(lane_tmem + C::kOCol + D + col, o1);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] = use1 ? fmaf(o1[c], w1, o[c]) : o[c];
         }
+#pragma unroll
+        for (int c = 0; c < 32; ++c) check = fmaf(o[c], 0.f, check);
+        if (live && whole) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            *reinterpret_cast<uint4*>(out + col + c) =
+                make_uint4(pack2<F16>(o[c], o[c + 1]), pack2<F16>(o[c + 2], o[c + 3]), pack2<F16>(o[c + 4], o[c + 5]),
+                           pack2<F16>(o[c + 6], o[c + 7]));
+        } else if (live) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 4)
+            *reinterpret_cast<float4*>(part + col + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+        }
+        __syncwarp();   // the next loads are the warp's
+      }
+      if (live && !whole && (it.pair || stream == 0)) a.part_ml[prow] = make_float2(top, lj);
+      if (!it.pair) {
         if (live && check != 0.f) s_bad[r] = 1;
-        if (live && !whole && stream == 0) a.part_ml[prow] = make_float2(top, lj);
         // also: both groups have read both O before either's next P lets O be overwritten
         warp_arrive(&x_bad);
         warp_wait(&x_bad, nx & 1);
@@ -1010,7 +1020,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p,
   if (e != cudaSuccess) return e;
   e = launch_pdl(paged_attn_kernel<D, F16>, dim3(p.ctas), dim3(kThreads), Cfg<D>::kSmem, s, maps, a);
   if (e != cudaSuccess) return e;
-  const int rows = std::min(8, (p.rows_cap + kCombineWarps - 1) / kCombineWarps);
+  const int rows = (p.rows_cap + kCombineWarps - 1) / kCombineWarps;
   return launch_pdl(paged_combine_kernel<D, F16>, dim3(p.ctas, rows), dim3(kCombineWarps * 32), 0, s, a);
 }
 
