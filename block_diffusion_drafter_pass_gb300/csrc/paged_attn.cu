@@ -130,7 +130,7 @@ struct Tile {
 
 __device__ __forceinline__ int steps_of(int keys) { return keys > 0 ? (keys + kStepKeys - 1) / kStepKeys : 0; }
 
-__device__ __forceinline__ Tile tile_at(const PagedAttnArgs& a, const Meta& m, int tile) {
+__device__ __noinline__ Tile tile_at(const PagedAttnArgs& a, const Meta& m, int tile) {
   Tile r;
   if (a.shared) {
     r.t0 = m.q[0] + tile * a.tile_tokens;
@@ -174,7 +174,7 @@ struct Step {
 struct StepWalk {
   Step s;
   int left;   // steps left in this run of keys
-  __device__ __forceinline__ void start(const PagedAttnArgs& a, const Meta& m, const Tile& t, int j) {
+  __device__ __noinline__ void start(const PagedAttnArgs& a, const Meta& m, const Tile& t, int j) {
     if (a.shared) {
       if (j < t.head_steps) {
         s = Step{-1, j * kStepKeys, a.prefix_len};
@@ -212,7 +212,7 @@ struct StepWalk {
 };
 
 // Whether some row of the tokens [ta, tb) of a tile sees a key of the step.
-__device__ __forceinline__ bool step_counts(const PagedAttnArgs& a, const Meta& m, const Step& s, int ta, int tb) {
+__device__ __noinline__ bool step_counts(const PagedAttnArgs& a, const Meta& m, const Step& s, int ta, int tb) {
   if (s.seq < 0) return true;
   const int q0 = m.q[s.seq], q1 = m.q[s.seq + 1];
   const int first = max(ta, q0), last = min(tb, q1) - 1;
@@ -230,7 +230,7 @@ struct Row {
   int lo, hi;
 };
 
-__device__ __forceinline__ Row row_at(const PagedAttnArgs& a, const Meta& m, const Tile& t, int stream, int r) {
+__device__ __noinline__ Row row_at(const PagedAttnArgs& a, const Meta& m, const Tile& t, int stream, int r) {
   Row x;
   const int j = r / a.b.group, token = t.t0 + stream * a.stream_tokens + j;
   x.token = j < a.stream_tokens && token < t.t0 + t.ntok ? token : -1;
@@ -281,7 +281,7 @@ __device__ __forceinline__ bool cut_item(Item& it) {
   return it.nj > 0;
 }
 
-__device__ __forceinline__ bool first_item(const PagedAttnArgs& a, const Meta& m, Item& it, const int* begin,
+__device__ __noinline__ bool first_item(const PagedAttnArgs& a, const Meta& m, Item& it, const int* begin,
                                            long long places) {
   if (places <= 0) return false;
   it.todo = places;
@@ -292,7 +292,7 @@ __device__ __forceinline__ bool first_item(const PagedAttnArgs& a, const Meta& m
   return cut_item(it);
 }
 
-__device__ __forceinline__ bool next_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
+__device__ __noinline__ bool next_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
   if (it.todo <= 0) return false;
   it.place = 0;
   if (++it.head == a.b.n_kv) {
@@ -352,6 +352,42 @@ __device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Meta& m, con
   }
 }
 
+// Barriers by shared-window address. The wait is a loop of a few instructions
+// in place (a called or clocked one costs every role's round a hundred and
+// more): each try gives up after a microsecond at the latest, and the wait
+// after kWaitTries of them or when *abort is set. False when it gave up.
+constexpr uint32_t kWaitTries = 1u << 21;
+
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 n, f;\n\tmov.b32 n, %4;\n"
+      "again:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+      "@p bra done;\n\t"
+      "ld.volatile.shared.b32 f, [%3];\n\t"
+      "setp.ne.b32 p, f, 0;\n\t"
+      "@p bra fail;\n\t"
+      "sub.u32 n, n, 1;\n\t"
+      "setp.ne.u32 p, n, 0;\n\t"
+      "@p bra again;\n"
+      "fail:\n\tmov.b32 %0, 0;\n\tbra over;\n"
+      "done:\n\tmov.b32 %0, 1;\n"
+      "over:\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(abort), "n"(kWaitTries)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void bar_commit(uint32_t bar) {   // tc_commit
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Sum over the threads before this one; `total` over all. One int64 per warp in s_part.
 __device__ __forceinline__ long long block_scan(long long v, long long* s_part, long long& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -390,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *s_q = s_ints, *s_len = s_ints + kPagedMaxSeqs + 1, *s_base = s_ints + 2 * (kPagedMaxSeqs + 1);
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], turn[2];
   __shared__ __align__(8) uint64_t x_ml, x_bad;   // the two softmax groups at an alternating tile's end
   __shared__ float2 s_ml[2][kRows];
   __shared__ uint8_t s_bad[kRows];
@@ -419,6 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);
       mbar_init(&o_done[s], 1);
+      mbar_init(&turn[s], 1);
     }
     mbar_init(&x_ml, 8);
     mbar_init(&x_bad, 8);
@@ -485,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item& it = s_item[warp];   // written by lane 0
   auto first = [&]() { return first_item(a, m, it, s_begin, x1 - x0); };
   auto next = [&]() { return next_item(a, m, it); };
+  const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag));
   auto give_up = [&]() {
     abort_flag = 1;
     latch_status(a.b.status, kDevTimeout);
@@ -524,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto q_now = [&]() {
         if (!q_due || dead) return;
-        if (!mbar_wait(&q_empty, (nq & 1) ^ 1, &abort_flag)) {
+        if (!bar_wait(smem_u32(&q_empty), (nq & 1) ^ 1, abort_at)) {
           give_up();
           dead = true;
           return;
@@ -638,74 +676,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     // passed over halves could meet a barrier a whole turn of the ring away.
     if (lane == 0) {
       const int s = warp - 1;
-      const uint32_t q_base = smem_u32(smem), ring = q_base + C::kQBytes;
-      int c = 0, steps = 0, k = 0, np = 0;   // ring halves, steps with scores, items, P tiles taken
-      bool dead = false;
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (dead || !mbar_wait(bar, parity, &abort_flag)) {
-          if (!dead) give_up();
-          dead = true;
-        }
-        tc_fence_after();
-      };
-      for (bool go = first(); go && !dead; go = next(), ++k) {
+      const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kQBytes >> 4);
+      const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+      const uint32_t s_at = smem_u32(&s_full[s]), p_at = smem_u32(&p_full[s]);
+      const uint32_t turn_at = smem_u32(&turn[s]), pass_at = smem_u32(&turn[s ^ 1]);
+      const uint32_t s_col = tmem + s * kStepKeys, o_col = tmem + C::kOCol + s * D;
+      int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
+      bool ok = true;
+      for (bool go = first(); go; go = next(), ++k) {
         const int pair = it.pair, nj = it.nj, lead = pair ? 1 : 2;
-        wait(&q_full, k & 1);
-        if (dead) break;
-        bool add = false;
+        const uint32_t q_at = q_low + (pair ? s * (C::kHalf >> 4) : 0);
+        ok = bar_wait(smem_u32(&q_full), k & 1, abort_at);
+        uint32_t add = 0;
         uint32_t takes = 0;   // bit i: the stream takes step j + i
 #pragma unroll 1
-        for (int j = -lead; j < nj && !dead; ++j) {
-          if (j >= 0) {   // O (+)= P V
-            const int slot = c % S;
-            wait(&kv_full[slot], (c / S) & 1);
-            if (takes & 1) {
-              wait(&p_full[s], np & 1);
-              if (dead) break;
-              const uint32_t vb = sdesc_low(ring + slot * C::kHalf);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_bf16_ts(tmem + C::kOCol + s * D, tmem + s * kStepKeys + kk * 8,
-                               sdesc_of(vb + (((kk >> 2) * (C::kHalf / 2) + (kk & 3) * 32) >> 4)), kIdescO,
-                               (add || kk > 0) ? 1u : 0u);
-              tc_commit(&kv_empty[slot]);
-              add = true;
-              ++np;
-            } else {
-              if (dead) break;
-              mbar_arrive(&kv_empty[slot]);
+        for (int j = -lead; j < nj && ok; ++j) {
+          const int pv = j >= 0, more = j + lead < nj;
+          const int ck = c + pv, vslot = c % S, kslot = ck % S;
+          if (pv) ok = bar_wait(full_at + vslot * 8, c / S & 1, abort_at);
+          // of a pair, whose steps are long, everything is waited for before the
+          // products, so that they follow each other; an alternating tile's
+          // values go back as soon as they can
+          bool take = ((j + lead) & 1) == s && more;
+          if (pair) {
+            if (more) {
+              ok = ok && bar_wait(full_at + kslot * 8, ck / S & 1, abort_at);
+              take = s_step[steps % kStepRing] >> (2 + s) & 1;
             }
-            ++c;
+            if (pv) ok = ok && bar_wait(p_at, np++ & 1, abort_at);
+            // the streams of a pair take turns: their products in one block
+            // each, so that one stream's run while the other's softmax does
+            if (s == 1 || turns > 0) ok = ok && bar_wait(turn_at, (s == 1 ? turns : turns - 1) & 1, abort_at);
+            ++turns;
+          } else if (takes & 1) {
+            ok = ok && bar_wait(p_at, np++ & 1, abort_at);
           }
-          if (j + lead < nj) {   // S = Q K^T
-            const int slot = c % S;
-            wait(&kv_full[slot], (c / S) & 1);
-            if (dead) break;
-            const bool take = pair ? s_step[steps % kStepRing] >> (2 + s) & 1 : ((j + lead) & 1) == s;
-            if (take) {
-              const uint32_t qb = sdesc_low(q_base + (pair ? s * C::kHalf : 0)), kb = sdesc_low(ring + slot * C::kHalf);
+          if (!ok) break;
+          tc_fence_after();
+          if (takes & 1) {   // O (+)= P V
+            const uint32_t v_at = ring_low + vslot * (C::kHalf >> 4);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
-                tc_mma_bf16(tmem + s * kStepKeys, sdesc_of(qb + off), sdesc_of(kb + off), kIdescS, kk > 0);
-              }
-              tc_commit(&s_full[s]);
-              tc_commit(&kv_empty[slot]);
-              takes |= 1u << lead;
-            } else {
-              mbar_arrive(&kv_empty[slot]);
-            }
-            ++c;
-            ++steps;
-            if (j + lead + 1 == nj) tc_commit(&q_empty);   // the item's queries are not needed any more
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (((kk >> 2) * (C::kHalf / 2) + (kk & 3) * 32) >> 4)),
+                             kIdescO, kk > 0 ? 1u : add);
+            bar_commit(empty_at + vslot * 8);
+            add = 1;
+          } else if (pv) {
+            bar_arrive(empty_at + vslot * 8);
           }
+          if (!pair && more) {
+            ok = bar_wait(full_at + kslot * 8, ck / S & 1, abort_at);
+            if (!ok) break;
+          }
+          if (take) {   // S = Q K^T
+            const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+              tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
+            }
+            bar_commit(s_at);
+            bar_commit(empty_at + kslot * 8);
+            takes |= 1u << lead;
+          } else if (more) {
+            if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
+            bar_arrive(empty_at + kslot * 8);
+          }
+          if (pair) bar_arrive(pass_at);
+          c = ck + more;
+          steps += more;
+          if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
           takes >>= 1;
         }
-        if (dead) break;
-        if (add) tc_commit(&o_done[s]);   // only then does the softmax wait for it
+        if (!ok) {
+          give_up();
+          break;
+        }
+        if (add) bar_commit(smem_u32(&o_done[s]));   // only then does the softmax wait for it
       }
       // every issued product completes before TMEM and shared memory are released
-      tc_commit(&mma_done);
+      bar_commit(smem_u32(&mma_done));
       mbar_wait(&mma_done, 0);
     }
   } else {
@@ -724,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // waits taken by all 32 lanes together, so the warp-collective TMEM
     // accesses after them never diverge (also when a wait runs out)
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar, parity, &abort_flag))) {
+      if (!__all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, abort_at))) {
         give_up();
         dead = true;
       }
@@ -742,16 +792,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!s_go[warp] || dead) break;
       ++items;
       const Row row = row_at(a, m, it.t, it.pair ? stream : 0, r);
-      const int ta = it.t.t0 + (stream ? a.stream_tokens : 0);
-      const int tb = min(ta + a.stream_tokens, it.t.t0 + it.t.ntok);
       float mref = -INFINITY, l = 0.f;   // the row's reference maximum (log2 units, less the bias), sum
       int done = 0;                      // steps of this item that this stream took
       StepWalk w;
       w.start(a, m, it.t, it.j);
       for (int j = 0; j < it.nj; ++j, w.next(a, m, it.t)) {
-        if (it.pair ? !step_counts(a, m, w.s, ta, tb) : ((j & 1) != stream)) continue;
+        if (!it.pair && (j & 1) != stream) continue;
         warp_wait(&s_full[stream], ns & 1);
         if (dead) break;
+        const int flags = s_step[(step0 + j) % kStepRing];
+        if (it.pair && !(flags >> (2 + stream) & 1)) {   // no row of the stream sees the step
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[stream]);
+          ++ns;
+          continue;
+        }
         // columns [0, c_hi) less those in [c_sink, c_lo) are seen
         const RowSpan sp = span_of(a, row, w.s);
         const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
@@ -762,33 +817,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c0 = 0; c0 < kStepKeys / 2; c0 += 16) tmem_st_u16(s_tmem + c0, zero);
         } else {
-          const int gone = s_step[(step0 + j) % kStepRing] & 3;
-          const bool plain =
-              __all_sync(0xffffffffu, c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys)) && gone == 0;
-          // a half of the scores (one page) at a time: for the maximum, and
-          // again for the weights
-          float sv[64];
-          auto load = [&](int u) {
-            tmem_ld64(s_tmem + u * kPage, sv);
-            if (!plain) {
-              const int c0 = u * kPage;
-              unsigned long long vis = slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
-              if (gone >> u & 1) vis = 0;
-              const uint32_t v0 = static_cast<uint32_t>(vis), v1 = static_cast<uint32_t>(vis >> 32);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                sv[c] = v0 >> c & 1 ? sv[c] : -INFINITY;
-                sv[32 + c] = v1 >> c & 1 ? sv[32 + c] : -INFINITY;
-              }
-            }
-          };
-          float mx = -INFINITY;
+          const int gone = flags & 3;
+          if (gone != 0 || !__all_sync(0xffffffffu, c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys))) {
+            // scores of keys that the row does not see become -inf in place
 #pragma unroll 1
-          for (int u = 0; u < 2; ++u) {
-            load(u);
-            mx = fmaxf(mx, row_max(sv));
+            for (int c0 = 0; c0 < kStepKeys; c0 += 32) {
+              const unsigned long long seen = slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
+              const uint32_t vis = gone >> (c0 / kPage) & 1 ? 0u : static_cast<uint32_t>(seen);
+              float x[32];
+              tmem_ld32(s_tmem + c0, x);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[c] = vis >> c & 1 ? x[c] : -INFINITY;
+              tmem_st32(s_tmem + c0, x);
+            }
+            tmem_wait_st();
           }
-          mx = mx * sl2 - kBias;
+          // a half of the scores (one page) at a time: the second for its
+          // maximum, the first for its maximum and weights, the second again
+          float sv[64];
+          auto load = [&](int u) { tmem_ld64(s_tmem + u * kPage, sv); };
+          load(1);
+          float mx = row_max(sv);
+          load(0);
+          mx = fmaxf(mx, row_max(sv)) * sl2 - kBias;
           if (__any_sync(0xffffffffu, mx > mref + kRescaleLog2)) {
             const float nm = fmaxf(mref, mx);
             const float alpha = nm == -INFINITY ? 1.f : ex2(mref - nm);
@@ -812,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
           for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
-            load(u);
+            if (u == 1) load(1);
             uint32_t pk[32];
             // exponentials, then packing, then sums: the three in turn for each
             // pair cost 5.7 instead of 5.2 cycles a value (two warps a scheduler)
