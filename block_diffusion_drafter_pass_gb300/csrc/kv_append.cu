@@ -168,8 +168,8 @@ const char* paged_check(const dflash_paged_batch* b) {
   if (!b) return "null batch";
   if (b->dtype != DFLASH_BF16 && b->dtype != DFLASH_FP16) return "dtype is neither DFLASH_BF16 nor DFLASH_FP16";
   if (b->head_dim != 64 && b->head_dim != 128) return "head_dim must be 64 or 128";
-  if (b->n_kv_heads < 1 || b->n_kv_heads > 1024 || b->n_heads < 1 || b->n_heads % b->n_kv_heads)
-    return "n_kv_heads must be 1..1024 and divide n_heads";
+  if (b->n_kv_heads < 1 || b->n_kv_heads > 128 || b->n_heads < 1 || b->n_heads % b->n_kv_heads)
+    return "n_kv_heads must be 1..128 and divide n_heads";
   if (b->n_heads / b->n_kv_heads > 128) return "more than 128 query heads per kv head";
   if (b->n_seq < 0 || b->n_seq > kPagedMaxSeqs) return "n_seq must be 0..1024";
   if (b->n_tokens < 0 || b->n_tokens > (1 << 24)) return "n_tokens must be 0..2^24";
@@ -178,7 +178,7 @@ const char* paged_check(const dflash_paged_batch* b) {
   if (misaligned16(b->pool)) return "the pool must be 16-byte aligned";
   if (b->n_pages < 1) return "n_pages must be positive";
   if (b->table_pages < 1 || b->table_pages > kPagedMaxTable || b->table_stride < b->table_pages)
-    return "table_pages must be 1..2^24, and table_stride at least that";
+    return "table_pages must be 1..2^20, and table_stride at least that";
   return nullptr;
 }
 

@@ -22,7 +22,7 @@
 namespace dfl {
 
 constexpr int kPagedMaxSeqs = 1024;      // sequences of one call (their bounds are held in shared memory)
-constexpr int kPagedMaxTable = 1 << 24;  // pages of one sequence: positions stay below 2^30
+constexpr int kPagedMaxTable = 1 << 20;  // pages of one sequence: positions stay below 2^26, a batch's steps of keys below 2^30
 
 // The batch as the kernels read it. All arrays are on the device.
 struct PagedView {

@@ -113,6 +113,28 @@ __device__ __forceinline__ float ex2_here(float x) {
   return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ unsigned long long bits2(float2 v) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+  return r;
+}
+__device__ __forceinline__ float2 floats2(unsigned long long v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)), "l"(bits2(z)));
+  return floats2(r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+  return floats2(r);
+}
+
 // The sequences' metadata in shared memory (bent into range when loaded).
 struct Meta {
   const int* q;      // [n_seq + 1]
@@ -223,6 +245,12 @@ __device__ __noinline__ bool step_counts(const PagedAttnArgs& a, const Meta& m, 
   return true;
 }
 
+// Bit s: stream s of a pair takes the step.
+__device__ __noinline__ int pair_takes(const PagedAttnArgs& a, const Meta& m, const Tile& t, const Step& s) {
+  const int mid = t.t0 + a.stream_tokens;
+  return (step_counts(a, m, s, t.t0, mid) ? 1 : 0) | (step_counts(a, m, s, mid, t.t0 + t.ntok) ? 2 : 0);
+}
+
 // The row of one softmax thread: what it sees of its sequence's cache, and (of
 // a shared prefix) prefix_len more.
 struct Row {
@@ -262,43 +290,37 @@ struct Item {
   int tile, head, j, nj;
   int pair;         // each stream has its own 128 rows (else: the same rows, every other step)
   int place;        // the run's place within this tile and head
-  long long todo;   // places of the CTA from this item on
+  int todo;         // places of the CTA from this item on
 };
 
 __device__ __forceinline__ int places_of(int steps) { return steps + kItemSteps; }
 
-__device__ __forceinline__ void set_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
-  it.t = tile_at(a, m, it.tile);
-  it.pair = it.t.ntok > a.stream_tokens;
-}
-
 // The item at the run's place; false when the run ends before its steps.
 __device__ __forceinline__ bool cut_item(Item& it) {
-  const int take = static_cast<int>(min(it.todo, static_cast<long long>(places_of(it.t.n) - it.place)));
+  const int take = min(it.todo, places_of(it.t.n) - it.place);
   it.j = max(it.place - kItemSteps, 0);
   it.nj = it.place + take - kItemSteps - it.j;
   it.todo -= take;
   return it.nj > 0;
 }
 
-__device__ __noinline__ bool first_item(const PagedAttnArgs& a, const Meta& m, Item& it, const int* begin,
-                                           long long places) {
-  if (places <= 0) return false;
-  it.todo = places;
-  it.tile = begin[0];
-  it.head = begin[1];
-  it.place = begin[2];
-  set_item(a, m, it);
-  return cut_item(it);
-}
-
+// The run's next item (its first: it.tile holds ~tile).
 __device__ __noinline__ bool next_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
   if (it.todo <= 0) return false;
-  it.place = 0;
-  if (++it.head == a.b.n_kv) {
-    it.head = 0;
-    ++it.tile;
-    set_item(a, m, it);
+  bool other = it.tile < 0;
+  if (other) {
+    it.tile = ~it.tile;
+  } else {
+    it.place = 0;
+    if (++it.head == a.b.n_kv) {
+      it.head = 0;
+      ++it.tile;
+      other = true;
+    }
+  }
+  if (other) {
+    it.t = tile_at(a, m, it.tile);
+    it.pair = it.t.ntok > a.stream_tokens;
   }
   return cut_item(it);
 }
@@ -356,7 +378,7 @@ __device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Meta& m, con
 // in place (a called or clocked one costs every role's round a hundred and
 // more): each try gives up after a microsecond at the latest, and the wait
 // after kWaitTries of them or when *abort is set. False when it gave up.
-constexpr uint32_t kWaitTries = 1u << 21;
+constexpr uint32_t kWaitTries = 1u << 21;   // with tries of 1 us at most: 2 s
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
   uint32_t ok;
@@ -386,6 +408,30 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 
 __device__ __forceinline__ void bar_commit(uint32_t bar) {   // tc_commit
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// The warp's lane 0's value, as one that the compiler knows to be the warp's.
+template <typename T>
+__device__ __forceinline__ T warp_uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// tma_load_3d by shared-window addresses.
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
 }
 
 // Sum over the threads before this one; `total` over all. One int64 per warp in s_part.
@@ -435,11 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of a pair takes the step
   __shared__ uint8_t s_step[kStepRing];
   __shared__ long long s_part[kThreads / 32];
-  __shared__ int s_begin[3];
+  __shared__ int s_begin[3];   // where this CTA's run begins: ~tile, kv head, place
   __shared__ Item s_item[kThreads / 32];
-  __shared__ int s_go[kThreads / 32];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
+  __shared__ int s_never;   // 0: the flag of waits that must not be cut short
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_seq = a.b.n_seq, n_kv = a.b.n_kv, G = a.b.group;
@@ -460,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&x_ml, 8);
     mbar_init(&x_bad, 8);
     abort_flag = 0;
-    s_begin[0] = -1;
+    s_never = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
@@ -470,9 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
-  // ---- the batch's shape, and this CTA's run of steps ----
+  // ---- the batch's shape, and this CTA's run of places ----
   load_q_start(a.b, s_q, reinterpret_cast<int*>(s_part));
   long long total = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < n_seq; i0 += kThreads) {
     const int i = i0 + tid;
     int v = 0;
@@ -494,25 +541,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (n_tiles + kThreads - 1) / kThreads;
   const int tile_a = min(tid * per, n_tiles), tile_b = min(tile_a + per, n_tiles);
   long long mine = 0;
+#pragma unroll 1
   for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(places_of(tile_at(a, m, t).n)) * n_kv;
   long long all;
   const long long before = block_scan(mine, s_part, all);
-  const long long ctas = min(static_cast<long long>(gridDim.x), all);
-  const bool works = blockIdx.x < ctas;
-  const long long x0 = works ? all * blockIdx.x / ctas : 0;
-  const long long x1 = works ? all * (blockIdx.x + 1) / ctas : 0;
-  if (works && x0 >= before && x0 < before + mine) {
+  // CTA c takes the places [c * run, (c + 1) * run)
+  const int run = static_cast<int>((all + gridDim.x - 1) / gridDim.x);
+  const long long x0 = static_cast<long long>(run) * blockIdx.x;
+  const int x_len = static_cast<int>(max(0ll, min(static_cast<long long>(run), all - x0)));
+  if (x_len > 0 && x0 >= before && x0 < before + mine) {
     long long rem = x0 - before;
-    for (int t = tile_a; t < tile_b; ++t) {
-      const int n = places_of(tile_at(a, m, t).n);
-      if (rem < static_cast<long long>(n) * n_kv) {
-        s_begin[0] = t;
-        s_begin[1] = static_cast<int>(rem / n);
-        s_begin[2] = static_cast<int>(rem % n);
-        break;
-      }
+    int t = tile_a, n;
+#pragma unroll 1
+    while (true) {
+      n = places_of(tile_at(a, m, t).n);
+      if (rem < static_cast<long long>(n) * n_kv) break;
       rem -= static_cast<long long>(n) * n_kv;
+      ++t;
     }
+    s_begin[0] = ~t;
+    s_begin[1] = static_cast<int>(rem / n);
+    s_begin[2] = static_cast<int>(rem - static_cast<long long>(s_begin[1]) * n);
   }
   tc_fence_before();
   __syncthreads();
@@ -520,9 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
 
   Item& it = s_item[warp];   // written by lane 0
-  auto first = [&]() { return first_item(a, m, it, s_begin, x1 - x0); };
-  auto next = [&]() { return next_item(a, m, it); };
-  const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag));
+  if (lane == 0) {
+    it.tile = s_begin[0];
+    it.head = s_begin[1];
+    it.place = s_begin[2];
+    it.todo = x_len;
+  }
+  const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag)), never_at = smem_u32(&s_never);
   auto give_up = [&]() {
     abort_flag = 1;
     latch_status(a.b.status, kDevTimeout);
@@ -538,89 +591,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   // and last steps of an item took 3 to 7 us each instead of 1).
 
   if (warp == 0) {
-    // ---------------- queries, keys and values ----------------
+    // ---------------- keys and values ----------------
     if (lane == 0) {
+      const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty), ring = smem_u32(smem) + C::kQBytes;
       int c = 0, steps = 0;   // ring halves, steps whose keys were brought
-      bool dead = false;
+      bool ok = true;
       int4 split = make_int4(0, 0, 0, 0);
-      // The queries of an item can come when the products S of the item before
-      // are done; its first keys and values need not wait for that, so the
-      // queries are brought in from the ring's waits.
-      int nq = 0;          // items whose queries are on their way
-      int q_pair = 0, q_head = 0, q_t0 = 0;   // the item whose queries are due
-      bool q_due = false;
-      auto bring_q = [&]() {
-        const int n = q_pair ? 2 : 1;
-        mbar_arrive_expect_tx(&q_full, n * (D / 64) * a.stream_tokens * G * 128);
-        for (int s = 0; s < n; ++s)
-#pragma unroll
-          for (int bx = 0; bx < D / 64; ++bx)
-            tma_load_3d(smem + s * C::kHalf + bx * C::kBox, &maps.q, &q_full, bx * 64, q_head * G,
-                        q_t0 + s * a.stream_tokens);
-        ++nq;
-        q_due = false;
-      };
-      auto q_now = [&]() {
-        if (!q_due || dead) return;
-        if (!bar_wait(smem_u32(&q_empty), (nq & 1) ^ 1, abort_at)) {
-          give_up();
-          dead = true;
-          return;
-        }
-        bring_q();
-      };
-      for (bool go = first(); go && !dead; go = next()) {
-        q_now();
-        q_pair = it.pair;
-        q_head = it.head;
-        q_t0 = it.t.t0;
-        q_due = true;
-        const int lead = it.pair ? 1 : 2;
+      while (ok && next_item(a, m, it)) {
+        const int lead = it.pair ? 1 : 2, nj = it.nj;
         // Page ids are copied kIdsAhead steps before their keys are due, so no
         // load waits for one.
         StepWalk wf, wk;   // of the ids, of the keys
         wf.start(a, m, it.t, it.j);
         wk = wf;
         const int step0 = steps;
-        int nf = 0;        // steps of this item whose ids are on their way
-        auto fetch_ids = [&]() {
-          if (nf < it.nj) {
-            const int32_t* table = table_of(a, wf.s.seq);
-            int* dst = s_page[(step0 + nf) % kIdRing];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int key0 = wf.s.base + u * kPage;
-              if (key0 < wf.s.end) copy_async4(dst + u, table + key0 / kPage);
-              else dst[u] = -1;
-            }
-            wf.next(a, m, it.t);
-            ++nf;
-          }
-          copy_async_commit();
-        };
-        for (int i = 0; i < kIdsAhead; ++i) fetch_ids();
 #pragma unroll 1
-        for (int i = -2 * lead; i < 2 * it.nj; ++i) {   // round i >> 1: values, then keys
+        for (int i = -2 * (lead + kIdsAhead); i < 2 * nj; ++i) {   // round i >> 1: values, then ids and keys
           const bool keys = i & 1;
           const int j = (i >> 1) + (keys ? lead : 0);
-          if (j < 0 || j >= it.nj) continue;
           if (keys) {
-            fetch_ids();
+            const int jf = j + kIdsAhead;
+            if (jf < nj) {
+              const int32_t* table = table_of(a, wf.s.seq);
+              int* dst = s_page[(step0 + jf) % kIdRing];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int key0 = wf.s.base + u * kPage;
+                if (key0 < wf.s.end) copy_async4(dst + u, table + key0 / kPage);
+                else dst[u] = -1;
+              }
+              wf.next(a, m, it.t);
+            }
+            copy_async_commit();
             copy_async_wait<kIdsAhead>();
           }
+          if (j < 0 || j >= nj) continue;
           const int slot = c % S;
-          const unsigned long long t_wait = global_ns();
-          while (true) {
-            if (q_due && mbar_test_wait(&q_empty, (nq & 1) ^ 1)) bring_q();
-            if (mbar_try_wait(&kv_empty[slot], ((c / S) & 1) ^ 1)) break;
-            if (abort_flag || global_ns() - t_wait > kWaitLimitNs) {
-              give_up();
-              dead = true;
-              break;
-            }
-          }
-          if (dead) break;
-          uint8_t* dst = smem + C::kQBytes + slot * C::kHalf;
+          ok = bar_wait(empty_at + slot * 8, (c / S & 1) ^ 1, abort_at);
+          if (!ok) break;
+          const uint32_t dst = ring + slot * C::kHalf, bar = full_at + slot * 8;
           // a page past the sequence's end, or none of the pool's, reads as
           // zeros: from behind the pool's last page
           int page[2], gone = 0;
@@ -634,39 +643,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (keys) {
             if (gone && wk.s.base + (gone == 2 ? kPage : 0) < wk.s.end) latch_status(a.b.status, kDevBounds);
             int flags = gone;
-            if (it.pair) {
-              const int mid = it.t.t0 + a.stream_tokens;
-              flags |= (step_counts(a, m, wk.s, it.t.t0, mid) ? 4 : 0) |
-                       (step_counts(a, m, wk.s, mid, it.t.t0 + it.t.ntok) ? 8 : 0);
-            }
+            if (it.pair) flags |= pair_takes(a, m, it.t, wk.s) << 2;
             wk.next(a, m, it.t);
             s_step[steps++ % kStepRing] = static_cast<uint8_t>(flags);   // read behind this half's barrier and the product's
           }
-          mbar_arrive_expect_tx(&kv_full[slot], C::kHalf);
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(C::kHalf) : "memory");
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             if (keys) {
 #pragma unroll
               for (int bx = 0; bx < D / 64; ++bx)
-                tma_load_3d(dst + bx * C::kBox + u * (C::kBox / 2), &maps.k, &kv_full[slot], bx * 64, it.head * kPage,
-                            page[u]);
+                box_load(dst + bx * C::kBox + u * (C::kBox / 2), &maps.k, bar, bx * 64, it.head * kPage, page[u]);
             } else {
-              tma_load_3d(dst + u * (C::kHalf / 2), &maps.v, &kv_full[slot], 0, it.head * D, page[u]);
+              box_load(dst + u * (C::kHalf / 2), &maps.v, bar, 0, it.head * D, page[u]);
             }
           }
           ++c;
         }
-        if (it.j == 0 && it.nj < it.t.n) {   // the run ends here: the tile's last place is in CTA c with all * c / ctas <= it
-          const long long last = x1 + it.t.n - it.nj - 1;
-          split = make_int4(it.t.t0, it.t.ntok, it.head,
-                            static_cast<int>(((last + 1) * ctas - 1) / all) - static_cast<int>(blockIdx.x) + 1);
+        if (!ok) {
+          give_up();
+          break;
+        }
+        if (it.j == 0 && nj < it.t.n) {   // the run ends here: the tile's last place is in CTA `place / run`
+          const long long last = x0 + x_len + it.t.n - nj - 1;
+          split = make_int4(it.t.t0, it.t.ntok, it.head, static_cast<int>(last / run) - static_cast<int>(blockIdx.x) + 1);
         }
       }
-      q_now();
       a.split[blockIdx.x] = split;
       // copies still in flight complete before shared memory is released
-      for (int j = max(0, c - S); j < c; ++j) mbar_wait(&kv_full[j % S], (j / S) & 1);
-      if (nq > 0) mbar_wait(&q_full, (nq - 1) & 1);
+#pragma unroll 1
+      for (int j = max(0, c - S); j < c; ++j) bar_wait(full_at + (j % S) * 8, j / S & 1, never_at);
     }
   } else if (warp < kSoftWarp0) {
     // ---------------- products of one stream ----------------
@@ -674,62 +680,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     // scores of the step `lead` later, where the stream takes them. Each stream
     // waits for every half and arrives for it, its own or not: a stream that
     // passed over halves could meet a barrier a whole turn of the ring away.
-    if (lane == 0) {
-      const int s = warp - 1;
-      const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kQBytes >> 4);
-      const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
-      const uint32_t s_at = smem_u32(&s_full[s]), p_at = smem_u32(&p_full[s]);
-      const uint32_t turn_at = smem_u32(&turn[s]), pass_at = smem_u32(&turn[s ^ 1]);
-      const uint32_t s_col = tmem + s * kStepKeys, o_col = tmem + C::kOCol + s * D;
-      int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
-      bool ok = true;
-      for (bool go = first(); go; go = next(), ++k) {
-        const int pair = it.pair, nj = it.nj, lead = pair ? 1 : 2;
-        const uint32_t q_at = q_low + (pair ? s * (C::kHalf >> 4) : 0);
-        ok = bar_wait(smem_u32(&q_full), k & 1, abort_at);
-        uint32_t add = 0;
-        uint32_t takes = 0;   // bit i: the stream takes step j + i
+    // The warp goes through this as one, with one elected lane in front of the
+    // instructions, so that descriptors stay in uniform registers: with one
+    // lane alone in here a product took 98 cycles to issue beside the softmax
+    // warps, against 64 to run.
+    const int s = warp_uniform(warp - 1);
+    const bool one = elect_one();
+    const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kQBytes >> 4);
+    const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+    const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0]) + s * 8;
+    const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
+    const uint32_t tm = warp_uniform(tmem);
+    const uint32_t s_col = tm + s * kStepKeys, o_col = tm + C::kOCol + s * D;
+    int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, abort_at));
+    };
+    while (true) {
+      int go = 0;
+      if (lane == 0) go = next_item(a, m, it);
+      __syncwarp();
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
+      if (s == 0) {   // the item's queries, when both streams are done with the last one's
+        if (k > 0) wait(smem_u32(&q_empty), (k - 1) & 1);
+        if (ok && one) {
+          const uint32_t bar = smem_u32(&q_full);
+          const int n = pair ? 2 : 1;
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                       "r"(n * (D / 64) * a.stream_tokens * G * 128)
+                       : "memory");
 #pragma unroll 1
-        for (int j = -lead; j < nj && ok; ++j) {
-          const int pv = j >= 0, more = j + lead < nj;
-          const int ck = c + pv, vslot = c % S, kslot = ck % S;
-          if (pv) ok = bar_wait(full_at + vslot * 8, c / S & 1, abort_at);
-          // of a pair, whose steps are long, everything is waited for before the
-          // products, so that they follow each other; an alternating tile's
-          // values go back as soon as they can
-          bool take = ((j + lead) & 1) == s && more;
-          if (pair) {
-            if (more) {
-              ok = ok && bar_wait(full_at + kslot * 8, ck / S & 1, abort_at);
-              take = s_step[steps % kStepRing] >> (2 + s) & 1;
-            }
-            if (pv) ok = ok && bar_wait(p_at, np++ & 1, abort_at);
-            // the streams of a pair take turns: their products in one block
-            // each, so that one stream's run while the other's softmax does
-            if (s == 1 || turns > 0) ok = ok && bar_wait(turn_at, (s == 1 ? turns : turns - 1) & 1, abort_at);
-            ++turns;
-          } else if (takes & 1) {
-            ok = ok && bar_wait(p_at, np++ & 1, abort_at);
+          for (int i = 0; i < n * (D / 64); ++i) {
+            const int st = i / (D / 64), bx = i % (D / 64);
+            box_load(smem_u32(smem) + st * C::kHalf + bx * C::kBox, &maps.q, bar, bx * 64, it.head * G,
+                     it.t.t0 + st * a.stream_tokens);
           }
-          if (!ok) break;
-          tc_fence_after();
-          if (takes & 1) {   // O (+)= P V
-            const uint32_t v_at = ring_low + vslot * (C::kHalf >> 4);
+        }
+        __syncwarp();
+      }
+      const uint32_t q_at = q_low + (pair ? s * (C::kHalf >> 4) : 0);
+      wait(smem_u32(&q_full), k & 1);
+      ++k;
+      uint32_t add = 0;
+      uint32_t takes = 0;   // bit i: the stream takes step j + i
+#pragma unroll 1
+      for (int j = -lead; j < nj && ok; ++j) {
+        const int pv = j >= 0, more = j + lead < nj;
+        const int ck = c + pv, vslot = c % S, kslot = ck % S;
+        if (pv) wait(full_at + vslot * 8, c / S & 1);
+        // of a pair, whose steps are long, everything is waited for before the
+        // products, so that they follow each other; an alternating tile's
+        // values go back as soon as they can
+        uint32_t take = ((j + lead) & 1) == s && more;
+        if (pair) {
+          if (more) {
+            wait(full_at + kslot * 8, ck / S & 1);
+            take = warp_uniform(s_step[steps % kStepRing] >> (2 + s) & 1);
+          }
+          if (pv) wait(p_at, np++ & 1);
+          // the streams of a pair take turns: their products in one block each,
+          // so that one stream's run while the other's softmax does
+          if (s == 1 || turns > 0) wait(turn_at, (s == 1 ? turns : turns - 1) & 1);
+          ++turns;
+        } else if (takes & 1) {
+          wait(p_at, np++ & 1);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        if (takes & 1) {   // O (+)= P V
+          const uint32_t v_at = ring_low + vslot * (C::kHalf >> 4);
+          if (one) {
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (((kk >> 2) * (C::kHalf / 2) + (kk & 3) * 32) >> 4)),
                              kIdescO, kk > 0 ? 1u : add);
             bar_commit(empty_at + vslot * 8);
-            add = 1;
-          } else if (pv) {
-            bar_arrive(empty_at + vslot * 8);
           }
-          if (!pair && more) {
-            ok = bar_wait(full_at + kslot * 8, ck / S & 1, abort_at);
-            if (!ok) break;
-          }
-          if (take) {   // S = Q K^T
-            const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
+          add = 1;
+        } else if (pv && one) {
+          bar_arrive(empty_at + vslot * 8);
+        }
+        __syncwarp();
+        if (!pair && more) {
+          wait(full_at + kslot * 8, ck / S & 1);
+          if (!ok) break;
+        }
+        if (take) {   // S = Q K^T
+          const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
+          if (one) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
@@ -737,27 +777,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bar_commit(s_at);
             bar_commit(empty_at + kslot * 8);
-            takes |= 1u << lead;
-          } else if (more) {
-            if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
-            bar_arrive(empty_at + kslot * 8);
           }
+          takes |= 1u << lead;
+        } else if (more && one) {
+          if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
+          bar_arrive(empty_at + kslot * 8);
+        }
+        if (one) {
           if (pair) bar_arrive(pass_at);
-          c = ck + more;
-          steps += more;
           if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
-          takes >>= 1;
         }
-        if (!ok) {
-          give_up();
-          break;
-        }
-        if (add) bar_commit(smem_u32(&o_done[s]));   // only then does the softmax wait for it
+        __syncwarp();
+        c = ck + more;
+        steps += more;
+        takes >>= 1;
       }
-      // every issued product completes before TMEM and shared memory are released
-      bar_commit(smem_u32(&mma_done));
-      mbar_wait(&mma_done, 0);
+      if (!ok) {
+        give_up();
+        break;
+      }
+      if (add && one) bar_commit(smem_u32(&o_done[0]) + s * 8);   // only then does the softmax wait for it
     }
+    // every issued product completes before TMEM and shared memory are released
+    if (one) bar_commit(smem_u32(&mma_done));
+    bar_wait(smem_u32(&mma_done), 0, never_at);
   } else {
     // ---------------- softmax and output ----------------
     const int stream = warp >= kSoftWarp0 + 4 ? 1 : 0;
@@ -768,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl2 = a.scale_log2;
     int ns = 0;         // S tiles taken by this stream
     int nx = 0;         // alternating tiles ended
-    int items = 0, outs = 0;   // items, those of them with products of this stream
+    int outs = 0;       // items with products of this stream
     int step0 = 0;      // steps of the CTA's items before this one
     bool dead = false;
     // waits taken by all 32 lanes together, so the warp-collective TMEM
@@ -785,12 +828,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    while (true) {
+    while (!dead) {
       __syncwarp();
-      if (lane == 0) s_go[warp] = items == 0 ? first() : next();
-      __syncwarp();
-      if (!s_go[warp] || dead) break;
-      ++items;
+      int go = 0;
+      if (lane == 0) go = next_item(a, m, it);
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
       const Row row = row_at(a, m, it.t, it.pair ? stream : 0, r);
       float mref = -INFINITY, l = 0.f;   // the row's reference maximum (log2 units, less the bias), sum
       int done = 0;                      // steps of this item that this stream took
@@ -860,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float neg = mref == -INFINITY ? 0.f : -mref;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
           for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
             if (u == 1) load(1);
@@ -868,14 +910,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             // exponentials, then packing, then sums: the three in turn for each
             // pair cost 5.7 instead of 5.2 cycles a value (two warps a scheduler)
 #pragma unroll
-            for (int c = 0; c < 64; ++c) sv[c] = ex2_here(fmaf(sv[c], sl2, neg));
+            for (int c = 0; c < 32; ++c) {
+              const float2 e = fma2(make_float2(sv[2 * c], sv[2 * c + 1]), make_float2(sl2, sl2), make_float2(neg, neg));
+              sv[2 * c] = ex2_here(e.x);
+              sv[2 * c + 1] = ex2_here(e.y);
+            }
 #pragma unroll
             for (int c = 0; c < 32; ++c) pk[c] = pack2<F16>(sv[2 * c], sv[2 * c + 1]);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) sum[c & 3] += sv[c];
+            for (int c = 0; c < 32; ++c) sum[c & 1] = add2(sum[c & 1], make_float2(sv[2 * c], sv[2 * c + 1]));
             tmem_st_u32(s_tmem + u * (kPage / 2), pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         }
         tmem_wait_st();
         warp_arrive(&p_full[stream]);
@@ -1164,7 +1210,7 @@ extern "C" dflash_status dflash_shared_prefix_attn(const dflash_paged_batch* b, 
                                                    long long out_stride, int causal, float scale, void* workspace,
                                                    size_t workspace_bytes, void* stream) {
   if (const char* why = attn_check(b, q, q_stride, out, out_stride, scale)) return refuse(why);
-  if (prefix_len < 0 || prefix_len > (1 << 30)) return refuse("prefix_len must be 0..2^30");
+  if (prefix_len < 0 || prefix_len > kPage * kPagedMaxTable) return refuse("prefix_len must be 0..2^26");
   if (b->n_seq == 0 || b->n_tokens == 0) return DFLASH_OK;
   if (prefix_len > 0 && !prefix_table) return refuse("null pointer");
   PagedAttnArgs a = attn_args(*b, q, q_stride, out, out_stride, causal, scale);

@@ -424,12 +424,12 @@ enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1 };
 typedef struct {
   int dtype;                 /* of pool and token buffers: DFLASH_BF16 or DFLASH_FP16 */
   int n_heads;               /* query heads; head h reads kv head h / (n_heads / n_kv_heads) */
-  int n_kv_heads;            /* divides n_heads, at most 128 query heads each       */
+  int n_kv_heads;            /* 1..128, divides n_heads, at most 128 query heads each */
   int head_dim;              /* d: 64 or 128                                        */
   int n_seq;                 /* 0..1024                                             */
   int n_tokens;              /* rows of the token buffers, 0..2^24                  */
   int n_pages;
-  int table_pages;           /* entries of a page-table row: 1..2^24                */
+  int table_pages;           /* entries of a page-table row: 1..2^20                */
   long long table_stride;    /* elements between page-table rows, >= table_pages    */
   void* pool;                /* device, 16-byte aligned                             */
   const int32_t* page_table; /* device [n_seq][table_stride]                        */
@@ -485,7 +485,7 @@ dflash_status dflash_paged_attn(const dflash_paged_batch* b, const void* q, long
  * lies before its own cache sees prefix keys up to its place only). Prefix
  * keys and values are read once for all tokens, not once for each sequence.
  *  prefix_table  device [ceil(prefix_len / 64)] page ids
- *  prefix_len    0..2^30 (0: dflash_paged_attn without a window)
+ *  prefix_len    0..2^26 (0: dflash_paged_attn without a window)
  * Errors: EINVAL, ECUDA. */
 dflash_status dflash_shared_prefix_attn(const dflash_paged_batch* b, const int32_t* prefix_table, int prefix_len,
                                         const void* q, long long q_stride, void* out, long long out_stride, int causal,
