@@ -83,6 +83,8 @@ struct PagedMaps {
   CUtensorMap k, v, q;
 };
 
+constexpr int kBatchBytes = 4 * (3 * kPagedMaxSeqs + 16);
+
 template <int D>
 struct Cfg {
   static constexpr int kBox = kRows * 128;                  // 128 rows of 64 elements, swizzled
@@ -90,8 +92,7 @@ struct Cfg {
   static constexpr int kSlots = D == 128 ? 4 : 8;
   static constexpr int kQBytes = 2 * kHalf;                 // queries of both streams
   static constexpr int kIntOff = kQBytes + kSlots * kHalf;
-  static constexpr int kInts = 3 * (kPagedMaxSeqs + 1);     // q_start, kv_len, tile or step bases
-  static constexpr int kSmem = kIntOff + kInts * 4 + 1024;
+  static constexpr int kSmem = kIntOff + kBatchBytes + 1024;
   static_assert(kSmem <= 227 * 1024 - 4096, "static shared variables need the rest");
   // TMEM columns: S of the streams (P over its first 64), then their O
   static constexpr uint32_t kOCol = 2 * kStepKeys;
@@ -135,12 +136,19 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return floats2(r);
 }
 
-// The sequences' metadata in shared memory (bent into range when loaded).
-struct Meta {
-  const int* q;      // [n_seq + 1]
-  const int* len;    // [n_seq]
-  const int* base;   // [n_seq + 1] own cache: tiles before a sequence; shared: own-cache steps before it
+// What the walk over the work needs, in shared memory: functions that are
+// called take it by reference, and a reference to registers or parameters
+// would put those into local memory.
+struct Batch {
+  int shared, causal, window, sinks, prefix_len;
+  int stream_tokens, tile_tokens;
+  int n_seq, n_kv, group;
+  int q[kPagedMaxSeqs + 1];      // the bounds of the sequences' tokens (bent into range)
+  int len[kPagedMaxSeqs];        // their cached tokens
+  int base[kPagedMaxSeqs + 1];   // own cache: tiles before a sequence; shared: own-cache steps before it
 };
+
+static_assert(sizeof(Batch) <= kBatchBytes, "room for the batch");
 
 struct Tile {
   int t0, ntok;         // tokens
@@ -152,35 +160,35 @@ struct Tile {
 
 __device__ __forceinline__ int steps_of(int keys) { return keys > 0 ? (keys + kStepKeys - 1) / kStepKeys : 0; }
 
-__device__ __noinline__ Tile tile_at(const PagedAttnArgs& a, const Meta& m, int tile) {
+__device__ __forceinline__ Tile tile_at(const Batch& b, int tile) {
   Tile r;
-  if (a.shared) {
-    r.t0 = m.q[0] + tile * a.tile_tokens;
-    r.ntok = min(a.tile_tokens, m.q[a.b.n_seq] - r.t0);
+  if (b.shared) {
+    r.t0 = b.q[0] + tile * b.tile_tokens;
+    r.ntok = min(b.tile_tokens, b.q[b.n_seq] - r.t0);
     const int last = r.t0 + r.ntok - 1;
-    r.seq0 = seq_of_token(m.q, a.b.n_seq, r.t0);
-    r.seq1 = seq_of_token(m.q, a.b.n_seq, last);
-    r.head_steps = steps_of(a.prefix_len);
+    r.seq0 = seq_of_token(b.q, b.n_seq, r.t0);
+    r.seq1 = seq_of_token(b.q, b.n_seq, last);
+    r.head_steps = steps_of(b.prefix_len);
     r.window_step = 0;
     // the last sequence may go on behind the tile: its keys up to the tile's last row
-    const int end = a.causal ? m.len[r.seq1] - (m.q[r.seq1 + 1] - 1 - last) : m.len[r.seq1];
-    r.n = max(1, r.head_steps + m.base[r.seq1] - m.base[r.seq0] + steps_of(end));
+    const int end = b.causal ? b.len[r.seq1] - (b.q[r.seq1 + 1] - 1 - last) : b.len[r.seq1];
+    r.n = max(1, r.head_steps + b.base[r.seq1] - b.base[r.seq0] + steps_of(end));
     return r;
   }
-  int lo = 0, hi = a.b.n_seq - 1;   // the last sequence whose tiles start at or before this one
+  int lo = 0, hi = b.n_seq - 1;   // the last sequence whose tiles start at or before this one
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (m.base[mid] <= tile) lo = mid;
+    if (b.base[mid] <= tile) lo = mid;
     else hi = mid - 1;
   }
   r.seq0 = r.seq1 = lo;
-  r.t0 = m.q[lo] + (tile - m.base[lo]) * a.tile_tokens;
-  r.ntok = min(a.tile_tokens, m.q[lo + 1] - r.t0);
-  const int pos0 = m.len[lo] - (m.q[lo + 1] - r.t0);
-  const int end = a.causal ? pos0 + r.ntok : m.len[lo];
+  r.t0 = b.q[lo] + (tile - b.base[lo]) * b.tile_tokens;
+  r.ntok = min(b.tile_tokens, b.q[lo + 1] - r.t0);
+  const int pos0 = b.len[lo] - (b.q[lo + 1] - r.t0);
+  const int end = b.causal ? pos0 + r.ntok : b.len[lo];
   const int w1 = steps_of(end);
-  const int w0 = a.window > 0 ? min(max(0, pos0 - a.window + 1) / kStepKeys, w1) : 0;
-  r.head_steps = min(steps_of(a.sinks), w0);
+  const int w0 = b.window > 0 ? min(max(0, pos0 - b.window + 1) / kStepKeys, w1) : 0;
+  r.head_steps = min(steps_of(b.sinks), w0);
   r.window_step = w0;
   r.n = max(1, r.head_steps + w1 - w0);
   return r;
@@ -196,59 +204,59 @@ struct Step {
 struct StepWalk {
   Step s;
   int left;   // steps left in this run of keys
-  __device__ __noinline__ void start(const PagedAttnArgs& a, const Meta& m, const Tile& t, int j) {
-    if (a.shared) {
+  __device__ __forceinline__ void start(const Batch& b, const Tile& t, int j) {
+    if (b.shared) {
       if (j < t.head_steps) {
-        s = Step{-1, j * kStepKeys, a.prefix_len};
+        s = Step{-1, j * kStepKeys, b.prefix_len};
         left = t.head_steps - j;
         return;
       }
-      const int want = m.base[t.seq0] + j - t.head_steps;
+      const int want = b.base[t.seq0] + j - t.head_steps;
       int lo = t.seq0, hi = t.seq1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (m.base[mid] <= want) lo = mid;
+        if (b.base[mid] <= want) lo = mid;
         else hi = mid - 1;
       }
-      s = Step{lo, (want - m.base[lo]) * kStepKeys, m.len[lo]};
-      left = lo < t.seq1 ? m.base[lo + 1] - want : INT32_MAX;
+      s = Step{lo, (want - b.base[lo]) * kStepKeys, b.len[lo]};
+      left = lo < t.seq1 ? b.base[lo + 1] - want : INT32_MAX;
       return;
     }
     const bool head = j < t.head_steps;
-    s = Step{t.seq0, (head ? j : t.window_step + j - t.head_steps) * kStepKeys, m.len[t.seq0]};
+    s = Step{t.seq0, (head ? j : t.window_step + j - t.head_steps) * kStepKeys, b.len[t.seq0]};
     left = head ? t.head_steps - j : INT32_MAX;
   }
-  __device__ __forceinline__ void next(const PagedAttnArgs& a, const Meta& m, const Tile& t) {
+  __device__ __forceinline__ void next(const Batch& b, const Tile& t) {
     s.base += kStepKeys;
     if (--left > 0) return;
-    if (!a.shared) {
+    if (!b.shared) {
       s.base = t.window_step * kStepKeys;
       left = INT32_MAX;
       return;
     }
     int i = s.seq < 0 ? t.seq0 : s.seq + 1;
-    while (i < t.seq1 && m.base[i + 1] == m.base[i]) ++i;
-    s = Step{i, 0, m.len[i]};
-    left = i < t.seq1 ? m.base[i + 1] - m.base[i] : INT32_MAX;
+    while (i < t.seq1 && b.base[i + 1] == b.base[i]) ++i;
+    s = Step{i, 0, b.len[i]};
+    left = i < t.seq1 ? b.base[i + 1] - b.base[i] : INT32_MAX;
   }
 };
 
 // Whether some row of the tokens [ta, tb) of a tile sees a key of the step.
-__device__ __noinline__ bool step_counts(const PagedAttnArgs& a, const Meta& m, const Step& s, int ta, int tb) {
-  if (s.seq < 0) return true;
-  const int q0 = m.q[s.seq], q1 = m.q[s.seq + 1];
+__device__ __forceinline__ bool step_counts(const Batch& b, int seq, int base, int ta, int tb) {
+  if (seq < 0) return true;
+  const int q0 = b.q[seq], q1 = b.q[seq + 1];
   const int first = max(ta, q0), last = min(tb, q1) - 1;
   if (first > last) return false;
-  const int shift = m.len[s.seq] - q1;   // position of token t: t + shift
-  if (a.causal && s.base > last + shift) return false;
-  if (a.window > 0 && s.base + kStepKeys - 1 < first + shift - a.window + 1 && s.base >= a.sinks) return false;
+  const int shift = b.len[seq] - q1;   // position of token t: t + shift
+  if (b.causal && base > last + shift) return false;
+  if (b.window > 0 && base + kStepKeys - 1 < first + shift - b.window + 1 && base >= b.sinks) return false;
   return true;
 }
 
 // Bit s: stream s of a pair takes the step.
-__device__ __noinline__ int pair_takes(const PagedAttnArgs& a, const Meta& m, const Tile& t, const Step& s) {
-  const int mid = t.t0 + a.stream_tokens;
-  return (step_counts(a, m, s, t.t0, mid) ? 1 : 0) | (step_counts(a, m, s, mid, t.t0 + t.ntok) ? 2 : 0);
+__device__ __noinline__ int pair_takes(const Batch& b, const Tile& t, int seq, int base) {
+  const int mid = t.t0 + b.stream_tokens;
+  return (step_counts(b, seq, base, t.t0, mid) ? 1 : 0) | (step_counts(b, seq, base, mid, t.t0 + t.ntok) ? 2 : 0);
 }
 
 // The row of one softmax thread: what it sees of its sequence's cache, and (of
@@ -258,22 +266,22 @@ struct Row {
   int lo, hi;
 };
 
-__device__ __noinline__ Row row_at(const PagedAttnArgs& a, const Meta& m, const Tile& t, int stream, int r) {
+__device__ __forceinline__ Row row_at(const Batch& b, const Tile& t, int stream, int r) {
   Row x;
-  const int j = r / a.b.group, token = t.t0 + stream * a.stream_tokens + j;
-  x.token = j < a.stream_tokens && token < t.t0 + t.ntok ? token : -1;
-  x.seq = t.seq0 == t.seq1 || x.token < 0 ? t.seq0 : seq_of_token(m.q, a.b.n_seq, x.token);
-  const int pos = m.len[x.seq] - m.q[x.seq + 1] + x.token;
-  x.lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  x.hi = a.causal ? pos : kNoEnd;
+  const int j = r / b.group, token = t.t0 + stream * b.stream_tokens + j;
+  x.token = j < b.stream_tokens && token < t.t0 + t.ntok ? token : -1;
+  x.seq = t.seq0 == t.seq1 || x.token < 0 ? t.seq0 : seq_of_token(b.q, b.n_seq, x.token);
+  const int pos = b.len[x.seq] - b.q[x.seq + 1] + x.token;
+  x.lo = b.window > 0 ? max(0, pos - b.window + 1) : 0;
+  x.hi = b.causal ? pos : kNoEnd;
   return x;
 }
 
 // Its span of a step's run of keys (empty: hi < 0).
-__device__ __forceinline__ RowSpan span_of(const PagedAttnArgs& a, const Row& x, const Step& s) {
+__device__ __forceinline__ RowSpan span_of(const Batch& b, const Row& x, const Step& s) {
   if (x.token < 0 || (s.seq >= 0 && s.seq != x.seq)) return RowSpan{0, -1, 0};
-  if (s.seq < 0) return RowSpan{0, x.hi + a.prefix_len, 0};
-  return RowSpan{x.lo, x.hi, a.sinks};
+  if (s.seq < 0) return RowSpan{0, x.hi + b.prefix_len, 0};
+  return RowSpan{x.lo, x.hi, b.sinks};
 }
 
 __device__ __forceinline__ const int32_t* table_of(const PagedAttnArgs& a, int seq) {
@@ -305,22 +313,22 @@ __device__ __forceinline__ bool cut_item(Item& it) {
 }
 
 // The run's next item (its first: it.tile holds ~tile).
-__device__ __noinline__ bool next_item(const PagedAttnArgs& a, const Meta& m, Item& it) {
+__device__ __noinline__ bool next_item(const Batch& b, Item& it) {
   if (it.todo <= 0) return false;
   bool other = it.tile < 0;
   if (other) {
     it.tile = ~it.tile;
   } else {
     it.place = 0;
-    if (++it.head == a.b.n_kv) {
+    if (++it.head == b.n_kv) {
       it.head = 0;
       ++it.tile;
       other = true;
     }
   }
   if (other) {
-    it.t = tile_at(a, m, it.tile);
-    it.pair = it.t.ntok > a.stream_tokens;
+    it.t = tile_at(b, it.tile);
+    it.pair = it.t.ntok > b.stream_tokens;
   }
   return cut_item(it);
 }
@@ -338,18 +346,18 @@ __device__ __forceinline__ uint16_t* out_row(const PagedAttnArgs& a, int token, 
 // the products gave: they met a non-finite value, which may have come from a
 // place that the row does not see (0 times infinity or NaN).
 template <int D, bool F16>
-__device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Meta& m, const Item& it, int stream, int r) {
+__device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Batch& b, const Item& it, int stream, int r) {
   const int lane = threadIdx.x & 31, rows_of = it.pair ? stream : 0;
-  const Row x = row_at(a, m, it.t, rows_of, r);
+  const Row x = row_at(b, it.t, rows_of, r);
   const int g = r % a.b.group;
   const uint16_t* q = a.q + x.token * a.q_stride + static_cast<long long>(it.head * a.b.group + g) * D;
   const size_t page_elems = static_cast<size_t>(2) * a.b.n_kv * kPage * D;
   RowState<D> st;
   st.clear();
   StepWalk w;
-  w.start(a, m, it.t, it.j);
-  for (int j = 0; j < it.nj; ++j, w.next(a, m, it.t)) {
-    const RowSpan sp = span_of(a, x, w.s);
+  w.start(b, it.t, it.j);
+  for (int j = 0; j < it.nj; ++j, w.next(b, it.t)) {
+    const RowSpan sp = span_of(b, x, w.s);
     for (int u = 0; u < 2; ++u) {
       const int key0 = w.s.base + u * kPage;
       const unsigned long long vis = sp.hi >= 0 ? row_sees(sp, key0, w.s.end) : 0ull;
@@ -456,6 +464,104 @@ __device__ __forceinline__ long long block_scan(long long v, long long* s_part, 
   return before + x - v;
 }
 
+// What the two softmax groups exchange at an alternating tile's end.
+struct Join {
+  uint64_t x_ml, x_bad;
+  float2 ml[2][kRows];
+  uint8_t bad[kRows];
+};
+
+// A stream's part of an item's end: O out of tensor memory, joined with the
+// other stream's where both have the same rows, to `out` when the item is the
+// whole tile, else to the partials. False when a wait ran out. (A function of
+// its own so that its registers are not the softmax loop's.)
+template <int D, bool F16>
+__device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b, const Item& it, Join& join, int stream,
+                                         uint32_t tmem, int token, float mref, float l, bool products, int parity,
+                                         uint32_t abort_at) {
+  const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
+  const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  auto meet = [&](uint64_t* bar) {   // of the two groups' eight warps
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) bar_arrive(smem_u32(bar));
+    const bool ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, abort_at));
+    tc_fence_after();
+    return ok;
+  };
+  const bool whole = it.nj == it.t.n;
+  const bool live = token >= 0;
+  const size_t prow = partial_row(a, it, stream, r);
+  uint16_t* out = out_row(a, token, it.head, r % b.group, D);
+  float* part = a.part_o + prow * D;
+  // A pair's stream has its rows' whole sums in its O. Of an alternating
+  // tile both streams hold a part of every row's: the groups exchange
+  // maxima and sums, and each joins half of the columns.
+  float w0 = 1.f, w1 = 0.f, top = mref, lj = l;   // out = w0 * O of stream s0 + w1 * O of stream 1
+  int col = 0, col_end = D, s0 = stream;
+  bool use0 = products && l != 0.f, use1 = false;   // a stream without a visible key has no O to read
+  if (!it.pair) {
+    if (stream == 0) join.bad[r] = 0;
+    join.ml[stream][r] = make_float2(mref, l);
+    if (!meet(&join.x_ml)) return false;
+    const float2 m0 = join.ml[0][r], m1 = join.ml[1][r];
+    top = fmaxf(m0.x, m1.x);
+    w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - top);
+    w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - top);
+    lj = m0.y * w0 + m1.y * w1;
+    use0 = m0.y != 0.f;
+    use1 = m1.y != 0.f;
+    s0 = 0;
+    col = stream * (D / 2);
+    col_end = col + D / 2;
+  }
+  if (whole) {
+    const float f = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
+    w0 *= f;
+    w1 *= f;
+  }
+  const bool any0 = __any_sync(0xffffffffu, use0), any1 = __any_sync(0xffffffffu, use1);
+  float check = 0.f;   // NaN once a stored value is not finite
+#pragma unroll 1
+  for (; col < col_end; col += 32) {
+    float o[32];
+    if (any0) tmem_ld32(lane_tmem + Cfg<D>::kOCol + s0 * D + col, o);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) o[c] = use0 ? o[c] * w0 : 0.f;
+    if (any1) {
+      float o1[32];
+      tmem_ld32(lane_tmem + Cfg<D>::kOCol + D + col, o1);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) o[c] = use1 ? fmaf(o1[c], w1, o[c]) : o[c];
+    }
+#pragma unroll
+    for (int c = 0; c < 32; ++c) check = fmaf(o[c], 0.f, check);
+    if (live && whole) {
+#pragma unroll
+      for (int c = 0; c < 32; c += 8)
+        *reinterpret_cast<uint4*>(out + col + c) =
+            make_uint4(pack2<F16>(o[c], o[c + 1]), pack2<F16>(o[c + 2], o[c + 3]), pack2<F16>(o[c + 4], o[c + 5]),
+                       pack2<F16>(o[c + 6], o[c + 7]));
+    } else if (live) {
+#pragma unroll
+      for (int c = 0; c < 32; c += 4)
+        *reinterpret_cast<float4*>(part + col + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+    }
+    __syncwarp();   // the next loads are the warp's
+  }
+  if (live && !whole && (it.pair || stream == 0)) a.part_ml[prow] = make_float2(top, lj);
+  if (!it.pair) {
+    if (live && check != 0.f) join.bad[r] = 1;
+    // also: both groups have read both O before either's next P lets O be overwritten
+    if (!meet(&join.x_bad)) return false;
+    check = stream == 0 && join.bad[r] ? 1.f : 0.f;
+  }
+  // rows that met a non-finite value: again, from what they see
+  for (uint32_t bad = __ballot_sync(0xffffffffu, live && check != 0.f); bad; bad &= bad - 1)
+    redo_row<D, F16>(a, b, it, stream, quarter * 32 + __ffs(bad) - 1);
+  return true;
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs a) {
@@ -468,14 +574,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kIdescO = F16 ? idesc_f16_f32(kRows, D) : idesc_bf16_f32(kRows, D);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  int* s_ints = reinterpret_cast<int*>(smem + C::kIntOff);
-  int *s_q = s_ints, *s_len = s_ints + kPagedMaxSeqs + 1, *s_base = s_ints + 2 * (kPagedMaxSeqs + 1);
+  Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], turn[2];
-  __shared__ __align__(8) uint64_t x_ml, x_bad;   // the two softmax groups at an alternating tile's end
-  __shared__ float2 s_ml[2][kRows];
-  __shared__ uint8_t s_bad[kRows];
+  __shared__ Join join;
   __shared__ int s_page[kIdRing][2];
   // of the CTA's recent steps: bit u, page u is not there; bit 2 + s, stream s
   // of a pair takes the step
@@ -503,10 +606,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&o_done[s], 1);
       mbar_init(&turn[s], 1);
     }
-    mbar_init(&x_ml, 8);
-    mbar_init(&x_bad, 8);
+    mbar_init(&join.x_ml, 8);
+    mbar_init(&join.x_bad, 8);
     abort_flag = 0;
     s_never = 0;
+    b.shared = a.shared;
+    b.causal = a.causal;
+    b.window = a.window;
+    b.sinks = a.sinks;
+    b.prefix_len = a.prefix_len;
+    b.stream_tokens = a.stream_tokens;
+    b.tile_tokens = a.tile_tokens;
+    b.n_seq = a.b.n_seq;
+    b.n_kv = a.b.n_kv;
+    b.group = a.b.group;
     fence_mbar_init();
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
@@ -517,32 +630,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
 
   // ---- the batch's shape, and this CTA's run of places ----
-  load_q_start(a.b, s_q, reinterpret_cast<int*>(s_part));
+  load_q_start(a.b, b.q, reinterpret_cast<int*>(s_part));
   long long total = 0;
 #pragma unroll 1
   for (int i0 = 0; i0 < n_seq; i0 += kThreads) {
     const int i = i0 + tid;
     int v = 0;
     if (i < n_seq) {
-      const int nq = s_q[i + 1] - s_q[i], len = cached_tokens(a.b, i);
-      s_len[i] = len;
+      const int nq = b.q[i + 1] - b.q[i], len = cached_tokens(a.b, i);
+      b.len[i] = len;
       if (a.shared) v = nq > 0 ? steps_of(len) : 0;
       else v = (nq + a.tile_tokens - 1) / a.tile_tokens;
     }
     long long part;
     const long long before = total + block_scan(v, s_part, part);
-    if (i < n_seq) s_base[i] = static_cast<int>(before);
+    if (i < n_seq) b.base[i] = static_cast<int>(before);
     total += part;
   }
-  if (tid == 0) s_base[n_seq] = static_cast<int>(total);
+  if (tid == 0) b.base[n_seq] = static_cast<int>(total);
   __syncthreads();
-  const Meta m{s_q, s_len, s_base};
-  const int n_tiles = a.shared ? (s_q[n_seq] - s_q[0] + a.tile_tokens - 1) / a.tile_tokens : static_cast<int>(total);
+  const int n_tiles = a.shared ? (b.q[n_seq] - b.q[0] + a.tile_tokens - 1) / a.tile_tokens : static_cast<int>(total);
   const int per = (n_tiles + kThreads - 1) / kThreads;
   const int tile_a = min(tid * per, n_tiles), tile_b = min(tile_a + per, n_tiles);
   long long mine = 0;
 #pragma unroll 1
-  for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(places_of(tile_at(a, m, t).n)) * n_kv;
+  for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(places_of(tile_at(b, t).n)) * n_kv;
   long long all;
   const long long before = block_scan(mine, s_part, all);
   // CTA c takes the places [c * run, (c + 1) * run)
@@ -554,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int t = tile_a, n;
 #pragma unroll 1
     while (true) {
-      n = places_of(tile_at(a, m, t).n);
+      n = places_of(tile_at(b, t).n);
       if (rem < static_cast<long long>(n) * n_kv) break;
       rem -= static_cast<long long>(n) * n_kv;
       ++t;
@@ -597,12 +709,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int c = 0, steps = 0;   // ring halves, steps whose keys were brought
       bool ok = true;
       int4 split = make_int4(0, 0, 0, 0);
-      while (ok && next_item(a, m, it)) {
+      while (ok && next_item(b, it)) {
         const int lead = it.pair ? 1 : 2, nj = it.nj;
         // Page ids are copied kIdsAhead steps before their keys are due, so no
         // load waits for one.
         StepWalk wf, wk;   // of the ids, of the keys
-        wf.start(a, m, it.t, it.j);
+        wf.start(b, it.t, it.j);
         wk = wf;
         const int step0 = steps;
 #pragma unroll 1
@@ -620,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (key0 < wf.s.end) copy_async4(dst + u, table + key0 / kPage);
                 else dst[u] = -1;
               }
-              wf.next(a, m, it.t);
+              wf.next(b, it.t);
             }
             copy_async_commit();
             copy_async_wait<kIdsAhead>();
@@ -643,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (keys) {
             if (gone && wk.s.base + (gone == 2 ? kPage : 0) < wk.s.end) latch_status(a.b.status, kDevBounds);
             int flags = gone;
-            if (it.pair) flags |= pair_takes(a, m, it.t, wk.s) << 2;
-            wk.next(a, m, it.t);
+            if (it.pair) flags |= pair_takes(b, it.t, wk.s.seq, wk.s.base) << 2;
+            wk.next(b, it.t);
             s_step[steps++ % kStepRing] = static_cast<uint8_t>(flags);   // read behind this half's barrier and the product's
           }
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(C::kHalf) : "memory");
@@ -699,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     while (true) {
       int go = 0;
-      if (lane == 0) go = next_item(a, m, it);
+      if (lane == 0) go = next_item(b, it);
       __syncwarp();
       if (!__shfl_sync(0xffffffffu, go, 0)) break;
       const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
@@ -813,14 +925,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int nx = 0;         // alternating tiles ended
     int outs = 0;       // items with products of this stream
     int step0 = 0;      // steps of the CTA's items before this one
-    bool dead = false;
+    bool ok = true;
     // waits taken by all 32 lanes together, so the warp-collective TMEM
     // accesses after them never diverge (also when a wait runs out)
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, abort_at))) {
-        give_up();
-        dead = true;
-      }
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, abort_at));
       tc_fence_after();
     };
     auto warp_arrive = [&](uint64_t* bar) {
@@ -828,20 +937,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    while (!dead) {
+    while (true) {
       __syncwarp();
       int go = 0;
-      if (lane == 0) go = next_item(a, m, it);
+      if (lane == 0) go = next_item(b, it);
       if (!__shfl_sync(0xffffffffu, go, 0)) break;
-      const Row row = row_at(a, m, it.t, it.pair ? stream : 0, r);
+      const Row row = row_at(b, it.t, it.pair ? stream : 0, r);
       float mref = -INFINITY, l = 0.f;   // the row's reference maximum (log2 units, less the bias), sum
       int done = 0;                      // steps of this item that this stream took
       StepWalk w;
-      w.start(a, m, it.t, it.j);
-      for (int j = 0; j < it.nj; ++j, w.next(a, m, it.t)) {
+      w.start(b, it.t, it.j);
+      for (int j = 0; j < it.nj; ++j, w.next(b, it.t)) {
         if (!it.pair && (j & 1) != stream) continue;
         warp_wait(&s_full[stream], ns & 1);
-        if (dead) break;
+        if (!ok) break;
         const int flags = s_step[(step0 + j) % kStepRing];
         if (it.pair && !(flags >> (2 + stream) & 1)) {   // no row of the stream sees the step
           __syncwarp();
@@ -850,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         // columns [0, c_hi) less those in [c_sink, c_lo) are seen
-        const RowSpan sp = span_of(a, row, w.s);
+        const RowSpan sp = span_of(b, row, w.s);
         const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
         const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
         const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
@@ -927,89 +1036,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&p_full[stream]);
         ++done;
         ++ns;
-        if (dead) break;
+        if (!ok) break;
       }
-      if (dead) break;
+      if (!ok) break;
       step0 += it.nj;
       if (done > 0) warp_wait(&o_done[stream], outs++ & 1);
-      if (dead) break;
+      if (!ok) break;
 
-      const bool whole = it.nj == it.t.n;
-      const bool live = row.token >= 0;
-      const size_t prow = partial_row(a, it, stream, r);
-      uint16_t* out = out_row(a, row.token, it.head, r % G, D);
-      float* part = a.part_o + prow * D;
-      // A pair's stream has its rows' whole sums in its O. Of an alternating
-      // tile both streams hold a part of every row's: the groups exchange
-      // maxima and sums, and each joins half of the columns.
-      float w0 = 1.f, w1 = 0.f, top = mref, lj = l;   // out = w0 * O of stream s0 + w1 * O of stream 1
-      int col = 0, col_end = D, s0 = stream;
-      bool use0 = done > 0 && l != 0.f, use1 = false;   // a stream without a visible key has no O to read
-      if (!it.pair) {
-        if (stream == 0) s_bad[r] = 0;
-        s_ml[stream][r] = make_float2(mref, l);
-        warp_arrive(&x_ml);
-        warp_wait(&x_ml, nx & 1);
-        if (dead) break;
-        const float2 m0 = s_ml[0][r], m1 = s_ml[1][r];
-        top = fmaxf(m0.x, m1.x);
-        w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - top);
-        w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - top);
-        lj = m0.y * w0 + m1.y * w1;
-        use0 = m0.y != 0.f;
-        use1 = m1.y != 0.f;
-        s0 = 0;
-        col = stream * (D / 2);
-        col_end = col + D / 2;
-      }
-      if (whole) {
-        const float f = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
-        w0 *= f;
-        w1 *= f;
-      }
-      const bool any0 = __any_sync(0xffffffffu, use0), any1 = __any_sync(0xffffffffu, use1);
-      float check = 0.f;   // NaN once a stored value is not finite
-#pragma unroll 1
-      for (; col < col_end; col += 32) {
-        float o[32];
-        if (any0) tmem_ld32(lane_tmem + C::kOCol + s0 * D + col, o);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = use0 ? o[c] * w0 : 0.f;
-        if (any1) {
-          float o1[32];
-          tmem_ld32(lane_tmem + C::kOCol + D + col, o1);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] = use1 ? fmaf(o1[c], w1, o[c]) : o[c];
-        }
-#pragma unroll
-        for (int c = 0; c < 32; ++c) check = fmaf(o[c], 0.f, check);
-        if (live && whole) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 8)
-            *reinterpret_cast<uint4*>(out + col + c) =
-                make_uint4(pack2<F16>(o[c], o[c + 1]), pack2<F16>(o[c + 2], o[c + 3]), pack2<F16>(o[c + 4], o[c + 5]),
-                           pack2<F16>(o[c + 6], o[c + 7]));
-        } else if (live) {
-#pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            *reinterpret_cast<float4*>(part + col + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
-        }
-        __syncwarp();   // the next loads are the warp's
-      }
-      if (live && !whole && (it.pair || stream == 0)) a.part_ml[prow] = make_float2(top, lj);
-      if (!it.pair) {
-        if (live && check != 0.f) s_bad[r] = 1;
-        // also: both groups have read both O before either's next P lets O be overwritten
-        warp_arrive(&x_bad);
-        warp_wait(&x_bad, nx & 1);
-        if (dead) break;
-        ++nx;
-        check = stream == 0 && s_bad[r] ? 1.f : 0.f;
-      }
-      // rows that met a non-finite value: again, from what they see
-      for (uint32_t bad = __ballot_sync(0xffffffffu, live && check != 0.f); bad; bad &= bad - 1)
-        redo_row<D, F16>(a, m, it, stream, quarter * 32 + __ffs(bad) - 1);
+      ok = finish_item<D, F16>(a, b, it, join, stream, tmem, row.token, mref, l, done > 0, nx & 1, abort_at);
+      nx += !it.pair;
+      if (!ok) break;
     }
+    if (!ok) give_up();
   }
   __syncwarp();
   tc_fence_before();
