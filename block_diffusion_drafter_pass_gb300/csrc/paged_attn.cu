@@ -54,7 +54,7 @@ constexpr int kRows = 128;            // rows of a stream: the MMA's M
 // ahead of the softmax (a step's values are not overwritten before its P).
 constexpr int kStepRing = 16;
 constexpr int kIdsAhead = 4, kIdRing = 16;   // steps
-constexpr int kItemSteps = 2;         // what an item costs beside its steps, in steps (dealing only)
+constexpr int kItemSteps = 4;         // what an item costs beside its steps, in steps (dealing only)
 constexpr int kNoEnd = 1 << 30;       // above every position
 constexpr float kRescaleLog2 = 8.f;   // rescale O when a row's maximum grows by more than 2^8
 
@@ -303,18 +303,19 @@ struct Item {
 
 __device__ __forceinline__ int places_of(int steps) { return steps + kItemSteps; }
 
-// The item at the run's place; false when the run ends before its steps.
-__device__ __forceinline__ bool cut_item(Item& it) {
+// The item at the run's place; nj <= 0 when the run ends before its steps.
+__device__ __forceinline__ void cut_item(Item& it) {
   const int take = min(it.todo, places_of(it.t.n) - it.place);
   it.j = max(it.place - kItemSteps, 0);
   it.nj = it.place + take - kItemSteps - it.j;
   it.todo -= take;
-  return it.nj > 0;
 }
 
-// The run's next item (its first: it.tile holds ~tile).
-__device__ __noinline__ bool next_item(const Batch& b, Item& it) {
-  if (it.todo <= 0) return false;
+// The run's item after `was` (its first: was.tile holds ~tile); nj = 0: none.
+__device__ __noinline__ void next_item(const Batch& b, const Item& was, Item& it) {
+  it = was;
+  it.nj = 0;
+  if (it.todo <= 0) return;
   bool other = it.tile < 0;
   if (other) {
     it.tile = ~it.tile;
@@ -330,7 +331,7 @@ __device__ __noinline__ bool next_item(const Batch& b, Item& it) {
     it.t = tile_at(b, it.tile);
     it.pair = it.t.ntok > b.stream_tokens;
   }
-  return cut_item(it);
+  cut_item(it);
 }
 
 // Row of a partial: [cta][slot][rows_cap], slot 1 for a tile that begins here.
@@ -492,8 +493,8 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
   const bool whole = it.nj == it.t.n;
   const bool live = token >= 0;
   const size_t prow = partial_row(a, it, stream, r);
-  uint16_t* out = out_row(a, token, it.head, r % b.group, D);
-  float* part = a.part_o + prow * D;
+  char* const to = whole ? reinterpret_cast<char*>(out_row(a, token, it.head, r % b.group, D))
+                         : reinterpret_cast<char*>(a.part_o + prow * D);
   // A pair's stream has its rows' whole sums in its O. Of an alternating
   // tile both streams hold a part of every row's: the groups exchange
   // maxima and sums, and each joins half of the columns.
@@ -522,30 +523,32 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
   }
   const bool any0 = __any_sync(0xffffffffu, use0), any1 = __any_sync(0xffffffffu, use1);
   float check = 0.f;   // NaN once a stored value is not finite
+  // sixteen columns at a time: this runs once an item, so it costs what its
+  // instructions cost to fetch, and more of them at a time were slower
 #pragma unroll 1
-  for (; col < col_end; col += 32) {
-    float o[32];
-    if (any0) tmem_ld32(lane_tmem + Cfg<D>::kOCol + s0 * D + col, o);
+  for (; col < col_end; col += 16) {
+    float o[16];
+    if (any0) tmem_ld16(lane_tmem + Cfg<D>::kOCol + s0 * D + col, o);
 #pragma unroll
-    for (int c = 0; c < 32; ++c) o[c] = use0 ? o[c] * w0 : 0.f;
+    for (int c = 0; c < 16; ++c) o[c] = use0 ? o[c] * w0 : 0.f;
     if (any1) {
-      float o1[32];
-      tmem_ld32(lane_tmem + Cfg<D>::kOCol + D + col, o1);
+      float o1[16];
+      tmem_ld16(lane_tmem + Cfg<D>::kOCol + D + col, o1);
 #pragma unroll
-      for (int c = 0; c < 32; ++c) o[c] = use1 ? fmaf(o1[c], w1, o[c]) : o[c];
+      for (int c = 0; c < 16; ++c) o[c] = use1 ? fmaf(o1[c], w1, o[c]) : o[c];
     }
 #pragma unroll
-    for (int c = 0; c < 32; ++c) check = fmaf(o[c], 0.f, check);
+    for (int c = 0; c < 16; ++c) check = fmaf(o[c], 0.f, check);
     if (live && whole) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 8)
-        *reinterpret_cast<uint4*>(out + col + c) =
+      for (int c = 0; c < 16; c += 8)
+        *reinterpret_cast<uint4*>(to + (col + c) * 2) =
             make_uint4(pack2<F16>(o[c], o[c + 1]), pack2<F16>(o[c + 2], o[c + 3]), pack2<F16>(o[c + 4], o[c + 5]),
                        pack2<F16>(o[c + 6], o[c + 7]));
     } else if (live) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 4)
-        *reinterpret_cast<float4*>(part + col + c) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+      for (int c = 0; c < 16; c += 4)
+        *reinterpret_cast<float4*>(to + (col + c) * 4) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
     }
     __syncwarp();   // the next loads are the warp's
   }
@@ -577,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
-  __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], turn[2];
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
   __shared__ Join join;
   __shared__ int s_page[kIdRing][2];
   // of the CTA's recent steps: bit u, page u is not there; bit 2 + s, stream s
@@ -585,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint8_t s_step[kStepRing];
   __shared__ long long s_part[kThreads / 32];
   __shared__ int s_begin[3];   // where this CTA's run begins: ~tile, kv head, place
-  __shared__ Item s_item[kThreads / 32];
+  __shared__ Item s_items[kThreads / 32][2];   // each warp's item and the one after it
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ int s_never;   // 0: the flag of waits that must not be cut short
@@ -602,7 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&mma_done, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&p_full[s][0], 4);
+      mbar_init(&p_full[s][1], 4);
       mbar_init(&o_done[s], 1);
       mbar_init(&turn[s], 1);
     }
@@ -657,8 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(places_of(tile_at(b, t).n)) * n_kv;
   long long all;
   const long long before = block_scan(mine, s_part, all);
-  // CTA c takes the places [c * run, (c + 1) * run)
-  const int run = static_cast<int>((all + gridDim.x - 1) / gridDim.x);
+  // CTA c takes the places [c * run, (c + 1) * run); of more than 2^31 the run
+  // is rounded up a little
+  const int up = all >> 31 ? 33 - __clzll(all) : 0;
+  const int run = static_cast<int>((static_cast<uint32_t>(all >> up) + (up ? gridDim.x : gridDim.x - 1)) / gridDim.x) << up;
   const long long x0 = static_cast<long long>(run) * blockIdx.x;
   const int x_len = static_cast<int>(max(0ll, min(static_cast<long long>(run), all - x0)));
   if (x_len > 0 && x0 >= before && x0 < before + mine) {
@@ -671,22 +677,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       rem -= static_cast<long long>(n) * n_kv;
       ++t;
     }
+    int head = 0;
+#pragma unroll 1
+    for (; rem >= n; rem -= n) ++head;
     s_begin[0] = ~t;
-    s_begin[1] = static_cast<int>(rem / n);
-    s_begin[2] = static_cast<int>(rem - static_cast<long long>(s_begin[1]) * n);
+    s_begin[1] = head;
+    s_begin[2] = static_cast<int>(rem);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  Item& it = s_item[warp];   // written by lane 0
+  Item* const items = s_items[warp];   // written by lane 0
   if (lane == 0) {
-    it.tile = s_begin[0];
-    it.head = s_begin[1];
-    it.place = s_begin[2];
-    it.todo = x_len;
+    Item& begin = items[1];
+    begin.tile = s_begin[0];
+    begin.head = s_begin[1];
+    begin.place = s_begin[2];
+    begin.todo = x_len;
+    next_item(b, begin, items[0]);
   }
+  __syncwarp();
   const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag)), never_at = smem_u32(&s_never);
   auto give_up = [&]() {
     abort_flag = 1;
@@ -709,7 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int c = 0, steps = 0;   // ring halves, steps whose keys were brought
       bool ok = true;
       int4 split = make_int4(0, 0, 0, 0);
-      while (ok && next_item(b, it)) {
+      for (int k = 0; items[k & 1].nj > 0; ++k) {
+        const Item& it = items[k & 1];
+        next_item(b, it, items[(k + 1) & 1]);
         const int lead = it.pair ? 1 : 2, nj = it.nj;
         // Page ids are copied kIdsAhead steps before their keys are due, so no
         // load waits for one.
@@ -776,9 +790,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           give_up();
           break;
         }
-        if (it.j == 0 && nj < it.t.n) {   // the run ends here: the tile's last place is in CTA `place / run`
-          const long long last = x0 + x_len + it.t.n - nj - 1;
-          split = make_int4(it.t.t0, it.t.ntok, it.head, static_cast<int>(last / run) - static_cast<int>(blockIdx.x) + 1);
+        if (it.j == 0 && nj < it.t.n) {   // the run ends here: the rest is the next CTAs'
+          int pieces = 1;
+#pragma unroll 1
+          for (int left = it.t.n - nj; left > 0; left -= run) ++pieces;
+          split = make_int4(it.t.t0, it.t.ntok, it.head, pieces);
         }
       }
       a.split[blockIdx.x] = split;
@@ -800,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool one = elect_one();
     const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kQBytes >> 4);
     const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
-    const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0]) + s * 8;
+    const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0][0]) + s * 16;
     const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
     const uint32_t tm = warp_uniform(tmem);
     const uint32_t s_col = tm + s * kStepKeys, o_col = tm + C::kOCol + s * D;
@@ -809,29 +825,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, abort_at));
     };
-    while (true) {
-      int go = 0;
-      if (lane == 0) go = next_item(b, it);
-      __syncwarp();
-      if (!__shfl_sync(0xffffffffu, go, 0)) break;
-      const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
-      if (s == 0) {   // the item's queries, when both streams are done with the last one's
-        if (k > 0) wait(smem_u32(&q_empty), (k - 1) & 1);
-        if (ok && one) {
-          const uint32_t bar = smem_u32(&q_full);
-          const int n = pair ? 2 : 1;
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
-                       "r"(n * (D / 64) * a.stream_tokens * G * 128)
-                       : "memory");
+    auto bring_q = [&](const Item& it) {   // an item's queries
+      if (ok && one) {
+        const uint32_t bar = smem_u32(&q_full);
+        const int n = it.pair ? 2 : 1;
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar),
+                     "r"(n * (D / 64) * a.stream_tokens * G * 128)
+                     : "memory");
 #pragma unroll 1
-          for (int i = 0; i < n * (D / 64); ++i) {
-            const int st = i / (D / 64), bx = i % (D / 64);
-            box_load(smem_u32(smem) + st * C::kHalf + bx * C::kBox, &maps.q, bar, bx * 64, it.head * G,
-                     it.t.t0 + st * a.stream_tokens);
-          }
+        for (int i = 0; i < n * (D / 64); ++i) {
+          const int st = i / (D / 64), bx = i % (D / 64);
+          box_load(smem_u32(smem) + st * C::kHalf + bx * C::kBox, &maps.q, bar, bx * 64, it.head * G,
+                   it.t.t0 + st * a.stream_tokens);
         }
-        __syncwarp();
       }
+      __syncwarp();
+    };
+    if (s == 0 && items[0].nj > 0) bring_q(items[0]);
+    while (true) {
+      const Item& it = items[k & 1];
+      const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
+      if (nj <= 0) break;
+      __syncwarp();
       const uint32_t q_at = q_low + (pair ? s * (C::kHalf >> 4) : 0);
       wait(smem_u32(&q_full), k & 1);
       ++k;
@@ -840,6 +855,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int j = -lead; j < nj && ok; ++j) {
         const int pv = j >= 0, more = j + lead < nj;
+        if (j == nj - lead) {   // the scores are all issued: on to the next item's queries
+          if (lane == 0) next_item(b, it, items[k & 1]);
+          __syncwarp();
+          if (s == 0 && items[k & 1].nj > 0) {
+            wait(smem_u32(&q_empty), (k - 1) & 1);
+            bring_q(items[k & 1]);
+          }
+        }
         const int ck = c + pv, vslot = c % S, kslot = ck % S;
         if (pv) wait(full_at + vslot * 8, c / S & 1);
         // of a pair, whose steps are long, everything is waited for before the
@@ -851,29 +874,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(full_at + kslot * 8, ck / S & 1);
             take = warp_uniform(s_step[steps % kStepRing] >> (2 + s) & 1);
           }
-          if (pv) wait(p_at, np++ & 1);
           // the streams of a pair take turns: their products in one block each,
           // so that one stream's run while the other's softmax does
           if (s == 1 || turns > 0) wait(turn_at, (s == 1 ? turns : turns - 1) & 1);
           ++turns;
-        } else if (takes & 1) {
-          wait(p_at, np++ & 1);
         }
+        const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
+        if (weights) wait(p_at, np & 1);
         if (!ok) break;
         tc_fence_after();
         if (takes & 1) {   // O (+)= P V
           const uint32_t v_at = ring_low + vslot * (C::kHalf >> 4);
+          // the first page's weights while the second's are still made
           if (one) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (((kk >> 2) * (C::kHalf / 2) + (kk & 3) * 32) >> 4)),
-                             kIdescO, kk > 0 ? 1u : add);
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 32 >> 4)), kIdescO, kk > 0 ? 1u : add);
+          }
+          __syncwarp();
+          wait(p_at + 8, np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (one) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16_ts(o_col, s_col + 32 + kk * 8, sdesc_of(v_at + ((C::kHalf / 2 + kk * 32) >> 4)), kIdescO, 1u);
             bar_commit(empty_at + vslot * 8);
           }
           add = 1;
-        } else if (pv && one) {
-          bar_arrive(empty_at + vslot * 8);
+        } else if (pv) {
+          if (weights) wait(p_at + 8, np & 1);
+          if (one) bar_arrive(empty_at + vslot * 8);
         }
+        np += weights;
         __syncwarp();
         if (!pair && more) {
           wait(full_at + kslot * 8, ck / S & 1);
@@ -924,6 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ns = 0;         // S tiles taken by this stream
     int nx = 0;         // alternating tiles ended
     int outs = 0;       // items with products of this stream
+    int k = 0;
     int step0 = 0;      // steps of the CTA's items before this one
     bool ok = true;
     // waits taken by all 32 lanes together, so the warp-collective TMEM
@@ -938,10 +972,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar);
     };
     while (true) {
+      const Item& it = items[k & 1];
+      if (it.nj <= 0) break;
       __syncwarp();
-      int go = 0;
-      if (lane == 0) go = next_item(b, it);
-      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      if (lane == 0) next_item(b, it, items[++k & 1]);
+      k = __shfl_sync(0xffffffffu, k, 0);
       const Row row = row_at(b, it.t, it.pair ? stream : 0, r);
       float mref = -INFINITY, l = 0.f;   // the row's reference maximum (log2 units, less the bias), sum
       int done = 0;                      // steps of this item that this stream took
@@ -954,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int flags = s_step[(step0 + j) % kStepRing];
         if (it.pair && !(flags >> (2 + stream) & 1)) {   // no row of the stream sees the step
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[stream]);
+          if (lane < 2) mbar_arrive(&p_full[stream][lane]);
           ++ns;
           continue;
         }
@@ -967,6 +1002,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t zero[16] = {};
 #pragma unroll 1
           for (int c0 = 0; c0 < kStepKeys / 2; c0 += 16) tmem_st_u16(s_tmem + c0, zero);
+          tmem_wait_st();
+          warp_arrive(&p_full[stream][0]);
+          warp_arrive(&p_full[stream][1]);
         } else {
           const int gone = flags & 3;
           if (gone != 0 || !__all_sync(0xffffffffu, c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys))) {
@@ -1000,12 +1038,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               // O holds the stream's products so far: they were issued before
               // the product whose scores these are, and end in that order
 #pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 32) {
-                float o[32];
-                tmem_ld32(o_tmem + c0, o);
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                float o[16];
+                uint32_t bits[16];
+                tmem_ld16(o_tmem + c0, o);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) o[c] *= alpha;
-                tmem_st32(o_tmem + c0, o);
+                for (int c = 0; c < 16; ++c) bits[c] = __float_as_uint(o[c] * alpha);
+                tmem_st_u16(o_tmem + c0, bits);
               }
               tmem_wait_st();
             }
@@ -1029,11 +1068,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 32; ++c) sum[c & 1] = add2(sum[c & 1], make_float2(sv[2 * c], sv[2 * c + 1]));
             tmem_st_u32(s_tmem + u * (kPage / 2), pk);
+            tmem_wait_st();
+            warp_arrive(&p_full[stream][u]);
           }
           l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
         }
-        tmem_wait_st();
-        warp_arrive(&p_full[stream]);
         ++done;
         ++ns;
         if (!ok) break;
@@ -1060,9 +1099,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Join the pieces of the tile that CTA blockIdx.x of the main kernel began and
 // did not end: piece 0 in its slot 1, the others in slot 0 of the CTAs after
-// it. One warp per row; lanes hold the pieces' maxima and sums, 32 pieces at a
-// time, then every piece's row is read as one coalesced load.
-constexpr int kCombineWarps = 8;
+// it. One warp per row, grid.y blocks of warps per tile; a row's pieces are read
+// kAtOnce at a time, all under way together.
+constexpr int kCombineWarps = 8, kAtOnce = 8;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
@@ -1070,48 +1109,58 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
   grid_dep_wait();
   grid_dep_launch();
   const int4 sp = a.split[blockIdx.x];   // first token, tokens, kv head, pieces
-  if (sp.w == 0) return;
   const int lane = threadIdx.x & 31, G = a.b.group, stream_rows = a.stream_tokens * G;
-  const int rows = sp.y * G;
-  for (int i = blockIdx.y * kCombineWarps + (threadIdx.x >> 5); i < rows; i += gridDim.y * kCombineWarps) {
-    const int row = i < stream_rows ? i : kRows + i - stream_rows;
-    auto at = [&](int p) {
-      return ((static_cast<size_t>(blockIdx.x) + p) * 2 + (p == 0 ? 1 : 0)) * a.rows_cap + row;
-    };
-    float top = -INFINITY;
-    for (int p = lane; p < sp.w; p += 32) top = fmaxf(top, a.part_ml[at(p)].x);
+  const int i = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
+  if (sp.w == 0 || i >= sp.y * G) return;
+  const int row = i < stream_rows ? i : kRows + i - stream_rows;
+  // piece p's row: the pieces after the first lie two slots apart
+  const size_t first = (static_cast<size_t>(blockIdx.x) * 2 + 1) * a.rows_cap + row;
+  const size_t step = static_cast<size_t>(2) * a.rows_cap;
+  auto at = [&](int p) { return p == 0 ? first : first + p * step - a.rows_cap; };
+  float top = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f, acc[kPer];
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  for (int p0 = 0; p0 < sp.w; p0 += kAtOnce) {
+    float2 ml[kAtOnce];
+    float2 v[kAtOnce][kPer / 2];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int p0 = 0; p0 < sp.w; p0 += 32) {
-      const float2 ml = p0 + lane < sp.w ? a.part_ml[at(p0 + lane)] : make_float2(-INFINITY, 0.f);
-      const float wl = exp2f(ml.x - ref);
-      l += wl * ml.y;
-      const int n = min(32, sp.w - p0);
-#pragma unroll 8
-      for (int p = 0; p < n; ++p) {
-        const float w = __shfl_sync(0xffffffffu, wl, p);
-        const float* src = a.part_o + at(p0 + p) * D + lane * kPer;
+    for (int u = 0; u < kAtOnce; ++u) {
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (p0 + u < sp.w) {
+        ml[u] = __ldcg(a.part_ml + at(p0 + u));
+        const float2* src = reinterpret_cast<const float2*>(a.part_o + at(p0 + u) * D + lane * kPer);
 #pragma unroll
-        for (int e = 0; e < kPer; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + e);
-          acc[e] = fmaf(w, v.x, acc[e]);
-          acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
-        }
+        for (int e = 0; e < kPer / 2; ++e) v[u][e] = __ldcg(src + e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer / 2; ++e) v[u][e] = make_float2(0.f, 0.f);
       }
     }
+    float nt = top;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-    const int j = i / G;
-    uint16_t* out = a.out + (sp.x + j) * a.out_stride + static_cast<long long>(sp.z * G + i - j * G) * D + lane * kPer;
+    for (int u = 0; u < kAtOnce; ++u) nt = fmaxf(nt, ml[u].x);
+    const float ref = nt == -INFINITY ? 0.f : nt, old = exp2f(top - ref);
+    top = nt;
+    l *= old;
 #pragma unroll
-    for (int e = 0; e < kPer; e += 2)
-      *reinterpret_cast<uint32_t*>(out + e) = pack2<F16>(acc[e] * f, acc[e + 1] * f);
+    for (int e = 0; e < kPer; ++e) acc[e] *= old;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const float w = exp2f(ml[u].x - ref);
+      l = fmaf(w, ml[u].y, l);
+#pragma unroll
+      for (int e = 0; e < kPer / 2; ++e) {
+        acc[2 * e] = fmaf(w, v[u][e].x, acc[2 * e]);
+        acc[2 * e + 1] = fmaf(w, v[u][e].y, acc[2 * e + 1]);
+      }
+    }
   }
+  const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+  const int j = i / G;
+  uint16_t* out = a.out + (sp.x + j) * a.out_stride + static_cast<long long>(sp.z * G + i - j * G) * D + lane * kPer;
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2)
+    *reinterpret_cast<uint32_t*>(out + e) = pack2<F16>(acc[e] * f, acc[e + 1] * f);
 }
 
 const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_stride, const void* out,
