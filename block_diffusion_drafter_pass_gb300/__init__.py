@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 from . import _build
@@ -87,6 +88,8 @@ class dflash_paged_batch(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("pool", "page_table", "q_start", "kv_len", "status")]
 
 
+_BATCH = struct.Struct("@8iq5P")   # dflash_paged_batch
+
 _lib = None
 
 
@@ -99,7 +102,7 @@ def load_library() -> ctypes.CDLL:
         raise DFlashError(DFLASH_ECUDA, f"{LIB_PATH} is missing; build it with __graft_entry__.build()")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, VP, LL, F = ctypes.POINTER, ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_float
-    batch = P(dflash_paged_batch)
+    batch = VP   # const dflash_paged_batch*, by reference or as its bytes
     i32p = P(ctypes.c_int32)
     sigs = {
         "dflash_create": ([P(dflash_config), P(dflash_weights), P(VP)], I),
@@ -225,75 +228,61 @@ def _refuse(message: str):
     raise DFlashError(DFLASH_EINVAL, message)
 
 
-def _rows_arg(name, t, pool, shape=None):
-    """A token buffer [T, heads, d] of the pool's type and device whose head
-    rows are contiguous; its stride between tokens."""
-    if t.dtype != pool.dtype or t.device != pool.device or t.dim() != 3:
-        _refuse(f"{name} must be a [tokens, heads, d] tensor of the pool's dtype and device")
-    T, h, d = t.shape
-    if shape is not None and t.shape != shape:
-        _refuse(f"{name} must have shape {tuple(shape)}")
+def _rows_arg(name, t, dtype, dev, shape):
+    """The stride between tokens of a token buffer of the given shape [T,
+    heads, d], which has the pool's type and device and contiguous head rows."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
+        _refuse(f"{name} must be a {shape} tensor of the pool's dtype and device")
+    T, h, d = shape
+    if T == 0:
+        return h * d
     s = t.stride()
-    if T and h and d and ((d > 1 and s[2] != 1) or (h > 1 and s[1] != d)):
+    if s[2] != 1 or (s[1] != d and h > 1):
         _refuse(f"{name}: the heads of a token must be contiguous")
     return s[0] if T > 1 else h * d   # one token: no stride is used
 
 
-def _i32_arg(name, t, device, shape):
-    import torch
-    if t.dtype != torch.int32 or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+def _i32_arg(name, t, i32, dev, shape):
+    if t.dtype is not i32 or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         _refuse(f"{name} must be a contiguous int32 tensor {shape} on the pool's device")
     return t.data_ptr()
 
 
-def _paged_batch(pool, n_heads, head_dim, n_tokens, q_start, kv_len, page_table, status):
-    import torch
-    if not pool.is_cuda or pool.dim() != 4 or pool.shape[1] != 2 or not pool.is_contiguous():
+def _paged_batch(torch, pool, dev, n_heads, head_dim, n_tokens, q_start, kv_len, page_table, status):
+    dtype, i32 = pool.dtype, torch.int32
+    if dev < 0 or pool.dim() != 4 or not pool.is_contiguous():
         _refuse("the pool must be a contiguous CUDA tensor [n_pages, 2, n_kv_heads, 64 * head_dim]")
-    if pool.dtype not in (torch.bfloat16, torch.float16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         _refuse("the pool must be bfloat16 or float16")
-    if pool.shape[3] != KV_PAGE * head_dim:
-        _refuse("the pool's last dimension must be 64 * head_dim")
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.device != pool.device:
+    n_pages, two, n_kv, width = pool.shape
+    if two != 2 or width != KV_PAGE * head_dim:
+        _refuse("the pool must be [n_pages, 2, n_kv_heads, 64 * head_dim]")
+    if page_table.dim() != 2 or page_table.dtype is not i32 or page_table.get_device() != dev:
         _refuse("page_table must be an int32 tensor [n_seq, pages] on the pool's device")
     n_seq, pages = page_table.shape
-    if pages > 1 and page_table.stride(1) != 1:
-        _refuse("the rows of page_table must be contiguous")
-    stride = page_table.stride(0) if n_seq > 1 else pages
-    if stride < pages:
-        _refuse("the rows of page_table must not overlap")
-    if pages == 0:   # no cache at all: nothing to read, and no row to point at
-        _refuse("page_table needs at least one column")
-    return dflash_paged_batch(
-        DFLASH_FP16 if pool.dtype == torch.float16 else DFLASH_BF16, n_heads, pool.shape[2], head_dim, n_seq, n_tokens,
-        pool.shape[0], pages, stride, _ptr(pool), _ptr(page_table),
-        _i32_arg("q_start", q_start, pool.device, (n_seq + 1,)), _i32_arg("kv_len", kv_len, pool.device, (n_seq,)),
-        0 if status is None else _i32_arg("status", status, pool.device, (1,)))
+    stride, inner = page_table.stride()
+    if n_seq <= 1:
+        stride = pages
+    if pages == 0 or stride < pages or (inner != 1 and pages > 1):
+        _refuse("page_table needs at least one column and contiguous rows that do not overlap")
+    # the struct's bytes (packing them is quicker than filling a ctypes structure)
+    return n_kv, _BATCH.pack(
+        DFLASH_FP16 if dtype is torch.float16 else DFLASH_BF16, n_heads, n_kv, head_dim, n_seq, n_tokens, n_pages,
+        pages, stride, pool.data_ptr(), page_table.data_ptr(), _i32_arg("q_start", q_start, i32, dev, (n_seq + 1,)),
+        _i32_arg("kv_len", kv_len, i32, dev, (n_seq,)),
+        0 if status is None else _i32_arg("status", status, i32, dev, (1,)))
 
 
-class _on:
-    """The device and stream that a call runs on: results and workspaces are
-    allocated there, so the caching allocator orders their reuse with it."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.cm = []
-        if torch.cuda.current_device() != device.index:
-            self.cm.append(torch.cuda.device(device))
-        if stream is not None:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.cm.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.cm:
-            c.__enter__()
-        import torch
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for c in reversed(self.cm):
-            c.__exit__(*exc)
+def _run_on(torch, dev, stream, call):
+    """call(raw stream) on the pool's device and the given stream (the current
+    one when None). Results and workspaces that it allocates belong to that
+    stream, so the caching allocator orders their reuse with it."""
+    if stream is None and torch.cuda.current_device() == dev:
+        return call(torch._C._cuda_getCurrentRawStream(dev))
+    if stream is not None and not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        return call(torch._C._cuda_getCurrentRawStream(dev))
 
 
 def dflash_kv_append(pool, k, v, q_start, kv_len, page_table, *, q=None, q_out=None, positions=None,
@@ -304,44 +293,57 @@ def dflash_kv_append(pool, k, v, q_start, kv_len, page_table, *, q=None, q_out=N
     [n_seq, pages] are int32 device tensors. Returns the rotated queries
     (q_out, which may be q itself), or None without q."""
     import torch
-    T, n_kv, d = k.shape if k.dim() == 3 else _refuse("k must be [tokens, n_kv_heads, d]")
-    ks, vs = _rows_arg("k", k, pool), _rows_arg("v", v, pool, k.shape)
-    n_heads = n_kv if q is None else q.shape[1] if q.dim() == 3 else _refuse("q must be [tokens, heads, d]")
-    b = _paged_batch(pool, n_heads, d, T, q_start, kv_len, page_table, status)
-    if n_kv != pool.shape[2]:
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        _refuse("k and q must be [tokens, heads, d]")
+    shape = k.shape
+    T, n_kv, d = shape
+    n_heads = n_kv if q is None else q.shape[1]
+    dtype, dev = pool.dtype, pool.get_device()
+    pool_heads, b = _paged_batch(torch, pool, dev, n_heads, d, T, q_start, kv_len, page_table, status)
+    if n_kv != pool_heads:
         _refuse("k and the pool have different numbers of heads")
-    if q is None and q_out is not None:
-        _refuse("q_out without q")
-    qs = 0 if q is None else _rows_arg("q", q, pool, (T, n_heads, d))
-    pos = 0 if positions is None else _i32_arg("positions", positions, pool.device, (T,))
-    with _on(pool.device, stream) as s:
-        if q is not None and q_out is None:
-            q_out = torch.empty(T, n_heads, d, dtype=q.dtype, device=q.device)
-        qos = 0 if q is None else _rows_arg("q_out", q_out, pool, (T, n_heads, d))
-        _check(load_library().dflash_kv_append(ctypes.byref(b), _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, _ptr(q_out), qos,
-                                               pos, float(rope_base), s))
-    return q_out
+    ks, vs = _rows_arg("k", k, dtype, dev, shape), _rows_arg("v", v, dtype, dev, shape)
+    pos = None if positions is None else _i32_arg("positions", positions, torch.int32, dev, (T,))
+    lib = _lib or load_library()
+    if q is None:
+        if q_out is not None:
+            _refuse("q_out without q")
+        _run_on(torch, dev, stream, lambda s: _check(lib.dflash_kv_append(
+            b, k.data_ptr(), ks, v.data_ptr(), vs, None, 0, None, 0, pos, rope_base, s)))
+        return None
+    qshape = (T, n_heads, d)
+    qs = _rows_arg("q", q, dtype, dev, qshape)
+
+    def call(s):
+        out = torch.empty(qshape, dtype=dtype, device=pool.device) if q_out is None else q_out
+        os_ = n_heads * d if q_out is None else _rows_arg("q_out", out, dtype, dev, qshape)
+        _check(lib.dflash_kv_append(b, k.data_ptr(), ks, v.data_ptr(), vs, q.data_ptr(), qs,
+                                    out.data_ptr(), os_, pos, rope_base, s))
+        return out
+    return _run_on(torch, dev, stream, call)
 
 
-def _attend(call, q, pool, q_start, kv_len, page_table, scale, out, status, stream):
-    import torch
+def _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status, stream):
     if q.dim() != 3:
         _refuse("q must be [tokens, heads, d]")
-    T, n_heads, d = q.shape
-    qs = _rows_arg("q", q, pool)
-    b = _paged_batch(pool, n_heads, d, T, q_start, kv_len, page_table, status)
+    shape = q.shape
+    T, n_heads, d = shape
+    dtype, dev = pool.dtype, pool.get_device()
+    _, b = _paged_batch(torch, pool, dev, n_heads, d, T, q_start, kv_len, page_table, status)
+    qs = _rows_arg("q", q, dtype, dev, shape)
     if scale is None:
         scale = d ** -0.5
-    lib = load_library()
-    with _on(pool.device, stream) as s:
+    lib = _lib or load_library()
+
+    def call(s):
         need = ctypes.c_size_t()
-        _check(lib.dflash_paged_attn_workspace(ctypes.byref(b), ctypes.byref(need)))
+        _check(lib.dflash_paged_attn_workspace(b, ctypes.byref(need)))
         ws = torch.empty(need.value, dtype=torch.uint8, device=pool.device)
-        if out is None:
-            out = torch.empty(T, n_heads, d, dtype=q.dtype, device=q.device)
-        os_ = _rows_arg("out", out, pool, q.shape)
-        _check(call(lib, b, _ptr(q), qs, _ptr(out), os_, float(scale), _ptr(ws), need.value, s))
-    return out
+        o = torch.empty(shape, dtype=dtype, device=pool.device) if out is None else out
+        os_ = n_heads * d if out is None else _rows_arg("out", o, dtype, dev, shape)
+        _check(run(lib, b, q.data_ptr(), qs, o.data_ptr(), os_, scale, ws.data_ptr(), need.value, s))
+        return o
+    return _run_on(torch, dev, stream, call)
 
 
 def dflash_paged_attn(q, pool, q_start, kv_len, page_table, *, window: int = 0, sinks: int = 0, causal: bool = True,
@@ -351,10 +353,11 @@ def dflash_paged_attn(q, pool, q_start, kv_len, page_table, *, window: int = 0, 
     window > 0: keys after position - window and the first `sinks` ones only.
     scale defaults to d ** -0.5. Rows of no sequence are left as they are (a
     fresh `out` is not initialised)."""
-    def call(lib, b, qp, qs, op, os_, sc, ws, wb, s):
-        return lib.dflash_paged_attn(ctypes.byref(b), qp, qs, op, os_, int(window), int(sinks), 1 if causal else 0, sc,
-                                     ws, wb, s)
-    return _attend(call, q, pool, q_start, kv_len, page_table, scale, out, status, stream)
+    import torch
+
+    def run(lib, b, qp, qs, op, os_, sc, ws, wb, s):
+        return lib.dflash_paged_attn(b, qp, qs, op, os_, window, sinks, 1 if causal else 0, sc, ws, wb, s)
+    return _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status, stream)
 
 
 def dflash_shared_prefix_attn(q, pool, q_start, kv_len, page_table, prefix_table, prefix_len: int, *,
@@ -363,16 +366,14 @@ def dflash_shared_prefix_attn(q, pool, q_start, kv_len, page_table, prefix_table
     (pages prefix_table, int32 on the device, in the same pool): every token
     sees the prefix and then its own cache (kv_len and page_table count the
     tokens behind the prefix). The prefix is read once for the whole batch."""
-    prefix_len = int(prefix_len)
-    need = (max(prefix_len, 0) + KV_PAGE - 1) // KV_PAGE
-    if prefix_table.dim() != 1 or prefix_table.shape[0] < need:
+    import torch
+    if prefix_table.dim() != 1 or prefix_table.shape[0] * KV_PAGE < prefix_len:
         _refuse("prefix_table must be one row of at least ceil(prefix_len / 64) page ids")
-    table = _i32_arg("prefix_table", prefix_table, pool.device, tuple(prefix_table.shape))
+    table = _i32_arg("prefix_table", prefix_table, torch.int32, pool.get_device(), prefix_table.shape)
 
-    def call(lib, b, qp, qs, op, os_, sc, ws, wb, s):
-        return lib.dflash_shared_prefix_attn(ctypes.byref(b), table, prefix_len, qp, qs, op, os_, 1 if causal else 0, sc,
-                                             ws, wb, s)
-    return _attend(call, q, pool, q_start, kv_len, page_table, scale, out, status, stream)
+    def run(lib, b, qp, qs, op, os_, sc, ws, wb, s):
+        return lib.dflash_shared_prefix_attn(b, table, prefix_len, qp, qs, op, os_, 1 if causal else 0, sc, ws, wb, s)
+    return _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status, stream)
 
 
 class BlockScheduler:

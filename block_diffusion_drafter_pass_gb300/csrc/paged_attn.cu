@@ -37,6 +37,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -1178,14 +1179,13 @@ const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_s
 
 // The tile's shape and the workspace's layout for a batch.
 struct Plan {
-  int ctas, stream_tokens, tile_tokens, rows_cap;
+  int device, ctas, stream_tokens, tile_tokens, rows_cap;
   size_t o_off, ml_off, bytes;   // the split records come first
 };
 
 bool make_plan(const dflash_paged_batch& b, Plan& p) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&p.ctas, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+  if (cudaGetDevice(&p.device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&p.ctas, cudaDevAttrMultiProcessorCount, p.device) != cudaSuccess)
     return false;
   const int group = b.n_heads / b.n_kv_heads;
   p.stream_tokens = kRows / group;
@@ -1200,8 +1200,14 @@ bool make_plan(const dflash_paged_batch& b, Plan& p) {
 
 template <int D, bool F16>
 cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
-  if (e != cudaSuccess) return e;
+  // the shared-memory limit is set once per device (setting it again changes nothing)
+  static std::atomic<uint64_t> set{0};
+  cudaError_t e = cudaSuccess;
+  if (p.device > 63 || !(set.load(std::memory_order_acquire) >> p.device & 1)) {
+    e = cudaFuncSetAttribute(paged_attn_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (p.device < 64) set.fetch_or(uint64_t(1) << p.device, std::memory_order_release);
+  }
   e = launch_pdl(paged_attn_kernel<D, F16>, dim3(p.ctas), dim3(kThreads), Cfg<D>::kSmem, s, maps, a);
   if (e != cudaSuccess) return e;
   const int rows = (p.rows_cap + kCombineWarps - 1) / kCombineWarps;

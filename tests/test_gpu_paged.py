@@ -475,7 +475,8 @@ def test_refused_tensors(dfl):
         dfl.dflash_kv_append(b.pool, b.k, b.v, b.q_start, b.kv_len, b.table, q_out=b.q)
     lib = dfl.load_library()
     import ctypes
-    pb = dfl._paged_batch(b.pool, 8, 64, b.T, b.q_start, b.kv_len, b.table, None)
+    pb = dfl.dflash_paged_batch(0, 8, 2, 64, 1, b.T, b.pool.shape[0], b.table.shape[1], b.table.stride(0), b.pool.data_ptr(),
+                                b.table.data_ptr(), b.q_start.data_ptr(), b.kv_len.data_ptr(), None)
     need = ctypes.c_size_t()
     assert lib.dflash_paged_attn_workspace(ctypes.byref(pb), ctypes.byref(need)) == dfl.DFLASH_OK
     if need.value:
