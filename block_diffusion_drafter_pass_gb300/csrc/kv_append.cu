@@ -49,7 +49,7 @@ __device__ __forceinline__ Place place_of(const PagedView& b, const int* s_q, in
   if (t >= b.n_tokens || t < s_q[0] || t >= s_q[b.n_seq]) return p;
   const int i = seq_of_token(s_q, b.n_seq, t);
   const int n_new = s_q[i + 1] - s_q[i];
-  p.pos = cached_tokens(b, i) - n_new + (t - s_q[i]);
+  p.pos = cached_tokens(b, b.kv_len[i]) - n_new + (t - s_q[i]);
   if (p.pos < 0) {   // more new tokens than the cache is said to hold
     latch_status(b.status, kDevBounds);
     return p;
@@ -66,12 +66,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   constexpr int kOct = D / 16;                 // threads of a token: 8 pairs each
   constexpr int kTokens = kThreads / kOct;
   __shared__ int s_q[kPagedMaxSeqs + 1];
-  __shared__ int s_part[kThreads / 32];
   __shared__ long long s_dst[kVTokens];        // values: element offset of the token's column, -1: none
   __shared__ uint32_t s_v[kVTokens][D / 2 + 1];
   grid_dep_wait();
   grid_dep_launch();
-  load_q_start(a.b, s_q, s_part);
+  load_q_start(a.b, s_q);
   const int tid = threadIdx.x;
   const int n_kv = a.b.n_kv;
   if (static_cast<int>(blockIdx.x) < a.qk_tiles * a.qk_groups) {

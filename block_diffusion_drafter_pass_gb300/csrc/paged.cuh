@@ -65,34 +65,22 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // non-decreasing numbers within [0, n_tokens]: what a caller's broken array
 // says otherwise is bent to that (and latched), so no index derived from it
 // leaves a buffer. All threads of the block call it; ends with a barrier.
-// s_part holds one int per warp.
-__device__ __forceinline__ void load_q_start(const PagedView& b, int* s_q, int* s_part) {
-  const int n = b.n_seq + 1, tid = threadIdx.x, nthr = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  int carry = 0;
+__device__ __forceinline__ void load_q_start(const PagedView& b, int* s_q) {
   bool bent = false;
-  for (int base = 0; base < n; base += nthr) {
-    const int i = base + tid;
-    const int raw = i < n ? b.q_start[i] : 0;
-    int v = min(max(raw, 0), b.n_tokens);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v = max(v, y);
-    }
-    if (lane == 31) s_part[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) v = max(v, s_part[w]);
-    v = max(v, carry);
-    int all = carry;
-    for (int w = 0; w < (nthr >> 5); ++w) all = max(all, s_part[w]);
-    carry = all;
-    if (i < n) {
-      s_q[i] = v;
-      bent |= v != raw;
+  for (int i = threadIdx.x; i <= b.n_seq; i += blockDim.x) {
+    const int raw = b.q_start[i], v = min(max(raw, 0), b.n_tokens);
+    s_q[i] = v;
+    bent |= v != raw;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < b.n_seq; i += blockDim.x) bent |= s_q[i + 1] < s_q[i];
+  if (__syncthreads_or(bent)) {
+    if (threadIdx.x == 0) {
+      latch_status(b.status, kDevBounds);
+      for (int i = 0; i < b.n_seq; ++i) s_q[i + 1] = max(s_q[i + 1], s_q[i]);
     }
     __syncthreads();
   }
-  if (bent) latch_status(b.status, kDevBounds);
 }
 
 // The sequence whose new tokens hold token t: the last i in [0, n_seq) with
@@ -108,9 +96,8 @@ __device__ __forceinline__ int seq_of_token(const int* s_q, int n_seq, int t) {
   return lo;
 }
 
-// Cached tokens of sequence i, bent to what its page-table row can hold.
-__device__ __forceinline__ int cached_tokens(const PagedView& b, int i) {
-  const int raw = b.kv_len[i];
+// Cached tokens (`raw`, as kv_len says), bent to what a page-table row can hold.
+__device__ __forceinline__ int cached_tokens(const PagedView& b, int raw) {
   const int v = min(max(raw, 0), b.table_pages * kPage);
   if (v != raw) latch_status(b.status, kDevBounds);
   return v;

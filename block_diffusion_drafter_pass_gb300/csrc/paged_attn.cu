@@ -77,7 +77,8 @@ struct PagedAttnArgs {
   int rows_cap;
   float* part_o;               // [cta][2][rows_cap][d]
   float2* part_ml;             // [cta][2][rows_cap] maximum (log2 units), sum
-  int4* split;                 // [cta] tile begun here and ended elsewhere: first token, tokens, kv head, CTAs (0: none)
+  int4* split;                 // [cta] tile begun here and ended elsewhere: first token, tokens, kv head, pieces (0: none)
+  int* piece;                  // [cta] which piece of a tile begun by an earlier CTA it holds (0: none)
 };
 
 struct PagedMaps {
@@ -444,26 +445,29 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Sum over the threads before this one; `total` over all. One int64 per warp in s_part.
-__device__ __forceinline__ long long block_scan(long long v, long long* s_part, long long& total) {
+// Sum over the threads before this one, and over all (s_sum[kThreads / 32]).
+__device__ __noinline__ long long block_scan(long long v, long long* s_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  __syncthreads();   // the previous use of s_part is read
-  if (lane == 31) s_part[warp] = x;
+  if (lane == 31) s_sum[warp] = x;
   __syncthreads();
-  long long before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += s_part[w];
-    total += s_part[w];
+  if (threadIdx.x == 0) {
+    long long all = 0;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long of = s_sum[w];
+      s_sum[w] = all;
+      all += of;
+    }
+    s_sum[kThreads / 32] = all;
   }
-  return before + x - v;
+  __syncthreads();
+  return s_sum[warp] + x - v;
 }
 
 // What the two softmax groups exchange at an alternating tile's end.
@@ -587,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of the CTA's recent steps: bit u, page u is not there; bit 2 + s, stream s
   // of a pair takes the step
   __shared__ uint8_t s_step[kStepRing];
-  __shared__ long long s_part[kThreads / 32];
+  __shared__ long long s_sum[kThreads / 32 + 1];
   __shared__ int s_begin[3];   // where this CTA's run begins: ~tile, kv head, place
   __shared__ Item s_items[kThreads / 32][2];   // each warp's item and the one after it
   __shared__ uint32_t tmem_slot;
@@ -635,33 +639,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_launch();
 
   // ---- the batch's shape, and this CTA's run of places ----
-  load_q_start(a.b, b.q, reinterpret_cast<int*>(s_part));
-  long long total = 0;
+  int raw_len = tid < n_seq ? a.b.kv_len[tid] : 0;   // under way with the bounds
+  load_q_start(a.b, b.q);
+  int total = 0;
 #pragma unroll 1
-  for (int i0 = 0; i0 < n_seq; i0 += kThreads) {
-    const int i = i0 + tid;
+  for (int i = tid, i0 = 0; i0 < n_seq; i0 += kThreads, i += kThreads) {
     int v = 0;
     if (i < n_seq) {
-      const int nq = b.q[i + 1] - b.q[i], len = cached_tokens(a.b, i);
+      const int nq = b.q[i + 1] - b.q[i], len = cached_tokens(a.b, i0 ? a.b.kv_len[i] : raw_len);
       b.len[i] = len;
       if (a.shared) v = nq > 0 ? steps_of(len) : 0;
       else v = (nq + a.tile_tokens - 1) / a.tile_tokens;
     }
-    long long part;
-    const long long before = total + block_scan(v, s_part, part);
-    if (i < n_seq) b.base[i] = static_cast<int>(before);
-    total += part;
+    const int before = total + static_cast<int>(block_scan(v, s_sum));
+    if (i < n_seq) b.base[i] = before;
+    total += static_cast<int>(s_sum[kThreads / 32]);
+    __syncthreads();   // the sums are read
   }
-  if (tid == 0) b.base[n_seq] = static_cast<int>(total);
+  if (tid == 0) b.base[n_seq] = total;
   __syncthreads();
-  const int n_tiles = a.shared ? (b.q[n_seq] - b.q[0] + a.tile_tokens - 1) / a.tile_tokens : static_cast<int>(total);
+  const int n_tiles = a.shared ? (b.q[n_seq] - b.q[0] + a.tile_tokens - 1) / a.tile_tokens : total;
   const int per = (n_tiles + kThreads - 1) / kThreads;
   const int tile_a = min(tid * per, n_tiles), tile_b = min(tile_a + per, n_tiles);
   long long mine = 0;
 #pragma unroll 1
   for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(places_of(tile_at(b, t).n)) * n_kv;
-  long long all;
-  const long long before = block_scan(mine, s_part, all);
+  const long long before = block_scan(mine, s_sum), all = s_sum[kThreads / 32];
   // CTA c takes the places [c * run, (c + 1) * run); of more than 2^31 the run
   // is rounded up a little
   const int up = all >> 31 ? 33 - __clzll(all) : 0;
@@ -722,6 +725,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int c = 0, steps = 0;   // ring halves, steps whose keys were brought
       bool ok = true;
       int4 split = make_int4(0, 0, 0, 0);
+      int piece = 0;
+#pragma unroll 1
+      for (int before = items[0].nj > 0 ? items[0].j : 0; before > 0; before -= run) ++piece;
       for (int k = 0; items[k & 1].nj > 0; ++k) {
         const Item& it = items[k & 1];
         next_item(b, it, items[(k + 1) & 1]);
@@ -799,6 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       a.split[blockIdx.x] = split;
+      a.piece[blockIdx.x] = piece;
       // copies still in flight complete before shared memory is released
 #pragma unroll 1
       for (int j = max(0, c - S); j < c; ++j) bar_wait(full_at + (j % S) * 8, j / S & 1, never_at);
@@ -1098,70 +1105,78 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Join the pieces of the tile that CTA blockIdx.x of the main kernel began and
-// did not end: piece 0 in its slot 1, the others in slot 0 of the CTAs after
-// it. One warp per row, grid.y blocks of warps per tile; a row's pieces are read
-// kAtOnce at a time, all under way together.
-constexpr int kCombineWarps = 8, kAtOnce = 8;
+// Join the pieces of the tiles that the main kernel split: piece 0 lies in slot
+// 1 of the CTA c that began the tile, piece p in slot 0 of CTA c + p. Every CTA
+// that holds a piece has blocks here which take their share of the tile's rows
+// (a tile in many pieces, whose rows cost more, gets more of them). One warp per
+// row; a row's pieces are read kAtOnce at a time, all under way together.
+constexpr int kCombineWarps = 8, kAtOnce = 8, kCombineBlocks = 8;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const __grid_constant__ PagedAttnArgs a) {
   constexpr int kPer = D / 32;
   grid_dep_wait();
   grid_dep_launch();
-  const int4 sp = a.split[blockIdx.x];   // first token, tokens, kv head, pieces
   const int lane = threadIdx.x & 31, G = a.b.group, stream_rows = a.stream_tokens * G;
-  const int i = blockIdx.y * kCombineWarps + (threadIdx.x >> 5);
-  if (sp.w == 0 || i >= sp.y * G) return;
-  const int row = i < stream_rows ? i : kRows + i - stream_rows;
-  // piece p's row: the pieces after the first lie two slots apart
-  const size_t first = (static_cast<size_t>(blockIdx.x) * 2 + 1) * a.rows_cap + row;
-  const size_t step = static_cast<size_t>(2) * a.rows_cap;
-  auto at = [&](int p) { return p == 0 ? first : first + p * step - a.rows_cap; };
-  float top = -INFINITY, l = 0.f, acc[kPer];
+  const int last_piece = a.piece[blockIdx.x];
+#pragma unroll 1
+  for (int own = last_piece > 0 ? 0 : 1; own < 2; ++own) {
+    const int share = own ? 0 : last_piece, cta = blockIdx.x - share;
+    const int4 sp = a.split[cta];   // first token, tokens, kv head, pieces
+    const int n = sp.w;
+#pragma unroll 1
+    for (int i = (blockIdx.y * kCombineWarps + (threadIdx.x >> 5)) * n + share; n > 0 && i < sp.y * G;
+         i += gridDim.y * kCombineWarps * n) {
+      const int row = i < stream_rows ? i : kRows + i - stream_rows;
+      const size_t first = (static_cast<size_t>(cta) * 2 + 1) * a.rows_cap + row;
+      const size_t step = static_cast<size_t>(2) * a.rows_cap;
+      auto at = [&](int p) { return p == 0 ? first : first + p * step - a.rows_cap; };
+      float top = -INFINITY, l = 0.f, acc[kPer];
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int p0 = 0; p0 < sp.w; p0 += kAtOnce) {
-    float2 ml[kAtOnce];
-    float2 v[kAtOnce][kPer / 2];
+      for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 1
+      for (int p0 = 0; p0 < n; p0 += kAtOnce) {
+        float2 ml[kAtOnce];
+        float2 v[kAtOnce][kPer / 2];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      ml[u] = make_float2(-INFINITY, 0.f);
-      if (p0 + u < sp.w) {
-        ml[u] = __ldcg(a.part_ml + at(p0 + u));
-        const float2* src = reinterpret_cast<const float2*>(a.part_o + at(p0 + u) * D + lane * kPer);
+        for (int u = 0; u < kAtOnce; ++u) {
+          ml[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int e = 0; e < kPer / 2; ++e) v[u][e] = __ldcg(src + e);
-      } else {
+          for (int e = 0; e < kPer / 2; ++e) v[u][e] = make_float2(0.f, 0.f);
+          if (p0 + u < n) {
+            ml[u] = __ldcg(a.part_ml + at(p0 + u));
+            const float2* src = reinterpret_cast<const float2*>(a.part_o + at(p0 + u) * D + lane * kPer);
 #pragma unroll
-        for (int e = 0; e < kPer / 2; ++e) v[u][e] = make_float2(0.f, 0.f);
+            for (int e = 0; e < kPer / 2; ++e) v[u][e] = __ldcg(src + e);
+          }
+        }
+        float nt = top;
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) nt = fmaxf(nt, ml[u].x);
+        const float ref = nt == -INFINITY ? 0.f : nt, old = ex2(top - ref);
+        top = nt;
+        l *= old;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] *= old;
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const float w = ex2(ml[u].x - ref);
+          l = fmaf(w, ml[u].y, l);
+#pragma unroll
+          for (int e = 0; e < kPer / 2; ++e) {
+            acc[2 * e] = fmaf(w, v[u][e].x, acc[2 * e]);
+            acc[2 * e + 1] = fmaf(w, v[u][e].y, acc[2 * e + 1]);
+          }
+        }
       }
-    }
-    float nt = top;
+      const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+      const int j = i / G;
+      uint16_t* out = out_row(a, sp.x + j, sp.z, i - j * G, D) + lane * kPer;
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) nt = fmaxf(nt, ml[u].x);
-    const float ref = nt == -INFINITY ? 0.f : nt, old = exp2f(top - ref);
-    top = nt;
-    l *= old;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] *= old;
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const float w = exp2f(ml[u].x - ref);
-      l = fmaf(w, ml[u].y, l);
-#pragma unroll
-      for (int e = 0; e < kPer / 2; ++e) {
-        acc[2 * e] = fmaf(w, v[u][e].x, acc[2 * e]);
-        acc[2 * e + 1] = fmaf(w, v[u][e].y, acc[2 * e + 1]);
-      }
+      for (int e = 0; e < kPer; e += 2)
+        *reinterpret_cast<uint32_t*>(out + e) = pack2<F16>(acc[e] * f, acc[e + 1] * f);
     }
   }
-  const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-  const int j = i / G;
-  uint16_t* out = a.out + (sp.x + j) * a.out_stride + static_cast<long long>(sp.z * G + i - j * G) * D + lane * kPer;
-#pragma unroll
-  for (int e = 0; e < kPer; e += 2)
-    *reinterpret_cast<uint32_t*>(out + e) = pack2<F16>(acc[e] * f, acc[e + 1] * f);
 }
 
 const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_stride, const void* out,
@@ -1180,7 +1195,7 @@ const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_s
 // The tile's shape and the workspace's layout for a batch.
 struct Plan {
   int device, ctas, stream_tokens, tile_tokens, rows_cap;
-  size_t o_off, ml_off, bytes;   // the split records come first
+  size_t piece_off, ml_off, o_off, bytes;   // the split records come first
 };
 
 bool make_plan(const dflash_paged_batch& b, Plan& p) {
@@ -1192,7 +1207,8 @@ bool make_plan(const dflash_paged_batch& b, Plan& p) {
   p.tile_tokens = 2 * p.stream_tokens;
   p.rows_cap = b.n_tokens > p.stream_tokens ? 2 * kRows : std::min(kRows, b.n_tokens * group);
   auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-  p.ml_off = up(sizeof(int4) * p.ctas);
+  p.piece_off = up(sizeof(int4) * p.ctas);
+  p.ml_off = p.piece_off + up(sizeof(int) * p.ctas);
   p.o_off = p.ml_off + up(sizeof(float2) * 2 * p.ctas * p.rows_cap);
   p.bytes = p.o_off + sizeof(float) * 2 * p.ctas * p.rows_cap * b.head_dim;
   return true;
@@ -1210,7 +1226,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p,
   }
   e = launch_pdl(paged_attn_kernel<D, F16>, dim3(p.ctas), dim3(kThreads), Cfg<D>::kSmem, s, maps, a);
   if (e != cudaSuccess) return e;
-  const int rows = (p.rows_cap + kCombineWarps - 1) / kCombineWarps;
+  const int rows = std::min(kCombineBlocks, (p.rows_cap + kCombineWarps - 1) / kCombineWarps);
   return launch_pdl(paged_combine_kernel<D, F16>, dim3(p.ctas, rows), dim3(kCombineWarps * 32), 0, s, a);
 }
 
@@ -1234,6 +1250,7 @@ dflash_status run(const dflash_paged_batch& b, PagedAttnArgs& a, void* workspace
   a.tile_tokens = p.tile_tokens;
   a.rows_cap = p.rows_cap;
   a.split = reinterpret_cast<int4*>(ws);
+  a.piece = reinterpret_cast<int*>(ws + p.piece_off);
   a.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
   const uint64_t d = b.head_dim, n_kv = b.n_kv_heads, pages = b.n_pages;
