@@ -413,6 +413,18 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t
   return ok != 0;
 }
 
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -872,24 +884,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int ck = c + pv, vslot = c % S, kslot = ck % S;
-        if (pv) wait(full_at + vslot * 8, c / S & 1);
-        // of a pair, whose steps are long, everything is waited for before the
-        // products, so that they follow each other; an alternating tile's
-        // values go back as soon as they can
-        uint32_t take = ((j + lead) & 1) == s && more;
-        if (pair) {
-          if (more) {
-            wait(full_at + kslot * 8, ck / S & 1);
-            take = warp_uniform(s_step[steps % kStepRing] >> (2 + s) & 1);
-          }
-          // the streams of a pair take turns: their products in one block each,
-          // so that one stream's run while the other's softmax does
-          if (s == 1 || turns > 0) wait(turn_at, (s == 1 ? turns : turns - 1) & 1);
-          ++turns;
-        }
+        // One lane for each thing to wait for, so that the waits are one (in a
+        // row they were 300 cycles each: the products keep shared memory busy).
+        // Of a pair, whose steps are long, that is everything but the second
+        // page's weights, and its streams take turns: their products in one
+        // block each, so that one stream's run while the other's softmax does.
+        // An alternating tile's values go back as soon as they can.
         const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
-        if (weights) wait(p_at, np & 1);
+        {
+          bool need = lane == 0 && pv;
+          uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
+          if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
+          if (lane == 2) need = weights, bar = p_at, parity = np & 1;
+          if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
+          int tries = 1 << 24;
+          while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
+            if (abort_flag || --tries == 0) { ok = false; break; }
+          }
+        }
+        turns += pair;
         if (!ok) break;
+        uint32_t take = ((j + lead) & 1) == s && more;
+        if (pair && more) take = warp_uniform(s_step[steps % kStepRing] >> (2 + s) & 1);
         tc_fence_after();
         if (takes & 1) {   // O (+)= P V
           const uint32_t v_at = ring_low + vslot * (C::kHalf >> 4);
@@ -920,6 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           wait(full_at + kslot * 8, ck / S & 1);
           if (!ok) break;
         }
+        if (pair && one) bar_arrive(pass_at);   // the other stream's waits pass under these products
         if (take) {   // S = Q K^T
           const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
           if (one) {
@@ -937,7 +954,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           bar_arrive(empty_at + kslot * 8);
         }
         if (one) {
-          if (pair) bar_arrive(pass_at);
           if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
         }
         __syncwarp();
