@@ -482,6 +482,12 @@ __device__ __noinline__ long long block_scan(long long v, long long* s_sum) {
   return s_sum[warp] + x - v;
 }
 
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // What the two softmax groups exchange at an alternating tile's end.
 struct Join {
   uint64_t x_ml, x_bad;
@@ -510,6 +516,9 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
   const bool whole = it.nj == it.t.n;
   const bool live = token >= 0;
   const size_t prow = partial_row(a, it, stream, r);
+  // a warp's store touches a line for each of its rows: 32 bytes at a time
+  // halves them (rows of partials and, where the caller's are aligned so, of out)
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | static_cast<uintptr_t>(a.out_stride * 2)) & 31) == 0;
   char* const to = whole ? reinterpret_cast<char*>(out_row(a, token, it.head, r % b.group, D))
                          : reinterpret_cast<char*>(a.part_o + prow * D);
   // A pair's stream has its rows' whole sums in its O. Of an alternating
@@ -557,15 +566,24 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
 #pragma unroll
     for (int c = 0; c < 16; ++c) check = fmaf(o[c], 0.f, check);
     if (live && whole) {
+      uint32_t w[8];
 #pragma unroll
-      for (int c = 0; c < 16; c += 8)
-        *reinterpret_cast<uint4*>(to + (col + c) * 2) =
-            make_uint4(pack2<F16>(o[c], o[c + 1]), pack2<F16>(o[c + 2], o[c + 3]), pack2<F16>(o[c + 4], o[c + 5]),
-                       pack2<F16>(o[c + 6], o[c + 7]));
+      for (int c = 0; c < 8; ++c) w[c] = pack2<F16>(o[2 * c], o[2 * c + 1]);
+      char* const p = to + col * 2;
+      if (wide) {
+        store32(p, w);
+      } else {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+      }
     } else if (live) {
 #pragma unroll
-      for (int c = 0; c < 16; c += 4)
-        *reinterpret_cast<float4*>(to + (col + c) * 4) = make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) w[c] = __float_as_uint(o[8 * h + c]);
+        store32(to + (col + 8 * h) * 4, w);
+      }
     }
     __syncwarp();   // the next loads are the warp's
   }
@@ -1259,8 +1277,8 @@ dflash_status fail_cuda(const char* why) {
 dflash_status run(const dflash_paged_batch& b, PagedAttnArgs& a, void* workspace, size_t workspace_bytes, void* stream) {
   Plan p;
   if (!make_plan(b, p)) return fail_cuda("paged attention: no CUDA device");
-  if (!workspace || misaligned16(workspace) || workspace_bytes < p.bytes)
-    return refuse("the workspace is null, not 16-byte aligned or smaller than dflash_paged_attn_workspace says");
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) & 31 || workspace_bytes < p.bytes)
+    return refuse("the workspace is null, not 32-byte aligned or smaller than dflash_paged_attn_workspace says");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.stream_tokens = p.stream_tokens;
   a.tile_tokens = p.tile_tokens;

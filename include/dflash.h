@@ -470,7 +470,7 @@ dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b, size_t* b
  *  window   > 0: of those, only keys after p - window and the first `sinks`
  *           keys; 0: all (sinks is then ignored)
  *  scale    positive and finite
- *  workspace  device, 16-byte aligned, at least dflash_paged_attn_workspace
+ *  workspace  device, 32-byte aligned, at least dflash_paged_attn_workspace
  * A token that sees no key gets zeros. Keys and values it does not see have no
  * influence on it, infinities and NaN included (non-finite values in hidden
  * places of a page cost time).
