@@ -54,7 +54,7 @@ constexpr int kRows = 128;            // rows of a stream: the MMA's M
 // The producer is at most the ring's 8 halves of values and 2 steps of keys
 // ahead of the softmax (a step's values are not overwritten before its P).
 constexpr int kStepRing = 16;
-constexpr int kIdsAhead = 4, kIdRing = 16;   // steps
+constexpr int kIdsAhead = 2, kIdRing = 16;   // steps
 constexpr int kItemSteps = 4;         // what an item costs beside its steps, in steps (dealing only)
 constexpr int kNoEnd = 1 << 30;       // above every position
 constexpr float kRescaleLog2 = 8.f;   // rescale O when a row's maximum grows by more than 2^8
