@@ -389,7 +389,7 @@ __device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Batch& b, co
 // in place (a called or clocked one costs every role's round a hundred and
 // more): each try gives up after a microsecond at the latest, and the wait
 // after kWaitTries of them or when *abort is set. False when it gave up.
-constexpr uint32_t kWaitTries = 1u << 21;   // with tries of 1 us at most: 2 s
+constexpr uint32_t kWaitTries = 1u << 23;   // with tries of 1 us at most: 8 s (rows done again take their time)
 
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
   uint32_t ok;
@@ -457,8 +457,9 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Sum over the threads before this one, and over all (s_sum[kThreads / 32]).
-__device__ __noinline__ long long block_scan(long long v, long long* s_sum) {
+// Sum over the threads before this one; `all`: over all. s_sum holds one for
+// each warp and is free again behind the next barrier.
+__device__ __forceinline__ long long block_scan(long long v, long long* s_sum, long long& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
 #pragma unroll 1
@@ -468,18 +469,15 @@ __device__ __noinline__ long long block_scan(long long v, long long* s_sum) {
   }
   if (lane == 31) s_sum[warp] = x;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    long long all = 0;
-#pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const long long of = s_sum[w];
-      s_sum[w] = all;
-      all += of;
-    }
-    s_sum[kThreads / 32] = all;
+  long long before = x - v;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long of = s_sum[w];
+    if (w < warp) before += of;
+    all += of;
   }
-  __syncthreads();
-  return s_sum[warp] + x - v;
+  return before;
 }
 
 __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
@@ -621,8 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // of the CTA's recent steps: bit u, page u is not there; bit 2 + s, stream s
   // of a pair takes the step
   __shared__ uint8_t s_step[kStepRing];
-  __shared__ long long s_sum[kThreads / 32 + 1];
-  __shared__ int s_begin[3];   // where this CTA's run begins: ~tile, kv head, place
+  __shared__ long long s_sum[kThreads / 32];
+  __shared__ Item s_first[2];   // the CTA's first item (and where its run begins)
   __shared__ Item s_items[kThreads / 32][2];   // each warp's item and the one after it
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
@@ -648,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&join.x_ml, 8);
     mbar_init(&join.x_bad, 8);
     abort_flag = 0;
+    s_first[0].nj = 0;
     s_never = 0;
     b.shared = a.shared;
     b.causal = a.causal;
@@ -681,9 +680,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.shared) v = nq > 0 ? steps_of(len) : 0;
       else v = (nq + a.tile_tokens - 1) / a.tile_tokens;
     }
-    const int before = total + static_cast<int>(block_scan(v, s_sum));
+    long long part;
+    const int before = total + static_cast<int>(block_scan(v, s_sum, part));
     if (i < n_seq) b.base[i] = before;
-    total += static_cast<int>(s_sum[kThreads / 32]);
+    total += static_cast<int>(part);
     __syncthreads();   // the sums are read
   }
   if (tid == 0) b.base[n_seq] = total;
@@ -692,31 +692,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (n_tiles + kThreads - 1) / kThreads;
   const int tile_a = min(tid * per, n_tiles), tile_b = min(tile_a + per, n_tiles);
   long long mine = 0;
+  int n = 0;   // places of one kv head of this thread's first tile
 #pragma unroll 1
-  for (int t = tile_a; t < tile_b; ++t) mine += static_cast<long long>(places_of(tile_at(b, t).n)) * n_kv;
-  const long long before = block_scan(mine, s_sum), all = s_sum[kThreads / 32];
+  for (int t = tile_b - 1; t >= tile_a; --t) {
+    n = places_of(tile_at(b, t).n);
+    mine += static_cast<long long>(n) * n_kv;
+  }
+  long long all;
+  const long long before = block_scan(mine, s_sum, all);
   // CTA c takes the places [c * run, (c + 1) * run); of more than 2^31 the run
   // is rounded up a little
   const int up = all >> 31 ? 33 - __clzll(all) : 0;
   const int run = static_cast<int>((static_cast<uint32_t>(all >> up) + (up ? gridDim.x : gridDim.x - 1)) / gridDim.x) << up;
   const long long x0 = static_cast<long long>(run) * blockIdx.x;
   const int x_len = static_cast<int>(max(0ll, min(static_cast<long long>(run), all - x0)));
-  if (x_len > 0 && x0 >= before && x0 < before + mine) {
+  if (x_len > 0 && x0 >= before && x0 < before + mine) {   // one thread: the run begins in its tiles
     long long rem = x0 - before;
-    int t = tile_a, n;
+    Item& begin = s_first[1];
+    begin.tile = tile_a;
 #pragma unroll 1
-    while (true) {
-      n = places_of(tile_at(b, t).n);
-      if (rem < static_cast<long long>(n) * n_kv) break;
+    while (rem >= static_cast<long long>(n) * n_kv) {
       rem -= static_cast<long long>(n) * n_kv;
-      ++t;
+      n = places_of(tile_at(b, ++begin.tile).n);
     }
-    int head = 0;
+    begin.head = 0;
 #pragma unroll 1
-    for (; rem >= n; rem -= n) ++head;
-    s_begin[0] = ~t;
-    s_begin[1] = head;
-    s_begin[2] = static_cast<int>(rem);
+    for (; rem >= n; rem -= n) ++begin.head;
+    begin.tile = ~begin.tile;
+    begin.place = static_cast<int>(rem);
+    begin.todo = x_len;
+    next_item(b, begin, s_first[0]);
   }
   tc_fence_before();
   __syncthreads();
@@ -724,14 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
 
   Item* const items = s_items[warp];   // written by lane 0
-  if (lane == 0) {
-    Item& begin = items[1];
-    begin.tile = s_begin[0];
-    begin.head = s_begin[1];
-    begin.place = s_begin[2];
-    begin.todo = x_len;
-    next_item(b, begin, items[0]);
-  }
+  if (lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
   __syncwarp();
   const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag)), never_at = smem_u32(&s_never);
   auto give_up = [&]() {
@@ -915,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
           if (lane == 2) need = weights, bar = p_at, parity = np & 1;
           if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
-          int tries = 1 << 24;
+          int tries = 1 << 27;
           while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
             if (abort_flag || --tries == 0) { ok = false; break; }
           }
