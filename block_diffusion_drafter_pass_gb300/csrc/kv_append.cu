@@ -10,10 +10,15 @@
 //
 // Bound: memory, q, k and v read once, q and the pages written once.
 // Queries and keys: one thread per (token, 8 pairs), which computes its 8
-// rotations once and walks kHeads heads with them: 16-byte loads and stores,
+// rotations once and walks up to 8 heads with them: 16-byte loads and stores,
 // 128 bytes of a head row in a row of lanes. Values: one block per (64
-// tokens, kv head) turns the rows over in shared memory, since the pages
-// hold them transposed.
+// tokens, kv head) turns the rows over in shared memory, since the pages hold
+// them transposed. Few tokens are cut finer (fewer heads a thread, ranges of
+// the values' dims), until the blocks fill the device: one token of 32
+// sequences (32 + 8 + 8 heads of 128) takes 3.4 us, with whole blocks 6.4;
+// 10.6 thousand tokens take 46 us, 83% of the copy bandwidth for q, k and v
+// read and written once.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -23,7 +28,8 @@ namespace dfl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 8;      // heads one thread rotates with the same angles
+constexpr int kMaxHeads = 8;   // heads one thread rotates with the same angles, at most
+constexpr int kAtOnce = 2;     // of them under way together (4 took registers, and 4% at 260 MB)
 constexpr int kVTokens = 64;   // tokens of a value block
 
 struct AppendArgs {
@@ -33,7 +39,9 @@ struct AppendArgs {
   uint16_t* q_out;
   const int32_t* positions;        // [n_tokens] rotation positions, or null: the cache positions
   int rotate;
+  int heads;                       // heads of a rotation block
   int qk_tiles, qk_groups;         // blocks of the rotation part: token tiles x head groups
+  int v_split;                     // value blocks that share a (tokens, head): ranges of dims
   unsigned long long turn[64];     // base^(-2i/d) / (2 pi) in units of 2^-64 turns
 };
 
@@ -44,12 +52,12 @@ struct Place {
 };
 
 template <int D>
-__device__ __forceinline__ Place place_of(const PagedView& b, const int* s_q, int t) {
+__device__ __forceinline__ Place place_of(const PagedView& b, const int* s_q, const int* s_len, int t) {
   Place p{-1, 0, -1};
   if (t >= b.n_tokens || t < s_q[0] || t >= s_q[b.n_seq]) return p;
   const int i = seq_of_token(s_q, b.n_seq, t);
   const int n_new = s_q[i + 1] - s_q[i];
-  p.pos = cached_tokens(b, b.kv_len[i]) - n_new + (t - s_q[i]);
+  p.pos = cached_tokens(b, s_len[i]) - n_new + (t - s_q[i]);
   if (p.pos < 0) {   // more new tokens than the cache is said to hold
     latch_status(b.status, kDevBounds);
     return p;
@@ -65,18 +73,34 @@ template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kOct = D / 16;                 // threads of a token: 8 pairs each
   constexpr int kTokens = kThreads / kOct;
-  __shared__ int s_q[kPagedMaxSeqs + 1];
+  __shared__ int s_q[kPagedMaxSeqs + 1], s_len[kPagedMaxSeqs];
   __shared__ long long s_dst[kVTokens];        // values: element offset of the token's column, -1: none
   __shared__ uint32_t s_v[kVTokens][D / 2 + 1];
   grid_dep_wait();
   grid_dep_launch();
-  load_q_start(a.b, s_q);
   const int tid = threadIdx.x;
   const int n_kv = a.b.n_kv;
+  for (int i = tid; i < a.b.n_seq; i += kThreads) s_len[i] = a.b.kv_len[i];
+  // The rows are read as soon as their addresses are known, before what says
+  // where they go (a short call is the chain of these reads).
   if (static_cast<int>(blockIdx.x) < a.qk_tiles * a.qk_groups) {
     const int tile = blockIdx.x / a.qk_groups, grp = blockIdx.x % a.qk_groups;
     const int t = tile * kTokens + tid / kOct, oct = tid % kOct;
-    const Place p = place_of<D>(a.b, s_q, t);
+    const int n_q = a.q ? a.b.n_heads : 0;
+    const int h0 = grp * a.heads, h1 = t < a.b.n_tokens ? min(n_q + n_kv, h0 + a.heads) : h0;
+    uint4 lo[kAtOnce], hi[kAtOnce];
+    auto read = [&](int h) {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (h + u >= h1) continue;
+        const uint16_t* src = h + u < n_q ? a.q + t * a.q_stride + (h + u) * D : a.k + t * a.k_stride + (h + u - n_q) * D;
+        lo[u] = __ldg(reinterpret_cast<const uint4*>(src + oct * 8));
+        hi[u] = __ldg(reinterpret_cast<const uint4*>(src + D / 2 + oct * 8));
+      }
+    };
+    read(h0);
+    load_q_start(a.b, s_q);
+    const Place p = place_of<D>(a.b, s_q, s_len, t);
     if (p.pos < 0) return;
     float cs[8], sn[8];
     if (a.rotate) {
@@ -89,50 +113,52 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         sincospif(half_turns, &sn[e], &cs[e]);
       }
     }
-    const int n_q = a.q ? a.b.n_heads : 0;
-    const int h1 = min(n_q + n_kv, (grp + 1) * kHeads);
-#pragma unroll 4
-    for (int h = grp * kHeads; h < h1; ++h) {
-      const bool is_q = h < n_q;
-      const uint16_t* src = is_q ? a.q + t * a.q_stride + h * D : a.k + t * a.k_stride + (h - n_q) * D;
-      uint16_t* dst;
-      if (is_q) {
-        dst = a.q_out + t * a.out_stride + h * D;
-      } else {
-        if (p.page < 0) continue;
-        dst = a.b.pool + p.page + (static_cast<long long>(h - n_q) * kPage + p.slot) * D;
-      }
-      const uint4 lo = *reinterpret_cast<const uint4*>(src + oct * 8);
-      const uint4 hi = *reinterpret_cast<const uint4*>(src + D / 2 + oct * 8);
-      uint4 ro = lo, rh = hi;
-      if (a.rotate) {
+#pragma unroll 1
+    for (int h = h0; h < h1; h += kAtOnce) {
+      if (h > h0) read(h);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float2 x = unpack2<F16>((&lo.x)[w]), y = unpack2<F16>((&hi.x)[w]);
-          (&ro.x)[w] = pack2<F16>(x.x * cs[2 * w] - y.x * sn[2 * w], x.y * cs[2 * w + 1] - y.y * sn[2 * w + 1]);
-          (&rh.x)[w] = pack2<F16>(y.x * cs[2 * w] + x.x * sn[2 * w], y.y * cs[2 * w + 1] + x.y * sn[2 * w + 1]);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const bool is_q = h + u < n_q;
+        if (h + u >= h1 || (!is_q && p.page < 0)) continue;
+        uint16_t* dst = is_q ? a.q_out + t * a.out_stride + (h + u) * D
+                             : a.b.pool + p.page + (static_cast<long long>(h + u - n_q) * kPage + p.slot) * D;
+        uint4 ro = lo[u], rh = hi[u];
+        if (a.rotate) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float2 x = unpack2<F16>((&lo[u].x)[w]), y = unpack2<F16>((&hi[u].x)[w]);
+            (&ro.x)[w] = pack2<F16>(x.x * cs[2 * w] - y.x * sn[2 * w], x.y * cs[2 * w + 1] - y.y * sn[2 * w + 1]);
+            (&rh.x)[w] = pack2<F16>(y.x * cs[2 * w] + x.x * sn[2 * w], y.y * cs[2 * w + 1] + x.y * sn[2 * w + 1]);
+          }
         }
+        *reinterpret_cast<uint4*>(dst + oct * 8) = ro;
+        *reinterpret_cast<uint4*>(dst + D / 2 + oct * 8) = rh;
       }
-      *reinterpret_cast<uint4*>(dst + oct * 8) = ro;
-      *reinterpret_cast<uint4*>(dst + D / 2 + oct * 8) = rh;
     }
     return;
   }
-  const int vb = blockIdx.x - a.qk_tiles * a.qk_groups;
+  const int vb = (blockIdx.x - a.qk_tiles * a.qk_groups) / a.v_split;
   const int t0 = vb / n_kv * kVTokens, h = vb % n_kv;
+  // this block's dims, in pieces of 8
+  const int of = D / 8 / a.v_split, c0 = (blockIdx.x - a.qk_tiles * a.qk_groups) % a.v_split * of, c1 = c0 + of;
+  constexpr int kPieces = kVTokens * (D / 8) / kThreads;
+  uint4 rows[kPieces];
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const int e = tid + u * kThreads, r = e / (D / 8), c = e % (D / 8);
+    rows[u] = make_uint4(0, 0, 0, 0);
+    if (t0 + r < a.b.n_tokens && c >= c0 && c < c1) rows[u] = __ldg(reinterpret_cast<const uint4*>(a.v + (t0 + r) * a.v_stride + h * D + c * 8));
+  }
+  load_q_start(a.b, s_q);
   if (tid < kVTokens) {
-    const Place p = place_of<D>(a.b, s_q, t0 + tid);
+    const Place p = place_of<D>(a.b, s_q, s_len, t0 + tid);
     s_dst[tid] = p.page < 0 ? -1 : p.page + (static_cast<long long>(n_kv) * kPage + h * kPage) * D + p.slot;
   }
-  for (int e = tid; e < kVTokens * (D / 8); e += kThreads) {
-    const int r = e / (D / 8), c = e % (D / 8);
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (t0 + r < a.b.n_tokens)
-      w = *reinterpret_cast<const uint4*>(a.v + (t0 + r) * a.v_stride + h * D + c * 8);
-    s_v[r][c * 4] = w.x;
-    s_v[r][c * 4 + 1] = w.y;
-    s_v[r][c * 4 + 2] = w.z;
-    s_v[r][c * 4 + 3] = w.w;
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const int e = tid + u * kThreads, r = e / (D / 8), c = e % (D / 8);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) s_v[r][c * 4 + w] = (&rows[u].x)[w];
   }
   __syncthreads();
   const int lane = tid & 31, warp = tid >> 5;
@@ -141,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     const int r = half * 32 + lane;
     const long long at = s_dst[r];
     if (at < 0) continue;
-    for (int c = warp; c < D / 2; c += kThreads / 32) {
+    for (int c = c0 * 4 + warp; c < c1 * 4; c += kThreads / 32) {
       const uint32_t w = s_v[r][c];
       a.b.pool[at + (2 * c) * kPage] = static_cast<uint16_t>(w);
       a.b.pool[at + (2 * c + 1) * kPage] = static_cast<uint16_t>(w >> 16);
@@ -151,11 +177,19 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
 
 template <int D, bool F16>
 cudaError_t launch(AppendArgs& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const long long enough = 2ll * sms;   // blocks that fill the device: few tokens are cut finer
   const int tokens = kThreads / (D / 16);
   const int heads = (a.q ? a.b.n_heads : 0) + a.b.n_kv;
   a.qk_tiles = (a.b.n_tokens + tokens - 1) / tokens;
-  a.qk_groups = (heads + kHeads - 1) / kHeads;
-  const long long v_blocks = static_cast<long long>((a.b.n_tokens + kVTokens - 1) / kVTokens) * a.b.n_kv;
+  a.heads = static_cast<int>(std::min<long long>(kMaxHeads, std::max<long long>(1, heads * static_cast<long long>(a.qk_tiles) / enough)));
+  a.qk_groups = (heads + a.heads - 1) / a.heads;
+  long long v_blocks = static_cast<long long>((a.b.n_tokens + kVTokens - 1) / kVTokens) * a.b.n_kv;
+  a.v_split = v_blocks * 4 <= enough ? 4 : v_blocks * 2 <= enough ? 2 : 1;
+  v_blocks *= a.v_split;
   const long long grid = static_cast<long long>(a.qk_tiles) * a.qk_groups + v_blocks;
   if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   return launch_pdl(kv_append_kernel<D, F16>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
