@@ -23,17 +23,32 @@
 // paged_combine_kernel joins. Every CTA finds its run from the lengths on the
 // device, so a captured launch follows them.
 //
-// Per CTA: warp 0 brings the queries, and keys and values into a ring of step
-// halves (128 keys, or their values transposed), by TMA; two streams, each
-// with its own S/P and O in tensor memory, have one warp that issues their
-// tcgen05.mma from one thread (one for both left the tensor cores waiting for
-// its bookkeeping: 390 us on the windowed prefill) and four softmax warps. A tile of more
-// than 128 rows gives each stream 128 rows and both read the same keys
-// ("pair": a key tile is loaded once for 256 rows, which is what a product of
-// this shape needs to stay off the L2's limit); a smaller tile gives both
-// streams the same rows and every other step ("alternate": a split over the
-// keys inside the CTA, joined in its epilogue). Either way one stream's
-// products run while the other's softmax does.
+// Per CTA: warp 0 brings keys and values by TMA into a ring of step halves (128
+// keys, or their values transposed). Two streams, each with its own S/P and O in
+// tensor memory, have one warp that issues their tcgen05.mma (one for both left
+// the tensor cores waiting for its bookkeeping; the first of them also brings
+// the queries) and four softmax warps. A tile of more than 128 rows gives each
+// stream 128 rows, and both read the same keys ("pair"); a smaller tile gives
+// both streams the same rows and every other step ("alternate": a split over
+// the keys inside the CTA, joined at its end). Either way one stream's products
+// run while the other's softmax does. With alternating tiles only, keys are
+// loaded twice as often: 328 against 236 us for the verify of 32 sequences of 16
+// tokens behind 32768 (32/8 heads of 128), and no more for one token of 64.
+//
+// Bounds and measurements (32/8 heads of 128, bf16, device time; floor: the
+// keys and values read once at the measured copy bandwidth, or the products at
+// the measured bf16 rate): 16 tokens over 262144 keys 163 us, floor 158 (memory);
+// 16 tokens of 32 sequences of 1024 to 8192 keys 112 us, floor 91 (memory, and
+// about 4 us each for the start, the joins and the items' ends); prefill of 8700
+// tokens with a window of 2048 284 us, floor 135 (products); one token of 64
+// sequences behind 32768 keys 79 us, floor 40; 16 tokens of 32 behind 32768 keys
+// 211 us, floor 144 (products, 1310 TFLOP/s). In the product-bound ones a step of
+// a pair takes 3400 cycles for 2048 of tensor work: scores -> maximum -> weights
+// -> P V -> the next scores is one chain per stream, and tensor memory (two S and
+// two O of 128 columns) holds no second S to break it. What was tried against
+// that and lost: two softmax warps per row (315 us: the scalar work of a step is
+// per warp), weights page by page without the second page's maximum (216),
+// products without turns (265).
 #include <cuda.h>
 
 #include <algorithm>
@@ -857,6 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = warp_uniform(tmem);
     const uint32_t s_col = tm + s * kStepKeys, o_col = tm + C::kOCol + s * D;
     int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
+    int brought = 0;    // items whose queries were called for
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, abort_at));
@@ -875,6 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                    it.t.t0 + st * a.stream_tokens);
         }
       }
+      brought += ok;
       __syncwarp();
     };
     if (s == 0 && items[0].nj > 0) bring_q(items[0]);
@@ -915,7 +932,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
           int tries = 1 << 27;
           while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
-            if (abort_flag || --tries == 0) { ok = false; break; }
+            if (__any_sync(0xffffffffu, abort_flag) || --tries == 0) {
+              ok = false;
+              break;
+            }
           }
         }
         turns += pair;
@@ -986,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // every issued product completes before TMEM and shared memory are released
     if (one) bar_commit(smem_u32(&mma_done));
     bar_wait(smem_u32(&mma_done), 0, never_at);
+    if (brought > 0) bar_wait(smem_u32(&q_full), (brought - 1) & 1, never_at);   // and every copy arrives
   } else {
     // ---------------- softmax and output ----------------
     const int stream = warp >= kSoftWarp0 + 4 ? 1 : 0;
