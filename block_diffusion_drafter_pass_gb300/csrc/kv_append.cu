@@ -256,6 +256,12 @@ extern "C" dflash_status dflash_kv_append(const dflash_paged_batch* b, const voi
     return refuse("token strides must be multiples of 8 elements and at least a token's row");
   if (misaligned16(k) || misaligned16(v) || misaligned16(q) || misaligned16(q_out))
     return refuse("k, v, q and q_out must be 16-byte aligned");
+  // each thread reads what it writes of a token's queries, and nothing else of them
+  if (q && ((q != q_out || q_stride != q_out_stride) && rows_overlap(q, q_stride, qw, q_out, q_out_stride, qw, b->n_tokens)))
+    return refuse("q_out must be q or not overlap it");
+  if (q && (rows_overlap(k, k_stride, kw, q_out, q_out_stride, qw, b->n_tokens) ||
+            rows_overlap(v, v_stride, kw, q_out, q_out_stride, qw, b->n_tokens)))
+    return refuse("q_out must not overlap k or v");
   AppendArgs a;
   std::memset(&a, 0, sizeof(a));
   a.b = paged_view(*b);

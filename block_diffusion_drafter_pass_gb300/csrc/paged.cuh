@@ -44,6 +44,19 @@ inline bool misaligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) 
 // A row stride, in elements, that rows of `width` elements with 16-byte loads allow.
 inline bool bad_stride(long long s, long long width) { return s < width || s % 8 || s > (1ll << 36); }
 
+// Whether two buffers of n rows of 16-bit elements share bytes. Columns of one
+// wider matrix (equal strides) interleave without sharing any; other interleaved
+// layouts count as shared.
+inline bool rows_overlap(const void* x, long long x_stride, long long x_width, const void* y, long long y_stride,
+                         long long y_width, long long n) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  if (a > b) return rows_overlap(y, y_stride, y_width, x, x_stride, x_width, n);
+  if (n < 1 || static_cast<uintptr_t>(((n - 1) * x_stride + x_width) * 2) <= b - a) return false;
+  if (x_stride != y_stride || n == 1) return true;
+  const long long off = static_cast<long long>((b - a) / 2 % x_stride);
+  return off < x_width || off + y_width > x_stride;
+}
+
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if constexpr (F16) {

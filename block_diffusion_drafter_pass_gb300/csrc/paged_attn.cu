@@ -715,6 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   long long all;
   const long long before = block_scan(mine, s_sum, all);
+  if (all >> 31 >= gridDim.x) {   // runs of 2^31 places: half an hour of work at least
+    if (tid == 0) latch_status(a.b.status, kDevBounds);
+    all = 0;
+  }
   // CTA c takes the places [c * run, (c + 1) * run); of more than 2^31 the run
   // is rounded up a little
   const int up = all >> 31 ? 33 - __clzll(all) : 0;
@@ -1242,6 +1246,7 @@ const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_s
   if (bad_stride(q_stride, width) || bad_stride(out_stride, width))
     return "token strides must be multiples of 8 elements and at least a token's row";
   if (misaligned16(q) || misaligned16(out)) return "q and out must be 16-byte aligned";
+  if (rows_overlap(q, q_stride, width, out, out_stride, width, b->n_tokens)) return "out must not overlap q";
   return nullptr;
 }
 

@@ -417,7 +417,8 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * Broken device arrays end in no access out of range: q_start is bent to
  * non-decreasing numbers within [0, n_tokens], kv_len to [0, 64*table_pages],
  * and tokens whose page id is outside [0, n_pages) are not written and not
- * seen. Each of these sets bit 2 (EDEVICE's) of *status, which the caller
+ * seen. (A batch whose steps of 128 keys, over all blocks of tokens and kv heads,
+ * pass 2^31 for each SM is not computed.) Each of these sets bit 2 (EDEVICE's) of *status, which the caller
  * clears. Slots past a length may hold any bits. */
 enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1 };
 
@@ -443,7 +444,8 @@ typedef struct {
  * exact to fp32 at any int32 position), and rotate the queries beside them.
  *  k, v       device [n_tokens][n_kv_heads][d], strides in elements between
  *             tokens (multiples of 8), 16-byte aligned
- *  q, q_out   device [n_tokens][n_heads][d], or both NULL; q_out may be q
+ *  q, q_out   device [n_tokens][n_heads][d], or both NULL; q_out is q,
+ *             or overlaps none of q, k and v
  *  positions  device [n_tokens] rotation positions, or NULL: the cache
  *             positions (callers behind a shared prefix add its length)
  *  rope_base  in (1, 1e12], or 0: nothing is rotated (q is copied)

@@ -396,6 +396,40 @@ def test_hidden_keys_may_hold_anything(dfl):
     assert not got[14:44].isfinite().any()
 
 
+def test_hidden_values_in_long_blocks(dfl):
+    """As above where each stream of a CTA has 128 rows, and where a block's keys are split between CTAs."""
+    for lens, at in (((200, 9000),), 8900), (((600, 700),), 400), (((16, 30000),), 29990):
+        b = Batch(lens, 8, 2, 128, BF)
+        _, values = dfl.kv_pool_views(b.pool, 128)
+        clean = b.attend(dfl)
+        first = at - (lens[0][1] - lens[0][0])        # the first new token that sees it
+        p, s = int(b.table[0, at // 64]), at % 64
+        for value in (float("nan"), float("inf")):
+            values[p][:, :, s] = value
+            got = b.attend(dfl)
+            assert (got[:first].float() - clean[:first].float()).abs().max() < 0.05
+            assert not got[first:].isfinite().any()
+
+
+def test_slots_past_the_lengths_of_a_wide_batch(dfl):
+    b = Batch([(8, 30 + 13 * i) for i in range(24)], 16, 1, 128, HF, prefix=1000)
+    poison(b, dfl, float("nan"))
+    check_attn(dfl, b)
+    check_attn(dfl, b, shared=True)
+
+
+def test_a_page_in_two_places(dfl):
+    """Tables that name a page twice, of one sequence and of two, and of the prefix and a sequence."""
+    b = Batch([(3, 300), (20, 200)], 8, 2, 64, BF, prefix=130)
+    b.table[0, 2] = b.table[0, 0]
+    b.table[1, 1] = b.table[0, 1]
+    b.prefix_table[0] = b.table[1, 0]
+    b.prefix_np = b.prefix_table.cpu().numpy()
+    check_attn(dfl, b)
+    check_attn(dfl, b, window=100, sinks=70)
+    check_attn(dfl, b, shared=True)
+
+
 def test_a_broken_neighbour_behind_the_same_prefix(dfl):
     """One sequence's cache is full of NaN: the others are unharmed, itself NaN."""
     b = Batch([(1, 60), (2, 100), (1, 33)], 8, 2, 64, HF, prefix=200)
@@ -465,6 +499,13 @@ def test_refused_tensors(dfl):
             dfl.dflash_paged_attn(f["q"], f["pool"], f["q_start"], f["kv_len"], f["table"])
     with pytest.raises(E):
         b.attend(dfl, window=-1)
+    with pytest.raises(E):
+        b.attend(dfl, out=b.q)
+    with pytest.raises(E):
+        b.attend_shared(dfl, out=b.q)
+    with pytest.raises(E):
+        dfl.dflash_kv_append(b.pool, b.k, b.v, b.q_start, b.kv_len, b.table, q=b.q,
+                             q_out=b.qkv.as_strided(b.q.shape, b.q.stride(), 64))
     with pytest.raises(E):
         b.attend(dfl, out=torch.empty(4, 8, 64, dtype=BF, device=DEV))
     with pytest.raises(E):

@@ -129,18 +129,19 @@ BAD_BATCH = [dict(dtype=2), dict(dtype=-1), dict(head_dim=32), dict(head_dim=256
              dict(n_kv_heads=3), dict(n_heads=258, n_kv_heads=2), dict(n_seq=-1), dict(n_seq=1025), dict(n_tokens=-1),
              dict(n_tokens=(1 << 24) + 1), dict(pool=None), dict(page_table=None), dict(q_start=None), dict(kv_len=None),
              dict(pool=FAKE + 2), dict(n_pages=0), dict(table_pages=0), dict(table_stride=1),
-             dict(table_pages=(1 << 24) + 1, table_stride=1 << 25)]
+             dict(table_pages=(1 << 24) + 1, table_stride=1 << 25),
+             dict(table_pages=(1 << 20) + 1, table_stride=1 << 25), dict(n_heads=129, n_kv_heads=129)]
 
 
 def append_call(lib, b, **kw):
-    f = dict(k=FAKE, ks=128, v=FAKE, vs=128, q=FAKE, qs=512, qo=FAKE, qos=512, pos=None, base=1e4)
+    f = dict(k=FAKE, ks=128, v=2 * FAKE, vs=128, q=3 * FAKE, qs=512, qo=3 * FAKE, qos=512, pos=None, base=1e4)
     f.update(kw)
     return lib.dflash_kv_append(b, f["k"], f["ks"], f["v"], f["vs"], f["q"], f["qs"], f["qo"], f["qos"], f["pos"],
                                 f["base"], None)
 
 
 def attn_call(lib, b, shared=False, **kw):
-    f = dict(q=FAKE, qs=512, out=FAKE, os=512, window=0, sinks=0, causal=1, scale=0.1, ws=FAKE, wb=1 << 40,
+    f = dict(q=FAKE, qs=512, out=2 * FAKE, os=512, window=0, sinks=0, causal=1, scale=0.1, ws=FAKE, wb=1 << 40,
              pt=FAKE, pl=100)
     f.update(kw)
     if shared:
@@ -164,7 +165,9 @@ def test_broken_batches_are_refused(lib, bad):
 @pytest.mark.parametrize("bad", [dict(k=None), dict(v=None), dict(k=FAKE + 8), dict(v=FAKE + 4), dict(ks=64),
                                  dict(vs=132), dict(q=None), dict(qo=None), dict(q=FAKE + 2), dict(qs=516),
                                  dict(qos=0), dict(base=1.0), dict(base=-5.0), dict(base=float("nan")),
-                                 dict(base=float("inf"))])
+                                 dict(base=float("inf")),
+                                 dict(qo=FAKE + 3 * 256 + 128), dict(qo=2 * FAKE - 3 * 1024), dict(qo=3 * FAKE + 16),
+                                 dict(qo=3 * FAKE, qos=1024)])
 def test_append_refusals(lib, bad):
     assert append_call(lib, ctypes.byref(batch()), **bad) == dfl.DFLASH_EINVAL
 
@@ -172,7 +175,9 @@ def test_append_refusals(lib, bad):
 @pytest.mark.parametrize("shared", [False, True])
 @pytest.mark.parametrize("bad", [dict(q=None), dict(out=None), dict(q=FAKE + 2), dict(out=FAKE + 8), dict(qs=504),
                                  dict(os=513), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-                                 dict(scale=float("inf"))])
+                                 dict(scale=float("inf")),
+                                 dict(out=FAKE), dict(out=FAKE + 3 * 1024 + 1008), dict(out=FAKE - 3 * 1024 - 16),
+                                 dict(qs=1024, os=1024, out=FAKE + 1008), dict(qs=1024, os=512, out=FAKE + 1024)])
 def test_attention_refusals(lib, bad, shared):
     assert attn_call(lib, ctypes.byref(batch()), shared=shared, **bad) == dfl.DFLASH_EINVAL
 
@@ -183,9 +188,18 @@ def test_window_and_prefix_refusals(lib):
     assert attn_call(lib, b, window=5, sinks=-1) == dfl.DFLASH_EINVAL
     assert attn_call(lib, b, shared=True, pl=-1) == dfl.DFLASH_EINVAL
     assert attn_call(lib, b, shared=True, pl=(1 << 30) + 1) == dfl.DFLASH_EINVAL
+    assert attn_call(lib, b, shared=True, pl=(1 << 26) + 1) == dfl.DFLASH_EINVAL
     assert attn_call(lib, b, shared=True, pt=None) == dfl.DFLASH_EINVAL
     assert lib.dflash_paged_attn_workspace(b, None) == dfl.DFLASH_EINVAL
     assert lib.dflash_kv_append(None, FAKE, 128, FAKE, 128, None, 0, None, 0, None, 0.0, None) == dfl.DFLASH_EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(out=FAKE + 4 * 1024), dict(out=FAKE - 4 * 1024),
+                                dict(qs=1024, os=1024, out=FAKE + 1024), dict(qs=1536, os=1536, out=FAKE - 1536)])
+def test_rows_that_share_nothing_pass_the_overlap_check(lib, kw):
+    """Neighbouring buffers, and column ranges of one wider matrix: refused for the workspace only."""
+    assert attn_call(lib, ctypes.byref(batch()), ws=None, **kw) in (dfl.DFLASH_EINVAL, dfl.DFLASH_ECUDA)
+    assert b"overlap" not in lib.dflash_last_error(None)
 
 
 def test_an_empty_batch_is_no_work(lib):
