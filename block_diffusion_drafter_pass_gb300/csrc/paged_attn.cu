@@ -276,6 +276,20 @@ __device__ __noinline__ int pair_takes(const Batch& b, const Tile& t, int seq, i
   return (step_counts(b, seq, base, t.t0, mid) ? 1 : 0) | (step_counts(b, seq, base, mid, t.t0 + t.ntok) ? 2 : 0);
 }
 
+// The producer's note on a step: bit u, page u is not there; bit 2 + s, stream s
+// of a pair takes the step; from bit 4 on the step's number + 1, so that a
+// reader may look for it before the barrier that says it is there (while the
+// products read shared memory a load takes 300 cycles, which is better spent
+// beside the wait than after it).
+__device__ __forceinline__ uint32_t step_note(int step, int bits) { return (static_cast<uint32_t>(step) + 1) << 4 | bits; }
+__device__ __forceinline__ uint32_t note_early(const uint32_t* s_step, int step) {
+  return *const_cast<const volatile uint32_t*>(s_step + step % kStepRing);
+}
+// After the barrier, what was read before it or else the note itself.
+__device__ __forceinline__ uint32_t note_of(const uint32_t* s_step, int step, uint32_t early) {
+  return early >> 4 == static_cast<uint32_t>(step) + 1 ? early : note_early(s_step, step);
+}
+
 // The row of one softmax thread: what it sees of its sequence's cache, and (of
 // a shared prefix) prefix_len more.
 struct Row {
@@ -631,9 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
   __shared__ Join join;
   __shared__ int s_page[kIdRing][2];
-  // of the CTA's recent steps: bit u, page u is not there; bit 2 + s, stream s
-  // of a pair takes the step
-  __shared__ uint8_t s_step[kStepRing];
+  __shared__ uint32_t s_step[kStepRing];
   __shared__ long long s_sum[kThreads / 32];
   __shared__ Item s_first[2];   // the CTA's first item (and where its run begins)
   __shared__ Item s_items[kThreads / 32][2];   // each warp's item and the one after it
@@ -678,6 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&maps.v);
     tma_prefetch_desc(&maps.q);
   }
+  if (tid < kStepRing) s_step[tid] = 0;   // no step's note (an earlier CTA's may lie here)
   if (warp == 1) tmem_alloc(&tmem_slot, C::kTmemCols);
   grid_dep_wait();
   grid_dep_launch();
@@ -825,7 +838,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int flags = gone;
             if (it.pair) flags |= pair_takes(b, it.t, wk.s.seq, wk.s.base) << 2;
             wk.next(b, it.t);
-            s_step[steps++ % kStepRing] = static_cast<uint8_t>(flags);   // read behind this half's barrier and the product's
+            const uint32_t note = step_note(steps, flags);
+            *const_cast<volatile uint32_t*>(s_step + steps++ % kStepRing) = note;
           }
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(C::kHalf) : "memory");
 #pragma unroll
@@ -928,7 +942,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // block each, so that one stream's run while the other's softmax does.
         // An alternating tile's values go back as soon as they can.
         const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
+        uint32_t early = 0;
         {
+          if (pair && more) early = note_early(s_step, steps);
           bool need = lane == 0 && pv;
           uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
           if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
@@ -945,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         turns += pair;
         if (!ok) break;
         uint32_t take = ((j + lead) & 1) == s && more;
-        if (pair && more) take = warp_uniform(s_step[steps % kStepRing] >> (2 + s) & 1);
+        if (pair && more) take = warp_uniform(note_of(s_step, steps, early) >> (2 + s) & 1);
         tc_fence_after();
         if (takes & 1) {   // O (+)= P V
           const uint32_t v_at = ring_low + vslot * (C::kHalf >> 4);
@@ -1024,6 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int outs = 0;       // items with products of this stream
     int k = 0;
     int step0 = 0;      // steps of the CTA's items before this one
+    const int prefix_len = b.prefix_len, sinks = b.sinks;
     bool ok = true;
     // waits taken by all 32 lanes together, so the warp-collective TMEM
     // accesses after them never diverge (also when a wait runs out)
@@ -1047,19 +1064,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       int done = 0;                      // steps of this item that this stream took
       StepWalk w;
       w.start(b, it.t, it.j);
-      for (int j = 0; j < it.nj; ++j, w.next(b, it.t)) {
-        if (!it.pair && (j & 1) != stream) continue;
+      const int pair = it.pair, nj = it.nj;
+      for (int j = 0; j < nj; ++j, w.next(b, it.t)) {
+        if (!pair && (j & 1) != stream) continue;
+        const uint32_t early = note_early(s_step, step0 + j);
         warp_wait(&s_full[stream], ns & 1);
         if (!ok) break;
-        const int flags = s_step[(step0 + j) % kStepRing];
-        if (it.pair && !(flags >> (2 + stream) & 1)) {   // no row of the stream sees the step
+        const int flags = note_of(s_step, step0 + j, early);
+        if (pair && !(flags >> (2 + stream) & 1)) {   // no row of the stream sees the step
           __syncwarp();
           if (lane < 2) mbar_arrive(&p_full[stream][lane]);
           ++ns;
           continue;
         }
         // columns [0, c_hi) less those in [c_sink, c_lo) are seen
-        const RowSpan sp = span_of(b, row, w.s);
+        const RowSpan sp = row.token < 0 || (w.s.seq >= 0 && w.s.seq != row.seq) ? RowSpan{0, -1, 0}
+                           : w.s.seq < 0 ? RowSpan{0, row.hi + prefix_len, 0} : RowSpan{row.lo, row.hi, sinks};
         const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
         const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
         const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
