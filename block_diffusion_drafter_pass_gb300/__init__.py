@@ -351,8 +351,8 @@ def dflash_paged_attn(q, pool, q_start, kv_len, page_table, *, window: int = 0, 
     """Attention of the new tokens q [T, n_heads, d] over their sequences'
     caches (their own keys and values appended before) -> [T, n_heads, d].
     window > 0: keys after position - window and the first `sinks` ones only.
-    scale defaults to d ** -0.5. Rows of no sequence are left as they are (a
-    fresh `out` is not initialised)."""
+    scale defaults to d ** -0.5. `out` must not overlap q. Rows of no sequence
+    are left as they are (a fresh `out` is not initialised)."""
     import torch
 
     def run(lib, b, qp, qs, op, os_, sc, ws, wb, s):

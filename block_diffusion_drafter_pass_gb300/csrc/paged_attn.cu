@@ -38,17 +38,22 @@
 // Bounds and measurements (32/8 heads of 128, bf16, device time; floor: the
 // keys and values read once at the measured copy bandwidth, or the products at
 // the measured bf16 rate): 16 tokens over 262144 keys 163 us, floor 158 (memory);
-// 16 tokens of 32 sequences of 1024 to 8192 keys 112 us, floor 91 (memory, and
+// 16 tokens of 32 sequences of 1024 to 8192 keys 113 us, floor 91 (memory, and
 // about 4 us each for the start, the joins and the items' ends); prefill of 8700
-// tokens with a window of 2048 284 us, floor 135 (products); one token of 64
-// sequences behind 32768 keys 79 us, floor 40; 16 tokens of 32 behind 32768 keys
-// 211 us, floor 144 (products, 1310 TFLOP/s). In the product-bound ones a step of
-// a pair takes 3400 cycles for 2048 of tensor work: scores -> maximum -> weights
-// -> P V -> the next scores is one chain per stream, and tensor memory (two S and
-// two O of 128 columns) holds no second S to break it. What was tried against
-// that and lost: two softmax warps per row (315 us: the scalar work of a step is
-// per warp), weights page by page without the second page's maximum (216),
-// products without turns (265).
+// tokens with a window of 2048 277 us, floor 135 (products); one token of 64
+// sequences behind 32768 keys 77 us, floor 40; 16 tokens of 32 behind 32768 keys
+// 209 us, floor 144 (products, 1325 TFLOP/s). In the product-bound ones a step of
+// a pair takes 3300 cycles for 2048 of tensor work: scores -> maximum -> weights
+// -> P V -> the next scores is one chain per stream, mostly hand-overs (with the
+// exponentials, the sums and 7/8 of the products taken out the last case still
+// takes 200 us), and tensor memory (two S and two O of 128 columns) holds no
+// second S to break it. What was tried against that and lost, for that case:
+// scores page by page into the place whose weights were just multiplied (230 us:
+// a product over 64 keys takes 3/4 of one over 128, and the softmax waits twice),
+// or only the second page's ahead (234), weights page by page without the second
+// page's maximum (216), products without turns (265), two softmax warps per row
+// (315: the scalar work of a step is per warp), the two streams' own caches step
+// by step in turn (209, and 2 to 3% more where own caches are long).
 #include <cuda.h>
 
 #include <algorithm>
@@ -70,7 +75,11 @@ constexpr int kRows = 128;            // rows of a stream: the MMA's M
 // ahead of the softmax (a step's values are not overwritten before its P).
 constexpr int kStepRing = 16;
 constexpr int kIdsAhead = 2, kIdRing = 16;   // steps
-constexpr int kItemSteps = 4;         // what an item costs beside its steps, in steps (dealing only)
+// What an item costs beside its steps, in steps (dealing only). With 2, uneven
+// short blocks take 25.5 us instead of 24.7, uneven blocks behind a prefix of
+// 5000 65.7 instead of 63.9 and one long sequence 171 instead of 164 (its runs
+// then end a little off the heads' ends); with 8, 26.5, 68.9 and 178.
+constexpr int kItemSteps = 4;
 constexpr int kNoEnd = 1 << 30;       // above every position
 constexpr float kRescaleLog2 = 8.f;   // rescale O when a row's maximum grows by more than 2^8
 
