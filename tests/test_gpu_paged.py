@@ -4,7 +4,8 @@
 Tolerances, from the arithmetic, u = half a step of the stored type (bf16
 2^-8, fp16 2^-11):
  - append: x cos - y sin in fp32 with cos and sin off by at most 2^-22, one
-   rounding: u |ref| + 2^-20 (|x| + |y|); values are copied, so they are equal.
+   rounding: u |ref| + 2^-20 (|x| + |y|), and for fp16 results below 2^-14, whose
+   steps are 2^-24, half of such a step; values are copied, so they are equal.
  - attention, A = sum of w |v|: the weights may be rounded to the stored type
    (u A) and the output is (u |o|). A score of size S = scale sum |q||k| is an
    fp32 sum over d in steps of 16, so it is off by at most (d/16 + 4) 2^-23 S,
@@ -25,6 +26,7 @@ from oracle import paged_cache as pc  # noqa: E402
 
 DEV = "cuda:0"
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+TINY = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -25}   # half a step of the smallest values
 BF, HF = torch.bfloat16, torch.float16
 
 
@@ -139,7 +141,7 @@ def check_append(dfl, b, base, positions=None, with_q=True, in_place=False):
     if with_q:
         g = f64(got)
         size = np.abs(q0) + np.abs(np.roll(q0, b.d // 2, axis=-1))
-        assert (np.abs(g - q)[owned] <= (u * np.abs(q) + 2.0 ** -20 * size)[owned] + (base == 0) * 0.0).all()
+        assert (np.abs(g - q)[owned] <= (u * np.abs(q) + 2.0 ** -20 * size + TINY[b.dtype])[owned]).all()
         if in_place:
             np.testing.assert_array_equal(g[~owned], q0[~owned])
         else:
@@ -150,7 +152,7 @@ def check_append(dfl, b, base, positions=None, with_q=True, in_place=False):
     np.testing.assert_array_equal(after[:, 1], pool[:, 1])          # values: copied, nothing else touched
     touched = pool[:, 0] != before[:, 0]
     np.testing.assert_array_equal(after[:, 0][~touched], before[:, 0][~touched])
-    tol = u * np.abs(pool[:, 0]) + 2.0 ** -20 * 2 * np.abs(k0).max()
+    tol = u * np.abs(pool[:, 0]) + 2.0 ** -20 * 2 * np.abs(k0).max() + TINY[b.dtype]
     assert (np.abs(after[:, 0] - pool[:, 0]) <= np.where(touched, tol, 0.0)).all()
 
 
@@ -183,6 +185,14 @@ def test_append_at_far_positions(dfl, base):
     b = Batch([(6, 6)], 8, 2, 128, HF, q_scale=1)
     far = torch.tensor([0, 262143, 2 ** 24 + 1, 2 ** 30, 2 ** 31 - 1, -5], dtype=torch.int32, device=DEV)
     check_append(dfl, b, base, positions=far)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_append_at_given_positions(dfl, dtype):
+    """Positions of the caller's (also negative ones), results of every size down to fp16's smallest steps."""
+    b = Batch([(33, 90), (5, 5), (200, 200)], 24, 2, 64, dtype)
+    at = np.random.default_rng(5).integers(-100, 1 << 20, b.T).astype(np.int32)
+    check_append(dfl, b, 1e4, positions=torch.from_numpy(at).to(DEV))
 
 
 def test_append_strided_padded_and_in_place(dfl):
@@ -416,6 +426,21 @@ def test_slots_past_the_lengths_of_a_wide_batch(dfl):
     poison(b, dfl, float("nan"))
     check_attn(dfl, b)
     check_attn(dfl, b, shared=True)
+
+
+@pytest.mark.parametrize("heads,tokens", [(8, 3), (64, 200)])
+def test_a_cache_of_millions_of_tokens(dfl, heads, tokens):
+    """A few pages over and over: the softmax over many copies of the same keys
+    is the softmax over one of them."""
+    b = Batch([(tokens, 1024)], heads, 1, 128, BF, prefix=1024)
+    copies = 4096 if tokens < 10 else 256
+    own, pre = b.table.repeat(1, copies), b.prefix_table.repeat(copies)
+    ref = b.oracle(causal=False)
+    one = dfl.dflash_paged_attn(b.q, b.pool, b.q_start, b.kv_len * copies, own, causal=False)
+    check(one, ref, BF, 128, 1024 * copies, 6.0)
+    ref = b.oracle(causal=False, prefix_table=b.prefix_np, prefix_len=1024)
+    two = dfl.dflash_shared_prefix_attn(b.q, b.pool, b.q_start, b.kv_len * copies, own, pre, 1024 * copies, causal=False)
+    check(two, ref, BF, 128, 2048 * copies, 6.0)
 
 
 def test_a_page_in_two_places(dfl):
