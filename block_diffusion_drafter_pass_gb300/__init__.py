@@ -323,25 +323,34 @@ def dflash_kv_append(pool, k, v, q_start, kv_len, page_table, *, q=None, q_out=N
     return _run_on(torch, dev, stream, call)
 
 
+_workspace_bytes = {}   # by all that they depend on; above 128 tokens they no longer grow
+
+
 def _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status, stream):
     if q.dim() != 3:
         _refuse("q must be [tokens, heads, d]")
     shape = q.shape
     T, n_heads, d = shape
     dtype, dev = pool.dtype, pool.get_device()
-    _, b = _paged_batch(torch, pool, dev, n_heads, d, T, q_start, kv_len, page_table, status)
+    n_kv, b = _paged_batch(torch, pool, dev, n_heads, d, T, q_start, kv_len, page_table, status)
     qs = _rows_arg("q", q, dtype, dev, shape)
     if scale is None:
         scale = d ** -0.5
     lib = _lib or load_library()
 
     def call(s):
-        need = ctypes.c_size_t()
-        _check(lib.dflash_paged_attn_workspace(b, ctypes.byref(need)))
-        ws = torch.empty(need.value, dtype=torch.uint8, device=pool.device)
+        key = (dev, n_heads, n_kv, d, min(T, 129))
+        need = _workspace_bytes.get(key)
+        if need is None:   # asked once: a library call between PyTorch's costs 3 us of cold code
+            size = ctypes.c_size_t()
+            _check(lib.dflash_paged_attn_workspace(b, ctypes.byref(size)))
+            need = size.value
+            if need:   # an empty batch needs none
+                _workspace_bytes[key] = need
+        ws = torch.empty(need, dtype=torch.uint8, device=pool.device)
         o = torch.empty(shape, dtype=dtype, device=pool.device) if out is None else out
         os_ = n_heads * d if out is None else _rows_arg("out", o, dtype, dev, shape)
-        _check(run(lib, b, q.data_ptr(), qs, o.data_ptr(), os_, scale, ws.data_ptr(), need.value, s))
+        _check(run(lib, b, q.data_ptr(), qs, o.data_ptr(), os_, scale, ws.data_ptr(), need, s))
         return o
     return _run_on(torch, dev, stream, call)
 

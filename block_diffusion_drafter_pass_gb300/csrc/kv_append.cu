@@ -6,7 +6,7 @@
 // and at far positions a float (or float product) has lost it, so the host
 // gives base^(-2i/d) / (2 pi) as a 64-bit fraction of a turn and the kernel
 // multiplies by p in integers: whole turns fall off the top, exactly, and
-// what is left is off by p * 2^-53 of the step. sincospif takes it from there.
+// what is left is off by p * 2^-52 of the step. sincospif takes it from there.
 //
 // Bound: memory, q, k and v read once, q and the pages written once.
 // Queries and keys: one thread per (token, 8 pairs), which computes its 8
@@ -276,12 +276,17 @@ extern "C" dflash_status dflash_kv_append(const dflash_paged_batch* b, const voi
   a.positions = positions;
   a.rotate = rope_base != 0.f;
   if (a.rotate) {
-    const double two_pi = 6.283185307179586476925286766559;
-    for (int i = 0; i < b->head_dim / 2; ++i) {
-      // theta_0 = 1 rad is 0.159 of a turn, so the product stays below 2^62
-      const double turns = std::pow(static_cast<double>(rope_base), -2.0 * i / b->head_dim) / two_pi;
-      a.turn[i] = static_cast<unsigned long long>(std::ldexp(turns, 64));
+    // base^(-2i/d) from two factors, since 64 powers are a quarter of the call's
+    // time; the first pair's, whose angle is the largest, are exact
+    const double two_pi = 6.283185307179586476925286766559, base = rope_base;
+    double coarse[8], fine[8];
+    for (int i = 0; i < 8; ++i) {
+      coarse[i] = std::pow(base, -16.0 * i / b->head_dim) / two_pi;
+      fine[i] = std::pow(base, -2.0 * i / b->head_dim);
     }
+    // theta_0 = 1 rad is 0.159 of a turn, so the product stays below 2^62
+    for (int i = 0; i < b->head_dim / 2; ++i)
+      a.turn[i] = static_cast<unsigned long long>(std::ldexp(coarse[i / 8] * fine[i % 8], 64));
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
