@@ -363,6 +363,8 @@ def dflash_paged_attn(q, pool, q_start, kv_len, page_table, *, window: int = 0, 
     scale defaults to d ** -0.5. `out` must not overlap q. Rows of no sequence
     are left as they are (a fresh `out` is not initialised)."""
     import torch
+    if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):   # a C int would wrap
+        _refuse("window and sinks must be 0..2^31 - 1")
 
     def run(lib, b, qp, qs, op, os_, sc, ws, wb, s):
         return lib.dflash_paged_attn(b, qp, qs, op, os_, window, sinks, 1 if causal else 0, sc, ws, wb, s)
@@ -376,6 +378,8 @@ def dflash_shared_prefix_attn(q, pool, q_start, kv_len, page_table, prefix_table
     sees the prefix and then its own cache (kv_len and page_table count the
     tokens behind the prefix). The prefix is read once for the whole batch."""
     import torch
+    if not 0 <= prefix_len <= 1 << 26:
+        _refuse("prefix_len must be 0..2^26")
     if prefix_table.dim() != 1 or prefix_table.shape[0] * KV_PAGE < prefix_len:
         _refuse("prefix_table must be one row of at least ceil(prefix_len / 64) page ids")
     table = _i32_arg("prefix_table", prefix_table, torch.int32, pool.get_device(), prefix_table.shape)

@@ -222,3 +222,10 @@ def test_tensors_of_the_wrong_kind_are_refused_before_the_library():
         dfl.dflash_paged_attn(q, pool, i(3), i(2), i(2, 2))
     with pytest.raises(dfl.DFlashError):
         dfl.dflash_shared_prefix_attn(q, pool, i(3), i(2), i(2, 2), i(1), 100)
+    # numbers that a C int would wrap
+    for kw in (dict(window=(1 << 32) + 100), dict(window=-1), dict(window=5, sinks=1 << 31)):
+        with pytest.raises(dfl.DFlashError, match="window and sinks"):
+            dfl.dflash_paged_attn(q, pool, i(3), i(2), i(2, 2), **kw)
+    for n in (-1, (1 << 26) + 1, (1 << 32) + 64):
+        with pytest.raises(dfl.DFlashError, match="prefix_len"):
+            dfl.dflash_shared_prefix_attn(q, pool, i(3), i(2), i(2, 2), i(1), n)
