@@ -32,8 +32,10 @@
 // both streams the same rows and every other step ("alternate": a split over
 // the keys inside the CTA, joined at its end). Either way one stream's products
 // run while the other's softmax does. With alternating tiles only, keys are
-// loaded twice as often: 328 against 236 us for the verify of 32 sequences of 16
-// tokens behind 32768 (32/8 heads of 128), and no more for one token of 64.
+// loaded twice as often and a step's hand-overs serve half the rows: 324 against
+// 209 us for 16 tokens of 32 sequences behind 32768, 365 against 277 for the
+// prefill below, 82 against 77 for one token of 64 sequences (whose own caches
+// then go faster). Rows that fit one stream have no second half to pair.
 //
 // Bounds and measurements (32/8 heads of 128, bf16, device time; floor: the
 // keys and values read once at the measured copy bandwidth, or the products at
