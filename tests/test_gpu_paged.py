@@ -597,6 +597,33 @@ def test_streams(dfl):
     assert all(torch.equal(x, ra) and torch.equal(y, rb) for x, y in got)
 
 
+def test_threads(dfl):
+    """Four host threads at once, each with a stream, a pool and shapes of its own."""
+    import threading
+    bs = [Batch([(1 + 5 * i, 400 + 300 * i), (i, 50)], 8, 2, d, dt, prefix=100 * i, seed=i)
+          for i, (d, dt) in enumerate(((64, BF), (64, HF), (128, BF), (128, HF)))]
+    ref = [(b.attend(dfl, window=90, sinks=3), b.attend_shared(dfl)) for b in bs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(b, r):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(50):
+                x, y = b.attend(dfl, window=90, sinks=3, stream=s), b.attend_shared(dfl, stream=s)
+                with pytest.raises(dfl.DFlashError):
+                    b.attend(dfl, scale=-1.0, stream=s)
+                s.synchronize()
+                if not (torch.equal(x, r[0]) and torch.equal(y, r[1])):
+                    wrong.append(b.d)
+        except BaseException as e:   # shown by the assertion below
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=a) for a in zip(bs, ref)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not wrong
+
+
 def test_captured_calls_follow_the_lengths(dfl):
     """One captured step replayed over growing caches, and two graphs with
     their own workspaces replayed in turn and at once."""
