@@ -638,6 +638,44 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
   return true;
 }
 
+// Slots past a length may hold any bits. Their weights are zero, but 0 times
+// infinity or NaN would spoil every row of the tile, so where a run of keys ends
+// inside a page, the values behind it are cleared before their product: those of
+// a step from its key `cut` to the end of that page (per page D rows of 64 slots,
+// 128 bytes, swizzled), in half `c` of the ring. By the four softmax warps of a
+// stream, a row for each thread, while their scores are made: in the issuing
+// warps the same cost 3% of a windowed prefill, in the producer's or in a warp of
+// its own 2 to 7% of all long cases. Here it costs 0.5% of that prefill, 1 us of
+// the shortest calls and 1.2 of one token of 64 sequences behind a prefix. (Left
+// to redo_row, 16 tokens of 32 sequences of 1024 to 8192 keys with NaN behind
+// their ends took 36 ms instead of 0.11.) s_bar: a barrier to wait for first, or
+// 0. False when a wait ran out.
+template <int D>
+__device__ __forceinline__ bool cut_values(uint32_t ring, uint32_t full_at, uint32_t abort_at, int c, int cut,
+                                           uint32_t s_bar, uint32_t s_parity) {
+  constexpr int S = Cfg<D>::kSlots;
+  bool ok = s_bar == 0 || bar_wait(s_bar, s_parity, abort_at);
+  ok = ok && bar_wait(full_at + c % S * 8, c / S & 1, abort_at);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  const int r = (threadIdx.x - kSoftWarp0 * 32) % kRows, keep = cut % kPage;
+  if (r < D) {
+    const uint32_t row = ring + c % S * Cfg<D>::kHalf + cut / kPage * (D * 128) + r * 128;
+#pragma unroll 1
+    for (int e = keep; e < kPage;) {
+      const uint32_t at = row + (((e >> 3) ^ (r & 7)) << 4) + (e & 7) * 2;
+      if (e % 8) {
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
+        ++e;
+      } else {
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+        e += 8;
+      }
+    }
+    fence_proxy_async_smem();
+  }
+  return true;
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_attn_kernel(const __grid_constant__ PagedMaps maps, const __grid_constant__ PagedAttnArgs a) {
@@ -1078,6 +1116,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pair = it.pair, nj = it.nj;
       for (int j = 0; j < nj; ++j, w.next(b, it.t)) {
         if (!pair && (j & 1) != stream) continue;
+        const uint32_t rest = w.s.end - w.s.base;
+        if (rest < kStepKeys && rest % kPage != 0 && (!pair || stream == 0)) {
+          // Of a pair the first stream's warps do it: its products' turn comes
+          // before the other's. In the ring an item's keys lead its values by 1
+          // step (pair) or 2, and the half that lay in the values' place must have
+          // come, or its barrier's phase would be taken for theirs: with 8 halves,
+          // or in a pair, the scores seen last say so, else the ones to come.
+          const int c = 2 * step0 + j + min(j + (pair ? 1 : 2), nj);
+          ok = cut_values<D>(smem_u32(smem) + C::kQBytes, smem_u32(kv_full), abort_at, c, rest,
+                             S == 4 && !pair ? smem_u32(&s_full[stream]) : 0, ns & 1);
+          if (!ok) break;
+        }
         const uint32_t early = note_early(s_step, step0 + j);
         warp_wait(&s_full[stream], ns & 1);
         if (!ok) break;

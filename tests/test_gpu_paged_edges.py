@@ -1,0 +1,33 @@
+"""Paged-cache operators at edges of the page pool and the lengths."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from tests.test_gpu_paged import BF, HF, Batch, dfl, poison  # noqa: E402, F401
+
+
+# Lengths that end in either page of a step of 128 keys, at its slots 1, 8, 13 and 63, and at its end.
+TAILS = [
+    ("own", dict(lens=[(1, 1), (1, 70), (16, 100), (3, 129), (40, 40), (1, 900), (5, 136), (2, 191), (7, 64), (9, 128)])),
+    ("own", dict(lens=[(200, 1101), (130, 141), (1, 13)])),       # rows of both streams of a CTA
+    ("own", dict(lens=[(16, 20013)])),                            # split between CTAs
+    ("window", dict(lens=[(300, 1103), (1, 513), (20, 77)])),
+    ("shared", dict(lens=[(1, 1 + 11 * i) for i in range(40)], prefix=1077)),
+    ("shared", dict(lens=[(16, 40), (0, 9), (3, 3), (90, 301)], prefix=8)),
+    ("shared", dict(lens=[(2, 63), (1, 65)], prefix=127)),
+]
+
+
+@pytest.mark.parametrize("heads,n_kv,d,dtype", [(8, 2, 128, BF), (28, 4, 64, HF), (4, 4, 64, BF), (8, 1, 128, HF)])
+@pytest.mark.parametrize("kind,shape", TAILS, ids=lambda x: str(x)[:40])
+def test_slots_past_a_length_change_no_bit(dfl, kind, shape, heads, n_kv, d, dtype):
+    """Not even by another way through the kernel: NaN or infinity there costs nothing."""
+    b = Batch(heads=heads, n_kv=n_kv, d=d, dtype=dtype, **shape)
+    call = {"own": lambda: b.attend(dfl), "window": lambda: b.attend(dfl, window=200, sinks=70),
+            "shared": lambda: b.attend_shared(dfl)}[kind]
+    clean = call()
+    assert clean.isfinite().all()
+    for value in (float("nan"), float("-inf")):
+        poison(b, dfl, value)
+        assert torch.equal(call(), clean)
