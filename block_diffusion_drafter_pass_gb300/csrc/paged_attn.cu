@@ -64,6 +64,7 @@
 #include <cstring>
 
 #include "paged.cuh"
+#include "paged_deal.h"
 #include "paged_row.cuh"
 
 namespace dfl {
@@ -777,14 +778,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   long long all;
   const long long before = block_scan(mine, s_sum, all);
-  if (all >> 31 >= gridDim.x) {   // runs of 2^31 places: half an hour of work at least
+  if (!deal_fits(all, gridDim.x)) {
     if (tid == 0) latch_status(a.b.status, kDevBounds);
     all = 0;
   }
-  // CTA c takes the places [c * run, (c + 1) * run); of more than 2^31 the run
-  // is rounded up a little
-  const int up = all >> 31 ? 33 - __clzll(all) : 0;
-  const int run = static_cast<int>((static_cast<uint32_t>(all >> up) + (up ? gridDim.x : gridDim.x - 1)) / gridDim.x) << up;
+  const int run = deal_run(all, gridDim.x);
   const long long x0 = static_cast<long long>(run) * blockIdx.x;
   const int x_len = static_cast<int>(max(0ll, min(static_cast<long long>(run), all - x0)));
   if (x_len > 0 && x0 >= before && x0 < before + mine) {   // one thread: the run begins in its tiles

@@ -418,8 +418,8 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * non-decreasing numbers within [0, n_tokens], kv_len to [0, 64*table_pages],
  * and tokens whose page id is outside [0, n_pages) are not written and not
  * seen. (A batch whose steps of 128 keys, over all blocks of tokens and kv heads,
- * pass 2^31 for each SM is not computed.) Each of these sets bit 2 (EDEVICE's) of *status, which the caller
- * clears. Slots past a length may hold any bits. */
+ * pass 2^29 for each SM is not computed.) Each of these sets bit 2 (EDEVICE's) of
+ * *status, which the caller clears. Slots past a length may hold any bits. */
 enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1 };
 
 typedef struct {

@@ -1,0 +1,46 @@
+"""Host-side checks of the paged-cache operators at edges (no GPU)."""
+import ctypes
+import os
+import random
+import shutil
+import subprocess
+
+import pytest
+
+from block_diffusion_drafter_pass_gb300 import _build
+
+
+# --- how places are dealt to the CTAs ------------------------------------------
+
+@pytest.fixture(scope="module")
+def deal(tmp_path_factory):
+    if not shutil.which("g++"):
+        pytest.skip("no g++")
+    d = tmp_path_factory.mktemp("deal")
+    src, lib = os.path.join(d, "deal.cpp"), os.path.join(d, "deal.so")
+    with open(src, "w") as f:
+        f.write('#include "paged_deal.h"\nextern "C" int run_of(long long all, int ctas) {\n'
+                '  return dfl::deal_fits(all, ctas) ? dfl::deal_run(all, ctas) : -1;\n}\n')
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-fsanitize=undefined", "-fno-sanitize-recover=all",
+                    "-static-libubsan", "-I", _build.CSRC, src, "-o", lib], check=True)
+    fn = ctypes.CDLL(lib).run_of
+    fn.argtypes, fn.restype = [ctypes.c_longlong, ctypes.c_int], ctypes.c_int
+    return fn
+
+
+def test_runs_hold_every_place(deal):
+    """All places are dealt, in runs no longer than they need to be (but for the
+    rounding of very long ones) whose halves of the ring an int counts; what is
+    longer than that does not fit."""
+    rng = random.Random(1)
+    for ctas in (1, 2, 7, 148, 152, 1024):
+        most = ctas * 2 ** 29
+        edges = [most + d for d in (-ctas, -1, 0, 1)] + [2 ** 31 + d for d in (-1, 0, 1)] + [4 * most, 2 ** 31 * ctas - 1]
+        for places in [0, 1, ctas, ctas + 1] + edges + [int(2 ** rng.uniform(0, 50)) for _ in range(300)]:
+            run = deal(places, ctas)
+            if places >= most:
+                assert run == -1
+            else:
+                up = 2 ** max(0, places.bit_length() - 31)
+                spare = 1 if up == 1 else 2 * up
+                assert run * ctas >= places and (run - spare) * ctas < max(places, 1) and 2 * run < 2 ** 31
