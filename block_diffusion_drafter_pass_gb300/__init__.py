@@ -280,7 +280,11 @@ def _run_on(torch, dev, stream, call):
     if stream is None and torch.cuda.current_device() == dev:
         return call(torch._C._cuda_getCurrentRawStream(dev))
     if stream is not None and not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        stream = int(stream)
+        if stream == 2:
+            _refuse("the per-thread default stream (2) has no place in PyTorch's allocator")
+        # 0 and cudaStreamLegacy (1) are the default stream: an ExternalStream of 0 is a new side stream
+        stream = torch.cuda.default_stream(dev) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device=dev)
     with torch.cuda.device(dev), torch.cuda.stream(stream):
         return call(torch._C._cuda_getCurrentRawStream(dev))
 

@@ -31,3 +31,28 @@ def test_slots_past_a_length_change_no_bit(dfl, kind, shape, heads, n_kv, d, dty
     for value in (float("nan"), float("-inf")):
         poison(b, dfl, value)
         assert torch.equal(call(), clean)
+
+
+# --- streams given as numbers --------------------------------------------------
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_stream_by_its_number(dfl, handle):
+    """0 is what `torch.cuda.current_stream().cuda_stream` says by default: the
+    calls are ordered behind what that stream does before, also a slow fill."""
+    b = Batch([(1, 300), (5, 90)], 8, 2, 64, BF, prefix=70)
+    other = Batch([(1, 300), (5, 90)], 8, 2, 64, BF, prefix=70, seed=1)
+    ref = other.attend(dfl), other.attend_shared(dfl)
+    torch.cuda.synchronize()
+    slow = torch.empty(1 << 28, device=b.pool.device)
+    for _ in range(10):
+        slow.fill_(1.0)                          # about 2 ms of work ahead of the copies
+    b.pool.copy_(other.pool)
+    b.qkv.copy_(other.qkv)
+    b.table.copy_(other.table)
+    b.prefix_table.copy_(other.prefix_table)
+    results = b.attend(dfl, stream=handle), b.attend_shared(dfl, stream=handle)
+    assert dfl._run_on(torch, 0, handle, lambda s: s) == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(results, ref))
+    with pytest.raises(dfl.DFlashError, match="per-thread"):
+        b.attend(dfl, stream=2)
