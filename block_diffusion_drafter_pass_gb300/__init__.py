@@ -285,6 +285,8 @@ def _run_on(torch, dev, stream, call):
             _refuse("the per-thread default stream (2) has no place in PyTorch's allocator")
         # 0 and cudaStreamLegacy (1) are the default stream: an ExternalStream of 0 is a new side stream
         stream = torch.cuda.default_stream(dev) if stream in (0, 1) else torch.cuda.ExternalStream(stream, device=dev)
+    if stream is not None and stream.device_index != dev:
+        _refuse("the stream is of another device than the pool")
     with torch.cuda.device(dev), torch.cuda.stream(stream):
         return call(torch._C._cuda_getCurrentRawStream(dev))
 

@@ -7,6 +7,7 @@ import subprocess
 
 import pytest
 
+import block_diffusion_drafter_pass_gb300 as dfl
 from block_diffusion_drafter_pass_gb300 import _build
 
 
@@ -44,3 +45,16 @@ def test_runs_hold_every_place(deal):
                 up = 2 ** max(0, places.bit_length() - 31)
                 spare = 1 if up == 1 else 2 * up
                 assert run * ctas >= places and (run - spare) * ctas < max(places, 1) and 2 * run < 2 ** 31
+
+
+# --- streams -------------------------------------------------------------------
+
+def test_a_stream_of_another_device_is_refused():
+    """Its work would run on the pool's device's current stream instead."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream, device_index = 12345, 1
+
+    with pytest.raises(dfl.DFlashError, match="another device"):
+        dfl._run_on(torch, 0, Stream(), lambda s: pytest.fail("the call ran"))
