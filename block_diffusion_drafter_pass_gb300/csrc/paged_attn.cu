@@ -1318,7 +1318,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
 const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_stride, const void* out,
                        long long out_stride, float scale) {
   if (const char* why = paged_check(b)) return why;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return "scale must be positive and finite";
+  // the exponents are taken to base 2, by a factor of scale * log2(e)
+  if (!(scale > 0.f && scale <= 0x1p127f)) return "scale must be in (0, 2^127]";
   if (b->n_seq == 0 || b->n_tokens == 0) return nullptr;
   const long long width = static_cast<long long>(b->n_heads) * b->head_dim;
   if (!q || !out) return "null pointer";

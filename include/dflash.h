@@ -471,7 +471,7 @@ dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b, size_t* b
  *  causal   1: the token at position p sees keys 0..p; 0: the whole cache
  *  window   > 0: of those, only keys after p - window and the first `sinks`
  *           keys; 0: all (sinks is then ignored)
- *  scale    positive and finite
+ *  scale    in (0, 2^127]
  *  workspace  device, 32-byte aligned, at least dflash_paged_attn_workspace
  * A token that sees no key gets zeros. Keys and values it does not see have no
  * influence on it, infinities and NaN included (non-finite values in hidden

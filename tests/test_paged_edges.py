@@ -58,3 +58,33 @@ def test_a_stream_of_another_device_is_refused():
 
     with pytest.raises(dfl.DFlashError, match="another device"):
         dfl._run_on(torch, 0, Stream(), lambda s: pytest.fail("the call ran"))
+
+
+# --- refusals ------------------------------------------------------------------
+
+FAKE = 1 << 20   # a non-null, aligned address that no refused call reads
+
+
+def batch(**kw):
+    f = dict(dtype=0, n_heads=8, n_kv_heads=2, head_dim=64, n_seq=2, n_tokens=4, n_pages=3, table_pages=2,
+             table_stride=2, pool=FAKE, page_table=FAKE, q_start=FAKE, kv_len=FAKE, status=None)
+    f.update(kw)
+    return ctypes.byref(dfl.dflash_paged_batch(*[f[n] for n, _ in dfl.dflash_paged_batch._fields_]))
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return dfl.load_library()
+
+
+@pytest.mark.parametrize("scale,refused", [(1.8e38, True), (3.4e38, True), (2.0 ** 127, False), (1e-45, False)])
+def test_scales_whose_product_with_log2_e_is_infinite_are_refused(lib, scale, refused):
+    """(Others are refused for their workspace, or fail without a GPU.)"""
+    for shared in (False, True):
+        args = (2 * FAKE, 512, 3 * FAKE, 512)
+        if shared:
+            r = lib.dflash_shared_prefix_attn(batch(), FAKE, 100, *args, 1, scale, None, 0, None)
+        else:
+            r = lib.dflash_paged_attn(batch(), *args, 0, 0, 1, scale, None, 0, None)
+        assert r != dfl.DFLASH_OK and (b"scale" in lib.dflash_last_error(None)) == refused
