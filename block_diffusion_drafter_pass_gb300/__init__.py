@@ -34,6 +34,7 @@ EXPORTED = (
     "dflash_debug_wait_timeout", "dflash_target_feature_layers", "dflash_target_create", "dflash_target_forward",
     "dflash_debug_read_kv_q8", "dflash_set_conv",
     "dflash_kv_append", "dflash_paged_attn", "dflash_shared_prefix_attn", "dflash_paged_attn_workspace",
+    "dflash_debug_paged_wait_tries",
 )
 SAMPLE_WIDTH = 32   # DFLASH_SAMPLE_WIDTH
 
@@ -139,6 +140,7 @@ def load_library() -> ctypes.CDLL:
         "dflash_target_create": ([P(dflash_config), P(dflash_weights), i32p, P(VP)], I),
         "dflash_target_forward": ([VP, i32p, I, VP, I, I, VP, VP, VP], I),
         "dflash_kv_append": ([batch, VP, LL, VP, LL, VP, LL, VP, LL, VP, F, VP], I),
+        "dflash_debug_paged_wait_tries": ([I], I),
         "dflash_paged_attn_workspace": ([batch, P(ctypes.c_size_t)], I),
         "dflash_paged_attn": ([batch, VP, LL, VP, LL, I, I, I, F, VP, ctypes.c_size_t, VP], I),
         "dflash_shared_prefix_attn": ([batch, VP, I, VP, LL, VP, LL, I, F, VP, ctypes.c_size_t, VP], I),
@@ -393,6 +395,11 @@ def dflash_shared_prefix_attn(q, pool, q_start, kv_len, page_table, prefix_table
     def run(lib, b, qp, qs, op, os_, sc, ws, wb, s):
         return lib.dflash_shared_prefix_attn(b, table, prefix_len, qp, qs, op, os_, 1 if causal else 0, sc, ws, wb, s)
     return _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status, stream)
+
+
+def dflash_debug_paged_wait_tries(tries: int = 1 << 23) -> None:
+    """In later attention calls over a page pool a wait inside the kernel gives up after that many tries."""
+    _check(load_library().dflash_debug_paged_wait_tries(int(tries)))
 
 
 class BlockScheduler:

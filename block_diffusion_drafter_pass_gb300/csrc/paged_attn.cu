@@ -97,6 +97,7 @@ struct PagedAttnArgs {
   long long out_stride;
   int window, sinks, causal;
   float scale_log2;
+  int wait_tries;              // of a wait in the kernel (bar_wait); 0: every one that has to wait gives up
   int stream_tokens;           // tokens of one stream's 128 rows
   int tile_tokens;             // tokens of a tile: one or two streams
   // partials: two slots per CTA (0: a tile begun by an earlier CTA, 1: a tile
@@ -386,11 +387,19 @@ __device__ __forceinline__ uint16_t* out_row(const PagedAttnArgs& a, int token, 
   return a.out + token * a.out_stride + static_cast<long long>(kvh * a.b.group + g) * d;
 }
 
+// Waits of a CTA give up together: its word of progress is negative from then
+// on. Before, it counts the pages of rows that are done again (redo_row), which
+// take as long as the rows have keys: the others wait on while they go on.
+constexpr int kGaveUp = INT32_MIN;
+constexpr int kWaitTries = 1 << 23;   // of a microsecond at most
+constexpr int kWaitPolls = 1 << 27;   // where barriers are polled
+
 // One row of an item again, read key by key by one warp, and written over what
 // the products gave: they met a non-finite value, which may have come from a
 // place that the row does not see (0 times infinity or NaN).
 template <int D, bool F16>
-__device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Batch& b, const Item& it, int stream, int r) {
+__device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Batch& b, const Item& it, int stream, int r,
+                                      uint32_t progress) {
   const int lane = threadIdx.x & 31, rows_of = it.pair ? stream : 0;
   const Row x = row_at(b, it.t, rows_of, r);
   const int g = r % a.b.group;
@@ -410,6 +419,7 @@ __device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Batch& b, co
       if (page < 0 || page >= a.b.n_pages) continue;
       const uint16_t* kp = a.b.pool + page * page_elems + static_cast<size_t>(it.head) * kPage * D;
       row_page<D, F16>(st, q, kp, kp + static_cast<size_t>(a.b.n_kv) * kPage * D, a.scale_log2, vis, lane);
+      if (lane == 0) asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(progress) : "memory");
     }
   }
   if (it.nj == it.t.n) {
@@ -428,20 +438,22 @@ __device__ __noinline__ void redo_row(const PagedAttnArgs& a, const Batch& b, co
 
 // Barriers by shared-window address. The wait is a loop of a few instructions
 // in place (a called or clocked one costs every role's round a hundred and
-// more): each try gives up after a microsecond at the latest, and the wait
-// after kWaitTries of them or when *abort is set. False when it gave up.
-constexpr uint32_t kWaitTries = 1u << 23;   // with tries of 1 us at most: 8 s (rows done again take their time)
-
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+// more): each try gives up after a microsecond at the latest, and the wait after
+// `tries` of them between which *progress did not change, or when that is
+// negative. False when it gave up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t progress, uint32_t tries) {
   uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b32 n, f;\n\tmov.b32 n, %4;\n"
+      "{\n\t.reg .pred p;\n\t.reg .b32 n, f, w;\n\tmov.b32 n, %4;\n\tmov.b32 w, 0;\n"
       "again:\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
       "@p bra done;\n\t"
       "ld.volatile.shared.b32 f, [%3];\n\t"
-      "setp.ne.b32 p, f, 0;\n\t"
+      "setp.lt.s32 p, f, 0;\n\t"
       "@p bra fail;\n\t"
+      "setp.ne.b32 p, f, w;\n\t"
+      "@p mov.b32 n, %4;\n\t"
+      "mov.b32 w, f;\n\t"
       "sub.u32 n, n, 1;\n\t"
       "setp.ne.u32 p, n, 0;\n\t"
       "@p bra again;\n"
@@ -449,7 +461,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t
       "done:\n\tmov.b32 %0, 1;\n"
       "over:\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(abort), "n"(kWaitTries)
+      : "r"(bar), "r"(parity), "r"(progress), "r"(tries)
       : "memory");
   return ok != 0;
 }
@@ -541,14 +553,14 @@ struct Join {
 template <int D, bool F16>
 __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b, const Item& it, Join& join, int stream,
                                          uint32_t tmem, int token, float mref, float l, bool products, int parity,
-                                         uint32_t abort_at) {
+                                         uint32_t progress) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
   const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   auto meet = [&](uint64_t* bar) {   // of the two groups' eight warps
     tc_fence_before();
     __syncwarp();
     if (lane == 0) bar_arrive(smem_u32(bar));
-    const bool ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, abort_at));
+    const bool ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, progress, a.wait_tries));
     tc_fence_after();
     return ok;
   };
@@ -635,7 +647,7 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
   }
   // rows that met a non-finite value: again, from what they see
   for (uint32_t bad = __ballot_sync(0xffffffffu, live && check != 0.f); bad; bad &= bad - 1)
-    redo_row<D, F16>(a, b, it, stream, quarter * 32 + __ffs(bad) - 1);
+    redo_row<D, F16>(a, b, it, stream, quarter * 32 + __ffs(bad) - 1, progress);
   return true;
 }
 
@@ -652,11 +664,11 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
 // their ends took 36 ms instead of 0.11.) s_bar: a barrier to wait for first, or
 // 0. False when a wait ran out.
 template <int D>
-__device__ __forceinline__ bool cut_values(uint32_t ring, uint32_t full_at, uint32_t abort_at, int c, int cut,
-                                           uint32_t s_bar, uint32_t s_parity) {
+__device__ __forceinline__ bool cut_values(uint32_t ring, uint32_t full_at, uint32_t progress, uint32_t tries, int c,
+                                           int cut, uint32_t s_bar, uint32_t s_parity) {
   constexpr int S = Cfg<D>::kSlots;
-  bool ok = s_bar == 0 || bar_wait(s_bar, s_parity, abort_at);
-  ok = ok && bar_wait(full_at + c % S * 8, c / S & 1, abort_at);
+  bool ok = s_bar == 0 || bar_wait(s_bar, s_parity, progress, tries);
+  ok = ok && bar_wait(full_at + c % S * 8, c / S & 1, progress, tries);
   if (!__all_sync(0xffffffffu, ok)) return false;
   const int r = (threadIdx.x - kSoftWarp0 * 32) % kRows, keep = cut % kPage;
   if (r < D) {
@@ -700,8 +712,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Item s_first[2];   // the CTA's first item (and where its run begins)
   __shared__ Item s_items[kThreads / 32][2];   // each warp's item and the one after it
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile int abort_flag;
-  __shared__ int s_never;   // 0: the flag of waits that must not be cut short
+  __shared__ int s_progress;
+  __shared__ int s_never;   // 0: the progress of waits that must not be cut short
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_seq = a.b.n_seq, n_kv = a.b.n_kv, G = a.b.group;
@@ -722,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&join.x_ml, 8);
     mbar_init(&join.x_bad, 8);
-    abort_flag = 0;
+    s_progress = a.wait_tries > 0 ? 0 : kGaveUp;
     s_first[0].nj = 0;
     s_never = 0;
     b.shared = a.shared;
@@ -810,9 +822,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item* const items = s_items[warp];   // written by lane 0
   if (lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
   __syncwarp();
-  const uint32_t abort_at = smem_u32(const_cast<int*>(&abort_flag)), never_at = smem_u32(&s_never);
+  const uint32_t progress_at = smem_u32(&s_progress), never_at = smem_u32(&s_never);
+  const uint32_t wait_tries = a.wait_tries;
   auto give_up = [&]() {
-    abort_flag = 1;
+    atomicOr(&s_progress, kGaveUp);
     latch_status(a.b.status, kDevTimeout);
   };
   // An item goes in rounds j = -lead .. nj-1: round j multiplies P of step j
@@ -867,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j < 0 || j >= nj) continue;
           const int slot = c % S;
-          ok = bar_wait(empty_at + slot * 8, (c / S & 1) ^ 1, abort_at);
+          ok = bar_wait(empty_at + slot * 8, (c / S & 1) ^ 1, progress_at, wait_tries);
           if (!ok) break;
           const uint32_t dst = ring + slot * C::kHalf, bar = full_at + slot * 8;
           // a page past the sequence's end, or none of the pool's, reads as
@@ -915,8 +928,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       a.split[blockIdx.x] = split;
       a.piece[blockIdx.x] = piece;
       // copies still in flight complete before shared memory is released
+      copy_async_wait<0>();
 #pragma unroll 1
-      for (int j = max(0, c - S); j < c; ++j) bar_wait(full_at + (j % S) * 8, j / S & 1, never_at);
+      for (int j = max(0, c - S); j < c; ++j) bar_wait(full_at + (j % S) * 8, j / S & 1, never_at, kWaitTries);
     }
   } else if (warp < kSoftWarp0) {
     // ---------------- products of one stream ----------------
@@ -940,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int brought = 0;    // items whose queries were called for
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, abort_at));
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
     };
     auto bring_q = [&](const Item& it) {   // an item's queries
       if (ok && one) {
@@ -997,9 +1011,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
           if (lane == 2) need = weights, bar = p_at, parity = np & 1;
           if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
-          int tries = 1 << 27;
+          int polls = kWaitPolls, seen = 0;
           while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
-            if (__any_sync(0xffffffffu, abort_flag) || --tries == 0) {
+            const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
+            if (progress != seen) polls = kWaitPolls;
+            seen = progress;
+            if (progress < 0 || --polls == 0) {
               ok = false;
               break;
             }
@@ -1072,8 +1089,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every issued product completes before TMEM and shared memory are released
     if (one) bar_commit(smem_u32(&mma_done));
-    bar_wait(smem_u32(&mma_done), 0, never_at);
-    if (brought > 0) bar_wait(smem_u32(&q_full), (brought - 1) & 1, never_at);   // and every copy arrives
+    bar_wait(smem_u32(&mma_done), 0, never_at, kWaitTries);
+    if (brought > 0) bar_wait(smem_u32(&q_full), (brought - 1) & 1, never_at, kWaitTries);   // and every copy arrives
   } else {
     // ---------------- softmax and output ----------------
     const int stream = warp >= kSoftWarp0 + 4 ? 1 : 0;
@@ -1092,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // waits taken by all 32 lanes together, so the warp-collective TMEM
     // accesses after them never diverge (also when a wait runs out)
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, abort_at));
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, progress_at, wait_tries));
       tc_fence_after();
     };
     auto warp_arrive = [&](uint64_t* bar) {
@@ -1122,7 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // come, or its barrier's phase would be taken for theirs: with 8 halves,
           // or in a pair, the scores seen last say so, else the ones to come.
           const int c = 2 * step0 + j + min(j + (pair ? 1 : 2), nj);
-          ok = cut_values<D>(smem_u32(smem) + C::kQBytes, smem_u32(kv_full), abort_at, c, rest,
+          ok = cut_values<D>(smem_u32(smem) + C::kQBytes, smem_u32(kv_full), progress_at, wait_tries, c, rest,
                              S == 4 && !pair ? smem_u32(&s_full[stream]) : 0, ns & 1);
           if (!ok) break;
         }
@@ -1226,7 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (done > 0) warp_wait(&o_done[stream], outs++ & 1);
       if (!ok) break;
 
-      ok = finish_item<D, F16>(a, b, it, join, stream, tmem, row.token, mref, l, done > 0, nx & 1, abort_at);
+      ok = finish_item<D, F16>(a, b, it, join, stream, tmem, row.token, mref, l, done > 0, nx & 1, progress_at);
       nx += !it.pair;
       if (!ok) break;
     }
@@ -1368,6 +1385,8 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p,
   return launch_pdl(paged_combine_kernel<D, F16>, dim3(p.ctas, rows), dim3(kCombineWarps * 32), 0, s, a);
 }
 
+std::atomic<int> g_wait_tries{kWaitTries};
+
 dflash_status refuse(const char* why) {
   set_unattached_error(why);
   return DFLASH_EINVAL;
@@ -1421,6 +1440,7 @@ PagedAttnArgs attn_args(const dflash_paged_batch& b, const void* q, long long q_
   a.out_stride = out_stride;
   a.causal = causal ? 1 : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.wait_tries = g_wait_tries.load(std::memory_order_relaxed);
   return a;
 }
 
@@ -1466,4 +1486,10 @@ extern "C" dflash_status dflash_shared_prefix_attn(const dflash_paged_batch* b, 
   a.prefix_len = prefix_len;
   a.shared = 1;
   return run(*b, a, workspace, workspace_bytes, stream);
+}
+
+extern "C" dflash_status dflash_debug_paged_wait_tries(int tries) {
+  if (tries < 0 || tries > kWaitTries) return refuse("tries must be 0..2^23");
+  g_wait_tries.store(tries, std::memory_order_relaxed);
+  return DFLASH_OK;
 }

@@ -418,8 +418,11 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * non-decreasing numbers within [0, n_tokens], kv_len to [0, 64*table_pages],
  * and tokens whose page id is outside [0, n_pages) are not written and not
  * seen. (A batch whose steps of 128 keys, over all blocks of tokens and kv heads,
- * pass 2^29 for each SM is not computed.) Each of these sets bit 2 (EDEVICE's) of
- * *status, which the caller clears. Slots past a length may hold any bits. */
+ * pass 2^29 for each SM is not computed.) Each of these sets bit 1 (value 2) of
+ * *status. Bit 0 (value 1): a wait inside an attention kernel ran out, which no
+ * arguments should bring about; `out` is then undefined. The caller clears
+ * *status; without one (NULL) nothing else tells of these. Slots past a length
+ * may hold any bits. */
 enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1 };
 
 typedef struct {
@@ -519,6 +522,12 @@ dflash_status dflash_debug_last_draft(dflash_ctx* ctx, float* hidden_out, float*
  * timeout bit, so the next dflash_sync returns DFLASH_ETIMEOUT (and clears it).
  * No fault, no trap; the context stays usable. Errors: EINVAL, ECUDA. */
 dflash_status dflash_debug_wait_timeout(dflash_ctx* ctx, int limit_us, void* stream);
+
+/* Failure-path check of the attention over a caller's page pool: in later calls
+ * of this process a wait inside the kernel gives up after that many tries of a
+ * microsecond at most (0 .. 2^23, the default; 0: at the first that fails).
+ * Errors: EINVAL. */
+dflash_status dflash_debug_paged_wait_tries(int tries);
 
 /* Selector state of the last dflash_draft call made with the selector
  * installed, per draft row r = i*(B-1) + t (host outputs, any may be NULL):

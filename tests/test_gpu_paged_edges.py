@@ -56,3 +56,55 @@ def test_the_default_stream_by_its_number(dfl, handle):
     assert all(torch.equal(x, y) for x, y in zip(results, ref))
     with pytest.raises(dfl.DFlashError, match="per-thread"):
         b.attend(dfl, stream=2)
+
+
+# --- waits that run out --------------------------------------------------------
+
+def broken_neighbour(dfl):
+    """32 sequences behind a prefix, the fourth with a cache of NaN: the rows of
+    the others in its tiles are done again, key by key, while the kernel's other
+    roles wait for milliseconds."""
+    b = Batch([(16, 40 + 7 * i) for i in range(32)], 32, 8, 128, BF, prefix=16000)
+    clean = b.attend_shared(dfl)
+    for p in b.table[3, :1].tolist():
+        b.pool[p] = float("nan")
+    return b, clean
+
+
+def check_broken(b, clean, got):
+    mine = torch.zeros(b.T, dtype=torch.bool, device=got.device)
+    mine[48:64] = True
+    assert got[mine].isnan().all() and (got[~mine].float() - clean[~mine].float()).abs().max() < 0.05
+
+
+def test_rows_that_are_done_again_keep_the_waits_going(dfl):
+    """They take longer than a wait may (about 70 ms), but each of their pages counts."""
+    b, clean = broken_neighbour(dfl)
+    status = torch.zeros(1, dtype=torch.int32, device=b.pool.device)
+    dfl.dflash_debug_paged_wait_tries(20000)   # 20 ms at most
+    try:
+        check_broken(b, clean, b.attend_shared(dfl, status=status))
+    finally:
+        dfl.dflash_debug_paged_wait_tries()
+    assert int(status) == 0
+
+
+def test_a_wait_that_runs_out_says_so(dfl):
+    """With no time at all the same call is given up: the status says so, nothing
+    hangs, and the next calls are right."""
+    b, clean = broken_neighbour(dfl)
+    status = torch.zeros(1, dtype=torch.int32, device=b.pool.device)
+    dfl.dflash_debug_paged_wait_tries(0)
+    try:
+        b.attend_shared(dfl, status=status)
+        torch.cuda.synchronize()
+    finally:
+        dfl.dflash_debug_paged_wait_tries()
+    assert int(status) == 1
+    status.zero_()
+    check_broken(b, clean, b.attend_shared(dfl, status=status))
+    assert int(status) == 0
+    with pytest.raises(dfl.DFlashError):
+        dfl.dflash_debug_paged_wait_tries(-1)
+    with pytest.raises(dfl.DFlashError):
+        dfl.dflash_debug_paged_wait_tries((1 << 23) + 1)
