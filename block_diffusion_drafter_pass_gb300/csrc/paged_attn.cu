@@ -289,6 +289,20 @@ __device__ __noinline__ int pair_takes(const Batch& b, const Tile& t, int seq, i
   return (step_counts(b, seq, base, t.t0, mid) ? 1 : 0) | (step_counts(b, seq, base, mid, t.t0 + t.ntok) ? 2 : 0);
 }
 
+// Whether a page of the step that is not there (bit u of gone: page u) has keys
+// which some row of the tile may see. (Pages of a step before the window or past
+// the end may have been given back.)
+__device__ __noinline__ bool misses_page(const Batch& b, const Tile& t, int seq, int base, int end, int gone) {
+  for (int u = 0; u < 2; ++u) {
+    const int key0 = base + u * kPage;
+    if (!(gone >> u & 1) || key0 >= end) continue;
+    if (seq < 0 || b.window == 0 || key0 < b.sinks) return true;
+    const int first = b.len[seq] - b.q[seq + 1] + t.t0;   // position of the tile's first row
+    if (key0 + kPage - 1 > first - b.window) return true;
+  }
+  return false;
+}
+
 // The producer's note on a step: bit u, page u is not there; bit 2 + s, stream s
 // of a pair takes the step; from bit 4 on the step's number + 1, so that a
 // reader may look for it before the barrier that says it is there (while the
@@ -894,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             gone |= 1 << u;
           }
           if (keys) {
-            if (gone && wk.s.base + (gone == 2 ? kPage : 0) < wk.s.end) latch_status(a.b.status, kDevBounds);
+            if (gone && misses_page(b, it.t, wk.s.seq, wk.s.base, wk.s.end, gone)) latch_status(a.b.status, kDevBounds);
             int flags = gone;
             if (it.pair) flags |= pair_takes(b, it.t, wk.s.seq, wk.s.base) << 2;
             wk.next(b, it.t);

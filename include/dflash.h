@@ -417,7 +417,8 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * Broken device arrays end in no access out of range: q_start is bent to
  * non-decreasing numbers within [0, n_tokens], kv_len to [0, 64*table_pages],
  * and tokens whose page id is outside [0, n_pages) are not written and not
- * seen. (A batch whose steps of 128 keys, over all blocks of tokens and kv heads,
+ * seen (in pages that no new token would see, a window being in front of them,
+ * any id will do). (A batch whose steps of 128 keys, over all blocks of tokens and kv heads,
  * pass 2^29 for each SM is not computed.) Each of these sets bit 1 (value 2) of
  * *status. Bit 0 (value 1): a wait inside an attention kernel ran out, which no
  * arguments should bring about; `out` is then undefined. The caller clears

@@ -108,3 +108,20 @@ def test_a_wait_that_runs_out_says_so(dfl):
         dfl.dflash_debug_paged_wait_tries(-1)
     with pytest.raises(dfl.DFlashError):
         dfl.dflash_debug_paged_wait_tries((1 << 23) + 1)
+
+
+# --- pages given back ----------------------------------------------------------
+
+@pytest.mark.parametrize("window,sinks,free", [(30, 0, 15), (41, 0, 14), (30, 4, 15), (30, 70, 15)])
+@pytest.mark.parametrize("new", [1, 3])
+def test_pages_before_the_window_may_be_given_back(dfl, window, sinks, free, new):
+    """Also the one that shares a step with the window's first; those of the first tokens stay."""
+    b = Batch([(new, 1000), (new, 70)], 8, 2, 128, BF)
+    status = torch.zeros(1, dtype=torch.int32, device=b.pool.device)
+    whole = b.attend(dfl, window=window, sinks=sinks)
+    b.table[0, (sinks + 63) // 64:free] = -1
+    assert torch.equal(b.attend(dfl, window=window, sinks=sinks, status=status), whole)
+    assert int(status) == 0
+    b.table[0, 15] = -1                                      # the window's own
+    b.attend(dfl, window=window, sinks=sinks, status=status)
+    assert int(status) == 2
