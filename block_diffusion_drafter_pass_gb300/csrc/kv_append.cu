@@ -262,6 +262,9 @@ extern "C" dflash_status dflash_kv_append(const dflash_paged_batch* b, const voi
   if (q && (rows_overlap(k, k_stride, kw, q_out, q_out_stride, qw, b->n_tokens) ||
             rows_overlap(v, v_stride, kw, q_out, q_out_stride, qw, b->n_tokens)))
     return refuse("q_out must not overlap k or v");
+  if (in_pool(*b, k, k_stride, kw) || in_pool(*b, v, v_stride, kw) ||
+      (q && (in_pool(*b, q, q_stride, qw) || in_pool(*b, q_out, q_out_stride, qw))))
+    return refuse("k, v, q and q_out must not lie in the pool");
   AppendArgs a;
   std::memset(&a, 0, sizeof(a));
   a.b = paged_view(*b);

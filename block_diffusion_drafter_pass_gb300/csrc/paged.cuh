@@ -57,6 +57,14 @@ inline bool rows_overlap(const void* x, long long x_stride, long long x_width, c
   return off < x_width || off + y_width > x_stride;
 }
 
+// Whether a token buffer reaches into the batch's pool.
+inline bool in_pool(const dflash_paged_batch& b, const void* x, long long stride, long long width) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(x), pool = reinterpret_cast<uintptr_t>(b.pool);
+  const uintptr_t end = at + static_cast<uintptr_t>(((b.n_tokens - 1) * stride + width) * 2);
+  const uintptr_t page = static_cast<uintptr_t>(2) * b.n_kv_heads * kPage * b.head_dim * 2;
+  return at < pool + b.n_pages * page && pool < end;
+}
+
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if constexpr (F16) {

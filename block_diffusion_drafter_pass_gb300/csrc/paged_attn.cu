@@ -1358,6 +1358,7 @@ const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_s
     return "token strides must be multiples of 8 elements and at least a token's row";
   if (misaligned16(q) || misaligned16(out)) return "q and out must be 16-byte aligned";
   if (rows_overlap(q, q_stride, width, out, out_stride, width, b->n_tokens)) return "out must not overlap q";
+  if (in_pool(*b, out, out_stride, width)) return "out must not lie in the pool";
   return nullptr;
 }
 

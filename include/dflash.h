@@ -449,7 +449,7 @@ typedef struct {
  *  k, v       device [n_tokens][n_kv_heads][d], strides in elements between
  *             tokens (multiples of 8), 16-byte aligned
  *  q, q_out   device [n_tokens][n_heads][d], or both NULL; q_out is q,
- *             or overlaps none of q, k and v
+ *             or overlaps none of q, k and v; none of the four lies in the pool
  *  positions  device [n_tokens] rotation positions, or NULL: the cache
  *             positions (callers behind a shared prefix add its length)
  *  rope_base  in (1, 1e12], or 0: nothing is rotated (q is copied)
@@ -471,7 +471,8 @@ dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b, size_t* b
  * keys and values appended before): softmax over the visible keys of
  * scale * q.k in fp32, times the values.
  *  q, out   device [n_tokens][n_heads][d], strides in elements between tokens
- *           (multiples of 8), 16-byte aligned; out must not overlap q
+ *           (multiples of 8), 16-byte aligned; out must not overlap q or the
+ *           pool
  *  causal   1: the token at position p sees keys 0..p; 0: the whole cache
  *  window   > 0: of those, only keys after p - window and the first `sinks`
  *           keys; 0: all (sinks is then ignored)

@@ -88,3 +88,29 @@ def test_scales_whose_product_with_log2_e_is_infinite_are_refused(lib, scale, re
         else:
             r = lib.dflash_paged_attn(batch(), *args, 0, 0, 1, scale, None, 0, None)
         assert r != dfl.DFLASH_OK and (b"scale" in lib.dflash_last_error(None)) == refused
+
+
+POOL = 3 * 2 * 2 * 64 * 64 * 2   # bytes of the pool of `batch`
+ROWS = (4 - 1) * 1024 + 1024     # and of four tokens' queries
+
+
+@pytest.mark.parametrize("at,refused", [(0, True), (POOL - 16, True), (16 - ROWS, True), (POOL, False), (-ROWS, False)])
+def test_outputs_in_the_pool_are_refused(lib, at, refused):
+    """(Others are refused for their workspace, or fail without a GPU.)"""
+    out = 8 * FAKE + at
+    pool = batch(pool=8 * FAKE)
+    for shared in (False, True):
+        args = (2 * FAKE, 512, out, 512)
+        if shared:
+            r = lib.dflash_shared_prefix_attn(pool, FAKE, 100, *args, 1, 0.1, None, 0, None)
+        else:
+            r = lib.dflash_paged_attn(pool, *args, 0, 0, 1, 0.1, None, 0, None)
+        assert r != dfl.DFLASH_OK and (b"in the pool" in lib.dflash_last_error(None)) == refused
+
+
+@pytest.mark.parametrize("name", ["k", "v", "q", "q_out"])
+def test_appended_rows_in_the_pool_are_refused(lib, name):
+    f = dict(k=FAKE, v=2 * FAKE, q=3 * FAKE, q_out=4 * FAKE)
+    f[name] = 8 * FAKE + 1024
+    r = lib.dflash_kv_append(batch(pool=8 * FAKE), f["k"], 128, f["v"], 128, f["q"], 512, f["q_out"], 512, None, 0.0, None)
+    assert r == dfl.DFLASH_EINVAL and b"in the pool" in lib.dflash_last_error(None)
