@@ -369,7 +369,9 @@ def dflash_paged_attn(q, pool, q_start, kv_len, page_table, *, window: int = 0, 
     caches (their own keys and values appended before) -> [T, n_heads, d].
     window > 0: keys after position - window and the first `sinks` ones only.
     scale defaults to d ** -0.5. `out` must not overlap q. Rows of no sequence
-    are left as they are (a fresh `out` is not initialised)."""
+    are left as they are (a fresh `out` is not initialised). `status` (int32 [1]
+    on the device, cleared by the caller) is what tells of broken device arrays
+    (2) and of a kernel that gave up (1: the result is undefined)."""
     import torch
     if not (0 <= window < 1 << 31 and 0 <= sinks < 1 << 31):   # a C int would wrap
         _refuse("window and sinks must be 0..2^31 - 1")

@@ -5,8 +5,11 @@
 // p * base^(-2i/d). The angle's fraction of a turn is what cos and sin need,
 // and at far positions a float (or float product) has lost it, so the host
 // gives base^(-2i/d) / (2 pi) as a 64-bit fraction of a turn and the kernel
-// multiplies by p in integers: whole turns fall off the top, exactly, and
-// what is left is off by p * 2^-52 of the step. sincospif takes it from there.
+// multiplies by p in integers: whole turns fall off the top, exactly. The
+// fraction comes from doubles: two powers (1 ulp each), 2 pi, a quotient and a
+// product, together less than 2^-50 of it, so the angle is off by at most
+// |p| * 2^-50 rad: 2^-24 at the farthest cache position (2^26), 2^-19 at the
+// farthest int32 (found over 400 bases: 2^-20.8). sincospif takes it from there.
 //
 // Bound: memory, q, k and v read once, q and the pages written once.
 // Queries and keys: one thread per (token, 8 pairs), which computes its 8
@@ -280,7 +283,8 @@ extern "C" dflash_status dflash_kv_append(const dflash_paged_batch* b, const voi
   a.rotate = rope_base != 0.f;
   if (a.rotate) {
     // base^(-2i/d) from two factors, since 64 powers are a quarter of the call's
-    // time; the first pair's, whose angle is the largest, are exact
+    // time; those of the first pair, whose angle is the largest, are 1 / (2 pi)
+    // rounded once and 1
     const double two_pi = 6.283185307179586476925286766559, base = rope_base;
     double coarse[8], fine[8];
     for (int i = 0; i < 8; ++i) {
