@@ -289,20 +289,6 @@ __device__ __noinline__ int pair_takes(const Batch& b, const Tile& t, int seq, i
   return (step_counts(b, seq, base, t.t0, mid) ? 1 : 0) | (step_counts(b, seq, base, mid, t.t0 + t.ntok) ? 2 : 0);
 }
 
-// Whether a page of the step that is not there (bit u of gone: page u) has keys
-// which some row of the tile may see. (Pages of a step before the window or past
-// the end may have been given back.)
-__device__ __noinline__ bool misses_page(const Batch& b, const Tile& t, int seq, int base, int end, int gone) {
-  for (int u = 0; u < 2; ++u) {
-    const int key0 = base + u * kPage;
-    if (!(gone >> u & 1) || key0 >= end) continue;
-    if (seq < 0 || b.window == 0 || key0 < b.sinks) return true;
-    const int first = b.len[seq] - b.q[seq + 1] + t.t0;   // position of the tile's first row
-    if (key0 + kPage - 1 > first - b.window) return true;
-  }
-  return false;
-}
-
 // The producer's note on a step: bit u, page u is not there; bit 2 + s, stream s
 // of a pair takes the step; from bit 4 on the step's number + 1, so that a
 // reader may look for it before the barrier that says it is there (while the
@@ -553,6 +539,20 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// Sets the status when a row would see a key of a page that is not there (bit u
+// of gone: page u of the step); pages in front of the window or past the end may
+// have been given back. Here since the row knows what it sees, and since the
+// producer is a chain of steps in one lane: asked there, 16 tokens over 262144
+// keys took 166 us instead of 162 (with heads of 64: 157 instead of 144).
+__device__ __noinline__ void report_gone(int* status, int gone, int c_lo, int c_hi, int c_sink) {
+#pragma unroll 1
+  for (int u = 0; u < 2; ++u) {
+    const int c0 = u * kPage;
+    const unsigned long long seen = slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
+    if ((gone >> u & 1) && seen) latch_status(status, kDevBounds);
+  }
+}
+
 // What the two softmax groups exchange at an alternating tile's end.
 struct Join {
   uint64_t x_ml, x_bad;
@@ -672,13 +672,13 @@ __device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b,
 // 128 bytes, swizzled), in half `c` of the ring. By the four softmax warps of a
 // stream, a row for each thread, while their scores are made: in the issuing
 // warps the same cost 3% of a windowed prefill, in the producer's or in a warp of
-// its own 2 to 7% of all long cases. Here it costs 0.5% of that prefill, 1 us of
-// the shortest calls and 1.2 of one token of 64 sequences behind a prefix. (Left
-// to redo_row, 16 tokens of 32 sequences of 1024 to 8192 keys with NaN behind
-// their ends took 36 ms instead of 0.11.) s_bar: a barrier to wait for first, or
-// 0. False when a wait ran out.
+// its own 2 to 7% of all long cases. Here it costs 1% of that prefill, half a
+// microsecond of the shortest calls and 2 of one token of 64 sequences behind a
+// prefix. (Left to redo_row, 16 tokens of 32 sequences of 1024 to 8192 keys with
+// NaN behind their ends took 36 ms instead of 0.11.) s_bar: a barrier to wait for
+// first, or 0. False when a wait ran out.
 template <int D>
-__device__ __forceinline__ bool cut_values(uint32_t ring, uint32_t full_at, uint32_t progress, uint32_t tries, int c,
+__device__ __noinline__ bool cut_values(uint32_t ring, uint32_t full_at, uint32_t progress, uint32_t tries, int c,
                                            int cut, uint32_t s_bar, uint32_t s_parity) {
   constexpr int S = Cfg<D>::kSlots;
   bool ok = s_bar == 0 || bar_wait(s_bar, s_parity, progress, tries);
@@ -908,7 +908,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             gone |= 1 << u;
           }
           if (keys) {
-            if (gone && misses_page(b, it.t, wk.s.seq, wk.s.base, wk.s.end, gone)) latch_status(a.b.status, kDevBounds);
             int flags = gone;
             if (it.pair) flags |= pair_takes(b, it.t, wk.s.seq, wk.s.base) << 2;
             wk.next(b, it.t);
@@ -1183,6 +1182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           const int gone = flags & 3;
           if (gone != 0 || !__all_sync(0xffffffffu, c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys))) {
+            if (gone != 0) report_gone(a.b.status, gone, c_lo, c_hi, c_sink);
             // scores of keys that the row does not see become -inf in place
 #pragma unroll 1
             for (int c0 = 0; c0 < kStepKeys; c0 += 32) {
