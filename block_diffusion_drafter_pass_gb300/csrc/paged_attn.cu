@@ -32,30 +32,34 @@
 // both streams the same rows and every other step ("alternate": a split over
 // the keys inside the CTA, joined at its end). Either way one stream's products
 // run while the other's softmax does. With alternating tiles only, keys are
-// loaded twice as often and a step's hand-overs serve half the rows: 324 against
-// 209 us for 16 tokens of 32 sequences behind 32768, 365 against 277 for the
-// prefill below, 82 against 77 for one token of 64 sequences (whose own caches
-// then go faster). Rows that fit one stream have no second half to pair.
+// loaded twice as often and a step's hand-overs serve half the rows: 299 against
+// 210 us for 16 tokens of 32 sequences behind 32768, 352 against 280 for the
+// prefill below, 87 against 81 for one token of 64 sequences. Rows that fit one
+// stream have no second half to pair.
 //
 // Bounds and measurements (32/8 heads of 128, bf16, device time; floor: the
 // keys and values read once at the measured copy bandwidth, or the products at
-// the measured bf16 rate): 16 tokens over 262144 keys 163 us, floor 158 (memory);
-// 16 tokens of 32 sequences of 1024 to 8192 keys 113 us, floor 91 (memory, and
+// the measured bf16 rate): 16 tokens over 262144 keys 162 us, floor 158 (memory);
+// 16 tokens of 32 sequences of 1024 to 8192 keys 112 us, floor 91 (memory, and
 // about 4 us each for the start, the joins and the items' ends); prefill of 8700
-// tokens with a window of 2048 277 us, floor 135 (products); one token of 64
-// sequences behind 32768 keys 77 us, floor 40; 16 tokens of 32 behind 32768 keys
-// 209 us, floor 144 (products, 1325 TFLOP/s). In the product-bound ones a step of
-// a pair takes 3300 cycles for 2048 of tensor work: scores -> maximum -> weights
-// -> P V -> the next scores is one chain per stream, mostly hand-overs (with the
-// exponentials, the sums and 7/8 of the products taken out the last case still
-// takes 200 us), and tensor memory (two S and two O of 128 columns) holds no
-// second S to break it. What was tried against that and lost, for that case:
-// scores page by page into the place whose weights were just multiplied (230 us:
-// a product over 64 keys takes 3/4 of one over 128, and the softmax waits twice),
-// or only the second page's ahead (234), weights page by page without the second
-// page's maximum (216), products without turns (265), two softmax warps per row
-// (315: the scalar work of a step is per warp), the two streams' own caches step
-// by step in turn (209, and 2 to 3% more where own caches are long).
+// tokens with a window of 2048 280 us, floor 135 (products; items' ends and masks
+// take a quarter); one token of 64 sequences behind 32768 keys 81 us, floor 40;
+// 16 tokens of 32 behind 32768 keys 210 us, floor 144 (products, 1320 TFLOP/s).
+// With heads of 64 a half step is 16 KB, and what the producer's one lane does
+// for each counts more than memory: 16 tokens over 262144 keys 143 us, floor 79
+// (157 when that lane also asked which rows miss a page). In the product-bound
+// cases a step of a pair takes 3300 cycles for 2048 of tensor work: scores ->
+// maximum -> weights -> P V -> the next scores is one chain per stream, mostly
+// hand-overs (with the exponentials, the sums and 7/8 of the products taken out
+// the last case still takes 200 us), and with heads of 128 tensor memory (two S
+// and two O of 128 columns) holds no second S to break it. What was tried against
+// that and lost, for that case: scores page by page into the place whose weights
+// were just multiplied (230 us: a product over 64 keys takes 3/4 of one over 128,
+// and the softmax waits twice), or only the second page's ahead (234), weights
+// page by page without the second page's maximum (216), products without turns
+// (265), two softmax warps per row (315: the scalar work of a step is per warp),
+// the two streams' own caches step by step in turn (209, and 2 to 3% more where
+// own caches are long).
 #include <cuda.h>
 
 #include <algorithm>
@@ -79,9 +83,9 @@ constexpr int kRows = 128;            // rows of a stream: the MMA's M
 constexpr int kStepRing = 16;
 constexpr int kIdsAhead = 2, kIdRing = 16;   // steps
 // What an item costs beside its steps, in steps (dealing only). With 2, uneven
-// short blocks take 25.5 us instead of 24.7, uneven blocks behind a prefix of
-// 5000 65.7 instead of 63.9 and one long sequence 171 instead of 164 (its runs
-// then end a little off the heads' ends); with 8, 26.5, 68.9 and 178.
+// short blocks take 27.5 us instead of 25.5, uneven blocks behind a prefix of
+// 5000 64.3 instead of 62.8 and one long sequence 170 instead of 162 (its runs
+// then end a little off the heads' ends); with 8, 26.8, 66.2 and 177.
 constexpr int kItemSteps = 4;
 constexpr int kNoEnd = 1 << 30;       // above every position
 constexpr float kRescaleLog2 = 8.f;   // rescale O when a row's maximum grows by more than 2^8
@@ -1230,6 +1234,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
             if (u == 1) load(1);
             uint32_t pk[32];
+            // ex2.approx is off by 2^-22 of a weight at most and takes those below
+            // 2^-126 for zero. For the product weights are rounded to the values'
+            // type, since its two operands have one (the sum takes them in fp32):
+            // half a step of each, which makes the error against 64 bits 0.0023
+            // instead of the 0.0017 of rounding the output alone (fp16: 0.0003 and
+            // 0.0002). Weights in two parts would double the product.
             // exponentials, then packing, then sums: the three in turn for each
             // pair cost 5.7 instead of 5.2 cycles a value (two warps a scheduler)
 #pragma unroll

@@ -404,12 +404,12 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * a captured call replays with the tables and lengths of that moment.
  *
  * A pool is n_pages pages of 64 tokens, each the keys [n_kv_heads][64][d] and
- * then the values transposed [n_kv_heads][d][64] (the layout of the contexts'
- * own pools). A batch is n_seq sequences; sequence i has the new tokens
- * q_start[i] .. q_start[i+1]-1 of the token buffers (q, k, v, out) and a cache
- * of kv_len[i] tokens with those new ones last: new token j is at position
- * kv_len[i] - (q_start[i+1] - q_start[i]) + j, and position p lies in slot
- * p % 64 of page page_table[i][p / 64]. A sequence may have no new tokens.
+ * then the values transposed [n_kv_heads][d][64] (as the contexts lay out their
+ * own pools, which no call hands out). A batch is n_seq sequences; sequence i
+ * has the new tokens q_start[i] .. q_start[i+1]-1 of the token buffers (q, k, v,
+ * out) and a cache of kv_len[i] tokens with those new ones last: new token j is
+ * at position kv_len[i] - (q_start[i+1] - q_start[i]) + j, and position p lies in
+ * slot p % 64 of page page_table[i][p / 64]. A sequence may have no new tokens.
  * Rows of the token buffers before q_start[0] and from q_start[n_seq] on are
  * left as they are. Head rows are contiguous; the stride between tokens is the
  * caller's (a column range of a wider matrix will do).
@@ -417,13 +417,13 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * Broken device arrays end in no access out of range: q_start is bent to
  * non-decreasing numbers within [0, n_tokens], kv_len to [0, 64*table_pages],
  * and tokens whose page id is outside [0, n_pages) are not written and not
- * seen (in pages that no new token would see, a window being in front of them,
- * any id will do). (A batch whose steps of 128 keys, over all blocks of tokens and kv heads,
- * pass 2^29 for each SM is not computed.) Each of these sets bit 1 (value 2) of
- * *status. Bit 0 (value 1): a wait inside an attention kernel ran out, which no
- * arguments should bring about; `out` is then undefined. The caller clears
- * *status; without one (NULL) nothing else tells of these. Slots past a length
- * may hold any bits. */
+ * seen. A batch whose steps of 128 keys, over all blocks of tokens and kv heads,
+ * pass 2^29 for each SM is not computed. Each of these sets bit 1 (value 2) of
+ * *status, a page id only where a new token would see or write a key of that
+ * page (those in front of a window may be any number). Bit 0 (value 1): a wait
+ * inside an attention kernel ran out, which no arguments should bring about;
+ * `out` is then undefined. The caller clears *status; without one (NULL) nothing
+ * else tells of these. Slots past a length may hold any bits. */
 enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1 };
 
 typedef struct {
