@@ -5,6 +5,7 @@ import pytest
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
+from oracle import paged_cache as pc  # noqa: E402
 from tests.test_gpu_paged import BF, DEV, HF, Batch, dfl, f64, poison  # noqa: E402, F401
 
 
@@ -111,6 +112,24 @@ def test_a_wait_that_runs_out_says_so(dfl):
         dfl.dflash_debug_paged_wait_tries((1 << 23) + 1)
 
 
+@pytest.mark.parametrize("lens,prefix", [([(1, 3000)], 0), ([(300, 900), (2, 70)], 0), ([(1, 90)] * 40, 700)], ids=str)
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+def test_any_call_that_is_given_up_ends_and_says_so(dfl, lens, prefix, d, dtype):
+    b = Batch(lens, 8, 2, d, dtype, prefix=prefix)
+    call = b.attend_shared if prefix else b.attend
+    clean = call(dfl)
+    status = torch.zeros(1, dtype=torch.int32, device=b.pool.device)
+    dfl.dflash_debug_paged_wait_tries(0)
+    try:
+        call(dfl, status=status)
+        torch.cuda.synchronize()
+    finally:
+        dfl.dflash_debug_paged_wait_tries()
+    assert int(status) == 1
+    status.zero_()
+    assert torch.equal(call(dfl, status=status), clean) and int(status) == 0
+
+
 # --- pages given back ----------------------------------------------------------
 
 @pytest.mark.parametrize("window,sinks,free", [(30, 0, 15), (41, 0, 14), (30, 4, 15), (30, 70, 15)])
@@ -126,6 +145,44 @@ def test_pages_before_the_window_may_be_given_back(dfl, window, sinks, free, new
     b.table[0, 15] = -1                                      # the window's own
     b.attend(dfl, window=window, sinks=sinks, status=status)
     assert int(status) == 2
+
+
+def misses(b, shared, window=0, sinks=0, causal=True):
+    """Whether some new token sees a key whose page is outside the pool."""
+    away = lambda ids: (ids < 0) | (ids >= b.pool.shape[0])
+    table, pre = b.table.cpu().numpy(), b.prefix_table.cpu().numpy()
+    for _, i, pos in pc.places(b.q_start.tolist(), b.kv_len.tolist()):
+        key = np.arange(int(b.kv_len[i]))
+        see = key <= (pos if causal else len(key))
+        if window:
+            see &= (key > pos - window) | (key < sinks)
+        if (see & away(table[i][key // 64])).any():
+            return True
+        key = np.arange(b.prefix if shared else 0)
+        if ((key <= (b.prefix + pos if causal else b.prefix)) & away(pre[key // 64])).any():
+            return True
+    return False
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_the_status_says_when_a_page_that_is_seen_is_missing(dfl, seed):
+    """And only then: pages past what the tokens see, or before their windows, may be missing."""
+    rng = np.random.default_rng(seed)
+    lens = [(int(a), int(a + n)) for a, n in zip(rng.integers(0, 40, 3), rng.integers(0, 500, 3))] + [(1, 1)]
+    b = Batch(lens, 8, 2, (64, 128)[seed % 2], BF, prefix=int(rng.integers(1, 400)), seed=seed)
+    for _ in range(rng.integers(1, 4)):
+        b.table[int(rng.integers(0, 4)), int(rng.integers(0, b.table.shape[1]))] = -1
+    if seed % 4 == 3:
+        b.prefix_table[int(rng.integers(0, len(b.prefix_table)))] = 2 ** 31 - 1
+    status = torch.zeros(1, dtype=torch.int32, device=b.pool.device)
+    for window, sinks, causal in ((0, 0, True), (0, 0, False), (60, 0, True), (130, 70, False), (3, 1, True)):
+        status.zero_()
+        b.attend(dfl, window=window, sinks=sinks, causal=causal, status=status)
+        assert int(status) == (2 if misses(b, False, window, sinks, causal) else 0), (window, sinks, causal)
+    for causal in (True, False):
+        status.zero_()
+        b.attend_shared(dfl, causal=causal, status=status)
+        assert int(status) == (2 if misses(b, True, causal=causal) else 0), causal
 
 
 # --- single pages far into a cache ---------------------------------------------
