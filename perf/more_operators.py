@@ -7,9 +7,9 @@ its plain form (elementary torch operations in 32 bits, rounded once); with
 `own` true by the calls of block_diffusion_drafter_pass_gb300.
 
 The pool of a case is bytes [n_pages, n_kv, 64 * (2 * d + 8)]: per page of 64
-tokens and head the key codes [64][d] (int8), the value codes [64][d] (int8),
-the key scales [64] and the value scales [64] (fp32). A row of d values x is
-held as codes round(x / s) with s = max |x| / 127 and stands for code * s.
+tokens and head the key codes [64][d], the value codes [64][d] (one byte each, code
++ 128), the key scales [64] and the value scales [64] (fp32). A row of d values
+x is held as codes round(x / s) with s = max |x| / 127 and stands for code * s.
 """
 import math
 
@@ -144,18 +144,18 @@ def work(case):
 
 
 def _quantised(x):
-    """Rows of d values, in 32 bits -> (codes int8, scales fp32)."""
+    """Rows of d values, in 32 bits -> (codes as bytes, scales fp32)."""
     top = x.abs().amax(dim=-1, keepdim=True)
     held = top >= 2.0 ** -100
     inv = torch.where(held, 127.0 / top, torch.zeros_like(top))
     scale = torch.where(held, top / 127.0, torch.zeros_like(top))
-    return torch.round(x * inv).to(torch.int8), scale.squeeze(-1)
+    return (torch.round(x * inv) + 128.0).to(torch.uint8), scale.squeeze(-1)
 
 
 def _views(pool, d):
     """Of a pool: key codes, value codes [n_pages, n_kv, 64, d] and key scales, value scales [n_pages, n_kv, 64]."""
     n, h, _ = pool.shape
-    codes = pool[..., :2 * PAGE * d].view(torch.int8).view(n, h, 2, PAGE, d)
+    codes = pool[..., :2 * PAGE * d].view(n, h, 2, PAGE, d)
     scales = pool[..., 2 * PAGE * d:].view(torch.float32).view(n, h, 2, PAGE)
     return codes[:, :, 0], codes[:, :, 1], scales[:, :, 0], scales[:, :, 1]
 
@@ -256,8 +256,8 @@ def _read(s):
     _, page, slot = _places(s)
     kc, vc, ks, vs = _views(s["pool"], s["dim"])
     dt = TYPES[s["dtype"]]
-    k = kc[page, :, slot].float() * ks[page, :, slot][..., None]
-    v = vc[page, :, slot].float() * vs[page, :, slot][..., None]
+    k = (kc[page, :, slot].float() - 128.0) * ks[page, :, slot][..., None]
+    v = (vc[page, :, slot].float() - 128.0) * vs[page, :, slot][..., None]
     return k.to(dt), v.to(dt)
 
 
@@ -265,8 +265,8 @@ def _pages(s, table):
     """Keys [..., n_kv, tokens, d] and values, in 32 bits, of the pages of `table` [..., pages]."""
     kc, vc, ks, vs = _views(s["pool"], s["dim"])
     t = table.long()
-    k = (kc[t].float() * ks[t][..., None]).movedim(-4, -3).flatten(-3, -2)
-    v = (vc[t].float() * vs[t][..., None]).movedim(-4, -3).flatten(-3, -2)
+    k = ((kc[t].float() - 128.0) * ks[t][..., None]).movedim(-4, -3).flatten(-3, -2)
+    v = ((vc[t].float() - 128.0) * vs[t][..., None]).movedim(-4, -3).flatten(-3, -2)
     return k, v
 
 
@@ -344,7 +344,7 @@ def exact(case, seed):
         """Keys (kv 0) or values (1) [n, count, d] of the first `count` tokens."""
         need = table[:(count + PAGE - 1) // PAGE].long()
         raw = pool[need]
-        code = raw[:, :, kv * PAGE * d:(kv + 1) * PAGE * d].contiguous().view(torch.int8).double().view(-1, n, PAGE, d)
+        code = raw[:, :, kv * PAGE * d:(kv + 1) * PAGE * d].double().view(-1, n, PAGE, d) - 128
         at = 2 * PAGE * d + kv * PAGE * 4
         scale = raw[:, :, at:at + PAGE * 4].contiguous().view(torch.float32).double()
         return (code * scale.unsqueeze(-1)).permute(1, 0, 2, 3).reshape(n, -1, d)[:, :count]
