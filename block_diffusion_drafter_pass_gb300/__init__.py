@@ -33,7 +33,7 @@ EXPORTED = (
     "dflash_block_sched_set_cost", "dflash_block_sched_expected_tau", "dflash_block_sched_choose",
     "dflash_debug_wait_timeout", "dflash_target_feature_layers", "dflash_target_create", "dflash_target_forward",
     "dflash_debug_read_kv_q8", "dflash_set_conv",
-    "dflash_kv_append", "dflash_paged_attn", "dflash_shared_prefix_attn", "dflash_paged_attn_workspace",
+    "dflash_kv_append", "dflash_kv_read", "dflash_paged_attn", "dflash_shared_prefix_attn", "dflash_paged_attn_workspace",
     "dflash_debug_paged_wait_tries",
 )
 SAMPLE_WIDTH = 32   # DFLASH_SAMPLE_WIDTH
@@ -80,6 +80,7 @@ class dflash_weights(ctypes.Structure):
 
 
 DFLASH_BF16, DFLASH_FP16 = 0, 1   # dflash_paged_batch.dtype
+DFLASH_POOL_Q8 = 16               # added to it: the pool has 8-bit pages
 KV_PAGE = 64                      # tokens per page
 
 
@@ -140,6 +141,7 @@ def load_library() -> ctypes.CDLL:
         "dflash_target_create": ([P(dflash_config), P(dflash_weights), i32p, P(VP)], I),
         "dflash_target_forward": ([VP, i32p, I, VP, I, I, VP, VP, VP], I),
         "dflash_kv_append": ([batch, VP, LL, VP, LL, VP, LL, VP, LL, VP, F, VP], I),
+        "dflash_kv_read": ([batch, VP, LL, VP, LL, VP], I),
         "dflash_debug_paged_wait_tries": ([I], I),
         "dflash_paged_attn_workspace": ([batch, P(ctypes.c_size_t)], I),
         "dflash_paged_attn": ([batch, VP, LL, VP, LL, I, I, I, F, VP, ctypes.c_size_t, VP], I),
@@ -226,15 +228,34 @@ def kv_pool_views(pool, head_dim: int):
     return pool[:, 0].view(n, h, KV_PAGE, head_dim), pool[:, 1].view(n, h, head_dim, KV_PAGE)
 
 
+def kv_pool_q8(n_pages: int, n_kv_heads: int, head_dim: int, device="cuda"):
+    """A zeroed pool of 8-bit pages, bytes [n_pages, n_kv_heads, 64 * (2 * head_dim + 8)]: per page and head
+    the key codes [64][d], the value codes [64][d] (each code + 128), the key scales [64] and the value
+    scales [64] (fp32). Half the size of kv_pool's; the calls below take either."""
+    import torch
+    return torch.zeros(n_pages, n_kv_heads, KV_PAGE * (2 * head_dim + 8), dtype=torch.uint8, device=device)
+
+
+def kv_pool_q8_views(pool, head_dim: int):
+    """(key codes, value codes [n_pages, n_kv, 64, d] as bytes, key scales, value scales [n_pages, n_kv, 64]) of a
+    pool of 8-bit pages, sharing its memory. A row stands for (codes - 128) * scale."""
+    import torch
+    n, h, _ = pool.shape
+    codes = pool[..., :2 * KV_PAGE * head_dim].view(n, h, 2, KV_PAGE, head_dim)
+    scales = pool[..., 2 * KV_PAGE * head_dim:].view(torch.float32).view(n, h, 2, KV_PAGE)
+    return codes[:, :, 0], codes[:, :, 1], scales[:, :, 0], scales[:, :, 1]
+
+
 def _refuse(message: str):
     raise DFlashError(DFLASH_EINVAL, message)
 
 
 def _rows_arg(name, t, dtype, dev, shape):
     """The stride between tokens of a token buffer of the given shape [T,
-    heads, d], which has the pool's type and device and contiguous head rows."""
+    heads, d], which has the tokens' type (the pool's, or over 8-bit pages one
+    for all), the pool's device and contiguous head rows."""
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape:
-        _refuse(f"{name} must be a {shape} tensor of the pool's dtype and device")
+        _refuse(f"{name} must be a {shape} tensor of {dtype} on the pool's device")
     T, h, d = shape
     if T == 0:
         return h * d
@@ -250,15 +271,27 @@ def _i32_arg(name, t, i32, dev, shape):
     return t.data_ptr()
 
 
-def _paged_batch(torch, pool, dev, n_heads, head_dim, n_tokens, q_start, kv_len, page_table, status):
-    dtype, i32 = pool.dtype, torch.int32
-    if dev < 0 or pool.dim() != 4 or not pool.is_contiguous():
-        _refuse("the pool must be a contiguous CUDA tensor [n_pages, 2, n_kv_heads, 64 * head_dim]")
+def _token_dtype(torch, pool, rows):
+    """The type of a call's token buffers: the pool's, or over 8-bit pages that of `rows`, one of them."""
+    return rows.dtype if pool.dtype is torch.uint8 else pool.dtype
+
+
+def _paged_batch(torch, pool, dev, dtype, n_heads, head_dim, n_tokens, q_start, kv_len, page_table, status):
+    i32 = torch.int32
+    if pool.dtype is torch.uint8:
+        if dev < 0 or pool.dim() != 3 or not pool.is_contiguous() or pool.shape[2] != KV_PAGE * (2 * head_dim + 8):
+            _refuse("a pool of 8-bit pages must be a contiguous CUDA tensor [n_pages, n_kv_heads, 64 * (2 * head_dim + 8)]")
+        n_pages, n_kv, _ = pool.shape
+        pages_of = DFLASH_POOL_Q8
+    else:
+        if dev < 0 or pool.dim() != 4 or not pool.is_contiguous():
+            _refuse("the pool must be a contiguous CUDA tensor [n_pages, 2, n_kv_heads, 64 * head_dim]")
+        n_pages, two, n_kv, width = pool.shape
+        if two != 2 or width != KV_PAGE * head_dim:
+            _refuse("the pool must be [n_pages, 2, n_kv_heads, 64 * head_dim]")
+        pages_of = 0
     if dtype is not torch.bfloat16 and dtype is not torch.float16:
-        _refuse("the pool must be bfloat16 or float16")
-    n_pages, two, n_kv, width = pool.shape
-    if two != 2 or width != KV_PAGE * head_dim:
-        _refuse("the pool must be [n_pages, 2, n_kv_heads, 64 * head_dim]")
+        _refuse("the token buffers and a pool of 16-bit pages must be bfloat16 or float16")
     if page_table.dim() != 2 or page_table.dtype is not i32 or page_table.get_device() != dev:
         _refuse("page_table must be an int32 tensor [n_seq, pages] on the pool's device")
     n_seq, pages = page_table.shape
@@ -269,7 +302,7 @@ def _paged_batch(torch, pool, dev, n_heads, head_dim, n_tokens, q_start, kv_len,
         _refuse("page_table needs at least one column and contiguous rows that do not overlap")
     # the struct's bytes (packing them is quicker than filling a ctypes structure)
     return n_kv, _BATCH.pack(
-        DFLASH_FP16 if dtype is torch.float16 else DFLASH_BF16, n_heads, n_kv, head_dim, n_seq, n_tokens, n_pages,
+        pages_of + (DFLASH_FP16 if dtype is torch.float16 else DFLASH_BF16), n_heads, n_kv, head_dim, n_seq, n_tokens, n_pages,
         pages, stride, pool.data_ptr(), page_table.data_ptr(), _i32_arg("q_start", q_start, i32, dev, (n_seq + 1,)),
         _i32_arg("kv_len", kv_len, i32, dev, (n_seq,)),
         0 if status is None else _i32_arg("status", status, i32, dev, (1,)))
@@ -299,15 +332,16 @@ def dflash_kv_append(pool, k, v, q_start, kv_len, page_table, *, q=None, q_out=N
     base rope_base; 0: not rotated) and rotate q [T, n_heads, d] beside them.
     q_start [n_seq + 1], kv_len [n_seq] (the new tokens counted) and page_table
     [n_seq, pages] are int32 device tensors. Returns the rotated queries
-    (q_out, which may be q itself), or None without q."""
+    (q_out, which may be q itself), or None without q. Into a pool of 8-bit
+    pages (kv_pool_q8) the rows are quantised as they are written."""
     import torch
     if k.dim() != 3 or (q is not None and q.dim() != 3):
         _refuse("k and q must be [tokens, heads, d]")
     shape = k.shape
     T, n_kv, d = shape
     n_heads = n_kv if q is None else q.shape[1]
-    dtype, dev = pool.dtype, pool.get_device()
-    pool_heads, b = _paged_batch(torch, pool, dev, n_heads, d, T, q_start, kv_len, page_table, status)
+    dtype, dev = _token_dtype(torch, pool, k), pool.get_device()
+    pool_heads, b = _paged_batch(torch, pool, dev, dtype, n_heads, d, T, q_start, kv_len, page_table, status)
     if n_kv != pool_heads:
         _refuse("k and the pool have different numbers of heads")
     ks, vs = _rows_arg("k", k, dtype, dev, shape), _rows_arg("v", v, dtype, dev, shape)
@@ -331,6 +365,41 @@ def dflash_kv_append(pool, k, v, q_start, kv_len, page_table, *, q=None, q_out=N
     return _run_on(torch, dev, stream, call)
 
 
+def dflash_kv_read(pool, n_tokens: int, q_start, kv_len, page_table, *, dtype=None, k_out=None, v_out=None, status=None,
+                   stream=None):
+    """The cached keys (as they were written, rotated) and values of the batch's
+    tokens -> (k, v) [n_tokens, n_kv, d]: row t is what dflash_kv_append with the
+    same q_start, kv_len and page_table would have written for token t. 16-bit
+    pages are copied; what 8-bit pages stand for is rounded once to `dtype`
+    (bfloat16 or float16; of k_out, when that is given, else bfloat16). Rows
+    without a page are left as they are (fresh outputs are not initialised)."""
+    import torch
+    if not 0 <= n_tokens <= 1 << 24:
+        _refuse("n_tokens must be 0..2^24")
+    q8, dev = pool.dtype is torch.uint8, pool.get_device()
+    if pool.dim() != (3 if q8 else 4):
+        _refuse("the pool must be one of kv_pool's or kv_pool_q8's")
+    width, n_kv = pool.shape[-1], pool.shape[-2]
+    d = (width // KV_PAGE - 8) // 2 if q8 else width // KV_PAGE
+    if dtype is None:
+        out = k_out if k_out is not None else v_out
+        dtype = pool.dtype if not q8 else torch.bfloat16 if out is None else out.dtype
+    elif not q8 and dtype is not pool.dtype:
+        _refuse("16-bit pages are read in their own type")
+    shape = (n_tokens, n_kv, d)
+    _, b = _paged_batch(torch, pool, dev, dtype, n_kv, d, n_tokens, q_start, kv_len, page_table, status)
+    ks = n_kv * d if k_out is None else _rows_arg("k_out", k_out, dtype, dev, shape)
+    vs = n_kv * d if v_out is None else _rows_arg("v_out", v_out, dtype, dev, shape)
+    lib = _lib or load_library()
+
+    def call(s):
+        k = torch.empty(shape, dtype=dtype, device=pool.device) if k_out is None else k_out
+        v = torch.empty(shape, dtype=dtype, device=pool.device) if v_out is None else v_out
+        _check(lib.dflash_kv_read(b, k.data_ptr(), ks, v.data_ptr(), vs, s))
+        return k, v
+    return _run_on(torch, dev, stream, call)
+
+
 _workspace_bytes = {}   # by all that they depend on; above 128 tokens they no longer grow
 
 
@@ -339,8 +408,8 @@ def _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status
         _refuse("q must be [tokens, heads, d]")
     shape = q.shape
     T, n_heads, d = shape
-    dtype, dev = pool.dtype, pool.get_device()
-    n_kv, b = _paged_batch(torch, pool, dev, n_heads, d, T, q_start, kv_len, page_table, status)
+    dtype, dev = _token_dtype(torch, pool, q), pool.get_device()
+    n_kv, b = _paged_batch(torch, pool, dev, dtype, n_heads, d, T, q_start, kv_len, page_table, status)
     qs = _rows_arg("q", q, dtype, dev, shape)
     if scale is None:
         scale = d ** -0.5
@@ -369,7 +438,8 @@ def dflash_paged_attn(q, pool, q_start, kv_len, page_table, *, window: int = 0, 
     caches (their own keys and values appended before) -> [T, n_heads, d].
     window > 0: keys after position - window and the first `sinks` ones only.
     scale defaults to d ** -0.5. `out` must not overlap q. Rows of no sequence
-    are left as they are (a fresh `out` is not initialised). `status` (int32 [1]
+    are left as they are (a fresh `out` is not initialised). The pool may be one
+    of 8-bit pages (kv_pool_q8). `status` (int32 [1]
     on the device, cleared by the caller) is what tells of broken device arrays
     (2) and of a kernel that gave up (1: the result is undefined)."""
     import torch

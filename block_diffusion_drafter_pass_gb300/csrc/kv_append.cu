@@ -48,28 +48,15 @@ struct AppendArgs {
   unsigned long long turn[64];     // base^(-2i/d) / (2 pi) in units of 2^-64 turns
 };
 
-// Where new token t goes: pool offset of its page and its slot, and its cache position.
-struct Place {
-  long long page;   // element offset of the page, -1: the token has no page
-  int slot, pos;    // pos < 0: the token is of no sequence or before its cache
-};
-
-template <int D>
-__device__ __forceinline__ Place place_of(const PagedView& b, const int* s_q, const int* s_len, int t) {
-  Place p{-1, 0, -1};
-  if (t >= b.n_tokens || t < s_q[0] || t >= s_q[b.n_seq]) return p;
-  const int i = seq_of_token(s_q, b.n_seq, t);
-  const int n_new = s_q[i + 1] - s_q[i];
-  p.pos = cached_tokens(b, s_len[i]) - n_new + (t - s_q[i]);
-  if (p.pos < 0) {   // more new tokens than the cache is said to hold
-    latch_status(b.status, kDevBounds);
-    return p;
+// The rotations of 8 pairs at position `at`.
+__device__ __forceinline__ void rotation(const AppendArgs& a, long long at, int oct, float (&cs)[8], float (&sn)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned long long turns = static_cast<unsigned long long>(at) * a.turn[oct * 8 + e];
+    // the signed upper half is the fraction of a turn in units of 2^-32
+    const float half_turns = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
+    sincospif(half_turns, &sn[e], &cs[e]);
   }
-  const int page = b.page_table[i * b.table_stride + p.pos / kPage];
-  p.slot = p.pos % kPage;
-  if (page < 0 || page >= b.n_pages) latch_status(b.status, kDevBounds);
-  else p.page = static_cast<long long>(page) * 2 * b.n_kv * kPage * D;
-  return p;
 }
 
 template <int D, bool F16>
@@ -103,19 +90,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     };
     read(h0);
     load_q_start(a.b, s_q);
-    const Place p = place_of<D>(a.b, s_q, s_len, t);
+    const Place p = place_of(a.b, s_q, s_len, t, 2ll * n_kv * kPage * D);
     if (p.pos < 0) return;
     float cs[8], sn[8];
-    if (a.rotate) {
-      const long long at = a.positions ? a.positions[t] : p.pos;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const unsigned long long turns = static_cast<unsigned long long>(at) * a.turn[oct * 8 + e];
-        // the signed upper half is the fraction of a turn in units of 2^-32
-        const float half_turns = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
-        sincospif(half_turns, &sn[e], &cs[e]);
-      }
-    }
+    if (a.rotate) rotation(a, a.positions ? a.positions[t] : p.pos, oct, cs, sn);
 #pragma unroll 1
     for (int h = h0; h < h1; h += kAtOnce) {
       if (h > h0) read(h);
@@ -154,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   }
   load_q_start(a.b, s_q);
   if (tid < kVTokens) {
-    const Place p = place_of<D>(a.b, s_q, s_len, t0 + tid);
+    const Place p = place_of(a.b, s_q, s_len, t0 + tid, 2ll * n_kv * kPage * D);
     s_dst[tid] = p.page < 0 ? -1 : p.page + (static_cast<long long>(n_kv) * kPage + h * kPage) * D + p.slot;
   }
 #pragma unroll
@@ -178,18 +156,130 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   }
 }
 
+// Rows for 8-bit pages, in blocks of kOct lanes: each holds 8 pairs (or, of
+// values, the same 16 places) of a head row. The row's largest magnitude is a
+// maximum of bit patterns, under which NaN and infinity come out on top; such a
+// row is held as the scale NaN, so that all of it reads back as NaN.
+template <int D>
+__device__ __forceinline__ void write_q8(const float (&x)[16], uint8_t* codes, float* scale, int oct, unsigned group) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = D / 32; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(group, top, o));
+  const float most = __uint_as_float(top);
+  const bool finite = top < 0x7F800000u, held = finite && most >= kQ8Least;
+  const float inv = held ? __fdiv_rn(kQ8Codes, most) : 0.f;
+  // the nearest code (halves to the even one) and 128, in the low byte of a float's bits
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t b[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) b[c] = __float_as_uint(__fadd_rn(__fmul_rn(x[4 * e + c], inv), 12582912.f + 128.f));
+    w[e] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+    if (!held) w[e] = 0x80808080u;
+  }
+  *reinterpret_cast<uint2*>(codes + oct * 8) = make_uint2(w[0], w[1]);
+  *reinterpret_cast<uint2*>(codes + D / 2 + oct * 8) = make_uint2(w[2], w[3]);
+  if (oct == 0) *scale = held ? __fdiv_rn(most, kQ8Codes) : finite ? 0.f : __uint_as_float(0x7FC00000u);
+}
+
+// The same work for 8-bit pages. Keys and values alike lie in rows there, so one
+// walk takes queries, keys and values, and a thread's 16 values of a row are
+// quantised where they are.
 template <int D, bool F16>
-cudaError_t launch(AppendArgs& a, cudaStream_t s) {
+__global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kOct = D / 16;                 // threads of a token: 8 pairs each
+  constexpr int kTokens = kThreads / kOct;
+  __shared__ int s_q[kPagedMaxSeqs + 1], s_len[kPagedMaxSeqs];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int tid = threadIdx.x, n_kv = a.b.n_kv;
+  for (int i = tid; i < a.b.n_seq; i += kThreads) s_len[i] = a.b.kv_len[i];
+  const int tile = blockIdx.x / a.qk_groups, grp = blockIdx.x % a.qk_groups;
+  const int t = tile * kTokens + tid / kOct, oct = tid % kOct;
+  const unsigned group = ((1u << kOct) - 1u) << (tid & 31 & ~(kOct - 1));   // the lanes of the token
+  const int n_q = a.q ? a.b.n_heads : 0;
+  const int h0 = grp * a.heads, h1 = t < a.b.n_tokens ? min(n_q + 2 * n_kv, h0 + a.heads) : h0;
+  uint4 lo[kAtOnce], hi[kAtOnce];
+  auto read = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = h + u - n_q;   // below 0: a query
+      if (h + u >= h1) continue;
+      const uint16_t* src = i < 0 ? a.q + t * a.q_stride + (h + u) * D
+                            : i < n_kv ? a.k + t * a.k_stride + i * D : a.v + t * a.v_stride + (i - n_kv) * D;
+      lo[u] = __ldg(reinterpret_cast<const uint4*>(src + oct * 8));
+      hi[u] = __ldg(reinterpret_cast<const uint4*>(src + D / 2 + oct * 8));
+    }
+  };
+  read(h0);
+  load_q_start(a.b, s_q);
+  const Place p = place_of(a.b, s_q, s_len, t, static_cast<long long>(n_kv) * q8_block_bytes(D));
+  if (p.pos < 0) return;
+  float cs[8], sn[8];
+  if (a.rotate && h0 < n_q + n_kv) rotation(a, a.positions ? a.positions[t] : p.pos, oct, cs, sn);
+  uint8_t* const page = reinterpret_cast<uint8_t*>(a.b.pool) + p.page;
+#pragma unroll 1
+  for (int h = h0; h < h1; h += kAtOnce) {
+    if (h > h0) read(h);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = h + u - n_q;
+      if (h + u >= h1 || (i >= 0 && p.page < 0)) continue;
+      float x[16];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 f = unpack2<F16>((&lo[u].x)[w]), g = unpack2<F16>((&hi[u].x)[w]);
+        x[2 * w] = f.x, x[2 * w + 1] = f.y, x[8 + 2 * w] = g.x, x[9 + 2 * w] = g.y;
+      }
+      if (a.rotate && i < n_kv) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float f = x[e], g = x[8 + e];
+          x[e] = f * cs[e] - g * sn[e];
+          x[8 + e] = g * cs[e] + f * sn[e];
+        }
+      }
+      if (i < 0) {
+        uint16_t* dst = a.q_out + t * a.out_stride + (h + u) * D;
+        uint4 ro = lo[u], rh = hi[u];
+        if (a.rotate) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            (&ro.x)[w] = pack2<F16>(x[2 * w], x[2 * w + 1]);
+            (&rh.x)[w] = pack2<F16>(x[8 + 2 * w], x[9 + 2 * w]);
+          }
+        }
+        *reinterpret_cast<uint4*>(dst + oct * 8) = ro;
+        *reinterpret_cast<uint4*>(dst + D / 2 + oct * 8) = rh;
+      } else {
+        const int v = i >= n_kv;
+        uint8_t* block = page + static_cast<long long>(v ? i - n_kv : i) * q8_block_bytes(D);
+        write_q8<D>(x, block + (v ? q8_values_at(D) : 0) + p.slot * D,
+                    reinterpret_cast<float*>(block + (v ? q8_value_scales_at(D) : q8_key_scales_at(D))) + p.slot, oct, group);
+      }
+    }
+  }
+}
+
+template <int D, bool F16>
+cudaError_t launch(AppendArgs& a, bool q8, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const long long enough = 2ll * sms;   // blocks that fill the device: few tokens are cut finer
   const int tokens = kThreads / (D / 16);
-  const int heads = (a.q ? a.b.n_heads : 0) + a.b.n_kv;
+  const int heads = (a.q ? a.b.n_heads : 0) + (q8 ? 2 : 1) * a.b.n_kv;
   a.qk_tiles = (a.b.n_tokens + tokens - 1) / tokens;
   a.heads = static_cast<int>(std::min<long long>(kMaxHeads, std::max<long long>(1, heads * static_cast<long long>(a.qk_tiles) / enough)));
   a.qk_groups = (heads + a.heads - 1) / a.heads;
+  if (q8) {
+    const long long grid = static_cast<long long>(a.qk_tiles) * a.qk_groups;
+    return launch_pdl(kv_append_q8_kernel<D, F16>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+  }
   long long v_blocks = static_cast<long long>((a.b.n_tokens + kVTokens - 1) / kVTokens) * a.b.n_kv;
   a.v_split = v_blocks * 4 <= enough ? 4 : v_blocks * 2 <= enough ? 2 : 1;
   v_blocks *= a.v_split;
@@ -202,7 +292,8 @@ cudaError_t launch(AppendArgs& a, cudaStream_t s) {
 
 const char* paged_check(const dflash_paged_batch* b) {
   if (!b) return "null batch";
-  if (b->dtype != DFLASH_BF16 && b->dtype != DFLASH_FP16) return "dtype is neither DFLASH_BF16 nor DFLASH_FP16";
+  const int tokens = b->dtype & ~DFLASH_POOL_Q8;
+  if (tokens != DFLASH_BF16 && tokens != DFLASH_FP16) return "dtype is neither DFLASH_BF16 nor DFLASH_FP16, with or without DFLASH_POOL_Q8";
   if (b->head_dim != 64 && b->head_dim != 128) return "head_dim must be 64 or 128";
   if (b->n_kv_heads < 1 || b->n_kv_heads > 128 || b->n_heads < 1 || b->n_heads % b->n_kv_heads)
     return "n_kv_heads must be 1..128 and divide n_heads";
@@ -297,8 +388,9 @@ extern "C" dflash_status dflash_kv_append(const dflash_paged_batch* b, const voi
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (b->head_dim == 128) e = b->dtype == DFLASH_FP16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
-  else e = b->dtype == DFLASH_FP16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+  const bool q8 = b->dtype & DFLASH_POOL_Q8, f16 = b->dtype & DFLASH_FP16;
+  if (b->head_dim == 128) e = f16 ? launch<128, true>(a, q8, s) : launch<128, false>(a, q8, s);
+  else e = f16 ? launch<64, true>(a, q8, s) : launch<64, false>(a, q8, s);
   if (e != cudaSuccess) {
     set_unattached_error("dflash_kv_append: kernel launch failed");
     return DFLASH_ECUDA;

@@ -24,6 +24,21 @@ namespace dfl {
 constexpr int kPagedMaxSeqs = 1024;      // sequences of one call (their bounds are held in shared memory)
 constexpr int kPagedMaxTable = 1 << 20;  // pages of one sequence: positions stay below 2^26, a batch's steps of keys below 2^30
 
+// 8-bit pages (dtype with DFLASH_POOL_Q8): per page and kv head one block of
+// key codes [64][d], value codes [64][d], key scales [64], value scales [64]
+// (fp32); a code is held as the byte code + 128, and stands for code * scale.
+// Values lie in rows like keys: who writes or reads tokens moves whole rows, and
+// the products take them either way. One scale a row, not one for 32 values as in
+// the contexts' own 8-bit pages: codes are whole numbers of 8 bits, exact in
+// either 16-bit type, and a scale that belongs to the key can be multiplied into
+// its score or its weight in fp32, so nothing is rounded on the way to a product.
+__host__ __device__ constexpr int q8_block_bytes(int d) { return kPage * (2 * d + 8); }
+__host__ __device__ constexpr int q8_values_at(int d) { return kPage * d; }
+__host__ __device__ constexpr int q8_key_scales_at(int d) { return 2 * kPage * d; }
+__host__ __device__ constexpr int q8_value_scales_at(int d) { return 2 * kPage * d + 4 * kPage; }
+constexpr float kQ8Codes = 127.f;       // the largest code
+constexpr float kQ8Least = 0x1p-100f;   // rows that stay below are held as zeros: 127 / max must be finite
+
 // The batch as the kernels read it. All arrays are on the device.
 struct PagedView {
   int n_heads, n_kv, group;   // query heads, kv heads, query heads per kv head
@@ -61,9 +76,18 @@ inline bool rows_overlap(const void* x, long long x_stride, long long x_width, c
 inline bool in_pool(const dflash_paged_batch& b, const void* x, long long stride, long long width) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(x), pool = reinterpret_cast<uintptr_t>(b.pool);
   const uintptr_t end = at + static_cast<uintptr_t>(((b.n_tokens - 1) * stride + width) * 2);
-  const uintptr_t page = static_cast<uintptr_t>(2) * b.n_kv_heads * kPage * b.head_dim * 2;
+  const uintptr_t block = b.dtype & DFLASH_POOL_Q8 ? q8_block_bytes(b.head_dim) : 4 * kPage * b.head_dim;
+  const uintptr_t page = b.n_kv_heads * block;
   return at < pool + b.n_pages * page && pool < end;
 }
+
+// Where token t of the token buffers lies: its page (an offset in the pool in
+// units of `page_size`; -1: the token has no page), its slot and its cache
+// position (< 0: the token is of no sequence, or before its cache).
+struct Place {
+  long long page;
+  int slot, pos;
+};
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -122,6 +146,23 @@ __device__ __forceinline__ int cached_tokens(const PagedView& b, int raw) {
   const int v = min(max(raw, 0), b.table_pages * kPage);
   if (v != raw) latch_status(b.status, kDevBounds);
   return v;
+}
+
+__device__ __forceinline__ Place place_of(const PagedView& b, const int* s_q, const int* s_len, int t, long long page_size) {
+  Place p{-1, 0, -1};
+  if (t >= b.n_tokens || t < s_q[0] || t >= s_q[b.n_seq]) return p;
+  const int i = seq_of_token(s_q, b.n_seq, t);
+  const int n_new = s_q[i + 1] - s_q[i];
+  p.pos = cached_tokens(b, s_len[i]) - n_new + (t - s_q[i]);
+  if (p.pos < 0) {   // more tokens than the cache is said to hold
+    latch_status(b.status, kDevBounds);
+    return p;
+  }
+  const int page = b.page_table[i * b.table_stride + p.pos / kPage];
+  p.slot = p.pos % kPage;
+  if (page < 0 || page >= b.n_pages) latch_status(b.status, kDevBounds);
+  else p.page = page * page_size;
+  return p;
 }
 
 }  // namespace dfl

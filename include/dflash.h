@@ -423,11 +423,22 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * page (those in front of a window may be any number). Bit 0 (value 1): a wait
  * inside an attention kernel ran out, which no arguments should bring about;
  * `out` is then undefined. The caller clears *status; without one (NULL) nothing
- * else tells of these. Slots past a length may hold any bits. */
-enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1 };
+ * else tells of these. Slots past a length may hold any bits.
+ *
+ * 8-bit pages (DFLASH_POOL_Q8 added to dtype, which is then the type of the token
+ * buffers only): a page is, for each kv head, one block of 64 * (2 d + 8) bytes:
+ * the key codes [64][d], the value codes [64][d], the key scales [64] and the
+ * value scales [64] (fp32). A token's row x of d keys (rotated) or values is held
+ * as codes c = x * (127 / m) rounded to the nearest whole number (halves to the
+ * even one), m = max |x|, each as the byte c + 128, and the scale m / 127; it
+ * stands for c * scale. Rows with m below 2^-100 are held as zeros, and a row with
+ * an infinity or a NaN stands for NaN throughout. Attention takes what the codes
+ * stand for without rounding it. */
+enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1, DFLASH_POOL_Q8 = 16 };
 
 typedef struct {
-  int dtype;                 /* of pool and token buffers: DFLASH_BF16 or DFLASH_FP16 */
+  int dtype;                 /* of pool and token buffers: DFLASH_BF16 or DFLASH_FP16;
+                                + DFLASH_POOL_Q8: token buffers, over 8-bit pages   */
   int n_heads;               /* query heads; head h reads kv head h / (n_heads / n_kv_heads) */
   int n_kv_heads;            /* 1..128, divides n_heads, at most 128 query heads each */
   int head_dim;              /* d: 64 or 128                                        */
@@ -461,6 +472,20 @@ typedef struct {
 dflash_status dflash_kv_append(const dflash_paged_batch* b, const void* k, long long k_stride, const void* v,
                                long long v_stride, const void* q, long long q_stride, void* q_out,
                                long long q_out_stride, const int32_t* positions, float rope_base, void* stream);
+
+/* Cached keys and values as rows of token buffers: row t of k_out and v_out
+ * gets what the cache holds for token t of the batch, at the position where
+ * dflash_kv_append would put it (a call with q_start counting whole caches reads
+ * whole caches). 16-bit pages are copied; what 8-bit pages stand for is rounded
+ * once to the tokens' type. Keys come out as they were written, rotated.
+ *  k_out, v_out  device [n_tokens][n_kv_heads][d], strides in elements between
+ *                tokens (multiples of 8), 16-byte aligned; they overlap neither
+ *                each other nor the pool
+ * Rows of tokens without a page, or before their cache, are left as they are and
+ * set the status. q is not involved: n_heads only has to pass the checks.
+ * Errors: EINVAL, ECUDA. */
+dflash_status dflash_kv_read(const dflash_paged_batch* b, void* k_out, long long k_stride, void* v_out,
+                             long long v_stride, void* stream);
 
 /* Device bytes that the two attention calls below need as workspace for this
  * batch's shape (it depends on n_heads, n_kv_heads, head_dim, n_tokens and the
