@@ -1,104 +1,812 @@
 // paged_attn_q8.cu - the attention of paged_attn.cu over 8-bit pages: the same
-// rows, masks and prefixes, with keys and values that stand for code * scale.
+// rows, masks, prefixes, tiles and steps, with keys and values that stand for
+// code * scale.
 //
-// One warp takes one row (token, head): lanes take keys for the scores and head
-// dims for the product with the values, page by page with a running maximum and
-// sum, everything in fp32.
+// Row q (times the softmax scale), key j with codes c_j and scale a_j, value
+// with codes d_j and scale b_j:
+//     s_j = a_j (q . c_j),   o = sum_j 2^(s_j - m) b_j d_j / sum_j 2^(s_j - m).
+// Codes are whole numbers of 8 bits, exact in fp16, so the products are of fp16
+// whatever the tokens' type: q.c_j with q taken to fp16 behind a power of two
+// that puts the row's largest value between 1/2 and 1 (values below 2^-14 of that
+// are rounded in steps of 2^-24 of it, all others are exact: bf16 has fewer bits),
+// then a_j in fp32 on the score, and b_j in fp32 on the weight, which is
+// then rounded to fp16 as the product's operand (half a step, 2^-12 of it). For
+// that fp16 is given its best place: a row's weights are 2^(s - m - E), m its
+// reference maximum less 7 and 2^E above every value scale so far, so that a
+// weight times its scale stays below 2^15, and 2^-31 of the largest one still
+// counts. Sum and output share the unit 2^-E, so it cancels; E is clamped below
+// at -80, so weights stay finite when all values are tiny.
+//
+// Per CTA: a warp walks the steps and writes down the pages of each half (128
+// keys, or their values); 4 warps take the halves from global memory
+// into registers, kAhead of them under way, and put them as fp16 into the ring
+// that the products read (and the queries of each item, scaled); two warps issue
+// the tcgen05.mma of a stream each and eight do the softmax, as in paged_attn.cu.
+// Values lie in rows of a token like keys; the product takes them as its
+// MN-major operand. Hidden or missing keys need no care in the products: every
+// code is finite, and weights of hidden keys are zero before their scale.
+#include <algorithm>
+#include <atomic>
+
+#define DFL_WALK_CALL __forceinline__
 #include "paged_walk.cuh"
 
 namespace dfl {
 namespace {
 
-constexpr int kRowWarps = 8;
+constexpr int kConvWarp0 = 8, kConvWarps = 4;   // the softmax's are 0..7: TMEM lanes go by warp % 4
+constexpr int kWalkWarp = 12, kMmaWarp0 = 13;   // warp 15 has no work
+constexpr int kThreads = 512;
+// Registers of a thread, by warpgroup: the launch's 128 x 512 (the kernel's
+// bounds make it that many) are dealt anew.
+constexpr int kLaunchRegs = 128, kSoftRegs = 120, kConvRegs = 200, kRestRegs = 72;
+static_assert(2 * kSoftRegs + kConvRegs + kRestRegs <= 4 * kLaunchRegs, "setmaxnreg waits for registers that the launch must have");
+static_assert(kSoftRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs && kConvRegs >= kLaunchRegs, "dec must go down and inc up");
+constexpr int kConvThreads = kConvWarps * 32;
+constexpr int kRecords = 16;     // halves that the walk may be ahead
+// Halves in the ring, and the records before them, bound how far the walk is
+// ahead of the products: 8 + 4 steps and the lead.
+constexpr int kStepRing = 32;
+constexpr int kScaleRing = 8;    // steps whose scales are held: the ring's 4 and the lead
+constexpr int kIdsAhead = 2, kIdRing = 32;
+constexpr float kBias = 7.f;
+constexpr int kLeastE = -80, kNoUnit = -(1 << 20);
+
+enum : int { kKeys = 0, kValues = 1, kQueries = 2, kEnd = 3 };
+
+// A half of a step, or an item's queries.
+struct Record {
+  int kind, head;
+  int number;   // of the step; queries: of the item
+  int rest;     // keys of the step that exist (may be above 128, or below 0); queries: whether each stream has rows of its own
+  int a, b;     // pages (-1: none); queries: first token, tokens
+};
+
+template <int D>
+struct Cfg {
+  static constexpr int kBox = kRows * 128;                  // 128 rows of 64 elements, swizzled
+  static constexpr int kHalf = (D / 64) * kBox;             // a step's keys, or its values
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kQBytes = 2 * kHalf;                 // queries of both streams
+  static constexpr int kIntOff = kQBytes + kSlots * kHalf;
+  static constexpr int kScaleOff = kIntOff + kBatchBytes;   // [kScaleRing][2][128] fp32
+  static constexpr int kSmem = kScaleOff + kScaleRing * 2 * kStepKeys * 4 + 1024;
+  static_assert(kSmem <= 227 * 1024 - 7168, "static shared variables need the rest");
+  static constexpr int kPieces = D / 16;                    // 16 bytes of a half for each converting thread
+  static constexpr int kAhead = D == 128 ? 4 : 6;           // halves under way in registers
+};
+
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
+  return floats2(r);
+}
+
+__device__ __forceinline__ uint4 load_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ void store_shared16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ float4 load_shared16(uint32_t at) {   // in place: read ahead, scales take the scores' registers
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+
+// Four codes (bytes, + 128) as fp16: behind the byte 0x64 a byte is 1024 + itself.
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
+  const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
+  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), off), b = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Descriptor of values as they lie in the ring, MN-major with 128-byte swizzle:
+// groups of 64 dims a box apart, groups of 8 keys 1024 bytes apart.
+template <int D>
+__device__ __forceinline__ uint32_t vdesc_low(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (static_cast<uint32_t>(Cfg<D>::kBox >> 4) << 16);
+}
+
+// A row's power of two 2^(e - 126), e the biased exponent of its largest value.
+__device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kRowWarps * 32) paged_rows_q8_kernel(const __grid_constant__ PagedAttnArgs a) {
-  __shared__ int s_q[kPagedMaxSeqs + 1];
-  grid_dep_wait();
-  grid_dep_launch();
-  load_q_start(a.b, s_q);
-  const int lane = threadIdx.x & 31, n_q = a.b.n_heads;
-  const long long row = static_cast<long long>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int t = static_cast<int>(row / n_q), head = static_cast<int>(row % n_q), kvh = head / a.b.group;
-  if (t < s_q[0] || t >= s_q[a.b.n_seq]) return;
-  const int i = seq_of_token(s_q, a.b.n_seq, t);
-  const int len = cached_tokens(a.b, a.b.kv_len[i]);
-  const int pos = len - s_q[i + 1] + t;
-  const uint16_t* q = a.q + t * a.q_stride + static_cast<long long>(head) * D;
-  float m = -INFINITY, l = 0.f, acc[D / 32] = {};
-  for (int run = 0; run < 2; ++run) {
-    if (run == 0 && a.prefix_len == 0) continue;
-    const int32_t* table = run == 0 ? a.prefix_table : a.b.page_table + i * a.b.table_stride;
-    const int end = run == 0 ? a.prefix_len : len;
-    RowSpan sp{0, a.causal ? pos : kNoEnd, 0};
-    if (run == 0) sp.hi = a.causal ? pos + a.prefix_len : kNoEnd;
-    else if (a.window > 0) sp.lo = max(0, pos - a.window + 1), sp.sinks = a.sinks;
-    for (int key0 = 0; key0 < end; key0 += kPage) {
-      const unsigned long long vis = sp.hi >= 0 ? row_sees(sp, key0, end) : 0ull;
-      if (vis == 0) continue;
-      const int page = table[key0 / kPage];
-      if (page < 0 || page >= a.b.n_pages) {
-        if (lane == 0) latch_status(a.b.status, kDevBounds);
-        continue;
+__device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Record& r, uint32_t q_at, float* s_qc, int ct) {
+  constexpr int kOf = D / 8, kPass = kConvThreads / kOf, kAtOnce = 4;
+  const int c = ct % kOf, G = a.b.group, stream_rows = a.stream_tokens * G;
+  const int n = (r.rest ? 2 : 1) * stream_rows, end = r.a + r.b;
+#pragma unroll 1
+  for (int base = 0; base < n; base += kPass * kAtOnce) {
+    uint4 w[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = base + u * kPass + ct / kOf, token = r.a + i / G;   // a stream's tokens follow the other's
+      w[u] = make_uint4(0, 0, 0, 0);
+      if (i < n && token < end)
+        w[u] = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + static_cast<long long>(r.head * G + i % G) * D) + c);
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = base + u * kPass + ct / kOf;
+      float x[8];
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack2<F16>((&w[u].x)[e]);
+        x[2 * e] = f.x, x[2 * e + 1] = f.y;
       }
-      const uint8_t* block = reinterpret_cast<const uint8_t*>(a.b.pool) + (static_cast<long long>(page) * a.b.n_kv + kvh) * q8_block_bytes(D);
-      const float* ks = reinterpret_cast<const float*>(block + q8_key_scales_at(D));
-      const float* vs = reinterpret_cast<const float*>(block + q8_value_scales_at(D));
-      float s[2] = {-INFINITY, -INFINITY};
-      for (int u = 0; u < 2; ++u) {
-        const int c = lane + 32 * u;
-        if (!(vis >> c & 1)) continue;
-        float x = 0.f;
-        for (int e = 0; e < D; e += 2) {
-          const float2 f = unpack2<F16>(*reinterpret_cast<const uint32_t*>(q + e));
-          x = fmaf(f.x, static_cast<int>(block[c * D + e]) - 128, x);
-          x = fmaf(f.y, static_cast<int>(block[c * D + e + 1]) - 128, x);
-        }
-        s[u] = x * ks[c] * a.scale_log2;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {   // of the finite ones: the others stay what they are
+        const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+        top = b < 0x7F800000u ? max(top, b) : top;
       }
-      float mx = fmaxf(s[0], s[1]);
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float nm = fmaxf(m, mx), ref = nm == -INFINITY ? 0.f : nm, alpha = exp2f(m - ref);
-      float p[2], w[2], sum = 0.f;
-      for (int u = 0; u < 2; ++u) {
-        const int c = lane + 32 * u;
-        const bool sees = vis >> c & 1;
-        p[u] = sees ? exp2f(s[u] - ref) : 0.f;
-        w[u] = sees ? p[u] * vs[c] : 0.f;
-        sum += p[u];
-      }
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      l = l * alpha + sum;
-      m = nm;
-      for (int e = 0; e < D / 32; ++e) acc[e] *= alpha;
-      for (int c = 0; c < kPage; ++c) {
-        const float wc = __shfl_sync(0xffffffffu, c < 32 ? w[0] : w[1], c & 31);
-        if (!(vis >> c & 1)) continue;
-        for (int e = 0; e < D / 32; ++e)
-          acc[e] = fmaf(wc, static_cast<int>(block[q8_values_at(D) + c * D + lane * (D / 32) + e]) - 128, acc[e]);
+#pragma unroll
+      for (int o = kOf / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = static_cast<int>(top >> 23), up = 126 - e;   // times 2^up, in two factors: -128..126
+      const float f0 = pow2_of(up >> 1), f1 = pow2_of(up - (up >> 1));
+      uint4 h;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) (&h.x)[k] = pack2<true>(x[2 * k] * f0 * f1, x[2 * k + 1] * f0 * f1);
+      if (i < n) {
+        const int stream = i >= stream_rows, row = i - stream * stream_rows;
+        store_shared16(q_at + stream * Cfg<D>::kHalf + (c >> 3) * Cfg<D>::kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4), h);
+        // key scales are held 2^-8 down, so that no product with a dot product (below 2^14) overflows
+        if (c == 0) s_qc[stream * kRows + row] = fminf(a.scale_log2 * pow2_of(-(up >> 1)) * pow2_of(-(up - (up >> 1))) * 256.f, 0x1.fffffep127f);
       }
     }
   }
-  const float f = l > 0.f || l != l ? 1.f / l : 0.f;
-  uint16_t* o = out_row(a, t, kvh, head % a.b.group, D) + lane * (D / 32);
-  for (int e = 0; e < D / 32; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack2<F16>(acc[e] * f, acc[e + 1] * f);
 }
 
-__global__ void no_pieces_kernel(const __grid_constant__ PagedAttnArgs a) {
+// The largest magnitude (bits) among a step's value scales whose keys the row sees.
+__device__ __forceinline__ uint32_t seen_scale(uint32_t value_scales, unsigned long long vis0, unsigned long long vis1) {
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int c = 0; c < 2 * kPage; c += 4) {
+    const float4 f = load_shared16(value_scales + c * 4);
+    const uint32_t v = static_cast<uint32_t>((c < kPage ? vis0 : vis1) >> (c % kPage));
+    if (v & 1) top = max(top, __float_as_uint(f.x) & 0x7FFFFFFFu);
+    if (v & 2) top = max(top, __float_as_uint(f.y) & 0x7FFFFFFFu);
+    if (v & 4) top = max(top, __float_as_uint(f.z) & 0x7FFFFFFFu);
+    if (v & 8) top = max(top, __float_as_uint(f.w) & 0x7FFFFFFFu);
+  }
+  return top;
+}
+
+struct NoRedo {
+  static constexpr bool kOn = false;
+};
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid_constant__ PagedAttnArgs a) {
+  using C = Cfg<D>;
+  constexpr int S = C::kSlots;
+  constexpr uint32_t kIdescS = idesc_f16_f32(kRows, kStepKeys);
+  constexpr uint32_t kIdescO = idesc_f16_f32(kRows, D) | (1u << 16);   // B is MN-major
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
+  float* const s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
+  __shared__ __align__(16) Record s_rec[kRecords];
+  __shared__ __align__(16) uint32_t s_vmax[kScaleRing][4];   // largest value scale (bits) of 32 keys
+  __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
+  __shared__ __align__(8) uint64_t rec_full[kRecords], rec_empty[kRecords];
+  __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
+  __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
+  __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
+  __shared__ Join join;
+  __shared__ int s_page[kIdRing][2];
+  __shared__ uint32_t s_step[kStepRing];
+  __shared__ long long s_sum[kThreads / 32];
+  __shared__ Item s_first[2];   // the CTA's first item (and where its run begins)
+  __shared__ Item s_items[11][2];   // an item and the one after it: softmax warps, walk, products
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_progress;
+  __shared__ int s_never;   // 0: the progress of waits that must not be cut short
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < kRecords; ++s) {
+      mbar_init(&rec_full[s], 1);
+      mbar_init(&rec_empty[s], kConvWarps);
+    }
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&kv_full[s], kConvWarps);
+      mbar_init(&kv_empty[s], 2);   // both streams
+    }
+    mbar_init(&q_full, kConvWarps);
+    mbar_init(&q_empty, 2);
+    mbar_init(&mma_done, 2);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s][0], 4);
+      mbar_init(&p_full[s][1], 4);
+      mbar_init(&o_done[s], 1);
+      mbar_init(&turn[s], 1);
+    }
+    mbar_init(&join.x_ml, 8);
+    mbar_init(&join.x_bad, 8);
+    s_progress = a.wait_tries > 0 ? 0 : kGaveUp;
+    s_first[0].nj = 0;
+    s_never = 0;
+    set_batch(a, b);
+    fence_mbar_init();
+  }
+  if (tid < kStepRing) s_step[tid] = 0;   // no step's note (an earlier CTA's may lie here)
+  if (warp == kMmaWarp0) tmem_alloc(&tmem_slot, kTmemCols);
   grid_dep_wait();
-  a.split[blockIdx.x] = make_int4(0, 0, 0, 0);
-  a.piece[blockIdx.x] = 0;
+  grid_dep_launch();
+  const int run = deal_batch<kThreads>(a, b, s_sum, s_first);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  const bool converts = warp >= kConvWarp0 && warp < kWalkWarp, idle = warp > kMmaWarp0 + 1;
+  Item* const items = s_items[warp < kConvWarp0 ? warp : converts || idle ? 0 : warp - kWalkWarp + kConvWarp0];   // written by lane 0
+  if (!converts && !idle && lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
+  __syncwarp();
+  const uint32_t progress_at = smem_u32(&s_progress), never_at = smem_u32(&s_never);
+  const uint32_t wait_tries = a.wait_tries;
+  auto give_up = [&]() {
+    atomicOr(&s_progress, kGaveUp);
+    latch_status(a.b.status, kDevTimeout);
+  };
+  // An item goes in rounds j = -lead .. nj-1: round j multiplies P of step j
+  // with its values and issues the scores of step j + lead, so the ring holds,
+  // in turn, the values of step j and the keys of step j + lead. lead is 1 for
+  // a pair (both streams take every step) and 2 for an alternating tile
+  // (stream s takes the steps of parity s).
+
+  if (warp >= kWalkWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+    if (warp == kWalkWarp && lane == 0) {
+      // ---------------- the walk over keys and values ----------------
+      const uint32_t full_at = smem_u32(rec_full), empty_at = smem_u32(rec_empty);
+      int n = 0, steps = 0;   // records, steps whose keys are written down
+      bool ok = true;
+      auto record = [&](int kind, int head, int number, int rest, int x, int y) {
+        ok = bar_wait(empty_at + n % kRecords * 8, (n / kRecords & 1) ^ 1, progress_at, wait_tries);
+        if (!ok) return;
+        s_rec[n % kRecords] = Record{kind, head, number, rest, x, y};
+        bar_arrive(full_at + n % kRecords * 8);
+        ++n;
+      };
+      int4 split = make_int4(0, 0, 0, 0);
+      int piece = 0;
+#pragma unroll 1
+      for (int before = items[0].nj > 0 ? items[0].j : 0; before > 0; before -= run) ++piece;
+      int k = 0;
+      for (; items[k & 1].nj > 0; ++k) {
+        const Item& it = items[k & 1];
+        next_item(b, it, items[(k + 1) & 1]);
+        const int lead = it.pair ? 1 : 2, nj = it.nj;
+        record(kQueries, it.head, k, it.pair, it.t.t0, it.t.ntok);
+        // Page ids are copied kIdsAhead steps before their keys are due, so no
+        // load waits for one.
+        StepWalk wf, wk, wv;   // of the ids, of the keys, of the values
+        wf.start(b, it.t, it.j);
+        wk = wf;
+        wv = wf;
+        const int step0 = steps;
+#pragma unroll 1
+        for (int i = -2 * (lead + kIdsAhead); i < 2 * nj && ok; ++i) {   // round i >> 1: values, then ids and keys
+          const bool keys = i & 1;
+          const int j = (i >> 1) + (keys ? lead : 0);
+          if (keys) {
+            const int jf = j + kIdsAhead;
+            if (jf < nj) {
+              const int32_t* table = table_of(a, wf.s.seq);
+              int* dst = s_page[(step0 + jf) % kIdRing];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int key0 = wf.s.base + u * kPage;
+                if (key0 < wf.s.end) copy_async4(dst + u, table + key0 / kPage);
+                else dst[u] = -1;
+              }
+              wf.next(b, it.t);
+            }
+            copy_async_commit();
+            copy_async_wait<kIdsAhead>();
+          }
+          if (j < 0 || j >= nj) continue;
+          int page[2], gone = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            page[u] = s_page[(step0 + j) % kIdRing][u];
+            if (page[u] >= 0 && page[u] < a.b.n_pages) continue;
+            page[u] = -1;
+            gone |= 1 << u;
+          }
+          StepWalk& w = keys ? wk : wv;
+          const int rest = w.s.end - w.s.base;
+          if (keys) {
+            int flags = gone;
+            if (it.pair) flags |= pair_takes(b, it.t, w.s.seq, w.s.base) << 2;
+            const uint32_t note = step_note(steps, flags);
+            *const_cast<volatile uint32_t*>(s_step + steps++ % kStepRing) = note;
+          }
+          w.next(b, it.t);
+          record(keys ? kKeys : kValues, it.head, step0 + j, rest, page[0], page[1]);
+        }
+        if (!ok) break;
+        if (it.j == 0 && nj < it.t.n) {   // the run ends here: the rest is the next CTAs'
+          int pieces = 1;
+#pragma unroll 1
+          for (int left = it.t.n - nj; left > 0; left -= run) ++pieces;
+          split = make_int4(it.t.t0, it.t.ntok, it.head, pieces);
+        }
+      }
+      if (ok) record(kEnd, 0, 0, 0, 0, 0);
+      if (!ok) give_up();
+      a.split[blockIdx.x] = split;
+      a.piece[blockIdx.x] = piece;
+      copy_async_wait<0>();
+    }
+    if (warp >= kMmaWarp0 && !idle) {
+      // ---------------- products of one stream ----------------
+      // As in paged_attn.cu: the warp goes through this as one, with one elected
+      // lane in front of the instructions.
+      const int s = warp_uniform(warp - kMmaWarp0);
+      const bool one = elect_one();
+      const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kQBytes >> 4);
+      const uint32_t vring_low = vdesc_low<D>(smem_u32(smem)) + (C::kQBytes >> 4);
+      const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+      const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0][0]) + s * 16;
+      const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
+      const uint32_t tm = warp_uniform(tmem);
+      const uint32_t s_col = tm + s * kStepKeys, o_col = tm + kOCol + s * D;
+      int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
+      };
+      while (true) {
+        const Item& it = items[k & 1];
+        const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
+        if (nj <= 0) break;
+        __syncwarp();
+        const uint32_t q_at = q_low + (pair ? s * (C::kHalf >> 4) : 0);
+        wait(smem_u32(&q_full), k & 1);
+        ++k;
+        uint32_t add = 0;
+        uint32_t takes = 0;   // bit i: the stream takes step j + i
+#pragma unroll 1
+        for (int j = -lead; j < nj && ok; ++j) {
+          const int pv = j >= 0, more = j + lead < nj;
+          if (j == nj - lead) {   // the scores are all issued
+            if (lane == 0) next_item(b, it, items[k & 1]);
+            __syncwarp();
+          }
+          const int ck = c + pv, vslot = c % S, kslot = ck % S;
+          // One lane for each thing to wait for, so that the waits are one. Of a
+          // pair that is everything but the second page's weights, and its streams
+          // take turns; an alternating tile's values go back as soon as they can.
+          const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
+          uint32_t early = 0;
+          {
+            if (pair && more) early = note_early<kStepRing>(s_step, steps);
+            bool need = lane == 0 && pv;
+            uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
+            if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
+            if (lane == 2) need = weights, bar = p_at, parity = np & 1;
+            if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
+            int polls = kWaitPolls, seen = 0;
+            while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
+              const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
+              if (progress != seen) polls = kWaitPolls;
+              seen = progress;
+              if (progress < 0 || --polls == 0) {
+                ok = false;
+                break;
+              }
+            }
+          }
+          turns += pair;
+          if (!ok) break;
+          uint32_t take = ((j + lead) & 1) == s && more;
+          if (pair && more) take = warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1);
+          tc_fence_after();
+          if (takes & 1) {   // O (+)= P V
+            const uint32_t v_at = vring_low + vslot * (C::kHalf >> 4);
+            // the first page's weights while the second's are still made
+            if (one) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, kk > 0 ? 1u : add);
+            }
+            __syncwarp();
+            wait(p_at + 8, np & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (one) {
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk)
+                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
+              bar_commit(empty_at + vslot * 8);
+            }
+            add = 1;
+          } else if (pv) {
+            if (weights) wait(p_at + 8, np & 1);
+            if (one) bar_arrive(empty_at + vslot * 8);
+          }
+          np += weights;
+          __syncwarp();
+          if (!pair && more) {
+            wait(full_at + kslot * 8, ck / S & 1);
+            if (!ok) break;
+          }
+          if (pair && one) bar_arrive(pass_at);   // the other stream's waits pass under these products
+          if (take) {   // S = Q K^T
+            const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
+            if (one) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+                tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
+              }
+              bar_commit(s_at);
+              bar_commit(empty_at + kslot * 8);
+            }
+            takes |= 1u << lead;
+          } else if (more && one) {
+            if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
+            bar_arrive(empty_at + kslot * 8);
+          }
+          if (one) {
+            if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
+          }
+          __syncwarp();
+          c = ck + more;
+          steps += more;
+          takes >>= 1;
+        }
+        if (!ok) {
+          give_up();
+          break;
+        }
+        if (add && one) bar_commit(smem_u32(&o_done[0]) + s * 8);   // only then does the softmax wait for it
+      }
+      // every issued product completes before TMEM and shared memory are released
+      if (one) bar_commit(smem_u32(&mma_done));
+      bar_wait(smem_u32(&mma_done), 0, never_at, kWaitTries);
+    }
+  } else if (converts) {
+    // ---------------- codes to fp16 ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConvRegs));
+    // Lanes take 16 bytes of a row each, in an order in which 8 neighbours meet
+    // all 8 bank groups of the swizzled rows that they write.
+    constexpr int NB = C::kAhead, P = C::kPieces, kRowsOf = kStepKeys / P;   // rows of a piece
+    const int ct = tid - kConvWarp0 * 32, cw = ct >> 5;
+    const int chunk = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
+    const int row0 = D == 128 ? cw * 4 + (lane >> 3 & 2) + (lane >> 2 & 1) : ct >> 2;
+    const uint32_t rec_full_at = smem_u32(rec_full), rec_empty_at = smem_u32(rec_empty);
+    const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+    const uint32_t ring = smem_u32(smem) + C::kQBytes;
+    // where the two 16-byte units of a thread's codes go, in the first row of its piece
+    const int unit = (chunk & 3) * 2, r7 = row0 & 7;
+    const uint32_t to = (chunk >> 2) * C::kBox + row0 * 128;
+    const uint32_t to0 = to + ((unit ^ r7) << 4), to1 = to + (((unit + 1) ^ r7) << 4);
+    const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
+    const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
+    int issued = 0, c = 0;   // records taken up, halves converted
+    bool ok = true, more = true;
+    uint4 code[NB][P];
+    float ks[NB], vs[NB];
+    int kind[NB], number[NB];
+    auto issue = [&](int u) {   // into place u
+      kind[u] = kEnd;
+      if (!more) return;
+      ok = __all_sync(0xffffffffu, bar_wait(rec_full_at + issued % kRecords * 8, issued / kRecords & 1, progress_at, wait_tries));
+      if (!ok) return;
+      const Record r = s_rec[issued % kRecords];
+      ++issued;
+      kind[u] = r.kind;
+      number[u] = r.number;
+      more = r.kind != kEnd;
+      if (r.kind > kValues) return;
+      const long long head_off = static_cast<long long>(r.head) * q8_block_bytes(D);
+      const uint8_t* const block0 = pool + r.a * page_bytes + head_off;
+      const uint8_t* const block1 = pool + r.b * page_bytes + head_off;
+      const int at = (r.kind == kValues ? q8_values_at(D) : 0) + row0 * D + chunk * 16;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const int row = row0 + p * kRowsOf;
+        const bool second = p * kRowsOf >= kPage;
+        code[u][p] = make_uint4(0, 0, 0, 0);
+        if ((second ? r.b : r.a) >= 0 && row < r.rest)
+          code[u][p] = load_once((second ? block1 : block0) + at + (p * kRowsOf % kPage) * D);
+      }
+      if (r.kind == kKeys) {   // a key each
+        ks[u] = vs[u] = 0.f;
+        if ((ct >= kPage ? r.b : r.a) >= 0 && ct < r.rest) {
+          const float* s = reinterpret_cast<const float*>((ct >= kPage ? block1 : block0) + q8_key_scales_at(D)) + ct % kPage;
+          ks[u] = __ldg(s);
+          vs[u] = __ldg(s + kPage);
+        }
+      }
+    };
+    auto convert = [&](int u, int n) {   // record n from place u
+      if (kind[u] == kQueries) {
+        const Record r = s_rec[n % kRecords];
+        if (r.number > 0) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&q_empty), (r.number - 1) & 1, progress_at, wait_tries));
+        if (!ok) return;
+        bring_queries<D, F16>(a, r, smem_u32(smem), s_qc[r.number & 1], ct);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(smem_u32(&q_full));
+          bar_arrive(rec_empty_at + n % kRecords * 8);
+        }
+        return;
+      }
+      if (lane == 0) bar_arrive(rec_empty_at + n % kRecords * 8);
+      ok = __all_sync(0xffffffffu, bar_wait(empty_at + c % S * 8, (c / S & 1) ^ 1, progress_at, wait_tries));
+      if (!ok) return;
+      const uint32_t slot = ring + c % S * C::kHalf;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const uint4 w = code[u][p];
+        const uint2 h0 = codes_to_f16(w.x), h1 = codes_to_f16(w.y), h2 = codes_to_f16(w.z), h3 = codes_to_f16(w.w);
+        store_shared16(slot + to0 + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
+        store_shared16(slot + to1 + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
+      }
+      if (kind[u] == kKeys) {
+        // A value scale that is no number becomes the score of whoever sees the
+        // key: as a weight's factor it would reach rows that do not.
+        float kx = ks[u] * 0x1p-8f, vx = vs[u];
+        const uint32_t mag = __float_as_uint(vx) & 0x7FFFFFFFu;
+        if (mag >= 0x7F800000u) {
+          kx = __uint_as_float(0x7FC00000u);
+          vx = 0.f;
+        }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, mag >= 0x7F800000u ? 0u : mag);
+        const int s = number[u] % kScaleRing;
+        s_scale[s * 2 * kStepKeys + ct] = kx;
+        s_scale[s * 2 * kStepKeys + kStepKeys + ct] = vx;
+        if (lane == 0) s_vmax[s][cw] = top;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(full_at + c % S * 8);
+      ++c;
+    };
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      if (ok) issue(u);
+      else kind[u] = kEnd;
+    }
+#pragma unroll 1
+    for (int n = 0; ok; n += NB) {
+      bool ended = false;
+#pragma unroll
+      for (int u = 0; u < NB; ++u) {
+        if (!ok || ended) continue;
+        if (kind[u] == kEnd) {
+          ended = true;
+          continue;
+        }
+        convert(u, n + u);
+        if (ok) issue(u);
+      }
+      if (ended) break;
+    }
+    if (!ok) give_up();
+  } else {
+    // ---------------- softmax and output ----------------
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    const int stream = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_tmem = lane_tmem + stream * kStepKeys;
+    const uint32_t o_tmem = lane_tmem + kOCol + stream * D;
+    int ns = 0;         // S tiles taken by this stream
+    int nx = 0;         // alternating tiles ended
+    int outs = 0;       // items with products of this stream
+    int k = 0;
+    int step0 = 0;      // steps of the CTA's items before this one
+    const int prefix_len = b.prefix_len, sinks = b.sinks;
+    const uint32_t scales_at = smem_u32(s_scale);
+    bool ok = true;
+    // waits taken by all 32 lanes together, so the warp-collective TMEM
+    // accesses after them never diverge (also when a wait runs out)
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, progress_at, wait_tries));
+      tc_fence_after();
+    };
+    auto warp_arrive = [&](uint64_t* bar) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    while (true) {
+      const Item& it = items[k & 1];
+      if (it.nj <= 0) break;
+      __syncwarp();
+      if (lane == 0) next_item(b, it, items[++k & 1]);
+      k = __shfl_sync(0xffffffffu, k, 0);
+      const Row row = row_at(b, it.t, it.pair ? stream : 0, r);
+      float mref = -INFINITY, l = 0.f;   // the row's reference maximum (log2 units, less the bias), sum
+      int unit = kNoUnit;                // E: weights and sum are in units of 2^-E
+      float cq = 0.f;                    // of the row's dot products
+      int done = 0;                      // steps of this item that this stream took
+      StepWalk w;
+      w.start(b, it.t, it.j);
+      const int pair = it.pair, nj = it.nj;
+      for (int j = 0; j < nj; ++j, w.next(b, it.t)) {
+        if (!pair && (j & 1) != stream) continue;
+        const uint32_t early = note_early<kStepRing>(s_step, step0 + j);
+        warp_wait(&s_full[stream], ns & 1);
+        if (!ok) break;
+        const int flags = note_of<kStepRing>(s_step, step0 + j, early);
+        if (pair && !(flags >> (2 + stream) & 1)) {   // no row of the stream sees the step
+          __syncwarp();
+          if (lane < 2) mbar_arrive(&p_full[stream][lane]);
+          ++ns;
+          continue;
+        }
+        if (done == 0) cq = s_qc[(k - 1) & 1][(pair ? stream * kRows : 0) + r];
+        // columns [0, c_hi) less those in [c_sink, c_lo) are seen (rows of no
+        // token, which nobody reads, need no mask)
+        const bool dead = row.token < 0;
+        const RowSpan sp = dead || (w.s.seq >= 0 && w.s.seq != row.seq) ? RowSpan{0, -1, 0}
+                           : w.s.seq < 0 ? RowSpan{0, row.hi + prefix_len, 0} : RowSpan{row.lo, row.hi, sinks};
+        const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
+        const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
+        const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
+        if (__all_sync(0xffffffffu, none)) {
+          const uint32_t zero[16] = {};
+#pragma unroll 1
+          for (int c0 = 0; c0 < kStepKeys / 2; c0 += 16) tmem_st_u16(s_tmem + c0, zero);
+          tmem_wait_st();
+          warp_arrive(&p_full[stream][0]);
+          warp_arrive(&p_full[stream][1]);
+        } else {
+          const int gone = flags & 3;
+          const bool masked = gone != 0 || !__all_sync(0xffffffffu, dead || (c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys)));
+          if (gone != 0) report_gone(a.b.status, gone, c_lo, c_hi, c_sink);
+          const int at = (step0 + j) % kScaleRing;
+          const uint32_t key_scales = scales_at + at * 8 * kStepKeys, value_scales = key_scales + 4 * kStepKeys;
+          auto sees = [&](int u) {   // keys of page u
+            const int c0 = u * kPage;
+            return gone >> u & 1 ? 0ull : slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
+          };
+          float sv[32];
+          // scores of 32 keys less the row's factor; -inf where the row does not see the key
+          auto load = [&](int q) {
+            tmem_ld32(s_tmem + q * 32, sv);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 f = load_shared16(key_scales + q * 128 + c * 16);
+              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(f.x, f.y));
+              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(f.z, f.w));
+              sv[4 * c] = x.x, sv[4 * c + 1] = x.y, sv[4 * c + 2] = y.x, sv[4 * c + 3] = y.y;
+            }
+            if (masked) {
+              const uint32_t vis = static_cast<uint32_t>(sees(q >> 1) >> (q & 1) * 32);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) sv[c] = vis >> c & 1 ? sv[c] : -INFINITY;
+            }
+          };
+          // 2^E above the value scales that the row sees (below 2^(exponent - 126))
+          uint32_t top;
+          if (!masked) {
+            const uint4 vm = *reinterpret_cast<const uint4*>(s_vmax[at]);
+            top = max(max(vm.x, vm.y), max(vm.z, vm.w));
+          } else {
+            top = seen_scale(value_scales, sees(0), sees(1));
+          }
+          const int need = masked && none ? kNoUnit : max(static_cast<int>(top >> 23) - 126, kLeastE);
+          float mx = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            load(q);
+            mx = fmaxf(mx, row_max(sv));
+          }
+          mx = fmaf(mx, cq, -kBias);
+          // each row by itself, so that it does not depend on its neighbours
+          const bool grows = need > unit || mx > mref + kRescaleLog2;
+          if (__any_sync(0xffffffffu, grows)) {
+            const float nm = grows ? fmaxf(mref, mx) : mref;
+            const int nu = need > unit ? need + 1 : unit;
+            const float alpha = !grows || nm == -INFINITY ? 1.f : ex2(mref - nm + static_cast<float>(unit - nu));
+            l *= alpha;
+            mref = nm;
+            unit = nu;
+            if (done > 0) {
+              // O holds the stream's products so far: they were issued before
+              // the product whose scores these are, and end in that order
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                float o[16];
+                uint32_t bits[16];
+                tmem_ld16(o_tmem + c0, o);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) bits[c] = __float_as_uint(o[c] * alpha);
+                tmem_st_u16(o_tmem + c0, bits);
+              }
+              tmem_wait_st();
+            }
+          }
+          const float neg = mref == -INFINITY ? 0.f : -mref - static_cast<float>(unit);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {   // P replaces scores that have been read
+            load(q);
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float2 e = fma2(make_float2(sv[2 * c], sv[2 * c + 1]), make_float2(cq, cq), make_float2(neg, neg));
+              sv[2 * c] = ex2_here(e.x);
+              sv[2 * c + 1] = ex2_here(e.y);
+            }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float4 f = load_shared16(value_scales + q * 128 + c * 16);
+              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(f.x, f.y));
+              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(f.z, f.w));
+              pk[2 * c] = pack2<true>(x.x, x.y);
+              pk[2 * c + 1] = pack2<true>(y.x, y.y);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) sum[c & 1] = add2(sum[c & 1], make_float2(sv[2 * c], sv[2 * c + 1]));
+            tmem_st_u16(s_tmem + q * 16, pk);
+            if (q & 1) {
+              tmem_wait_st();
+              warp_arrive(&p_full[stream][q >> 1]);
+            }
+          }
+          l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        }
+        ++done;
+        ++ns;
+        if (!ok) break;
+      }
+      if (!ok) break;
+      step0 += it.nj;
+      if (done > 0) warp_wait(&o_done[stream], outs++ & 1);
+      if (!ok) break;
+
+      // what others join is the maximum in the unit's terms
+      ok = finish_item<D, F16, NoRedo>(a, b, it, join, stream, tmem, row.token, mref + static_cast<float>(unit), l, done > 0, nx & 1,
+                                       progress_at);
+      nx += !it.pair;
+      if (!ok) break;
+    }
+    if (!ok) give_up();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool F16>
+cudaError_t launch(const PagedAttnArgs& a, int device, int ctas, cudaStream_t s) {
+  // the shared-memory limit is set once per device (setting it again changes nothing)
+  static std::atomic<uint64_t> set{0};
+  if (device > 63 || !(set.load(std::memory_order_acquire) >> device & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(paged_attn_q8_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (device < 64) set.fetch_or(uint64_t(1) << device, std::memory_order_release);
+  }
+  return launch_pdl(paged_attn_q8_kernel<D, F16>, dim3(ctas), dim3(kThreads), Cfg<D>::kSmem, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn_q8(const PagedAttnArgs& a, int head_dim, bool f16, int, int ctas, cudaStream_t s) {
-  const long long blocks = (static_cast<long long>(a.b.n_tokens) * a.b.n_heads + kRowWarps - 1) / kRowWarps;
-  cudaError_t e = launch_pdl(no_pieces_kernel, dim3(ctas), dim3(1), 0, s, a);
-  if (e != cudaSuccess) return e;
-  auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kRowWarps * 32), 0, s, a); };
-  if (head_dim == 128) return f16 ? go(paged_rows_q8_kernel<128, true>) : go(paged_rows_q8_kernel<128, false>);
-  return f16 ? go(paged_rows_q8_kernel<64, true>) : go(paged_rows_q8_kernel<64, false>);
+cudaError_t launch_paged_attn_q8(const PagedAttnArgs& a, int head_dim, bool f16, int device, int ctas, cudaStream_t s) {
+  if (head_dim == 128) return f16 ? launch<128, true>(a, device, ctas, s) : launch<128, false>(a, device, ctas, s);
+  return f16 ? launch<64, true>(a, device, ctas, s) : launch<64, false>(a, device, ctas, s);
 }
 
 }  // namespace dfl
