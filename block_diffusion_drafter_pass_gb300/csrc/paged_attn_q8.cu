@@ -28,66 +28,63 @@
 #include <algorithm>
 #include <atomic>
 
-#define DFL_WALK_CALL __forceinline__
 #include "paged_walk.cuh"
 
 namespace dfl {
 namespace {
 
 constexpr int kConvWarp0 = 8, kConvWarps = 4;   // the softmax's are 0..7: TMEM lanes go by warp % 4
-constexpr int kWalkWarp = 12, kMmaWarp0 = 13;   // warp 15 has no work
-constexpr int kThreads = 512;
-// Registers of a thread, by warpgroup: the launch's 128 x 512 (the kernel's
-// bounds make it that many) are dealt anew.
-constexpr int kLaunchRegs = 128, kSoftRegs = 120, kConvRegs = 200, kRestRegs = 72;
-static_assert(2 * kSoftRegs + kConvRegs + kRestRegs <= 4 * kLaunchRegs, "setmaxnreg waits for registers that the launch must have");
-static_assert(kSoftRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs && kConvRegs >= kLaunchRegs, "dec must go down and inc up");
-constexpr int kConvThreads = kConvWarps * 32;
-constexpr int kRecords = 16;     // halves that the walk may be ahead
-// Halves in the ring, and the records before them, bound how far the walk is
-// ahead of the products: 8 + 4 steps and the lead.
-constexpr int kStepRing = 32;
-constexpr int kScaleRing = 8;    // steps whose scales are held: the ring's 4 and the lead
-constexpr int kIdsAhead = 2, kIdRing = 32;
+constexpr int kWalkWarp = 12, kMmaWarp0 = 13;
+constexpr int kThreads = 15 * 32;
+// The walk is ahead of the products by the halves of both rings and the lead: 7
+// steps at most, of which the scales of those behind the first ring are held.
+constexpr int kStepRing = 16;
+constexpr int kScaleRing = 8;
+constexpr int kIdsAhead = 2, kIdRing = 16;
 constexpr float kBias = 7.f;
 constexpr int kLeastE = -80, kNoUnit = -(1 << 20);
 
 enum : int { kKeys = 0, kValues = 1, kQueries = 2, kEnd = 3 };
 
-// A half of a step, or an item's queries.
+// What a place of the raw ring holds: a half of a step, or notice of an item's queries.
 struct Record {
   int kind, head;
   int number;   // of the step; queries: of the item
   int rest;     // keys of the step that exist (may be above 128, or below 0); queries: whether each stream has rows of its own
-  int a, b;     // pages (-1: none); queries: first token, tokens
+  int a, b;     // bit u: page u is missing; queries: first token, tokens
+  int next;     // place of the next record
+  int unused;
 };
 
 template <int D>
 struct Cfg {
   static constexpr int kBox = kRows * 128;                  // 128 rows of 64 elements, swizzled
-  static constexpr int kHalf = (D / 64) * kBox;             // a step's keys, or its values
-  static constexpr int kSlots = D == 128 ? 4 : 8;
-  static constexpr int kQBytes = 2 * kHalf;                 // queries of both streams
-  static constexpr int kIntOff = kQBytes + kSlots * kHalf;
+  static constexpr int kHalf = (D / 64) * kBox;             // a step's keys, or its values, or a stream's queries
+  static constexpr int kSlots = D == 128 ? 3 : 6;           // halves as fp16
+  // Raw halves: codes [128][d], and behind keys per page its key and value
+  // scales. The last two places lie where the second stream's queries go, so
+  // only tiles without those use them.
+  static constexpr int kRawCodes = kStepKeys * D;
+  static constexpr int kRaw = kRawCodes + 1024;
+  static constexpr int kRawSlots = D == 128 ? 4 : 6, kRawPair = kRawSlots - 2;
+  static constexpr int kQ1Off = kHalf;
+  static constexpr int kRawOff = kQ1Off + 2 * kRaw;         // of place 0; the last two before it
+  static constexpr int kRingOff = kRawOff + kRawPair * kRaw;
+  static constexpr int kIntOff = kRingOff + kSlots * kHalf;
   static constexpr int kScaleOff = kIntOff + kBatchBytes;   // [kScaleRing][2][128] fp32
   static constexpr int kSmem = kScaleOff + kScaleRing * 2 * kStepKeys * 4 + 1024;
-  static_assert(kSmem <= 227 * 1024 - 7168, "static shared variables need the rest");
+  static_assert(2 * kRaw >= kHalf && kRaw % 1024 == 0, "queries over raw places, halves in whole swizzle atoms");
+  static_assert(kSmem <= 226 * 1024 - 5120, "static shared variables need the rest");
   static constexpr int kPieces = D / 16;                    // 16 bytes of a half for each converting thread
-  static constexpr int kAhead = D == 128 ? 4 : 6;           // halves under way in registers
+  static __device__ __forceinline__ int raw_at(int place) {
+    return place < kRawPair ? kRawOff + place * kRaw : kQ1Off + (place - kRawPair) * kRaw;
+  }
 };
 
 __device__ __forceinline__ float2 mul2(float2 x, float2 y) {
   unsigned long long r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
   return floats2(r);
-}
-
-__device__ __forceinline__ uint4 load_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
 }
 
 __device__ __forceinline__ void store_shared16(uint32_t at, uint4 v) {
@@ -98,6 +95,18 @@ __device__ __forceinline__ float4 load_shared16(uint32_t at) {   // in place: re
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
   return v;
+}
+
+__device__ __forceinline__ uint4 load_shared_codes(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {   // bulk_load
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 // Four codes (bytes, + 128) as fp16: behind the byte 0x64 a byte is 1024 + itself.
@@ -119,8 +128,8 @@ __device__ __forceinline__ uint32_t vdesc_low(uint32_t saddr) {
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
 template <int D, bool F16>
-__device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Record& r, uint32_t q_at, float* s_qc, int ct) {
-  constexpr int kOf = D / 8, kPass = kConvThreads / kOf, kAtOnce = 4;
+__device__ __noinline__ void bring_queries(const PagedAttnArgs& a, const Record& r, uint32_t q_at, float* s_qc, int ct) {
+  constexpr int kOf = D / 8, kPass = kConvWarps * 32 / kOf, kAtOnce = 4;
   const int c = ct % kOf, G = a.b.group, stream_rows = a.stream_tokens * G;
   const int n = (r.rest ? 2 : 1) * stream_rows, end = r.a + r.b;
 #pragma unroll 1
@@ -157,7 +166,7 @@ __device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Reco
       for (int k = 0; k < 4; ++k) (&h.x)[k] = pack2<true>(x[2 * k] * f0 * f1, x[2 * k + 1] * f0 * f1);
       if (i < n) {
         const int stream = i >= stream_rows, row = i - stream * stream_rows;
-        store_shared16(q_at + stream * Cfg<D>::kHalf + (c >> 3) * Cfg<D>::kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4), h);
+        store_shared16(q_at + stream * Cfg<D>::kQ1Off + (c >> 3) * Cfg<D>::kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4), h);
         // key scales are held 2^-8 down, so that no product with a dot product (below 2^14) overflows
         if (c == 0) s_qc[stream * kRows + row] = fminf(a.scale_log2 * pow2_of(-(up >> 1)) * pow2_of(-(up - (up >> 1))) * 256.f, 0x1.fffffep127f);
       }
@@ -166,7 +175,7 @@ __device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Reco
 }
 
 // The largest magnitude (bits) among a step's value scales whose keys the row sees.
-__device__ __forceinline__ uint32_t seen_scale(uint32_t value_scales, unsigned long long vis0, unsigned long long vis1) {
+__device__ __noinline__ uint32_t seen_scale(uint32_t value_scales, unsigned long long vis0, unsigned long long vis1) {
   uint32_t top = 0;
 #pragma unroll 1
   for (int c = 0; c < 2 * kPage; c += 4) {
@@ -194,15 +203,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
   float* const s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
-  __shared__ __align__(16) Record s_rec[kRecords];
+  __shared__ __align__(16) Record s_rec[C::kRawSlots];
   __shared__ __align__(16) uint32_t s_vmax[kScaleRing][4];   // largest value scale (bits) of 32 keys
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
-  __shared__ __align__(8) uint64_t rec_full[kRecords], rec_empty[kRecords];
+  __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], conv_meet;
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
   __shared__ Join join;
-  __shared__ int s_page[kIdRing][2];
+  __shared__ int s_page[kIdRing][2], s_rest[kIdRing];
   __shared__ uint32_t s_step[kStepRing];
   __shared__ long long s_sum[kThreads / 32];
   __shared__ Item s_first[2];   // the CTA's first item (and where its run begins)
@@ -213,10 +222,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int s = 0; s < kRecords; ++s) {
-      mbar_init(&rec_full[s], 1);
-      mbar_init(&rec_empty[s], kConvWarps);
+    for (int s = 0; s < C::kRawSlots; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], kConvWarps);
     }
+    mbar_init(&conv_meet, kConvWarps);
     for (int s = 0; s < S; ++s) {
       mbar_init(&kv_full[s], kConvWarps);
       mbar_init(&kv_empty[s], 2);   // both streams
@@ -249,9 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  const bool converts = warp >= kConvWarp0 && warp < kWalkWarp, idle = warp > kMmaWarp0 + 1;
-  Item* const items = s_items[warp < kConvWarp0 ? warp : converts || idle ? 0 : warp - kWalkWarp + kConvWarp0];   // written by lane 0
-  if (!converts && !idle && lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
+  const bool converts = warp >= kConvWarp0 && warp < kWalkWarp;
+  Item* const items = s_items[warp < kConvWarp0 ? warp : converts ? 0 : warp - kWalkWarp + kConvWarp0];   // written by lane 0
+  if (!converts && lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
   __syncwarp();
   const uint32_t progress_at = smem_u32(&s_progress), never_at = smem_u32(&s_never);
   const uint32_t wait_tries = a.wait_tries;
@@ -265,39 +275,55 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   // a pair (both streams take every step) and 2 for an alternating tile
   // (stream s takes the steps of parity s).
 
-  if (warp >= kWalkWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
-    if (warp == kWalkWarp && lane == 0) {
-      // ---------------- the walk over keys and values ----------------
-      const uint32_t full_at = smem_u32(rec_full), empty_at = smem_u32(rec_empty);
-      int n = 0, steps = 0;   // records, steps whose keys are written down
+  if (warp == kWalkWarp) {
+    // ---------------- the walk over keys and values, and their copies ----------------
+    if (lane == 0) {
+      const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
+      const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
+      const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
+      int at = 0, steps = 0;      // place in the raw ring, steps whose keys were brought
+      uint32_t used = 0, sent = 0;   // by place: parity of its records, copies to wait for at the end
       bool ok = true;
-      auto record = [&](int kind, int head, int number, int rest, int x, int y) {
-        ok = bar_wait(empty_at + n % kRecords * 8, (n / kRecords & 1) ^ 1, progress_at, wait_tries);
-        if (!ok) return;
-        s_rec[n % kRecords] = Record{kind, head, number, rest, x, y};
-        bar_arrive(full_at + n % kRecords * 8);
-        ++n;
-      };
       int4 split = make_int4(0, 0, 0, 0);
       int piece = 0;
 #pragma unroll 1
       for (int before = items[0].nj > 0 ? items[0].j : 0; before > 0; before -= run) ++piece;
-      int k = 0;
+      int k = 0, places = C::kRawSlots;   // places in use: the pair's, or all
+      // Waits for the record's place; what arrives on it ends the record.
+      auto take = [&]() {
+        ok = bar_wait(empty_at + at * 8, (used >> at & 1) ^ 1, progress_at, wait_tries);
+        return ok;
+      };
+      auto pass = [&](const Record& r, int n_places) {
+        s_rec[at] = r;
+        s_rec[at].next = at + 1 < n_places ? at + 1 : 0;
+      };
+      auto step_on = [&](int n_places) {
+        used ^= 1u << at;
+        at = at + 1 < n_places ? at + 1 : 0;
+      };
+#pragma unroll 1
       for (; items[k & 1].nj > 0; ++k) {
         const Item& it = items[k & 1];
         next_item(b, it, items[(k + 1) & 1]);
         const int lead = it.pair ? 1 : 2, nj = it.nj;
-        record(kQueries, it.head, k, it.pair, it.t.t0, it.t.ntok);
+        const int was = places;
+        places = it.pair ? C::kRawPair : C::kRawSlots;
+        if (!take()) break;
+        // behind a pair's queries: their place is free when its last scores are
+        if (places > was) ok = bar_wait(smem_u32(&q_empty), (k - 1) & 1, progress_at, wait_tries);
+        if (!ok) break;
+        pass(Record{kQueries, it.head, k, it.pair, it.t.t0, it.t.ntok, 0, 0}, places);
+        bar_arrive(full_at + at * 8);
+        step_on(places);
         // Page ids are copied kIdsAhead steps before their keys are due, so no
         // load waits for one.
-        StepWalk wf, wk, wv;   // of the ids, of the keys, of the values
+        StepWalk wf, wk;   // of the ids, of the keys
         wf.start(b, it.t, it.j);
         wk = wf;
-        wv = wf;
         const int step0 = steps;
 #pragma unroll 1
-        for (int i = -2 * (lead + kIdsAhead); i < 2 * nj && ok; ++i) {   // round i >> 1: values, then ids and keys
+        for (int i = -2 * (lead + kIdsAhead); i < 2 * nj; ++i) {   // round i >> 1: values, then ids and keys
           const bool keys = i & 1;
           const int j = (i >> 1) + (keys ? lead : 0);
           if (keys) {
@@ -317,24 +343,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             copy_async_wait<kIdsAhead>();
           }
           if (j < 0 || j >= nj) continue;
-          int page[2], gone = 0;
+          if (!take()) break;
+          int rest;   // of the step: kept for its values
+          if (keys) rest = s_rest[(step0 + j) % kIdRing] = wk.s.end - wk.s.base;
+          else rest = s_rest[(step0 + j) % kIdRing];
+          int gone = 0;
+          uint32_t bytes[2];
+          const uint8_t* src[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            page[u] = s_page[(step0 + j) % kIdRing][u];
-            if (page[u] >= 0 && page[u] < a.b.n_pages) continue;
-            page[u] = -1;
-            gone |= 1 << u;
+            const int page = s_page[(step0 + j) % kIdRing][u];
+            const bool there = page >= 0 && page < a.b.n_pages;
+            gone |= there ? 0 : 1 << u;
+            src[u] = pool + page * page_bytes + static_cast<long long>(it.head) * q8_block_bytes(D);
+            bytes[u] = there ? min(max(rest - u * kPage, 0), kPage) * D : 0;   // rows that are keys
           }
-          StepWalk& w = keys ? wk : wv;
-          const int rest = w.s.end - w.s.base;
           if (keys) {
             int flags = gone;
-            if (it.pair) flags |= pair_takes(b, it.t, w.s.seq, w.s.base) << 2;
+            if (it.pair) flags |= pair_takes(b, it.t, wk.s.seq, wk.s.base) << 2;
+            wk.next(b, it.t);
             const uint32_t note = step_note(steps, flags);
             *const_cast<volatile uint32_t*>(s_step + steps++ % kStepRing) = note;
           }
-          w.next(b, it.t);
-          record(keys ? kKeys : kValues, it.head, step0 + j, rest, page[0], page[1]);
+          pass(Record{keys ? kKeys : kValues, it.head, step0 + j, rest, gone, 0, 0, 0}, places);
+          const uint32_t bar = full_at + at * 8, dst = base_at + C::raw_at(at);
+          const uint32_t scales = keys ? (bytes[0] ? 512 : 0) + (bytes[1] ? 512 : 0) : 0;
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes[0] + bytes[1] + scales) : "memory");
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (bytes[u] == 0) continue;
+            bulk_copy(dst + u * kPage * D, src[u] + (keys ? 0 : q8_values_at(D)), bytes[u], bar);
+            if (keys) bulk_copy(dst + C::kRawCodes + u * 512, src[u] + q8_key_scales_at(D), 512, bar);
+          }
+          sent |= 1u << at;
+          step_on(places);
         }
         if (!ok) break;
         if (it.j == 0 && nj < it.t.n) {   // the run ends here: the rest is the next CTAs'
@@ -344,264 +386,229 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           split = make_int4(it.t.t0, it.t.ntok, it.head, pieces);
         }
       }
-      if (ok) record(kEnd, 0, 0, 0, 0, 0);
+      if (ok && take()) {
+        pass(Record{kEnd, 0, 0, 0, 0, 0, 0, 0}, places);
+        bar_arrive(full_at + at * 8);
+        used ^= 1u << at;
+      }
       if (!ok) give_up();
       a.split[blockIdx.x] = split;
       a.piece[blockIdx.x] = piece;
+      // copies still in flight complete before shared memory is released
       copy_async_wait<0>();
-    }
-    if (warp >= kMmaWarp0 && !idle) {
-      // ---------------- products of one stream ----------------
-      // As in paged_attn.cu: the warp goes through this as one, with one elected
-      // lane in front of the instructions.
-      const int s = warp_uniform(warp - kMmaWarp0);
-      const bool one = elect_one();
-      const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kQBytes >> 4);
-      const uint32_t vring_low = vdesc_low<D>(smem_u32(smem)) + (C::kQBytes >> 4);
-      const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
-      const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0][0]) + s * 16;
-      const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
-      const uint32_t tm = warp_uniform(tmem);
-      const uint32_t s_col = tm + s * kStepKeys, o_col = tm + kOCol + s * D;
-      int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
-      bool ok = true;
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
-      };
-      while (true) {
-        const Item& it = items[k & 1];
-        const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
-        if (nj <= 0) break;
-        __syncwarp();
-        const uint32_t q_at = q_low + (pair ? s * (C::kHalf >> 4) : 0);
-        wait(smem_u32(&q_full), k & 1);
-        ++k;
-        uint32_t add = 0;
-        uint32_t takes = 0;   // bit i: the stream takes step j + i
 #pragma unroll 1
-        for (int j = -lead; j < nj && ok; ++j) {
-          const int pv = j >= 0, more = j + lead < nj;
-          if (j == nj - lead) {   // the scores are all issued
-            if (lane == 0) next_item(b, it, items[k & 1]);
-            __syncwarp();
-          }
-          const int ck = c + pv, vslot = c % S, kslot = ck % S;
-          // One lane for each thing to wait for, so that the waits are one. Of a
-          // pair that is everything but the second page's weights, and its streams
-          // take turns; an alternating tile's values go back as soon as they can.
-          const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
-          uint32_t early = 0;
-          {
-            if (pair && more) early = note_early<kStepRing>(s_step, steps);
-            bool need = lane == 0 && pv;
-            uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
-            if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
-            if (lane == 2) need = weights, bar = p_at, parity = np & 1;
-            if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
-            int polls = kWaitPolls, seen = 0;
-            while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
-              const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
-              if (progress != seen) polls = kWaitPolls;
-              seen = progress;
-              if (progress < 0 || --polls == 0) {
-                ok = false;
-                break;
-              }
-            }
-          }
-          turns += pair;
-          if (!ok) break;
-          uint32_t take = ((j + lead) & 1) == s && more;
-          if (pair && more) take = warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1);
-          tc_fence_after();
-          if (takes & 1) {   // O (+)= P V
-            const uint32_t v_at = vring_low + vslot * (C::kHalf >> 4);
-            // the first page's weights while the second's are still made
-            if (one) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, kk > 0 ? 1u : add);
-            }
-            __syncwarp();
-            wait(p_at + 8, np & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (one) {
-#pragma unroll
-              for (int kk = 4; kk < 8; ++kk)
-                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
-              bar_commit(empty_at + vslot * 8);
-            }
-            add = 1;
-          } else if (pv) {
-            if (weights) wait(p_at + 8, np & 1);
-            if (one) bar_arrive(empty_at + vslot * 8);
-          }
-          np += weights;
-          __syncwarp();
-          if (!pair && more) {
-            wait(full_at + kslot * 8, ck / S & 1);
-            if (!ok) break;
-          }
-          if (pair && one) bar_arrive(pass_at);   // the other stream's waits pass under these products
-          if (take) {   // S = Q K^T
-            const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
-            if (one) {
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
-                tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
-              }
-              bar_commit(s_at);
-              bar_commit(empty_at + kslot * 8);
-            }
-            takes |= 1u << lead;
-          } else if (more && one) {
-            if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
-            bar_arrive(empty_at + kslot * 8);
-          }
-          if (one) {
-            if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
-          }
-          __syncwarp();
-          c = ck + more;
-          steps += more;
-          takes >>= 1;
-        }
-        if (!ok) {
-          give_up();
-          break;
-        }
-        if (add && one) bar_commit(smem_u32(&o_done[0]) + s * 8);   // only then does the softmax wait for it
-      }
-      // every issued product completes before TMEM and shared memory are released
-      if (one) bar_commit(smem_u32(&mma_done));
-      bar_wait(smem_u32(&mma_done), 0, never_at, kWaitTries);
+      for (int p = 0; p < C::kRawSlots; ++p)
+        if (sent >> p & 1) bar_wait(full_at + p * 8, (used >> p & 1) ^ 1, never_at, kWaitTries);
     }
+  } else if (warp >= kMmaWarp0) {
+    // ---------------- products of one stream ----------------
+    // As in paged_attn.cu: the warp goes through this as one, with one elected
+    // lane in front of the instructions.
+    const int s = warp_uniform(warp - kMmaWarp0);
+    const bool one = elect_one();
+    const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kRingOff >> 4);
+    const uint32_t vring_low = vdesc_low<D>(smem_u32(smem)) + (C::kRingOff >> 4);
+    const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+    const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0][0]) + s * 16;
+    const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
+    const uint32_t tm = warp_uniform(tmem);
+    const uint32_t s_col = tm + s * kStepKeys, o_col = tm + kOCol + s * D;
+    int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
+    };
+    while (true) {
+      const Item& it = items[k & 1];
+      const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
+      if (nj <= 0) break;
+      __syncwarp();
+      const uint32_t q_at = q_low + (pair ? s * (C::kQ1Off >> 4) : 0);
+      wait(smem_u32(&q_full), k & 1);
+      ++k;
+      uint32_t add = 0;
+      uint32_t takes = 0;   // bit i: the stream takes step j + i
+#pragma unroll 1
+      for (int j = -lead; j < nj && ok; ++j) {
+        const int pv = j >= 0, more = j + lead < nj;
+        if (j == nj - lead) {   // the scores are all issued
+          if (lane == 0) next_item(b, it, items[k & 1]);
+          __syncwarp();
+        }
+        const int ck = c + pv, vslot = c % S, kslot = ck % S;
+        // One lane for each thing to wait for, so that the waits are one. Of a
+        // pair that is everything but the second page's weights, and its streams
+        // take turns; an alternating tile's values go back as soon as they can.
+        const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
+        uint32_t early = 0;
+        {
+          if (pair && more) early = note_early<kStepRing>(s_step, steps);
+          bool need = lane == 0 && pv;
+          uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
+          if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
+          if (lane == 2) need = weights, bar = p_at, parity = np & 1;
+          if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
+          int polls = kWaitPolls, seen = 0;
+          while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
+            const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
+            if (progress != seen) polls = kWaitPolls;
+            seen = progress;
+            if (progress < 0 || --polls == 0) {
+              ok = false;
+              break;
+            }
+          }
+        }
+        turns += pair;
+        if (!ok) break;
+        uint32_t take = ((j + lead) & 1) == s && more;
+        if (pair && more) take = warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1);
+        tc_fence_after();
+        if (takes & 1) {   // O (+)= P V
+          const uint32_t v_at = vring_low + vslot * (C::kHalf >> 4);
+          // the first page's weights while the second's are still made
+          if (one) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, kk > 0 ? 1u : add);
+          }
+          __syncwarp();
+          wait(p_at + 8, np & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (one) {
+#pragma unroll
+            for (int kk = 4; kk < 8; ++kk)
+              tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
+            bar_commit(empty_at + vslot * 8);
+          }
+          add = 1;
+        } else if (pv) {
+          if (weights) wait(p_at + 8, np & 1);
+          if (one) bar_arrive(empty_at + vslot * 8);
+        }
+        np += weights;
+        __syncwarp();
+        if (!pair && more) {
+          wait(full_at + kslot * 8, ck / S & 1);
+          if (!ok) break;
+        }
+        if (pair && one) bar_arrive(pass_at);   // the other stream's waits pass under these products
+        if (take) {   // S = Q K^T
+          const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
+          if (one) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+              tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
+            }
+            bar_commit(s_at);
+            bar_commit(empty_at + kslot * 8);
+          }
+          takes |= 1u << lead;
+        } else if (more && one) {
+          if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
+          bar_arrive(empty_at + kslot * 8);
+        }
+        if (one) {
+          if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
+        }
+        __syncwarp();
+        c = ck + more;
+        steps += more;
+        takes >>= 1;
+      }
+      if (!ok) {
+        give_up();
+        break;
+      }
+      if (add && one) bar_commit(smem_u32(&o_done[0]) + s * 8);   // only then does the softmax wait for it
+    }
+    // every issued product completes before TMEM and shared memory are released
+    if (one) bar_commit(smem_u32(&mma_done));
+    bar_wait(smem_u32(&mma_done), 0, never_at, kWaitTries);
   } else if (converts) {
     // ---------------- codes to fp16 ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConvRegs));
-    // Lanes take 16 bytes of a row each, in an order in which 8 neighbours meet
-    // all 8 bank groups of the swizzled rows that they write.
-    constexpr int NB = C::kAhead, P = C::kPieces, kRowsOf = kStepKeys / P;   // rows of a piece
+    // A lane takes 16 bytes of a row at a time, in an order in which 8
+    // neighbours meet all 8 bank groups both of the rows that they read and of
+    // the swizzled rows that they write.
+    constexpr int P = C::kPieces, kRowsOf = kStepKeys / P;   // rows of a piece
     const int ct = tid - kConvWarp0 * 32, cw = ct >> 5;
-    const int chunk = D == 128 ? (lane & 3) | (lane >> 1 & 4) : lane & 3;
-    const int row0 = D == 128 ? cw * 4 + (lane >> 3 & 2) + (lane >> 2 & 1) : ct >> 2;
-    const uint32_t rec_full_at = smem_u32(rec_full), rec_empty_at = smem_u32(rec_empty);
-    const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
-    const uint32_t ring = smem_u32(smem) + C::kQBytes;
-    // where the two 16-byte units of a thread's codes go, in the first row of its piece
-    const int unit = (chunk & 3) * 2, r7 = row0 & 7;
-    const uint32_t to = (chunk >> 2) * C::kBox + row0 * 128;
-    const uint32_t to0 = to + ((unit ^ r7) << 4), to1 = to + (((unit + 1) ^ r7) << 4);
-    const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
-    const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
-    int issued = 0, c = 0;   // records taken up, halves converted
-    bool ok = true, more = true;
-    uint4 code[NB][P];
-    float ks[NB], vs[NB];
-    int kind[NB], number[NB];
-    auto issue = [&](int u) {   // into place u
-      kind[u] = kEnd;
-      if (!more) return;
-      ok = __all_sync(0xffffffffu, bar_wait(rec_full_at + issued % kRecords * 8, issued / kRecords & 1, progress_at, wait_tries));
-      if (!ok) return;
-      const Record r = s_rec[issued % kRecords];
-      ++issued;
-      kind[u] = r.kind;
-      number[u] = r.number;
-      more = r.kind != kEnd;
-      if (r.kind > kValues) return;
-      const long long head_off = static_cast<long long>(r.head) * q8_block_bytes(D);
-      const uint8_t* const block0 = pool + r.a * page_bytes + head_off;
-      const uint8_t* const block1 = pool + r.b * page_bytes + head_off;
-      const int at = (r.kind == kValues ? q8_values_at(D) : 0) + row0 * D + chunk * 16;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const int row = row0 + p * kRowsOf;
-        const bool second = p * kRowsOf >= kPage;
-        code[u][p] = make_uint4(0, 0, 0, 0);
-        if ((second ? r.b : r.a) >= 0 && row < r.rest)
-          code[u][p] = load_once((second ? block1 : block0) + at + (p * kRowsOf % kPage) * D);
-      }
-      if (r.kind == kKeys) {   // a key each
-        ks[u] = vs[u] = 0.f;
-        if ((ct >= kPage ? r.b : r.a) >= 0 && ct < r.rest) {
-          const float* s = reinterpret_cast<const float*>((ct >= kPage ? block1 : block0) + q8_key_scales_at(D)) + ct % kPage;
-          ks[u] = __ldg(s);
-          vs[u] = __ldg(s + kPage);
-        }
-      }
+    const int box = D == 128 ? lane >> 2 & 1 : 0, chunk = lane & 3;
+    const int row0 = D == 128 ? cw * 4 + (lane >> 4) * 2 + (box ^ (lane >> 3 & 1)) : ct >> 2;
+    const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
+    const uint32_t from = row0 * D + box * 64 + chunk * 16;
+    const uint32_t to = box * C::kBox + row0 * 128 + ((chunk * 2 ^ (row0 & 7)) << 4);   // its neighbour: ^ 16
+    int at = 0, c = 0, met = 0;   // place in the raw ring, halves converted, meetings
+    uint32_t used = 0;            // by place: parity of its records
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
     };
-    auto convert = [&](int u, int n) {   // record n from place u
-      if (kind[u] == kQueries) {
-        const Record r = s_rec[n % kRecords];
-        if (r.number > 0) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&q_empty), (r.number - 1) & 1, progress_at, wait_tries));
-        if (!ok) return;
-        bring_queries<D, F16>(a, r, smem_u32(smem), s_qc[r.number & 1], ct);
+#pragma unroll 1
+    while (true) {
+      wait(full_at + at * 8, used >> at & 1);
+      if (!ok) break;
+      used ^= 1u << at;
+      const Record r = s_rec[at];
+      if (r.kind == kEnd) break;
+      if (r.kind == kQueries) {
+        if (r.number > 0) wait(smem_u32(&q_empty), (r.number - 1) & 1);
+        // the second stream's lie over raw places that the other warps may still read
+        if (lane == 0) bar_arrive(smem_u32(&conv_meet));
+        wait(smem_u32(&conv_meet), met++ & 1);
+        if (!ok) break;
+        bring_queries<D, F16>(a, r, base_at, s_qc[r.number & 1], ct);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           bar_arrive(smem_u32(&q_full));
-          bar_arrive(rec_empty_at + n % kRecords * 8);
+          bar_arrive(empty_at + at * 8);
         }
-        return;
+        at = r.next;
+        continue;
       }
-      if (lane == 0) bar_arrive(rec_empty_at + n % kRecords * 8);
-      ok = __all_sync(0xffffffffu, bar_wait(empty_at + c % S * 8, (c / S & 1) ^ 1, progress_at, wait_tries));
-      if (!ok) return;
-      const uint32_t slot = ring + c % S * C::kHalf;
-#pragma unroll
+      wait(smem_u32(kv_empty) + c % S * 8, (c / S & 1) ^ 1);
+      if (!ok) break;
+      const uint32_t src = base_at + C::raw_at(at) + from, dst = base_at + C::kRingOff + c % S * C::kHalf + to;
+#pragma unroll 2
       for (int p = 0; p < P; ++p) {
-        const uint4 w = code[u][p];
+        const uint4 w = load_shared_codes(src + p * kRowsOf * D);
         const uint2 h0 = codes_to_f16(w.x), h1 = codes_to_f16(w.y), h2 = codes_to_f16(w.z), h3 = codes_to_f16(w.w);
-        store_shared16(slot + to0 + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
-        store_shared16(slot + to1 + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
+        store_shared16(dst + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
+        store_shared16((dst ^ 16) + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
       }
-      if (kind[u] == kKeys) {
+      if (r.kind == kKeys) {   // a key each
+        const int u = ct / kPage;
+        const float* scales = reinterpret_cast<const float*>(smem + C::raw_at(at) + C::kRawCodes + u * 512) + ct % kPage;
+        const bool there = ct < r.rest && !(r.a >> u & 1);
         // A value scale that is no number becomes the score of whoever sees the
         // key: as a weight's factor it would reach rows that do not.
-        float kx = ks[u] * 0x1p-8f, vx = vs[u];
-        const uint32_t mag = __float_as_uint(vx) & 0x7FFFFFFFu;
+        float kx = there ? scales[0] * 0x1p-8f : 0.f, vx = there ? scales[kPage] : 0.f;
+        uint32_t mag = __float_as_uint(vx) & 0x7FFFFFFFu;
         if (mag >= 0x7F800000u) {
           kx = __uint_as_float(0x7FC00000u);
           vx = 0.f;
+          mag = 0;
         }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, mag >= 0x7F800000u ? 0u : mag);
-        const int s = number[u] % kScaleRing;
+        mag = __reduce_max_sync(0xffffffffu, mag);
+        const int s = r.number % kScaleRing;
         s_scale[s * 2 * kStepKeys + ct] = kx;
         s_scale[s * 2 * kStepKeys + kStepKeys + ct] = vx;
-        if (lane == 0) s_vmax[s][cw] = top;
+        if (lane == 0) s_vmax[s][cw] = mag;
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) bar_arrive(full_at + c % S * 8);
-      ++c;
-    };
-#pragma unroll
-    for (int u = 0; u < NB; ++u) {
-      if (ok) issue(u);
-      else kind[u] = kEnd;
-    }
-#pragma unroll 1
-    for (int n = 0; ok; n += NB) {
-      bool ended = false;
-#pragma unroll
-      for (int u = 0; u < NB; ++u) {
-        if (!ok || ended) continue;
-        if (kind[u] == kEnd) {
-          ended = true;
-          continue;
-        }
-        convert(u, n + u);
-        if (ok) issue(u);
+      if (lane == 0) {
+        bar_arrive(empty_at + at * 8);
+        bar_arrive(smem_u32(kv_full) + c % S * 8);
       }
-      if (ended) break;
+      ++c;
+      at = r.next;
     }
     if (!ok) give_up();
   } else {
     // ---------------- softmax and output ----------------
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     const int stream = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t s_tmem = lane_tmem + stream * kStepKeys;
@@ -659,6 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
                            : w.s.seq < 0 ? RowSpan{0, row.hi + prefix_len, 0} : RowSpan{row.lo, row.hi, sinks};
         const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
         const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
+        if (__all_sync(0xffffffffu, dead)) {
+          if (lane < 2) mbar_arrive(&p_full[stream][lane]);
+          ++done;
+          ++ns;
+          continue;
+        }
         const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
         if (__all_sync(0xffffffffu, none)) {
           const uint32_t zero[16] = {};
