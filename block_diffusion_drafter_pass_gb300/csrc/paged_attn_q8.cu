@@ -36,11 +36,11 @@ namespace {
 constexpr int kConvWarp0 = 8, kConvWarps = 4;   // the softmax's are 0..7: TMEM lanes go by warp % 4
 constexpr int kWalkWarp = 12, kMmaWarp0 = 13;
 constexpr int kThreads = 15 * 32;
-// The walk is ahead of the products by the halves of both rings and the lead: 7
-// steps at most, of which the scales of those behind the first ring are held.
-constexpr int kStepRing = 16;
+constexpr int kAhead = 16;       // steps that the walk looks up at a time
+// The walk is ahead of the products by these and the halves of both rings (8
+// steps at most); scales are held of what is behind the first ring.
+constexpr int kStepRing = 32;
 constexpr int kScaleRing = 8;
-constexpr int kIdsAhead = 2, kIdRing = 16;
 constexpr float kBias = 7.f;
 constexpr int kLeastE = -80, kNoUnit = -(1 << 20);
 
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
   __shared__ Join join;
-  __shared__ int s_page[kIdRing][2], s_rest[kIdRing];
+  __shared__ __align__(16) int4 s_steps[kStepRing];
   __shared__ uint32_t s_step[kStepRing];
   __shared__ long long s_sum[kThreads / 32];
   __shared__ Item s_first[2];   // the CTA's first item (and where its run begins)
@@ -277,129 +277,128 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
 
   if (warp == kWalkWarp) {
     // ---------------- the walk over keys and values, and their copies ----------------
-    if (lane == 0) {
-      const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
-      const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
-      const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
-      int at = 0, steps = 0;      // place in the raw ring, steps whose keys were brought
-      uint32_t used = 0, sent = 0;   // by place: parity of its records, copies to wait for at the end
-      bool ok = true;
-      int4 split = make_int4(0, 0, 0, 0);
-      int piece = 0;
+    // The whole warp: a lane looks up a step (kAhead steps at a time, the next
+    // while these are brought), and a half's copies go out from a lane each. One
+    // lane for all of it took 3000 cycles a step, 2.1 times what memory does.
+    const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
+    const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
+    const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
+    int at = 0, steps = 0, k = 0;      // place in the raw ring, steps of the items before this one, items
+    int places = C::kRawSlots;         // places in use: the pair's, or all
+    uint32_t used = 0, sent = 0;       // by place: parity of its records, whether there are copies to wait for at the end
+    bool ok = true;
+    int4 split = make_int4(0, 0, 0, 0), found = make_int4(-1, -1, 0, 0);   // found: pages, keys, note bits of the lane's step
+    int piece = 0;
 #pragma unroll 1
-      for (int before = items[0].nj > 0 ? items[0].j : 0; before > 0; before -= run) ++piece;
-      int k = 0, places = C::kRawSlots;   // places in use: the pair's, or all
-      // Waits for the record's place; what arrives on it ends the record.
-      auto take = [&]() {
-        ok = bar_wait(empty_at + at * 8, (used >> at & 1) ^ 1, progress_at, wait_tries);
-        return ok;
-      };
-      auto pass = [&](const Record& r, int n_places) {
-        s_rec[at] = r;
-        s_rec[at].next = at + 1 < n_places ? at + 1 : 0;
-      };
-      auto step_on = [&](int n_places) {
-        used ^= 1u << at;
-        at = at + 1 < n_places ? at + 1 : 0;
-      };
+    for (int before = items[0].nj > 0 ? items[0].j : 0; before > 0; before -= run) ++piece;
+    auto look_up = [&](const Item& it, int j) {   // of step j + lane of the item
+      j += lane;
+      if (lane >= kAhead || j >= it.nj) return;
+      StepWalk w;
+      w.start(b, it.t, it.j + j);
+      const int32_t* table = table_of(a, w.s.seq) + w.s.base / kPage;
+      found.x = w.s.base < w.s.end ? table[0] : -1;
+      found.y = w.s.base + kPage < w.s.end ? table[1] : -1;
+      found.z = w.s.end - w.s.base;
+      found.w = it.pair ? pair_takes(b, it.t, w.s.seq, w.s.base) << 2 : 0;
+    };
+    auto take = [&]() {   // the record's place
+      ok = __all_sync(0xffffffffu, bar_wait(empty_at + at * 8, (used >> at & 1) ^ 1, progress_at, wait_tries));
+      return ok;
+    };
+    auto pass = [&](const Record& r) {   // lane 0
+      s_rec[at] = r;
+      s_rec[at].next = at + 1 < places ? at + 1 : 0;
+    };
+    auto go_on = [&]() {
+      used ^= 1u << at;
+      at = at + 1 < places ? at + 1 : 0;
+    };
+    if (items[0].nj > 0) look_up(items[0], 0);
 #pragma unroll 1
-      for (; items[k & 1].nj > 0; ++k) {
-        const Item& it = items[k & 1];
-        next_item(b, it, items[(k + 1) & 1]);
-        const int lead = it.pair ? 1 : 2, nj = it.nj;
-        const int was = places;
-        places = it.pair ? C::kRawPair : C::kRawSlots;
+    while (true) {
+      const Item& it = items[k & 1];
+      const Item& after = items[(k + 1) & 1];
+      const int nj = it.nj, pair = it.pair, head = it.head, lead = pair ? 1 : 2;
+      if (nj <= 0) break;
+      __syncwarp();
+      if (lane == 0) next_item(b, it, items[(k + 1) & 1]);
+      __syncwarp();
+      const int was = places;
+      places = pair ? C::kRawPair : C::kRawSlots;
+      if (!take()) break;
+      // behind a pair's queries: their place is free when its last scores are
+      if (places > was) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&q_empty), (k - 1) & 1, progress_at, wait_tries));
+      if (!ok) break;
+      if (lane == 0) {
+        pass(Record{kQueries, head, k, pair, it.t.t0, it.t.ntok, 0, 0});
+        bar_arrive(full_at + at * 8);
+      }
+      go_on();
+#pragma unroll 1
+      for (int i = 1 - 2 * lead; i < 2 * nj; ++i) {   // round i >> 1: values, then keys
+        const bool keys = i & 1;
+        const int j = (i >> 1) + (keys ? lead : 0);
+        if (j < 0 || j >= nj) continue;
+        if (keys && j % kAhead == 0) {
+          int4 f = found;
+          if (lane < kAhead && j + lane < nj) {
+            if (f.x < 0 || f.x >= a.b.n_pages) f.x = -1, f.w |= 1;
+            if (f.y < 0 || f.y >= a.b.n_pages) f.y = -1, f.w |= 2;
+            s_steps[(steps + j + lane) % kStepRing] = f;
+            s_step[(steps + j + lane) % kStepRing] = step_note(steps + j + lane, f.w);
+          }
+          if (j + kAhead < nj) look_up(it, j + kAhead);
+          else if (after.nj > 0) look_up(after, 0);
+          __syncwarp();
+        }
         if (!take()) break;
-        // behind a pair's queries: their place is free when its last scores are
-        if (places > was) ok = bar_wait(smem_u32(&q_empty), (k - 1) & 1, progress_at, wait_tries);
-        if (!ok) break;
-        pass(Record{kQueries, it.head, k, it.pair, it.t.t0, it.t.ntok, 0, 0}, places);
-        bar_arrive(full_at + at * 8);
-        step_on(places);
-        // Page ids are copied kIdsAhead steps before their keys are due, so no
-        // load waits for one.
-        StepWalk wf, wk;   // of the ids, of the keys
-        wf.start(b, it.t, it.j);
-        wk = wf;
-        const int step0 = steps;
-#pragma unroll 1
-        for (int i = -2 * (lead + kIdsAhead); i < 2 * nj; ++i) {   // round i >> 1: values, then ids and keys
-          const bool keys = i & 1;
-          const int j = (i >> 1) + (keys ? lead : 0);
-          if (keys) {
-            const int jf = j + kIdsAhead;
-            if (jf < nj) {
-              const int32_t* table = table_of(a, wf.s.seq);
-              int* dst = s_page[(step0 + jf) % kIdRing];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int key0 = wf.s.base + u * kPage;
-                if (key0 < wf.s.end) copy_async4(dst + u, table + key0 / kPage);
-                else dst[u] = -1;
-              }
-              wf.next(b, it.t);
-            }
-            copy_async_commit();
-            copy_async_wait<kIdsAhead>();
-          }
-          if (j < 0 || j >= nj) continue;
-          if (!take()) break;
-          int rest;   // of the step: kept for its values
-          if (keys) rest = s_rest[(step0 + j) % kIdRing] = wk.s.end - wk.s.base;
-          else rest = s_rest[(step0 + j) % kIdRing];
-          int gone = 0;
-          uint32_t bytes[2];
-          const uint8_t* src[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int page = s_page[(step0 + j) % kIdRing][u];
-            const bool there = page >= 0 && page < a.b.n_pages;
-            gone |= there ? 0 : 1 << u;
-            src[u] = pool + page * page_bytes + static_cast<long long>(it.head) * q8_block_bytes(D);
-            bytes[u] = there ? min(max(rest - u * kPage, 0), kPage) * D : 0;   // rows that are keys
-          }
-          if (keys) {
-            int flags = gone;
-            if (it.pair) flags |= pair_takes(b, it.t, wk.s.seq, wk.s.base) << 2;
-            wk.next(b, it.t);
-            const uint32_t note = step_note(steps, flags);
-            *const_cast<volatile uint32_t*>(s_step + steps++ % kStepRing) = note;
-          }
-          pass(Record{keys ? kKeys : kValues, it.head, step0 + j, rest, gone, 0, 0, 0}, places);
-          const uint32_t bar = full_at + at * 8, dst = base_at + C::raw_at(at);
-          const uint32_t scales = keys ? (bytes[0] ? 512 : 0) + (bytes[1] ? 512 : 0) : 0;
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes[0] + bytes[1] + scales) : "memory");
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (bytes[u] == 0) continue;
-            bulk_copy(dst + u * kPage * D, src[u] + (keys ? 0 : q8_values_at(D)), bytes[u], bar);
-            if (keys) bulk_copy(dst + C::kRawCodes + u * 512, src[u] + q8_key_scales_at(D), 512, bar);
-          }
-          sent |= 1u << at;
-          step_on(places);
+        const int4 f = s_steps[(steps + j) % kStepRing];
+        // lanes 0, 1: the codes of a page's keys that exist; 2, 3: the scales of both kinds
+        const int rows0 = f.x < 0 ? 0 : min(max(f.z, 0), kPage), rows1 = f.y < 0 ? 0 : min(max(f.z - kPage, 0), kPage);
+        const int u = lane & 1, rows = u ? rows1 : rows0;
+        const uint32_t bytes = rows == 0 ? 0 : lane < 2 ? rows * D : keys ? 512 : 0;
+        const uint32_t bar = full_at + at * 8;
+        if (lane == 0) {
+          pass(Record{keys ? kKeys : kValues, head, steps + j, f.z, f.w & 3, 0, 0, 0});
+          const uint32_t all = (rows0 + rows1) * D + (keys ? (rows0 ? 512 : 0) + (rows1 ? 512 : 0) : 0);
+          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(all) : "memory");
         }
-        if (!ok) break;
-        if (it.j == 0 && nj < it.t.n) {   // the run ends here: the rest is the next CTAs'
-          int pieces = 1;
-#pragma unroll 1
-          for (int left = it.t.n - nj; left > 0; left -= run) ++pieces;
-          split = make_int4(it.t.t0, it.t.ntok, it.head, pieces);
+        __syncwarp();
+        if (lane < 4 && bytes > 0) {
+          const uint8_t* block = pool + (u ? f.y : f.x) * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
+          const uint32_t to = base_at + C::raw_at(at) + (lane < 2 ? u * kPage * D : C::kRawCodes + u * 512);
+          bulk_copy(to, block + (lane >= 2 ? q8_key_scales_at(D) : keys ? 0 : q8_values_at(D)), bytes, bar);
         }
+        sent |= 1u << at;
+        go_on();
       }
-      if (ok && take()) {
-        pass(Record{kEnd, 0, 0, 0, 0, 0, 0, 0}, places);
+      if (!ok) break;
+      steps += nj;
+      if (it.j == 0 && nj < it.t.n) {   // the run ends here: the rest is the next CTAs'
+        int pieces = 1;
+#pragma unroll 1
+        for (int left = it.t.n - nj; left > 0; left -= run) ++pieces;
+        split = make_int4(it.t.t0, it.t.ntok, it.head, pieces);
+      }
+      ++k;
+    }
+    if (ok && take()) {
+      if (lane == 0) {
+        pass(Record{kEnd, 0, 0, 0, 0, 0, 0, 0});
         bar_arrive(full_at + at * 8);
-        used ^= 1u << at;
       }
-      if (!ok) give_up();
+      used ^= 1u << at;
+    }
+    if (!ok) give_up();
+    if (lane == 0) {
       a.split[blockIdx.x] = split;
       a.piece[blockIdx.x] = piece;
-      // copies still in flight complete before shared memory is released
-      copy_async_wait<0>();
-#pragma unroll 1
-      for (int p = 0; p < C::kRawSlots; ++p)
-        if (sent >> p & 1) bar_wait(full_at + p * 8, (used >> p & 1) ^ 1, never_at, kWaitTries);
     }
+    // copies still in flight complete before shared memory is released
+#pragma unroll 1
+    for (int p = 0; p < C::kRawSlots; ++p)
+      if (sent >> p & 1) bar_wait(full_at + p * 8, (used >> p & 1) ^ 1, never_at, kWaitTries);
   } else if (warp >= kMmaWarp0) {
     // ---------------- products of one stream ----------------
     // As in paged_attn.cu: the warp goes through this as one, with one elected
