@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
   float* const s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
   __shared__ __align__(16) Record s_rec[C::kRawSlots];
-  __shared__ __align__(16) uint32_t s_vmax[kScaleRing][4];   // largest value scale (bits) of 32 keys
+  __shared__ __align__(16) uint32_t s_vmax[kScaleRing][4], s_kmax[kScaleRing][4];   // largest value and key scale (bits) of 32 keys
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
   __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], conv_meet;
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
@@ -567,12 +567,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         at = r.next;
         continue;
       }
+      // all loads first: while the products read shared memory each takes 300 cycles
+      const uint32_t src = base_at + C::raw_at(at) + from;
+      uint4 code[P];
+#pragma unroll
+      for (int p = 0; p < P; ++p) code[p] = load_shared_codes(src + p * kRowsOf * D);
       wait(smem_u32(kv_empty) + c % S * 8, (c / S & 1) ^ 1);
       if (!ok) break;
-      const uint32_t src = base_at + C::raw_at(at) + from, dst = base_at + C::kRingOff + c % S * C::kHalf + to;
-#pragma unroll 2
+      const uint32_t dst = base_at + C::kRingOff + c % S * C::kHalf + to;
+#pragma unroll
       for (int p = 0; p < P; ++p) {
-        const uint4 w = load_shared_codes(src + p * kRowsOf * D);
+        const uint4 w = code[p];
         const uint2 h0 = codes_to_f16(w.x), h1 = codes_to_f16(w.y), h2 = codes_to_f16(w.z), h3 = codes_to_f16(w.w);
         store_shared16(dst + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
         store_shared16((dst ^ 16) + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
@@ -591,10 +596,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           mag = 0;
         }
         mag = __reduce_max_sync(0xffffffffu, mag);
+        // a key scale below zero would turn a largest dot product into a least score: no bound then
+        const uint32_t most = __reduce_max_sync(0xffffffffu, kx < 0.f ? 0x7F800000u : kx == kx ? __float_as_uint(kx) : 0u);
         const int s = r.number % kScaleRing;
         s_scale[s * 2 * kStepKeys + ct] = kx;
         s_scale[s * 2 * kStepKeys + kStepKeys + ct] = vx;
-        if (lane == 0) s_vmax[s][cw] = mag;
+        if (lane == 0) {
+          s_vmax[s][cw] = mag;
+          s_kmax[s][cw] = most;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -692,12 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           float sv[32];
           // scores of 32 keys less the row's factor; -inf where the row does not see the key
           auto load = [&](int q) {
+            float4 f[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) f[c] = load_shared16(key_scales + q * 128 + c * 16);
             tmem_ld32(s_tmem + q * 32, sv);
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float4 f = load_shared16(key_scales + q * 128 + c * 16);
-              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(f.x, f.y));
-              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(f.z, f.w));
+              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(f[c].x, f[c].y));
+              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(f[c].z, f[c].w));
               sv[4 * c] = x.x, sv[4 * c + 1] = x.y, sv[4 * c + 2] = y.x, sv[4 * c + 3] = y.y;
             }
             if (masked) {
@@ -715,15 +727,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             top = seen_scale(value_scales, sees(0), sees(1));
           }
           const int need = masked && none ? kNoUnit : max(static_cast<int>(top >> 23) - 126, kLeastE);
+          // The row's largest score: while dot products, each 32 with the largest of
+          // their scales, stay below what the reference allows, nothing more is
+          // needed; else the scores themselves.
           float mx = -INFINITY;
+          bool bound = !masked;
+          if (bound) {
+            const uint4 km = *reinterpret_cast<const uint4*>(s_kmax[at]);
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            load(q);
-            mx = fmaxf(mx, row_max(sv));
+            for (int q = 0; q < 4; ++q) {
+              tmem_ld32(s_tmem + q * 32, sv);
+              mx = fmaxf(mx, fmaxf(row_max(sv), 0.f) * __uint_as_float(q & 2 ? (q & 1 ? km.w : km.z) : q & 1 ? km.y : km.x));
+            }
+            mx = fmaf(mx, cq, -kBias);
+            bound = !__any_sync(0xffffffffu, need > unit || !(mx <= mref + kRescaleLog2));
           }
-          mx = fmaf(mx, cq, -kBias);
+          if (!bound) {
+            mx = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              load(q);
+              mx = fmaxf(mx, row_max(sv));
+            }
+            mx = fmaf(mx, cq, -kBias);
+          }
           // each row by itself, so that it does not depend on its neighbours
-          const bool grows = need > unit || mx > mref + kRescaleLog2;
+          const bool grows = !bound && (need > unit || mx > mref + kRescaleLog2);
           if (__any_sync(0xffffffffu, grows)) {
             const float nm = grows ? fmaxf(mref, mx) : mref;
             const int nu = need > unit ? need + 1 : unit;
@@ -751,6 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {   // P replaces scores that have been read
             load(q);
+            float4 g[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) g[c] = load_shared16(value_scales + q * 128 + c * 16);
             uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
@@ -760,9 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             }
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              const float4 f = load_shared16(value_scales + q * 128 + c * 16);
-              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(f.x, f.y));
-              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(f.z, f.w));
+              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(g[c].x, g[c].y));
+              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(g[c].z, g[c].w));
               pk[2 * c] = pack2<true>(x.x, x.y);
               pk[2 * c + 1] = pack2<true>(y.x, y.y);
             }
