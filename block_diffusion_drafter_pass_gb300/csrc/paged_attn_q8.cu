@@ -44,16 +44,10 @@ constexpr int kScaleRing = 8;
 constexpr float kBias = 7.f;
 constexpr int kLeastE = -80, kNoUnit = -(1 << 20);
 
-enum : int { kKeys = 0, kValues = 1, kQueries = 2, kEnd = 3 };
-
-// What a place of the raw ring holds: a half of a step, or notice of an item's queries.
-struct Record {
-  int kind, head;
-  int number;   // of the step; queries: of the item
-  int rest;     // keys of the step that exist (may be above 128, or below 0); queries: whether each stream has rows of its own
-  int a, b;     // bit u: page u is missing; queries: first token, tokens
-  int next;     // place of the next record
-  int unused;
+// Notice of an item's queries; nj = 0: the run's end.
+struct Notice {
+  int nj, pair, head, t0, ntok;
+  int unused[3];
 };
 
 template <int D>
@@ -75,7 +69,7 @@ struct Cfg {
   static constexpr int kSmem = kScaleOff + kScaleRing * 2 * kStepKeys * 4 + 1024;
   static_assert(2 * kRaw >= kHalf && kRaw % 1024 == 0, "queries over raw places, halves in whole swizzle atoms");
   static_assert(kSmem <= 226 * 1024 - 5120, "static shared variables need the rest");
-  static constexpr int kPieces = D / 16;                    // 16 bytes of a half for each converting thread
+  static constexpr int kPieces = D / 8;                     // 16 bytes of a half for each converting thread
   static __device__ __forceinline__ int raw_at(int place) {
     return place < kRawPair ? kRawOff + place * kRaw : kQ1Off + (place - kRawPair) * kRaw;
   }
@@ -128,16 +122,16 @@ __device__ __forceinline__ uint32_t vdesc_low(uint32_t saddr) {
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
 template <int D, bool F16>
-__device__ __noinline__ void bring_queries(const PagedAttnArgs& a, const Record& r, uint32_t q_at, float* s_qc, int ct) {
+__device__ __noinline__ void bring_queries(const PagedAttnArgs& a, const Notice& r, uint32_t q_at, float* s_qc, int ct) {
   constexpr int kOf = D / 8, kPass = kConvWarps * 32 / kOf, kAtOnce = 4;
   const int c = ct % kOf, G = a.b.group, stream_rows = a.stream_tokens * G;
-  const int n = (r.rest ? 2 : 1) * stream_rows, end = r.a + r.b;
+  const int n = (r.pair ? 2 : 1) * stream_rows, end = r.t0 + r.ntok;
 #pragma unroll 1
   for (int base = 0; base < n; base += kPass * kAtOnce) {
     uint4 w[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      const int i = base + u * kPass + ct / kOf, token = r.a + i / G;   // a stream's tokens follow the other's
+      const int i = base + u * kPass + ct / kOf, token = r.t0 + i / G;   // a stream's tokens follow the other's
       w[u] = make_uint4(0, 0, 0, 0);
       if (i < n && token < end)
         w[u] = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + static_cast<long long>(r.head * G + i % G) * D) + c);
@@ -203,10 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
   float* const s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
-  __shared__ __align__(16) Record s_rec[C::kRawSlots];
+  __shared__ __align__(16) Notice s_notice[2];
   __shared__ __align__(16) uint32_t s_vmax[kScaleRing][4], s_kmax[kScaleRing][4];   // largest value and key scale (bits) of 32 keys
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
-  __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], conv_meet;
+  __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], note_full[2], note_empty[2], conv_meet;
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
@@ -224,11 +218,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   if (tid == 0) {
     for (int s = 0; s < C::kRawSlots; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], kConvWarps);
+      mbar_init(&raw_empty[s], kConvWarps / 2);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&note_full[s], 1);
+      mbar_init(&note_empty[s], kConvWarps);
     }
     mbar_init(&conv_meet, kConvWarps);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&kv_full[s], kConvWarps);
+      mbar_init(&kv_full[s], kConvWarps / 2);
       mbar_init(&kv_empty[s], 2);   // both streams
     }
     mbar_init(&q_full, kConvWarps);
@@ -302,13 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       found.z = w.s.end - w.s.base;
       found.w = it.pair ? pair_takes(b, it.t, w.s.seq, w.s.base) << 2 : 0;
     };
-    auto take = [&]() {   // the record's place
-      ok = __all_sync(0xffffffffu, bar_wait(empty_at + at * 8, (used >> at & 1) ^ 1, progress_at, wait_tries));
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
       return ok;
     };
-    auto pass = [&](const Record& r) {   // lane 0
-      s_rec[at] = r;
-      s_rec[at].next = at + 1 < places ? at + 1 : 0;
+    auto notice = [&](const Notice& n) {
+      if (!wait(smem_u32(note_empty) + (k & 1) * 8, (k >> 1 & 1) ^ 1)) return false;
+      if (lane == 0) {
+        s_notice[k & 1] = n;
+        bar_arrive(smem_u32(note_full) + (k & 1) * 8);
+      }
+      return true;
     };
     auto go_on = [&]() {
       used ^= 1u << at;
@@ -326,15 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       __syncwarp();
       const int was = places;
       places = pair ? C::kRawPair : C::kRawSlots;
-      if (!take()) break;
       // behind a pair's queries: their place is free when its last scores are
-      if (places > was) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&q_empty), (k - 1) & 1, progress_at, wait_tries));
-      if (!ok) break;
-      if (lane == 0) {
-        pass(Record{kQueries, head, k, pair, it.t.t0, it.t.ntok, 0, 0});
-        bar_arrive(full_at + at * 8);
-      }
-      go_on();
+      if (places > was) wait(smem_u32(&q_empty), (k - 1) & 1);
+      if (at >= places) at = 0;
+      if (!ok || !notice(Notice{nj, pair, head, it.t.t0, it.t.ntok, {}})) break;
 #pragma unroll 1
       for (int i = 1 - 2 * lead; i < 2 * nj; ++i) {   // round i >> 1: values, then keys
         const bool keys = i & 1;
@@ -352,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           else if (after.nj > 0) look_up(after, 0);
           __syncwarp();
         }
-        if (!take()) break;
+        if (!wait(empty_at + at * 8, (used >> at & 1) ^ 1)) break;
         const int4 f = s_steps[(steps + j) % kStepRing];
         // lanes 0, 1: the codes of a page's keys that exist; 2, 3: the scales of both kinds
         const int rows0 = f.x < 0 ? 0 : min(max(f.z, 0), kPage), rows1 = f.y < 0 ? 0 : min(max(f.z - kPage, 0), kPage);
@@ -360,7 +357,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         const uint32_t bytes = rows == 0 ? 0 : lane < 2 ? rows * D : keys ? 512 : 0;
         const uint32_t bar = full_at + at * 8;
         if (lane == 0) {
-          pass(Record{keys ? kKeys : kValues, head, steps + j, f.z, f.w & 3, 0, 0, 0});
           const uint32_t all = (rows0 + rows1) * D + (keys ? (rows0 ? 512 : 0) + (rows1 ? 512 : 0) : 0);
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(all) : "memory");
         }
@@ -383,13 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       }
       ++k;
     }
-    if (ok && take()) {
-      if (lane == 0) {
-        pass(Record{kEnd, 0, 0, 0, 0, 0, 0, 0});
-        bar_arrive(full_at + at * 8);
-      }
-      used ^= 1u << at;
-    }
+    if (ok) notice(Notice{});
     if (!ok) give_up();
     if (lane == 0) {
       a.split[blockIdx.x] = split;
@@ -528,92 +518,106 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
     bar_wait(smem_u32(&mma_done), 0, never_at, kWaitTries);
   } else if (converts) {
     // ---------------- codes to fp16 ----------------
-    // A lane takes 16 bytes of a row at a time, in an order in which 8
-    // neighbours meet all 8 bank groups both of the rows that they read and of
-    // the swizzled rows that they write.
+    // Two teams of two warps take every other half, so that one's waits pass
+    // under the other's work. A lane takes 16 bytes of a row at a time, in an
+    // order in which 8 neighbours meet all 8 bank groups both of the rows that
+    // they read and of the swizzled rows that they write.
     constexpr int P = C::kPieces, kRowsOf = kStepKeys / P;   // rows of a piece
-    const int ct = tid - kConvWarp0 * 32, cw = ct >> 5;
+    const int ct = tid - kConvWarp0 * 32, team = ct >> 6, tt = ct & 63;
     const int box = D == 128 ? lane >> 2 & 1 : 0, chunk = lane & 3;
-    const int row0 = D == 128 ? cw * 4 + (lane >> 4) * 2 + (box ^ (lane >> 3 & 1)) : ct >> 2;
+    const int row0 = D == 128 ? (tt >> 5) * 4 + (lane >> 4) * 2 + (box ^ (lane >> 3 & 1)) : tt >> 2;
     const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
     const uint32_t from = row0 * D + box * 64 + chunk * 16;
     const uint32_t to = box * C::kBox + row0 * 128 + ((chunk * 2 ^ (row0 & 7)) << 4);   // its neighbour: ^ 16
-    int at = 0, c = 0, met = 0;   // place in the raw ring, halves converted, meetings
-    uint32_t used = 0;            // by place: parity of its records
+    int at = 0, c = 0, steps = 0;   // place in the raw ring, halves, steps of the items before this one
+    uint32_t used = 0;              // by place: parity of its halves
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
       if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
+      return ok;
     };
 #pragma unroll 1
-    while (true) {
-      wait(full_at + at * 8, used >> at & 1);
-      if (!ok) break;
-      used ^= 1u << at;
-      const Record r = s_rec[at];
-      if (r.kind == kEnd) break;
-      if (r.kind == kQueries) {
-        if (r.number > 0) wait(smem_u32(&q_empty), (r.number - 1) & 1);
-        // the second stream's lie over raw places that the other warps may still read
-        if (lane == 0) bar_arrive(smem_u32(&conv_meet));
-        wait(smem_u32(&conv_meet), met++ & 1);
-        if (!ok) break;
-        bring_queries<D, F16>(a, r, base_at, s_qc[r.number & 1], ct);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          bar_arrive(smem_u32(&q_full));
-          bar_arrive(empty_at + at * 8);
-        }
-        at = r.next;
-        continue;
-      }
-      // all loads first: while the products read shared memory each takes 300 cycles
-      const uint32_t src = base_at + C::raw_at(at) + from;
-      uint4 code[P];
-#pragma unroll
-      for (int p = 0; p < P; ++p) code[p] = load_shared_codes(src + p * kRowsOf * D);
-      wait(smem_u32(kv_empty) + c % S * 8, (c / S & 1) ^ 1);
-      if (!ok) break;
-      const uint32_t dst = base_at + C::kRingOff + c % S * C::kHalf + to;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const uint4 w = code[p];
-        const uint2 h0 = codes_to_f16(w.x), h1 = codes_to_f16(w.y), h2 = codes_to_f16(w.z), h3 = codes_to_f16(w.w);
-        store_shared16(dst + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
-        store_shared16((dst ^ 16) + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
-      }
-      if (r.kind == kKeys) {   // a key each
-        const int u = ct / kPage;
-        const float* scales = reinterpret_cast<const float*>(smem + C::raw_at(at) + C::kRawCodes + u * 512) + ct % kPage;
-        const bool there = ct < r.rest && !(r.a >> u & 1);
-        // A value scale that is no number becomes the score of whoever sees the
-        // key: as a weight's factor it would reach rows that do not.
-        float kx = there ? scales[0] * 0x1p-8f : 0.f, vx = there ? scales[kPage] : 0.f;
-        uint32_t mag = __float_as_uint(vx) & 0x7FFFFFFFu;
-        if (mag >= 0x7F800000u) {
-          kx = __uint_as_float(0x7FC00000u);
-          vx = 0.f;
-          mag = 0;
-        }
-        mag = __reduce_max_sync(0xffffffffu, mag);
-        // a key scale below zero would turn a largest dot product into a least score: no bound then
-        const uint32_t most = __reduce_max_sync(0xffffffffu, kx < 0.f ? 0x7F800000u : kx == kx ? __float_as_uint(kx) : 0u);
-        const int s = r.number % kScaleRing;
-        s_scale[s * 2 * kStepKeys + ct] = kx;
-        s_scale[s * 2 * kStepKeys + kStepKeys + ct] = vx;
-        if (lane == 0) {
-          s_vmax[s][cw] = mag;
-          s_kmax[s][cw] = most;
-        }
-      }
+    for (int k = 0;; ++k) {
+      if (!wait(smem_u32(note_full) + (k & 1) * 8, k >> 1 & 1)) break;
+      const Notice& n = s_notice[k & 1];
+      const int nj = n.nj, pair = n.pair, lead = pair ? 1 : 2;
+      if (nj == 0) break;
+      const int places = pair ? C::kRawPair : C::kRawSlots;
+      if (at >= places) at = 0;
+      if (k > 0) wait(smem_u32(&q_empty), (k - 1) & 1);
+      // the second stream's queries lie over raw places that the other warps may still read
+      if (lane == 0) bar_arrive(smem_u32(&conv_meet));
+      if (!wait(smem_u32(&conv_meet), k & 1)) break;
+      bring_queries<D, F16>(a, n, base_at, s_qc[k & 1], ct);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        bar_arrive(empty_at + at * 8);
-        bar_arrive(smem_u32(kv_full) + c % S * 8);
+        bar_arrive(smem_u32(&q_full));
+        bar_arrive(smem_u32(note_empty) + (k & 1) * 8);
       }
-      ++c;
-      at = r.next;
+#pragma unroll 1
+      for (int i = 1 - 2 * lead; i < 2 * nj; ++i) {   // as the walk does
+        const bool keys = i & 1;
+        const int j = (i >> 1) + (keys ? lead : 0);
+        if (j < 0 || j >= nj) continue;
+        const int place = at, half = c++, parity = used >> at & 1;
+        used ^= 1u << at;
+        at = at + 1 < places ? at + 1 : 0;
+        if ((half & 1) != team) continue;
+        if (!wait(full_at + place * 8, parity)) break;
+        const uint32_t src = base_at + C::raw_at(place) + from, dst = base_at + C::kRingOff + half % S * C::kHalf + to;
+#pragma unroll 1
+        for (int p0 = 0; p0 < P; p0 += 8) {
+          // all loads first: while the products read shared memory each takes 300 cycles
+          uint4 code[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) code[p] = load_shared_codes(src + (p0 + p) * kRowsOf * D);
+          if (p0 == 0 && !wait(smem_u32(kv_empty) + half % S * 8, (half / S & 1) ^ 1)) break;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const uint4 w = code[p];
+            const uint2 h0 = codes_to_f16(w.x), h1 = codes_to_f16(w.y), h2 = codes_to_f16(w.z), h3 = codes_to_f16(w.w);
+            store_shared16(dst + (p0 + p) * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
+            store_shared16((dst ^ 16) + (p0 + p) * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
+          }
+        }
+        if (!ok) break;
+        if (keys) {   // two keys' scales each
+          const int4 f = s_steps[(steps + j) % kStepRing];
+          const int slot = (steps + j) % kScaleRing;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {   // of page u
+            const float* scales = reinterpret_cast<const float*>(smem + C::raw_at(place) + C::kRawCodes + u * 512) + tt;
+            const bool there = u * kPage + tt < f.z && !(f.w >> u & 1);
+            // A value scale that is no number becomes the score of whoever sees the
+            // key: as a weight's factor it would reach rows that do not.
+            float kx = there ? scales[0] * 0x1p-8f : 0.f, vx = there ? scales[kPage] : 0.f;
+            uint32_t mag = __float_as_uint(vx) & 0x7FFFFFFFu;
+            if (mag >= 0x7F800000u) {
+              kx = __uint_as_float(0x7FC00000u);
+              vx = 0.f;
+              mag = 0;
+            }
+            mag = __reduce_max_sync(0xffffffffu, mag);
+            // a key scale below zero would turn a largest dot product into a least score: no bound then
+            const uint32_t most = __reduce_max_sync(0xffffffffu, kx < 0.f ? 0x7F800000u : kx == kx ? __float_as_uint(kx) : 0u);
+            s_scale[slot * 2 * kStepKeys + u * kPage + tt] = kx;
+            s_scale[slot * 2 * kStepKeys + kStepKeys + u * kPage + tt] = vx;
+            if (lane == 0) {
+              s_vmax[slot][u * 2 + (tt >> 5)] = mag;
+              s_kmax[slot][u * 2 + (tt >> 5)] = most;
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(empty_at + place * 8);
+          bar_arrive(smem_u32(kv_full) + half % S * 8);
+        }
+      }
+      if (!ok) break;
+      steps += nj;
     }
     if (!ok) give_up();
   } else {
