@@ -4,18 +4,21 @@
 //
 // Row q (times the softmax scale), key j with codes c_j and scale a_j, value
 // with codes d_j and scale b_j:
-//     s_j = a_j (q . c_j),   o = sum_j 2^(s_j - m) b_j d_j / sum_j 2^(s_j - m).
-// Codes are whole numbers of 8 bits, exact in fp16, so the products are of fp16
-// whatever the tokens' type: q.c_j with q taken to fp16 behind a power of two
-// that puts the row's largest value between 1/2 and 1 (values below 2^-14 of that
-// are rounded in steps of 2^-24 of it, all others are exact: bf16 has fewer bits),
-// then a_j in fp32 on the score, and b_j in fp32 on the weight, which is
-// then rounded to fp16 as the product's operand (half a step, 2^-12 of it). For
-// that fp16 is given its best place: a row's weights are 2^(s - m - E), m its
-// reference maximum less 7 and 2^E above every value scale so far, so that a
-// weight times its scale stays below 2^15, and 2^-31 of the largest one still
-// counts. Sum and output share the unit 2^-E, so it cancels; E is clamped below
-// at -80, so weights stay finite when all values are tiny.
+//     s_j = q . (a_j c_j),   o = sum_j 2^(s_j - m) b_j d_j / sum_j 2^(s_j - m).
+// The products are of fp16 whatever the tokens' type. Queries are taken to it
+// behind a power of two that puts the row's largest value between 1/2 and 1
+// (values below 2^-13 of that are rounded in steps of 2^-24, all others of bf16
+// are exact). Keys and values are a code times its scale, which is
+// rounded to fp16 behind a power of two 2^(7 - e) that all 128 of a step share (its
+// largest scale comes to lie between 2^7 and 2^8), and the product once more: a
+// step of fp16 in all, an eighth of what rounding them to bf16 would cost. (Scales
+// multiplied onto scores and weights in fp32 instead are exact, but each row
+// then needs all 256 of a step: 364 us instead of @@ for 16 tokens of 32
+// sequences behind 32768.) Weights are rounded to fp16 for the product with the
+// values, in its best place: a row's weights are 2^(s - m - E + e) for a step of
+// value exponent e, m its reference maximum less 7 and E at least every e so far,
+// so that they stay below 2^15 and 2^-31 of the largest contribution still counts.
+// Sum and output share the unit, so it cancels.
 //
 // Per CTA: a warp walks the steps and writes down the pages of each half (128
 // keys, or their values); 4 warps take the halves from global memory
@@ -38,11 +41,11 @@ constexpr int kWalkWarp = 12, kMmaWarp0 = 13;
 constexpr int kThreads = 15 * 32;
 constexpr int kAhead = 16;       // steps that the walk looks up at a time
 // The walk is ahead of the products by these and the halves of both rings (8
-// steps at most); scales are held of what is behind the first ring.
+// steps at most); exponents are held of what is behind the first ring.
 constexpr int kStepRing = 32;
-constexpr int kScaleRing = 8;
+constexpr int kUnitRing = 8;
 constexpr float kBias = 7.f;
-constexpr int kLeastE = -80, kNoUnit = -(1 << 20);
+constexpr int kLeastE = -80, kNoUnit = -(1 << 20);   // smaller scales count as 2^-80
 
 // Notice of an item's queries; nj = 0: the run's end.
 struct Notice {
@@ -55,8 +58,8 @@ struct Cfg {
   static constexpr int kBox = kRows * 128;                  // 128 rows of 64 elements, swizzled
   static constexpr int kHalf = (D / 64) * kBox;             // a step's keys, or its values, or a stream's queries
   static constexpr int kSlots = D == 128 ? 3 : 6;           // halves as fp16
-  // Raw halves: codes [128][d], and behind keys per page its key and value
-  // scales. The last two places lie where the second stream's queries go, so
+  // Raw halves: codes [128][d], and per page its key and value scales (behind
+  // values the latter only). The last two places lie where the second stream's queries go, so
   // only tiles without those use them.
   static constexpr int kRawCodes = kStepKeys * D;
   static constexpr int kRaw = kRawCodes + 1024;
@@ -65,8 +68,7 @@ struct Cfg {
   static constexpr int kRawOff = kQ1Off + 2 * kRaw;         // of place 0; the last two before it
   static constexpr int kRingOff = kRawOff + kRawPair * kRaw;
   static constexpr int kIntOff = kRingOff + kSlots * kHalf;
-  static constexpr int kScaleOff = kIntOff + kBatchBytes;   // [kScaleRing][2][128] fp32
-  static constexpr int kSmem = kScaleOff + kScaleRing * 2 * kStepKeys * 4 + 1024;
+  static constexpr int kSmem = kIntOff + kBatchBytes + 1024;
   static_assert(2 * kRaw >= kHalf && kRaw % 1024 == 0, "queries over raw places, halves in whole swizzle atoms");
   static_assert(kSmem <= 226 * 1024 - 5120, "static shared variables need the rest");
   static constexpr int kPieces = D / 8;                     // 16 bytes of a half for each converting thread
@@ -75,20 +77,8 @@ struct Cfg {
   }
 };
 
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(x)), "l"(bits2(y)));
-  return floats2(r);
-}
-
 __device__ __forceinline__ void store_shared16(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
-__device__ __forceinline__ float4 load_shared16(uint32_t at) {   // in place: read ahead, scales take the scores' registers
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
-  return v;
 }
 
 __device__ __forceinline__ uint4 load_shared_codes(uint32_t at) {
@@ -103,12 +93,25 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// Four codes (bytes, + 128) as fp16: behind the byte 0x64 a byte is 1024 + itself.
-__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
+// Four codes (bytes, + 128) times a scale (twice in a register), as fp16: behind
+// the byte 0x64 a byte is 1024 + itself.
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 scale) {
   const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
   const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-  const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&lo), off), b = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
+  const __half2 a = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&lo), off), scale);
+  const __half2 b = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&hi), off), scale);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// The exponent of the largest finite scale of a step, of which each lane has four.
+__device__ __forceinline__ int step_exponent(const float (&x)[4]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t mag = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+    top = mag < 0x7F800000u ? max(top, mag) : top;
+  }
+  return max(static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 23) - 127, kLeastE);
 }
 
 // Descriptor of values as they lie in the ring, MN-major with 128-byte swizzle:
@@ -161,26 +164,10 @@ __device__ __noinline__ void bring_queries(const PagedAttnArgs& a, const Notice&
       if (i < n) {
         const int stream = i >= stream_rows, row = i - stream * stream_rows;
         store_shared16(q_at + stream * Cfg<D>::kQ1Off + (c >> 3) * Cfg<D>::kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4), h);
-        // key scales are held 2^-8 down, so that no product with a dot product (below 2^14) overflows
-        if (c == 0) s_qc[stream * kRows + row] = fminf(a.scale_log2 * pow2_of(-(up >> 1)) * pow2_of(-(up - (up >> 1))) * 256.f, 0x1.fffffep127f);
+        if (c == 0) s_qc[stream * kRows + row] = a.scale_log2 * pow2_of(-(up >> 1)) * pow2_of(-(up - (up >> 1)));
       }
     }
   }
-}
-
-// The largest magnitude (bits) among a step's value scales whose keys the row sees.
-__device__ __noinline__ uint32_t seen_scale(uint32_t value_scales, unsigned long long vis0, unsigned long long vis1) {
-  uint32_t top = 0;
-#pragma unroll 1
-  for (int c = 0; c < 2 * kPage; c += 4) {
-    const float4 f = load_shared16(value_scales + c * 4);
-    const uint32_t v = static_cast<uint32_t>((c < kPage ? vis0 : vis1) >> (c % kPage));
-    if (v & 1) top = max(top, __float_as_uint(f.x) & 0x7FFFFFFFu);
-    if (v & 2) top = max(top, __float_as_uint(f.y) & 0x7FFFFFFFu);
-    if (v & 4) top = max(top, __float_as_uint(f.z) & 0x7FFFFFFFu);
-    if (v & 8) top = max(top, __float_as_uint(f.w) & 0x7FFFFFFFu);
-  }
-  return top;
 }
 
 struct NoRedo {
@@ -196,9 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
-  float* const s_scale = reinterpret_cast<float*>(smem + C::kScaleOff);
   __shared__ __align__(16) Notice s_notice[2];
-  __shared__ __align__(16) uint32_t s_vmax[kScaleRing][4], s_kmax[kScaleRing][4];   // largest value and key scale (bits) of 32 keys
+  __shared__ __align__(8) int2 s_unit[kUnitRing];   // exponents of a step's key and value scales
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
   __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], note_full[2], note_empty[2], conv_meet;
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
@@ -351,20 +337,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         }
         if (!wait(empty_at + at * 8, (used >> at & 1) ^ 1)) break;
         const int4 f = s_steps[(steps + j) % kStepRing];
-        // lanes 0, 1: the codes of a page's keys that exist; 2, 3: the scales of both kinds
+        // lanes 0, 1: the codes of a page's keys that exist; 2, 3: its scales (keys: of both kinds)
         const int rows0 = f.x < 0 ? 0 : min(max(f.z, 0), kPage), rows1 = f.y < 0 ? 0 : min(max(f.z - kPage, 0), kPage);
         const int u = lane & 1, rows = u ? rows1 : rows0;
-        const uint32_t bytes = rows == 0 ? 0 : lane < 2 ? rows * D : keys ? 512 : 0;
+        const uint32_t scales = keys ? 512 : 256, bytes = rows == 0 ? 0 : lane < 2 ? rows * D : scales;
         const uint32_t bar = full_at + at * 8;
         if (lane == 0) {
-          const uint32_t all = (rows0 + rows1) * D + (keys ? (rows0 ? 512 : 0) + (rows1 ? 512 : 0) : 0);
+          const uint32_t all = (rows0 + rows1) * D + (rows0 ? scales : 0) + (rows1 ? scales : 0);
           asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(all) : "memory");
         }
         __syncwarp();
         if (lane < 4 && bytes > 0) {
           const uint8_t* block = pool + (u ? f.y : f.x) * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
-          const uint32_t to = base_at + C::raw_at(at) + (lane < 2 ? u * kPage * D : C::kRawCodes + u * 512);
-          bulk_copy(to, block + (lane >= 2 ? q8_key_scales_at(D) : keys ? 0 : q8_values_at(D)), bytes, bar);
+          const uint32_t to = base_at + C::raw_at(at) + (lane < 2 ? u * kPage * D : C::kRawCodes + u * 512 + 512 - scales);
+          bulk_copy(to, block + (lane >= 2 ? q8_key_scales_at(D) + 512 - scales : keys ? 0 : q8_values_at(D)), bytes, bar);
         }
         sent |= 1u << at;
         go_on();
@@ -566,48 +552,47 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         if ((half & 1) != team) continue;
         if (!wait(full_at + place * 8, parity)) break;
         const uint32_t src = base_at + C::raw_at(place) + from, dst = base_at + C::kRingOff + half % S * C::kHalf + to;
-#pragma unroll 1
-        for (int p0 = 0; p0 < P; p0 += 8) {
-          // all loads first: while the products read shared memory each takes 300 cycles
-          uint4 code[8];
+        // all loads first: while the products read shared memory each takes 300 cycles
+        uint4 code[P];
 #pragma unroll
-          for (int p = 0; p < 8; ++p) code[p] = load_shared_codes(src + (p0 + p) * kRowsOf * D);
-          if (p0 == 0 && !wait(smem_u32(kv_empty) + half % S * 8, (half / S & 1) ^ 1)) break;
+        for (int p = 0; p < P; ++p) code[p] = load_shared_codes(src + p * kRowsOf * D);
+        const int4 f = s_steps[(steps + j) % kStepRing];
+        float x[4], y[4];   // scales of the half and, of keys, their values', of keys lane + 32 e
+        {
+          const float* scales = reinterpret_cast<const float*>(smem + C::raw_at(place) + C::kRawCodes) + lane + (keys ? 0 : kPage);
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            const uint4 w = code[p];
-            const uint2 h0 = codes_to_f16(w.x), h1 = codes_to_f16(w.y), h2 = codes_to_f16(w.z), h3 = codes_to_f16(w.w);
-            store_shared16(dst + (p0 + p) * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
-            store_shared16((dst ^ 16) + (p0 + p) * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
+          for (int e = 0; e < 4; ++e) {
+            const bool there = lane + 32 * e < f.z && !(f.w >> (e >> 1) & 1);
+            x[e] = there ? scales[(e >> 1) * 128 + (e & 1) * 32] : 0.f;
+            y[e] = there && keys ? scales[(e >> 1) * 128 + (e & 1) * 32 + kPage] : 0.f;
           }
         }
-        if (!ok) break;
-        if (keys) {   // two keys' scales each
-          const int4 f = s_steps[(steps + j) % kStepRing];
-          const int slot = (steps + j) % kScaleRing;
+        const int ex = step_exponent(x);
+        // A value scale that is no number becomes the score of whoever sees the
+        // key: as a factor of a weight it would reach rows that do not.
+        if (keys) {
+          const int ey = step_exponent(y);
+          if (tt == 0) s_unit[(steps + j) % kUnitRing] = make_int2(ex, ey);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {   // of page u
-            const float* scales = reinterpret_cast<const float*>(smem + C::raw_at(place) + C::kRawCodes + u * 512) + tt;
-            const bool there = u * kPage + tt < f.z && !(f.w >> u & 1);
-            // A value scale that is no number becomes the score of whoever sees the
-            // key: as a weight's factor it would reach rows that do not.
-            float kx = there ? scales[0] * 0x1p-8f : 0.f, vx = there ? scales[kPage] : 0.f;
-            uint32_t mag = __float_as_uint(vx) & 0x7FFFFFFFu;
-            if (mag >= 0x7F800000u) {
-              kx = __uint_as_float(0x7FC00000u);
-              vx = 0.f;
-              mag = 0;
-            }
-            mag = __reduce_max_sync(0xffffffffu, mag);
-            // a key scale below zero would turn a largest dot product into a least score: no bound then
-            const uint32_t most = __reduce_max_sync(0xffffffffu, kx < 0.f ? 0x7F800000u : kx == kx ? __float_as_uint(kx) : 0u);
-            s_scale[slot * 2 * kStepKeys + u * kPage + tt] = kx;
-            s_scale[slot * 2 * kStepKeys + kStepKeys + u * kPage + tt] = vx;
-            if (lane == 0) {
-              s_vmax[slot][u * 2 + (tt >> 5)] = mag;
-              s_kmax[slot][u * 2 + (tt >> 5)] = most;
-            }
-          }
+          for (int e = 0; e < 4; ++e) x[e] = y[e] * 0.f == 0.f ? x[e] : __uint_as_float(0x7FC00000u);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = x[e] * 0.f == 0.f ? x[e] : 0.f;
+        }
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = pack2<true>(x[e] * pow2_of(7 - ex), x[e] * pow2_of(7 - ex));
+        if (!wait(smem_u32(kv_empty) + half % S * 8, (half / S & 1) ^ 1)) break;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const uint4 w = code[p];
+          // of row row0 + p * kRowsOf
+          const uint32_t sc = __shfl_sync(0xffffffffu, h[p * kRowsOf / 32], (row0 + p * kRowsOf) % 32);
+          const __half2 scale = *reinterpret_cast<const __half2*>(&sc);
+          const uint2 h0 = codes_to_f16(w.x, scale), h1 = codes_to_f16(w.y, scale);
+          const uint2 h2 = codes_to_f16(w.z, scale), h3 = codes_to_f16(w.w, scale);
+          store_shared16(dst + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
+          store_shared16((dst ^ 16) + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -632,7 +617,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
     int k = 0;
     int step0 = 0;      // steps of the CTA's items before this one
     const int prefix_len = b.prefix_len, sinks = b.sinks;
-    const uint32_t scales_at = smem_u32(s_scale);
     bool ok = true;
     // waits taken by all 32 lanes together, so the warp-collective TMEM
     // accesses after them never diverge (also when a wait runs out)
@@ -697,66 +681,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           const int gone = flags & 3;
           const bool masked = gone != 0 || !__all_sync(0xffffffffu, dead || (c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys)));
           if (gone != 0) report_gone(a.b.status, gone, c_lo, c_hi, c_sink);
-          const int at = (step0 + j) % kScaleRing;
-          const uint32_t key_scales = scales_at + at * 8 * kStepKeys, value_scales = key_scales + 4 * kStepKeys;
-          auto sees = [&](int u) {   // keys of page u
-            const int c0 = u * kPage;
-            return gone >> u & 1 ? 0ull : slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
-          };
-          float sv[32];
-          // scores of 32 keys less the row's factor; -inf where the row does not see the key
-          auto load = [&](int q) {
-            float4 f[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] = load_shared16(key_scales + q * 128 + c * 16);
-            tmem_ld32(s_tmem + q * 32, sv);
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(f[c].x, f[c].y));
-              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(f[c].z, f[c].w));
-              sv[4 * c] = x.x, sv[4 * c + 1] = x.y, sv[4 * c + 2] = y.x, sv[4 * c + 3] = y.y;
-            }
-            if (masked) {
-              const uint32_t vis = static_cast<uint32_t>(sees(q >> 1) >> (q & 1) * 32);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) sv[c] = vis >> c & 1 ? sv[c] : -INFINITY;
-            }
-          };
-          // 2^E above the value scales that the row sees (below 2^(exponent - 126))
-          uint32_t top;
-          if (!masked) {
-            const uint4 vm = *reinterpret_cast<const uint4*>(s_vmax[at]);
-            top = max(max(vm.x, vm.y), max(vm.z, vm.w));
-          } else {
-            top = seen_scale(value_scales, sees(0), sees(1));
-          }
-          const int need = masked && none ? kNoUnit : max(static_cast<int>(top >> 23) - 126, kLeastE);
-          // The row's largest score: while dot products, each 32 with the largest of
-          // their scales, stay below what the reference allows, nothing more is
-          // needed; else the scores themselves.
-          float mx = -INFINITY;
-          bool bound = !masked;
-          if (bound) {
-            const uint4 km = *reinterpret_cast<const uint4*>(s_kmax[at]);
+          if (masked) {
+            // scores of keys that the row does not see become -inf in place
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              tmem_ld32(s_tmem + q * 32, sv);
-              mx = fmaxf(mx, fmaxf(row_max(sv), 0.f) * __uint_as_float(q & 2 ? (q & 1 ? km.w : km.z) : q & 1 ? km.y : km.x));
+            for (int c0 = 0; c0 < kStepKeys; c0 += 32) {
+              const unsigned long long seen = slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
+              const uint32_t vis = gone >> (c0 / kPage) & 1 ? 0u : static_cast<uint32_t>(seen);
+              float x[32];
+              tmem_ld32(s_tmem + c0, x);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) x[c] = vis >> c & 1 ? x[c] : -INFINITY;
+              tmem_st32(s_tmem + c0, x);
             }
-            mx = fmaf(mx, cq, -kBias);
-            bound = !__any_sync(0xffffffffu, need > unit || !(mx <= mref + kRescaleLog2));
+            tmem_wait_st();
           }
-          if (!bound) {
-            mx = -INFINITY;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              load(q);
-              mx = fmaxf(mx, row_max(sv));
-            }
-            mx = fmaf(mx, cq, -kBias);
-          }
+          // the step's factor of dot products, with room for -inf at both ends
+          const int2 un = s_unit[(step0 + j) % kUnitRing];
+          const float cs = fminf(fmaxf(cq * pow2_of(un.x - 7), 0x1p-126f), 0x1p127f);
+          // a half of the scores (one page) at a time: the second for its
+          // maximum, the first for its maximum and weights, the second again
+          float sv[64];
+          auto load = [&](int u) { tmem_ld64(s_tmem + u * kPage, sv); };
+          load(1);
+          float mx = row_max(sv);
+          load(0);
+          mx = fmaf(fmaxf(mx, row_max(sv)), cs, -kBias);
           // each row by itself, so that it does not depend on its neighbours
-          const bool grows = !bound && (need > unit || mx > mref + kRescaleLog2);
+          const int need = masked && none ? kNoUnit : un.y;
+          const bool grows = need > unit || mx > mref + kRescaleLog2;
           if (__any_sync(0xffffffffu, grows)) {
             const float nm = grows ? fmaxf(mref, mx) : mref;
             const int nu = need > unit ? need + 1 : unit;
@@ -779,37 +731,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
               tmem_wait_st();
             }
           }
-          const float neg = mref == -INFINITY ? 0.f : -mref - static_cast<float>(unit);
+          const float neg = mref == -INFINITY ? 0.f : -mref - static_cast<float>(unit - un.y);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {   // P replaces scores that have been read
-            load(q);
-            float4 g[8];
+          for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
+            if (u == 1) load(1);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) g[c] = load_shared16(value_scales + q * 128 + c * 16);
-            uint32_t pk[16];
+            for (int h = 0; h < 64; h += 32) {
+              uint32_t pk[16];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const float2 e = fma2(make_float2(sv[2 * c], sv[2 * c + 1]), make_float2(cq, cq), make_float2(neg, neg));
-              sv[2 * c] = ex2_here(e.x);
-              sv[2 * c + 1] = ex2_here(e.y);
+              for (int c = h; c < h + 32; c += 2) {
+                const float2 e = fma2(make_float2(sv[c], sv[c + 1]), make_float2(cs, cs), make_float2(neg, neg));
+                sv[c] = ex2_here(e.x);
+                sv[c + 1] = ex2_here(e.y);
+              }
+#pragma unroll
+              for (int c = 0; c < 16; ++c) pk[c] = pack2<true>(sv[h + 2 * c], sv[h + 2 * c + 1]);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) sum[c & 1] = add2(sum[c & 1], make_float2(sv[h + 2 * c], sv[h + 2 * c + 1]));
+              tmem_st_u16(s_tmem + u * (kPage / 2) + h / 2, pk);
             }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              const float2 x = mul2(make_float2(sv[4 * c], sv[4 * c + 1]), make_float2(g[c].x, g[c].y));
-              const float2 y = mul2(make_float2(sv[4 * c + 2], sv[4 * c + 3]), make_float2(g[c].z, g[c].w));
-              pk[2 * c] = pack2<true>(x.x, x.y);
-              pk[2 * c + 1] = pack2<true>(y.x, y.y);
-            }
-#pragma unroll
-            for (int c = 0; c < 16; ++c) sum[c & 1] = add2(sum[c & 1], make_float2(sv[2 * c], sv[2 * c + 1]));
-            tmem_st_u16(s_tmem + q * 16, pk);
-            if (q & 1) {
-              tmem_wait_st();
-              warp_arrive(&p_full[stream][q >> 1]);
-            }
+            tmem_wait_st();
+            warp_arrive(&p_full[stream][u]);
           }
-          l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+          l = fmaf((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y), pow2_of(7 - un.y), l);
         }
         ++done;
         ++ns;

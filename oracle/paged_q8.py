@@ -36,12 +36,20 @@ def parts(pool, d):
     return codes[:, :, 0], codes[:, :, 1], scales[:, :, 0], scales[:, :, 1]
 
 
-def decode(pool, d):
-    """The pool [n_pages, 2, n_kv, 64 * d] in fp64 that the bytes stand for."""
+def rounded(x, bits):
+    """x to `bits` significant bits, halves to the even one."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(np.ldexp(m, bits)), e - bits)
+
+
+def decode(pool, d, bits=None):
+    """The pool [n_pages, 2, n_kv, 64 * d] in fp64 that the bytes stand for; with
+    `bits`, scales and products are rounded to so many significant bits."""
     kc, vc, ks, vs = parts(pool, d)
     n, h = ks.shape[:2]
+    to = (lambda x: x) if bits is None else (lambda x: rounded(x, bits))
     with np.errstate(invalid="ignore"):
-        k, v = kc * ks[..., None], vc * vs[..., None]
+        k, v = to(kc * to(ks)[..., None]), to(vc * to(vs)[..., None])
     return np.stack([k.reshape(n, h, -1), v.transpose(0, 1, 3, 2).reshape(n, h, -1)], axis=1)
 
 

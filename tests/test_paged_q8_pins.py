@@ -49,6 +49,14 @@ def test_the_bytes_stand_for_the_rows():
     assert there.all() and np.abs(got[69] - k[0, :, 5]).max() < 0.02
 
 
+def test_rounding_to_bits_is_fp16s():
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal(2000) * np.exp(rng.standard_normal(2000))
+    x = x[np.abs(x) > 2.0 ** -13]
+    np.testing.assert_array_equal(p8.rounded(x, 11), x.astype(np.float16).astype(np.float64))
+    assert p8.rounded(np.array([0.0, 3.0, 2049.0, 2051.0]), 11).tolist() == [0.0, 3.0, 2048.0, 2052.0]
+
+
 def test_the_views_of_a_pool_are_its_parts():
     torch = pytest.importorskip("torch")
     rng = np.random.default_rng(2)
