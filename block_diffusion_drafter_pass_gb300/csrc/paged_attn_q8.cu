@@ -21,7 +21,7 @@
 // Sum and output share the unit, so it cancels.
 //
 // Per CTA: a warp walks the steps and writes down the pages of each half (128
-// keys, or their values); 4 warps take the halves from global memory
+// keys, or their values); 8 warps take the halves from global memory
 // into registers, kAhead of them under way, and put them as fp16 into the ring
 // that the products read (and the queries of each item, scaled); two warps issue
 // the tcgen05.mma of a stream each and eight do the softmax, as in paged_attn.cu.
@@ -31,14 +31,20 @@
 #include <algorithm>
 #include <atomic>
 
+#define DFL_WALK_CALL __forceinline__
 #include "paged_walk.cuh"
 
 namespace dfl {
 namespace {
 
-constexpr int kConvWarp0 = 8, kConvWarps = 4;   // the softmax's are 0..7: TMEM lanes go by warp % 4
-constexpr int kWalkWarp = 12, kMmaWarp0 = 13;
-constexpr int kThreads = 15 * 32;
+constexpr int kConvWarp0 = 8, kConvWarps = 8;   // the softmax's are 0..7: TMEM lanes go by warp % 4
+constexpr int kWalkWarp = 16, kMmaWarp0 = 17;   // warp 19 has no work
+constexpr int kThreads = 20 * 32;
+// Registers of a thread, by warpgroup: the launch's (96, as the kernel's bounds
+// make it) are dealt anew.
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kConvRegs = 64, kRestRegs = 80;
+static_assert(2 * kSoftRegs + 2 * kConvRegs + kRestRegs <= 5 * kLaunchRegs, "setmaxnreg waits for registers that the launch must have");
+static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs, "inc must go up and dec down");
 constexpr int kAhead = 16;       // steps that the walk looks up at a time
 // The walk is ahead of the products by these and the halves of both rings (8
 // steps at most); exponents are held of what is behind the first ring.
@@ -71,7 +77,7 @@ struct Cfg {
   static constexpr int kSmem = kIntOff + kBatchBytes + 1024;
   static_assert(2 * kRaw >= kHalf && kRaw % 1024 == 0, "queries over raw places, halves in whole swizzle atoms");
   static_assert(kSmem <= 226 * 1024 - 5120, "static shared variables need the rest");
-  static constexpr int kPieces = D / 8;                     // 16 bytes of a half for each converting thread
+  static constexpr int kPieces = D / 16;                    // 16 bytes of a half for each converting thread
   static __device__ __forceinline__ int raw_at(int place) {
     return place < kRawPair ? kRawOff + place * kRaw : kQ1Off + (place - kRawPair) * kRaw;
   }
@@ -84,6 +90,12 @@ __device__ __forceinline__ void store_shared16(uint32_t at, uint4 v) {
 __device__ __forceinline__ uint4 load_shared_codes(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
+__device__ __forceinline__ float load_shared_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
   return v;
 }
 
@@ -125,7 +137,7 @@ __device__ __forceinline__ uint32_t vdesc_low(uint32_t saddr) {
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
 template <int D, bool F16>
-__device__ __noinline__ void bring_queries(const PagedAttnArgs& a, const Notice& r, uint32_t q_at, float* s_qc, int ct) {
+__device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Notice& r, uint32_t q_at, float* s_qc, int ct) {
   constexpr int kOf = D / 8, kPass = kConvWarps * 32 / kOf, kAtOnce = 4;
   const int c = ct % kOf, G = a.b.group, stream_rows = a.stream_tokens * G;
   const int n = (r.pair ? 2 : 1) * stream_rows, end = r.t0 + r.ntok;
@@ -168,6 +180,15 @@ __device__ __noinline__ void bring_queries(const PagedAttnArgs& a, const Notice&
       }
     }
   }
+}
+
+// Step j of an item: its pages, its keys, and in bits 2, 3 which streams of a pair take it.
+__device__ __forceinline__ int4 look_up(const PagedAttnArgs& a, const Batch& b, const Item& it, int j) {
+  StepWalk w;
+  w.start(b, it.t, it.j + j);
+  const int32_t* table = table_of(a, w.s.seq) + w.s.base / kPage;
+  return make_int4(w.s.base < w.s.end ? table[0] : -1, w.s.base + kPage < w.s.end ? table[1] : -1, w.s.end - w.s.base,
+                   it.pair ? pair_takes(b, it.t, w.s.seq, w.s.base) << 2 : 0);
 }
 
 struct NoRedo {
@@ -244,8 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   const uint32_t tmem = tmem_slot;
 
   const bool converts = warp >= kConvWarp0 && warp < kWalkWarp;
-  Item* const items = s_items[warp < kConvWarp0 ? warp : converts ? 0 : warp - kWalkWarp + kConvWarp0];   // written by lane 0
-  if (!converts && lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
+  const bool walks = warp < kConvWarp0 || (warp >= kWalkWarp && warp <= kMmaWarp0 + 1);   // has items of its own
+  Item* const items = s_items[!walks ? 0 : warp < kConvWarp0 ? warp : warp - kWalkWarp + kConvWarp0];   // written by lane 0
+  if (walks && lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
   __syncwarp();
   const uint32_t progress_at = smem_u32(&s_progress), never_at = smem_u32(&s_never);
   const uint32_t wait_tries = a.wait_tries;
@@ -259,257 +281,252 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   // a pair (both streams take every step) and 2 for an alternating tile
   // (stream s takes the steps of parity s).
 
-  if (warp == kWalkWarp) {
-    // ---------------- the walk over keys and values, and their copies ----------------
-    // The whole warp: a lane looks up a step (kAhead steps at a time, the next
-    // while these are brought), and a half's copies go out from a lane each. One
-    // lane for all of it took 3000 cycles a step, 2.1 times what memory does.
-    const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
-    const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
-    const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
-    int at = 0, steps = 0, k = 0;      // place in the raw ring, steps of the items before this one, items
-    int places = C::kRawSlots;         // places in use: the pair's, or all
-    uint32_t used = 0, sent = 0;       // by place: parity of its records, whether there are copies to wait for at the end
-    bool ok = true;
-    int4 split = make_int4(0, 0, 0, 0), found = make_int4(-1, -1, 0, 0);   // found: pages, keys, note bits of the lane's step
-    int piece = 0;
+  if (warp >= kWalkWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
+    if (warp == kWalkWarp) {
+      // ---------------- the walk over keys and values, and their copies ----------------
+      // The whole warp: a lane looks up a step (kAhead steps at a time, the next
+      // while these are brought), and a half's copies go out from a lane each. One
+      // lane for all of it took 3000 cycles a step, 2.1 times what memory does.
+      const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
+      const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
+      const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
+      int at = 0, steps = 0, k = 0;      // place in the raw ring, steps of the items before this one, items
+      int places = C::kRawSlots;         // places in use: the pair's, or all
+      uint32_t used = 0, sent = 0;       // by place: parity of its records, whether there are copies to wait for at the end
+      bool ok = true;
+      int4 split = make_int4(0, 0, 0, 0), found = make_int4(-1, -1, 0, 0);   // found: pages, keys, note bits of the lane's step
+      int piece = 0;
 #pragma unroll 1
-    for (int before = items[0].nj > 0 ? items[0].j : 0; before > 0; before -= run) ++piece;
-    auto look_up = [&](const Item& it, int j) {   // of step j + lane of the item
-      j += lane;
-      if (lane >= kAhead || j >= it.nj) return;
-      StepWalk w;
-      w.start(b, it.t, it.j + j);
-      const int32_t* table = table_of(a, w.s.seq) + w.s.base / kPage;
-      found.x = w.s.base < w.s.end ? table[0] : -1;
-      found.y = w.s.base + kPage < w.s.end ? table[1] : -1;
-      found.z = w.s.end - w.s.base;
-      found.w = it.pair ? pair_takes(b, it.t, w.s.seq, w.s.base) << 2 : 0;
-    };
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
-      return ok;
-    };
-    auto notice = [&](const Notice& n) {
-      if (!wait(smem_u32(note_empty) + (k & 1) * 8, (k >> 1 & 1) ^ 1)) return false;
-      if (lane == 0) {
-        s_notice[k & 1] = n;
-        bar_arrive(smem_u32(note_full) + (k & 1) * 8);
-      }
-      return true;
-    };
-    auto go_on = [&]() {
-      used ^= 1u << at;
-      at = at + 1 < places ? at + 1 : 0;
-    };
-    if (items[0].nj > 0) look_up(items[0], 0);
-#pragma unroll 1
-    while (true) {
-      const Item& it = items[k & 1];
-      const Item& after = items[(k + 1) & 1];
-      const int nj = it.nj, pair = it.pair, head = it.head, lead = pair ? 1 : 2;
-      if (nj <= 0) break;
-      __syncwarp();
-      if (lane == 0) next_item(b, it, items[(k + 1) & 1]);
-      __syncwarp();
-      const int was = places;
-      places = pair ? C::kRawPair : C::kRawSlots;
-      // behind a pair's queries: their place is free when its last scores are
-      if (places > was) wait(smem_u32(&q_empty), (k - 1) & 1);
-      if (at >= places) at = 0;
-      if (!ok || !notice(Notice{nj, pair, head, it.t.t0, it.t.ntok, {}})) break;
-#pragma unroll 1
-      for (int i = 1 - 2 * lead; i < 2 * nj; ++i) {   // round i >> 1: values, then keys
-        const bool keys = i & 1;
-        const int j = (i >> 1) + (keys ? lead : 0);
-        if (j < 0 || j >= nj) continue;
-        if (keys && j % kAhead == 0) {
-          int4 f = found;
-          if (lane < kAhead && j + lane < nj) {
-            if (f.x < 0 || f.x >= a.b.n_pages) f.x = -1, f.w |= 1;
-            if (f.y < 0 || f.y >= a.b.n_pages) f.y = -1, f.w |= 2;
-            s_steps[(steps + j + lane) % kStepRing] = f;
-            s_step[(steps + j + lane) % kStepRing] = step_note(steps + j + lane, f.w);
-          }
-          if (j + kAhead < nj) look_up(it, j + kAhead);
-          else if (after.nj > 0) look_up(after, 0);
-          __syncwarp();
-        }
-        if (!wait(empty_at + at * 8, (used >> at & 1) ^ 1)) break;
-        const int4 f = s_steps[(steps + j) % kStepRing];
-        // lanes 0, 1: the codes of a page's keys that exist; 2, 3: its scales (keys: of both kinds)
-        const int rows0 = f.x < 0 ? 0 : min(max(f.z, 0), kPage), rows1 = f.y < 0 ? 0 : min(max(f.z - kPage, 0), kPage);
-        const int u = lane & 1, rows = u ? rows1 : rows0;
-        const uint32_t scales = keys ? 512 : 256, bytes = rows == 0 ? 0 : lane < 2 ? rows * D : scales;
-        const uint32_t bar = full_at + at * 8;
+      for (int before = items[0].nj > 0 ? items[0].j : 0; before > 0; before -= run) ++piece;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
+        return ok;
+      };
+      auto notice = [&](const Notice& n) {
+        if (!wait(smem_u32(note_empty) + (k & 1) * 8, (k >> 1 & 1) ^ 1)) return false;
         if (lane == 0) {
-          const uint32_t all = (rows0 + rows1) * D + (rows0 ? scales : 0) + (rows1 ? scales : 0);
-          asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(all) : "memory");
+          s_notice[k & 1] = n;
+          bar_arrive(smem_u32(note_full) + (k & 1) * 8);
         }
+        return true;
+      };
+      auto go_on = [&]() {
+        used ^= 1u << at;
+        at = at + 1 < places ? at + 1 : 0;
+      };
+      if (lane < kAhead && lane < items[0].nj) found = look_up(a, b, items[0], lane);
+#pragma unroll 1
+      while (true) {
+        const Item& it = items[k & 1];
+        const Item& after = items[(k + 1) & 1];
+        const int nj = it.nj, pair = it.pair, head = it.head, lead = pair ? 1 : 2;
+        if (nj <= 0) break;
         __syncwarp();
-        if (lane < 4 && bytes > 0) {
-          const uint8_t* block = pool + (u ? f.y : f.x) * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
-          const uint32_t to = base_at + C::raw_at(at) + (lane < 2 ? u * kPage * D : C::kRawCodes + u * 512 + 512 - scales);
-          bulk_copy(to, block + (lane >= 2 ? q8_key_scales_at(D) + 512 - scales : keys ? 0 : q8_values_at(D)), bytes, bar);
-        }
-        sent |= 1u << at;
-        go_on();
-      }
-      if (!ok) break;
-      steps += nj;
-      if (it.j == 0 && nj < it.t.n) {   // the run ends here: the rest is the next CTAs'
-        int pieces = 1;
+        if (lane == 0) next_item(b, it, items[(k + 1) & 1]);
+        __syncwarp();
+        const int was = places;
+        places = pair ? C::kRawPair : C::kRawSlots;
+        // behind a pair's queries: their place is free when its last scores are
+        if (places > was) wait(smem_u32(&q_empty), (k - 1) & 1);
+        if (at >= places) at = 0;
+        if (!ok || !notice(Notice{nj, pair, head, it.t.t0, it.t.ntok, {}})) break;
 #pragma unroll 1
-        for (int left = it.t.n - nj; left > 0; left -= run) ++pieces;
-        split = make_int4(it.t.t0, it.t.ntok, it.head, pieces);
-      }
-      ++k;
-    }
-    if (ok) notice(Notice{});
-    if (!ok) give_up();
-    if (lane == 0) {
-      a.split[blockIdx.x] = split;
-      a.piece[blockIdx.x] = piece;
-    }
-    // copies still in flight complete before shared memory is released
-#pragma unroll 1
-    for (int p = 0; p < C::kRawSlots; ++p)
-      if (sent >> p & 1) bar_wait(full_at + p * 8, (used >> p & 1) ^ 1, never_at, kWaitTries);
-  } else if (warp >= kMmaWarp0) {
-    // ---------------- products of one stream ----------------
-    // As in paged_attn.cu: the warp goes through this as one, with one elected
-    // lane in front of the instructions.
-    const int s = warp_uniform(warp - kMmaWarp0);
-    const bool one = elect_one();
-    const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kRingOff >> 4);
-    const uint32_t vring_low = vdesc_low<D>(smem_u32(smem)) + (C::kRingOff >> 4);
-    const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
-    const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0][0]) + s * 16;
-    const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
-    const uint32_t tm = warp_uniform(tmem);
-    const uint32_t s_col = tm + s * kStepKeys, o_col = tm + kOCol + s * D;
-    int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
-    bool ok = true;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
-    };
-    while (true) {
-      const Item& it = items[k & 1];
-      const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
-      if (nj <= 0) break;
-      __syncwarp();
-      const uint32_t q_at = q_low + (pair ? s * (C::kQ1Off >> 4) : 0);
-      wait(smem_u32(&q_full), k & 1);
-      ++k;
-      uint32_t add = 0;
-      uint32_t takes = 0;   // bit i: the stream takes step j + i
-#pragma unroll 1
-      for (int j = -lead; j < nj && ok; ++j) {
-        const int pv = j >= 0, more = j + lead < nj;
-        if (j == nj - lead) {   // the scores are all issued
-          if (lane == 0) next_item(b, it, items[k & 1]);
-          __syncwarp();
-        }
-        const int ck = c + pv, vslot = c % S, kslot = ck % S;
-        // One lane for each thing to wait for, so that the waits are one. Of a
-        // pair that is everything but the second page's weights, and its streams
-        // take turns; an alternating tile's values go back as soon as they can.
-        const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
-        uint32_t early = 0;
-        {
-          if (pair && more) early = note_early<kStepRing>(s_step, steps);
-          bool need = lane == 0 && pv;
-          uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
-          if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
-          if (lane == 2) need = weights, bar = p_at, parity = np & 1;
-          if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
-          int polls = kWaitPolls, seen = 0;
-          while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
-            const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
-            if (progress != seen) polls = kWaitPolls;
-            seen = progress;
-            if (progress < 0 || --polls == 0) {
-              ok = false;
-              break;
+        for (int i = 1 - 2 * lead; i < 2 * nj; ++i) {   // round i >> 1: values, then keys
+          const bool keys = i & 1;
+          const int j = (i >> 1) + (keys ? lead : 0);
+          if (j < 0 || j >= nj) continue;
+          if (keys && j % kAhead == 0) {
+            int4 f = found;
+            if (lane < kAhead && j + lane < nj) {
+              if (f.x < 0 || f.x >= a.b.n_pages) f.x = -1, f.w |= 1;
+              if (f.y < 0 || f.y >= a.b.n_pages) f.y = -1, f.w |= 2;
+              s_steps[(steps + j + lane) % kStepRing] = f;
+              s_step[(steps + j + lane) % kStepRing] = step_note(steps + j + lane, f.w);
             }
+            const bool same = j + kAhead < nj;   // else the next item's first
+            const Item& of = same ? it : after;
+            const int of_j = (same ? j + kAhead : 0) + lane;
+            if (lane < kAhead && of_j < of.nj) found = look_up(a, b, of, of_j);
+            __syncwarp();
           }
+          if (!wait(empty_at + at * 8, (used >> at & 1) ^ 1)) break;
+          const int4 f = s_steps[(steps + j) % kStepRing];
+          // lanes 0, 1: the codes of a page's keys that exist; 2, 3: its scales (keys: of both kinds)
+          const int rows0 = f.x < 0 ? 0 : min(max(f.z, 0), kPage), rows1 = f.y < 0 ? 0 : min(max(f.z - kPage, 0), kPage);
+          const int u = lane & 1, rows = u ? rows1 : rows0;
+          const uint32_t scales = keys ? 512 : 256, bytes = rows == 0 ? 0 : lane < 2 ? rows * D : scales;
+          const uint32_t bar = full_at + at * 8;
+          if (lane == 0) {
+            const uint32_t all = (rows0 + rows1) * D + (rows0 ? scales : 0) + (rows1 ? scales : 0);
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(all) : "memory");
+          }
+          __syncwarp();
+          if (lane < 4 && bytes > 0) {
+            const uint8_t* block = pool + (u ? f.y : f.x) * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
+            const uint32_t to = base_at + C::raw_at(at) + (lane < 2 ? u * kPage * D : C::kRawCodes + u * 512 + 512 - scales);
+            bulk_copy(to, block + (lane >= 2 ? q8_key_scales_at(D) + 512 - scales : keys ? 0 : q8_values_at(D)), bytes, bar);
+          }
+          sent |= 1u << at;
+          go_on();
         }
-        turns += pair;
         if (!ok) break;
-        uint32_t take = ((j + lead) & 1) == s && more;
-        if (pair && more) take = warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1);
-        tc_fence_after();
-        if (takes & 1) {   // O (+)= P V
-          const uint32_t v_at = vring_low + vslot * (C::kHalf >> 4);
-          // the first page's weights while the second's are still made
-          if (one) {
+        steps += nj;
+        if (it.j == 0 && nj < it.t.n) {   // the run ends here: the rest is the next CTAs'
+          int pieces = 1;
+#pragma unroll 1
+          for (int left = it.t.n - nj; left > 0; left -= run) ++pieces;
+          split = make_int4(it.t.t0, it.t.ntok, it.head, pieces);
+        }
+        ++k;
+      }
+      if (ok) notice(Notice{});
+      if (!ok) give_up();
+      if (lane == 0) {
+        a.split[blockIdx.x] = split;
+        a.piece[blockIdx.x] = piece;
+      }
+      // copies still in flight complete before shared memory is released
+#pragma unroll 1
+      for (int p = 0; p < C::kRawSlots; ++p)
+        if (sent >> p & 1) bar_wait(full_at + p * 8, (used >> p & 1) ^ 1, never_at, kWaitTries);
+    } else if (warp <= kMmaWarp0 + 1) {
+      // ---------------- products of one stream ----------------
+      // As in paged_attn.cu: the warp goes through this as one, with one elected
+      // lane in front of the instructions.
+      const int s = warp_uniform(warp - kMmaWarp0);
+      const bool one = elect_one();
+      const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kRingOff >> 4);
+      const uint32_t vring_low = vdesc_low<D>(smem_u32(smem)) + (C::kRingOff >> 4);
+      const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+      const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0][0]) + s * 16;
+      const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
+      const uint32_t tm = warp_uniform(tmem);
+      const uint32_t s_col = tm + s * kStepKeys, o_col = tm + kOCol + s * D;
+      int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
+      };
+      while (true) {
+        const Item& it = items[k & 1];
+        const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
+        if (nj <= 0) break;
+        __syncwarp();
+        const uint32_t q_at = q_low + (pair ? s * (C::kQ1Off >> 4) : 0);
+        wait(smem_u32(&q_full), k & 1);
+        ++k;
+        uint32_t add = 0;
+        uint32_t takes = 0;   // bit i: the stream takes step j + i
+#pragma unroll 1
+        for (int j = -lead; j < nj && ok; ++j) {
+          const int pv = j >= 0, more = j + lead < nj;
+          if (j == nj - lead) {   // the scores are all issued
+            if (lane == 0) next_item(b, it, items[k & 1]);
+            __syncwarp();
+          }
+          const int ck = c + pv, vslot = c % S, kslot = ck % S;
+          // One lane for each thing to wait for, so that the waits are one. Of a
+          // pair that is everything but the second page's weights, and its streams
+          // take turns; an alternating tile's values go back as soon as they can.
+          const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
+          uint32_t early = 0;
+          {
+            if (pair && more) early = note_early<kStepRing>(s_step, steps);
+            bool need = lane == 0 && pv;
+            uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
+            if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
+            if (lane == 2) need = weights, bar = p_at, parity = np & 1;
+            if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
+            int polls = kWaitPolls, seen = 0;
+            while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
+              const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
+              if (progress != seen) polls = kWaitPolls;
+              seen = progress;
+              if (progress < 0 || --polls == 0) {
+                ok = false;
+                break;
+              }
+            }
+          }
+          turns += pair;
+          if (!ok) break;
+          uint32_t take = ((j + lead) & 1) == s && more;
+          if (pair && more) take = warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1);
+          tc_fence_after();
+          if (takes & 1) {   // O (+)= P V
+            const uint32_t v_at = vring_low + vslot * (C::kHalf >> 4);
+            // the first page's weights while the second's are still made
+            if (one) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, kk > 0 ? 1u : add);
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, kk > 0 ? 1u : add);
+            }
+            __syncwarp();
+            wait(p_at + 8, np & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (one) {
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk)
+                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
+              bar_commit(empty_at + vslot * 8);
+            }
+            add = 1;
+          } else if (pv) {
+            if (weights) wait(p_at + 8, np & 1);
+            if (one) bar_arrive(empty_at + vslot * 8);
+          }
+          np += weights;
+          __syncwarp();
+          if (!pair && more) {
+            wait(full_at + kslot * 8, ck / S & 1);
+            if (!ok) break;
+          }
+          if (pair && one) bar_arrive(pass_at);   // the other stream's waits pass under these products
+          if (take) {   // S = Q K^T
+            const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
+            if (one) {
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+                tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
+              }
+              bar_commit(s_at);
+              bar_commit(empty_at + kslot * 8);
+            }
+            takes |= 1u << lead;
+          } else if (more && one) {
+            if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
+            bar_arrive(empty_at + kslot * 8);
+          }
+          if (one) {
+            if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
           }
           __syncwarp();
-          wait(p_at + 8, np & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (one) {
-#pragma unroll
-            for (int kk = 4; kk < 8; ++kk)
-              tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
-            bar_commit(empty_at + vslot * 8);
-          }
-          add = 1;
-        } else if (pv) {
-          if (weights) wait(p_at + 8, np & 1);
-          if (one) bar_arrive(empty_at + vslot * 8);
+          c = ck + more;
+          steps += more;
+          takes >>= 1;
         }
-        np += weights;
-        __syncwarp();
-        if (!pair && more) {
-          wait(full_at + kslot * 8, ck / S & 1);
-          if (!ok) break;
+        if (!ok) {
+          give_up();
+          break;
         }
-        if (pair && one) bar_arrive(pass_at);   // the other stream's waits pass under these products
-        if (take) {   // S = Q K^T
-          const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
-          if (one) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
-              tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
-            }
-            bar_commit(s_at);
-            bar_commit(empty_at + kslot * 8);
-          }
-          takes |= 1u << lead;
-        } else if (more && one) {
-          if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
-          bar_arrive(empty_at + kslot * 8);
-        }
-        if (one) {
-          if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
-        }
-        __syncwarp();
-        c = ck + more;
-        steps += more;
-        takes >>= 1;
+        if (add && one) bar_commit(smem_u32(&o_done[0]) + s * 8);   // only then does the softmax wait for it
       }
-      if (!ok) {
-        give_up();
-        break;
-      }
-      if (add && one) bar_commit(smem_u32(&o_done[0]) + s * 8);   // only then does the softmax wait for it
+      // every issued product completes before TMEM and shared memory are released
+      if (one) bar_commit(smem_u32(&mma_done));
+      bar_wait(smem_u32(&mma_done), 0, never_at, kWaitTries);
     }
-    // every issued product completes before TMEM and shared memory are released
-    if (one) bar_commit(smem_u32(&mma_done));
-    bar_wait(smem_u32(&mma_done), 0, never_at, kWaitTries);
   } else if (converts) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvRegs));
     // ---------------- codes to fp16 ----------------
-    // Two teams of two warps take every other half, so that one's waits pass
+    // Two teams of four warps take every other half, so that one's waits pass
     // under the other's work. A lane takes 16 bytes of a row at a time, in an
     // order in which 8 neighbours meet all 8 bank groups both of the rows that
     // they read and of the swizzled rows that they write.
     constexpr int P = C::kPieces, kRowsOf = kStepKeys / P;   // rows of a piece
-    const int ct = tid - kConvWarp0 * 32, team = ct >> 6, tt = ct & 63;
+    const int ct = tid - kConvWarp0 * 32, team = ct >> 7, tt = ct & 127;
     const int box = D == 128 ? lane >> 2 & 1 : 0, chunk = lane & 3;
     const int row0 = D == 128 ? (tt >> 5) * 4 + (lane >> 4) * 2 + (box ^ (lane >> 3 & 1)) : tt >> 2;
     const uint32_t full_at = smem_u32(raw_full), empty_at = smem_u32(raw_empty), base_at = smem_u32(smem);
@@ -552,47 +569,51 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         if ((half & 1) != team) continue;
         if (!wait(full_at + place * 8, parity)) break;
         const uint32_t src = base_at + C::raw_at(place) + from, dst = base_at + C::kRingOff + half % S * C::kHalf + to;
-        // all loads first: while the products read shared memory each takes 300 cycles
-        uint4 code[P];
+        uint4 code[4];
 #pragma unroll
-        for (int p = 0; p < P; ++p) code[p] = load_shared_codes(src + p * kRowsOf * D);
+        for (int p = 0; p < 4; ++p) code[p] = load_shared_codes(src + p * kRowsOf * D);
         const int4 f = s_steps[(steps + j) % kStepRing];
-        float x[4], y[4];   // scales of the half and, of keys, their values', of keys lane + 32 e
-        {
-          const float* scales = reinterpret_cast<const float*>(smem + C::raw_at(place) + C::kRawCodes) + lane + (keys ? 0 : kPage);
+        // Scales of keys lane + 32 e: the half's, and the values'. One way for both
+        // kinds of halves: a branch here doubles the code that follows.
+        float x[4], y[4];
+        const uint32_t scales = base_at + C::raw_at(place) + C::kRawCodes + lane * 4 + 256;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool there = lane + 32 * e < f.z && !(f.w >> (e >> 1) & 1);
-            x[e] = there ? scales[(e >> 1) * 128 + (e & 1) * 32] : 0.f;
-            y[e] = there && keys ? scales[(e >> 1) * 128 + (e & 1) * 32 + kPage] : 0.f;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const bool there = lane + 32 * e < f.z && !(f.w >> (e >> 1) & 1);
+          const uint32_t from_e = scales + (e >> 1) * 512 + (e & 1) * 128;
+          x[e] = there ? load_shared_f32(from_e - (keys ? 256 : 0)) : 0.f;
+          y[e] = there ? load_shared_f32(from_e) : 0.f;
         }
-        const int ex = step_exponent(x);
+        const int ex = step_exponent(x), ey = step_exponent(y);
+        if (keys && tt == 0) s_unit[(steps + j) % kUnitRing] = make_int2(ex, ey);
         // A value scale that is no number becomes the score of whoever sees the
         // key: as a factor of a weight it would reach rows that do not.
-        if (keys) {
-          const int ey = step_exponent(y);
-          if (tt == 0) s_unit[(steps + j) % kUnitRing] = make_int2(ex, ey);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = y[e] * 0.f == 0.f ? x[e] : __uint_as_float(0x7FC00000u);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = x[e] * 0.f == 0.f ? x[e] : 0.f;
-        }
+        const float instead = keys ? __uint_as_float(0x7FC00000u) : 0.f, unit = pow2_of(7 - ex);
         uint32_t h[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = pack2<true>(x[e] * pow2_of(7 - ex), x[e] * pow2_of(7 - ex));
+        for (int e = 0; e < 4; ++e) {
+          x[e] = y[e] * 0.f == 0.f ? x[e] * unit : instead;
+          h[e] = pack2<true>(x[e], x[e]);
+        }
         if (!wait(smem_u32(kv_empty) + half % S * 8, (half / S & 1) ^ 1)) break;
+        // the next pieces are read while these are converted; kept short: code that
+        // does not stay in the instruction caches costs more than the loop
+#pragma unroll 1
+        for (int p0 = 0; p0 < P; p0 += 4) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const uint4 w = code[p];
-          // of row row0 + p * kRowsOf
-          const uint32_t sc = __shfl_sync(0xffffffffu, h[p * kRowsOf / 32], (row0 + p * kRowsOf) % 32);
-          const __half2 scale = *reinterpret_cast<const __half2*>(&sc);
-          const uint2 h0 = codes_to_f16(w.x, scale), h1 = codes_to_f16(w.y, scale);
-          const uint2 h2 = codes_to_f16(w.z, scale), h3 = codes_to_f16(w.w, scale);
-          store_shared16(dst + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
-          store_shared16((dst ^ 16) + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
+          for (int p = 0; p < 4; ++p) {
+            const uint4 w = code[p];
+            // of row row0 + (p0 + p) * kRowsOf
+            const int row = (p0 + p) * kRowsOf;
+            const uint32_t sc = __shfl_sync(0xffffffffu, row < 64 ? (row < 32 ? h[0] : h[1]) : row < 96 ? h[2] : h[3], (row0 + row) % 32);
+            const __half2 scale = *reinterpret_cast<const __half2*>(&sc);
+            if (p0 + 4 < P) code[p] = load_shared_codes(src + (p0 + 4 + p) * kRowsOf * D);
+            const uint2 h0 = codes_to_f16(w.x, scale), h1 = codes_to_f16(w.y, scale);
+            const uint2 h2 = codes_to_f16(w.z, scale), h3 = codes_to_f16(w.w, scale);
+            const uint32_t at16 = dst + row * 128;
+            store_shared16(at16, make_uint4(h0.x, h0.y, h1.x, h1.y));
+            store_shared16(at16 ^ 16, make_uint4(h2.x, h2.y, h3.x, h3.y));
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -606,6 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
     }
     if (!ok) give_up();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------- softmax and output ----------------
     const int stream = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);

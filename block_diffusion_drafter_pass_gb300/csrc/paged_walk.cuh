@@ -11,6 +11,12 @@
 #include "paged_deal.h"
 #include "paged_row.cuh"
 
+// Functions that are not worth their place in line, unless the kernel deals its
+// registers to its warps by setmaxnreg, under which ptxas takes no calls.
+#ifndef DFL_WALK_CALL
+#define DFL_WALK_CALL __noinline__
+#endif
+
 namespace dfl {
 
 constexpr int kStepKeys = 2 * kPage;
@@ -212,7 +218,7 @@ __device__ __forceinline__ bool step_counts(const Batch& b, int seq, int base, i
 }
 
 // Bit s: stream s of a pair takes the step.
-__device__ __noinline__ int pair_takes(const Batch& b, const Tile& t, int seq, int base) {
+__device__ DFL_WALK_CALL int pair_takes(const Batch& b, const Tile& t, int seq, int base) {
   const int mid = t.t0 + b.stream_tokens;
   return (step_counts(b, seq, base, t.t0, mid) ? 1 : 0) | (step_counts(b, seq, base, mid, t.t0 + t.ntok) ? 2 : 0);
 }
@@ -286,7 +292,7 @@ __device__ __forceinline__ void cut_item(Item& it) {
 }
 
 // The run's item after `was` (its first: was.tile holds ~tile); nj = 0: none.
-__device__ __noinline__ void next_item(const Batch& b, const Item& was, Item& it) {
+__device__ DFL_WALK_CALL void next_item(const Batch& b, const Item& was, Item& it) {
   it = was;
   it.nj = 0;
   if (it.todo <= 0) return;
@@ -512,7 +518,7 @@ __device__ __forceinline__ int deal_batch(const PagedAttnArgs& a, Batch& b, long
 // have been given back. Here since the row knows what it sees, and since the
 // producer is a chain of steps in one lane: asked there, 16 tokens over 262144
 // keys took 166 us instead of 162 (with heads of 64: 157 instead of 144).
-__device__ __noinline__ void report_gone(int* status, int gone, int c_lo, int c_hi, int c_sink) {
+__device__ DFL_WALK_CALL void report_gone(int* status, int gone, int c_lo, int c_hi, int c_sink) {
 #pragma unroll 1
   for (int u = 0; u < 2; ++u) {
     const int c0 = u * kPage;
@@ -533,7 +539,7 @@ struct Join {
 // whole tile, else to the partials. False when a wait ran out. (A function of
 // its own so that its registers are not the softmax loop's.)
 template <int D, bool F16, class Again>
-__device__ __noinline__ bool finish_item(const PagedAttnArgs& a, const Batch& b, const Item& it, Join& join, int stream,
+__device__ DFL_WALK_CALL bool finish_item(const PagedAttnArgs& a, const Batch& b, const Item& it, Join& join, int stream,
                                          uint32_t tmem, int token, float mref, float l, bool products, int parity,
                                          uint32_t progress) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
