@@ -38,7 +38,7 @@ namespace dfl {
 namespace {
 
 constexpr int kConvWarp0 = 8, kConvWarps = 8;   // the softmax's are 0..7: TMEM lanes go by warp % 4
-constexpr int kWalkWarp = 16, kMmaWarp0 = 17;   // warp 19 has no work
+constexpr int kWalkWarp = 16, kMmaWarp0 = 17, kScaleWarp = 19;
 constexpr int kThreads = 20 * 32;
 // Registers of a thread, by warpgroup: the launch's (96, as the kernel's bounds
 // make it) are dealt anew.
@@ -47,9 +47,9 @@ static_assert(2 * kSoftRegs + 2 * kConvRegs + kRestRegs <= 5 * kLaunchRegs, "set
 static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs, "inc must go up and dec down");
 constexpr int kAhead = 16;       // steps that the walk looks up at a time
 // The walk is ahead of the products by these and the halves of both rings (8
-// steps at most); exponents are held of what is behind the first ring.
+// steps at most); scales are held of what is behind the first ring.
 constexpr int kStepRing = 32;
-constexpr int kUnitRing = 8;
+constexpr int kScaleRing = 8;
 constexpr float kBias = 7.f;
 constexpr int kLeastE = -80, kNoUnit = -(1 << 20);   // smaller scales count as 2^-80
 
@@ -64,17 +64,18 @@ struct Cfg {
   static constexpr int kBox = kRows * 128;                  // 128 rows of 64 elements, swizzled
   static constexpr int kHalf = (D / 64) * kBox;             // a step's keys, or its values, or a stream's queries
   static constexpr int kSlots = D == 128 ? 3 : 6;           // halves as fp16
-  // Raw halves: codes [128][d], and per page its key and value scales (behind
-  // values the latter only). The last two places lie where the second stream's queries go, so
-  // only tiles without those use them.
-  static constexpr int kRawCodes = kStepKeys * D;
-  static constexpr int kRaw = kRawCodes + 1024;
+  // Raw halves: codes [128][d]. The last two places lie where the second
+  // stream's queries go, so only tiles without those use them.
+  static constexpr int kRaw = kStepKeys * D;
   static constexpr int kRawSlots = D == 128 ? 4 : 6, kRawPair = kRawSlots - 2;
   static constexpr int kQ1Off = kHalf;
   static constexpr int kRawOff = kQ1Off + 2 * kRaw;         // of place 0; the last two before it
   static constexpr int kRingOff = kRawOff + kRawPair * kRaw;
   static constexpr int kIntOff = kRingOff + kSlots * kHalf;
-  static constexpr int kSmem = kIntOff + kBatchBytes + 1024;
+  // A step's scales: per page those of its keys and of its values, as they come
+  // (fp32), then as two fp16 each.
+  static constexpr int kScaleOff = kIntOff + kBatchBytes;
+  static constexpr int kSmem = kScaleOff + kScaleRing * 1024 + 1024;
   static_assert(2 * kRaw >= kHalf && kRaw % 1024 == 0, "queries over raw places, halves in whole swizzle atoms");
   static_assert(kSmem <= 226 * 1024 - 5120, "static shared variables need the rest");
   static constexpr int kPieces = D / 16;                    // 16 bytes of a half for each converting thread
@@ -93,9 +94,9 @@ __device__ __forceinline__ uint4 load_shared_codes(uint32_t at) {
   return v;
 }
 
-__device__ __forceinline__ float load_shared_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+__device__ __forceinline__ uint32_t load_shared_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
   return v;
 }
 
@@ -205,9 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
   __shared__ __align__(16) Notice s_notice[2];
-  __shared__ __align__(8) int2 s_unit[kUnitRing];   // exponents of a step's key and value scales
+  __shared__ __align__(8) int2 s_unit[kScaleRing];   // exponents of a step's key and value scales
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
   __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], note_full[2], note_empty[2], conv_meet;
+  __shared__ __align__(8) uint64_t scale_raw[kScaleRing], scale_full[kScaleRing];
   __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
@@ -229,7 +231,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&note_full[s], 1);
-      mbar_init(&note_empty[s], kConvWarps);
+      mbar_init(&note_empty[s], kConvWarps + 1);
+    }
+    for (int s = 0; s < kScaleRing; ++s) {
+      mbar_init(&scale_raw[s], 1);
+      mbar_init(&scale_full[s], 1);
     }
     mbar_init(&conv_meet, kConvWarps);
     for (int s = 0; s < S; ++s) {
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   const uint32_t tmem = tmem_slot;
 
   const bool converts = warp >= kConvWarp0 && warp < kWalkWarp;
-  const bool walks = warp < kConvWarp0 || (warp >= kWalkWarp && warp <= kMmaWarp0 + 1);   // has items of its own
+  const bool walks = warp < kConvWarp0 || (warp >= kWalkWarp && warp < kScaleWarp);   // has items of its own
   Item* const items = s_items[!walks ? 0 : warp < kConvWarp0 ? warp : warp - kWalkWarp + kConvWarp0];   // written by lane 0
   if (walks && lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
   __syncwarp();
@@ -293,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
       int at = 0, steps = 0, k = 0;      // place in the raw ring, steps of the items before this one, items
       int places = C::kRawSlots;         // places in use: the pair's, or all
+      int keyed = 0;                     // steps whose scales are on their way
       uint32_t used = 0, sent = 0;       // by place: parity of its records, whether there are copies to wait for at the end
       bool ok = true;
       int4 split = make_int4(0, 0, 0, 0), found = make_int4(-1, -1, 0, 0);   // found: pages, keys, note bits of the lane's step
@@ -352,21 +359,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           }
           if (!wait(empty_at + at * 8, (used >> at & 1) ^ 1)) break;
           const int4 f = s_steps[(steps + j) % kStepRing];
-          // lanes 0, 1: the codes of a page's keys that exist; 2, 3: its scales (keys: of both kinds)
+          // lanes 0, 1: the codes of a page's keys that exist; 2, 3: with keys the scales of both kinds
           const int rows0 = f.x < 0 ? 0 : min(max(f.z, 0), kPage), rows1 = f.y < 0 ? 0 : min(max(f.z - kPage, 0), kPage);
           const int u = lane & 1, rows = u ? rows1 : rows0;
-          const uint32_t scales = keys ? 512 : 256, bytes = rows == 0 ? 0 : lane < 2 ? rows * D : scales;
-          const uint32_t bar = full_at + at * 8;
+          const int slot = (steps + j) % kScaleRing;
+          const uint32_t bytes = rows == 0 ? 0 : lane < 2 ? rows * D : keys ? 512 : 0;
+          const uint32_t bar = full_at + at * 8, scale_bar = smem_u32(scale_raw) + slot * 8;
           if (lane == 0) {
-            const uint32_t all = (rows0 + rows1) * D + (rows0 ? scales : 0) + (rows1 ? scales : 0);
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(all) : "memory");
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((rows0 + rows1) * D) : "memory");
+            if (keys)
+              asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(scale_bar),
+                           "r"((rows0 ? 512 : 0) + (rows1 ? 512 : 0))
+                           : "memory");
           }
           __syncwarp();
           if (lane < 4 && bytes > 0) {
             const uint8_t* block = pool + (u ? f.y : f.x) * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
-            const uint32_t to = base_at + C::raw_at(at) + (lane < 2 ? u * kPage * D : C::kRawCodes + u * 512 + 512 - scales);
-            bulk_copy(to, block + (lane >= 2 ? q8_key_scales_at(D) + 512 - scales : keys ? 0 : q8_values_at(D)), bytes, bar);
+            if (lane < 2) bulk_copy(base_at + C::raw_at(at) + u * kPage * D, block + (keys ? 0 : q8_values_at(D)), bytes, bar);
+            else bulk_copy(base_at + C::kScaleOff + slot * 1024 + u * 512, block + q8_key_scales_at(D), bytes, scale_bar);
           }
+          keyed += keys;
           sent |= 1u << at;
           go_on();
         }
@@ -390,7 +402,60 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
 #pragma unroll 1
       for (int p = 0; p < C::kRawSlots; ++p)
         if (sent >> p & 1) bar_wait(full_at + p * 8, (used >> p & 1) ^ 1, never_at, kWaitTries);
-    } else if (warp <= kMmaWarp0 + 1) {
+#pragma unroll 1
+      for (int t = max(0, keyed - kScaleRing); t < keyed; ++t)
+        bar_wait(smem_u32(scale_raw) + t % kScaleRing * 8, t / kScaleRing & 1, never_at, kWaitTries);
+    } else if (warp == kScaleWarp) {
+      // ---------------- scales ----------------
+      // A step's exponents, and its scales as what the codes are multiplied by;
+      // those of keys that are not there become 0.
+      const uint32_t base_at = smem_u32(smem);
+      bool ok = true;
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
+        return ok;
+      };
+      int steps = 0;   // of the items before this one
+#pragma unroll 1
+      for (int k = 0;; ++k) {
+        if (!wait(smem_u32(note_full) + (k & 1) * 8, k >> 1 & 1)) break;
+        const int nj = s_notice[k & 1].nj;
+        __syncwarp();
+        if (nj == 0) break;
+        if (lane == 0) bar_arrive(smem_u32(note_empty) + (k & 1) * 8);
+#pragma unroll 1
+        for (int j = 0; j < nj; ++j, ++steps) {
+          const int slot = steps % kScaleRing;
+          if (!wait(smem_u32(scale_raw) + slot * 8, steps / kScaleRing & 1)) break;
+          const int4 f = s_steps[steps % kStepRing];
+          const uint32_t at = base_at + C::kScaleOff + slot * 1024 + lane * 4;   // of keys lane + 32 e
+          float x[4], y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool there = lane + 32 * e < f.z && !(f.w >> (e >> 1) & 1);
+            const uint32_t from = at + (e >> 1) * 512 + (e & 1) * 128;
+            x[e] = there ? __uint_as_float(load_shared_u32(from)) : 0.f;
+            y[e] = there ? __uint_as_float(load_shared_u32(from + 256)) : 0.f;
+          }
+          const int ex = step_exponent(x), ey = step_exponent(y);
+          if (lane == 0) s_unit[slot] = make_int2(ex, ey);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            // A value scale that is no number becomes the score of whoever sees the
+            // key: as a factor of a weight it would reach rows that do not.
+            const bool number = y[e] * 0.f == 0.f;
+            const float kx = number ? x[e] * pow2_of(7 - ex) : __uint_as_float(0x7FC00000u), vx = number ? y[e] * pow2_of(7 - ey) : 0.f;
+            const uint32_t to = at + (e >> 1) * 512 + (e & 1) * 128;
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(pack2<true>(kx, kx)) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 256), "r"(pack2<true>(vx, vx)) : "memory");
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_u32(scale_full) + slot * 8);
+        }
+        if (!ok) break;
+      }
+      if (!ok) give_up();
+    } else {
       // ---------------- products of one stream ----------------
       // As in paged_attn.cu: the warp goes through this as one, with one elected
       // lane in front of the instructions.
@@ -569,51 +634,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         if ((half & 1) != team) continue;
         if (!wait(full_at + place * 8, parity)) break;
         const uint32_t src = base_at + C::raw_at(place) + from, dst = base_at + C::kRingOff + half % S * C::kHalf + to;
-        uint4 code[4];
+        const int slot = (steps + j) % kScaleRing;
+        if (!wait(smem_u32(scale_full) + slot * 8, (steps + j) / kScaleRing & 1)) break;
+        // all loads first: a load takes 300 cycles
+        const uint32_t scales = base_at + C::kScaleOff + slot * 1024 + (keys ? 0 : 256) + row0 * 4;
+        uint4 code[P];
+        uint32_t scale[P];
 #pragma unroll
-        for (int p = 0; p < 4; ++p) code[p] = load_shared_codes(src + p * kRowsOf * D);
-        const int4 f = s_steps[(steps + j) % kStepRing];
-        // Scales of keys lane + 32 e: the half's, and the values'. One way for both
-        // kinds of halves: a branch here doubles the code that follows.
-        float x[4], y[4];
-        const uint32_t scales = base_at + C::raw_at(place) + C::kRawCodes + lane * 4 + 256;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool there = lane + 32 * e < f.z && !(f.w >> (e >> 1) & 1);
-          const uint32_t from_e = scales + (e >> 1) * 512 + (e & 1) * 128;
-          x[e] = there ? load_shared_f32(from_e - (keys ? 256 : 0)) : 0.f;
-          y[e] = there ? load_shared_f32(from_e) : 0.f;
-        }
-        const int ex = step_exponent(x), ey = step_exponent(y);
-        if (keys && tt == 0) s_unit[(steps + j) % kUnitRing] = make_int2(ex, ey);
-        // A value scale that is no number becomes the score of whoever sees the
-        // key: as a factor of a weight it would reach rows that do not.
-        const float instead = keys ? __uint_as_float(0x7FC00000u) : 0.f, unit = pow2_of(7 - ex);
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = y[e] * 0.f == 0.f ? x[e] * unit : instead;
-          h[e] = pack2<true>(x[e], x[e]);
+        for (int p = 0; p < P; ++p) {
+          code[p] = load_shared_codes(src + p * kRowsOf * D);
+          scale[p] = load_shared_u32(scales + (p * kRowsOf / kPage) * 512 + p * kRowsOf % kPage * 4);
         }
         if (!wait(smem_u32(kv_empty) + half % S * 8, (half / S & 1) ^ 1)) break;
-        // the next pieces are read while these are converted; kept short: code that
-        // does not stay in the instruction caches costs more than the loop
-#pragma unroll 1
-        for (int p0 = 0; p0 < P; p0 += 4) {
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            const uint4 w = code[p];
-            // of row row0 + (p0 + p) * kRowsOf
-            const int row = (p0 + p) * kRowsOf;
-            const uint32_t sc = __shfl_sync(0xffffffffu, row < 64 ? (row < 32 ? h[0] : h[1]) : row < 96 ? h[2] : h[3], (row0 + row) % 32);
-            const __half2 scale = *reinterpret_cast<const __half2*>(&sc);
-            if (p0 + 4 < P) code[p] = load_shared_codes(src + (p0 + 4 + p) * kRowsOf * D);
-            const uint2 h0 = codes_to_f16(w.x, scale), h1 = codes_to_f16(w.y, scale);
-            const uint2 h2 = codes_to_f16(w.z, scale), h3 = codes_to_f16(w.w, scale);
-            const uint32_t at16 = dst + row * 128;
-            store_shared16(at16, make_uint4(h0.x, h0.y, h1.x, h1.y));
-            store_shared16(at16 ^ 16, make_uint4(h2.x, h2.y, h3.x, h3.y));
-          }
+        for (int p = 0; p < P; ++p) {
+          const uint4 w = code[p];
+          const __half2 by = *reinterpret_cast<const __half2*>(&scale[p]);
+          const uint2 h0 = codes_to_f16(w.x, by), h1 = codes_to_f16(w.y, by);
+          const uint2 h2 = codes_to_f16(w.z, by), h3 = codes_to_f16(w.w, by);
+          store_shared16(dst + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
+          store_shared16((dst ^ 16) + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -646,11 +686,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       if (ok) ok = __all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, progress_at, wait_tries));
       tc_fence_after();
     };
-    auto warp_arrive = [&](uint64_t* bar) {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
     while (true) {
       const Item& it = items[k & 1];
       if (it.nj <= 0) break;
@@ -665,7 +700,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       StepWalk w;
       w.start(b, it.t, it.j);
       const int pair = it.pair, nj = it.nj;
-      for (int j = 0; j < nj; ++j, w.next(b, it.t)) {
+      // Of an alternating tile of few rows the stream's first warp arrives for
+      // those that have none, and these pass over the steps.
+      const int idle = pair ? 0 : 4 - (it.t.ntok * b.group + 31) / 32;
+      const uint32_t arrivals = quarter == 0 ? 1 + idle : 1;
+      auto weights_there = [&](int u) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&p_full[stream][u])), "r"(arrivals) : "memory");
+      };
+      if (quarter >= 4 - idle) {
+        done = (nj + 1 - stream) / 2;
+        ns += done;
+      }
+      for (int j = quarter >= 4 - idle ? nj : 0; j < nj; ++j, w.next(b, it.t)) {
         if (!pair && (j & 1) != stream) continue;
         const uint32_t early = note_early<kStepRing>(s_step, step0 + j);
         warp_wait(&s_full[stream], ns & 1);
@@ -685,20 +733,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
                            : w.s.seq < 0 ? RowSpan{0, row.hi + prefix_len, 0} : RowSpan{row.lo, row.hi, sinks};
         const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
         const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
-        if (__all_sync(0xffffffffu, dead)) {
-          if (lane < 2) mbar_arrive(&p_full[stream][lane]);
-          ++done;
-          ++ns;
-          continue;
-        }
         const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
         if (__all_sync(0xffffffffu, none)) {
           const uint32_t zero[16] = {};
 #pragma unroll 1
           for (int c0 = 0; c0 < kStepKeys / 2; c0 += 16) tmem_st_u16(s_tmem + c0, zero);
           tmem_wait_st();
-          warp_arrive(&p_full[stream][0]);
-          warp_arrive(&p_full[stream][1]);
+          weights_there(0);
+          weights_there(1);
         } else {
           const int gone = flags & 3;
           const bool masked = gone != 0 || !__all_sync(0xffffffffu, dead || (c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys)));
@@ -718,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             tmem_wait_st();
           }
           // the step's factor of dot products, with room for -inf at both ends
-          const int2 un = s_unit[(step0 + j) % kUnitRing];
+          const int2 un = s_unit[(step0 + j) % kScaleRing];
           const float cs = fminf(fmaxf(cq * pow2_of(un.x - 7), 0x1p-126f), 0x1p127f);
           // a half of the scores (one page) at a time: the second for its
           // maximum, the first for its maximum and weights, the second again
@@ -774,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
               tmem_st_u16(s_tmem + u * (kPage / 2) + h / 2, pk);
             }
             tmem_wait_st();
-            warp_arrive(&p_full[stream][u]);
+            weights_there(u);
           }
           l = fmaf((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y), pow2_of(7 - un.y), l);
         }
