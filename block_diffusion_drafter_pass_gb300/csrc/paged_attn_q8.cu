@@ -37,8 +37,9 @@
 namespace dfl {
 namespace {
 
-constexpr int kConvWarp0 = 8, kConvWarps = 8;   // the softmax's are 0..7: TMEM lanes go by warp % 4
-constexpr int kWalkWarp = 16, kMmaWarp0 = 17, kScaleWarp = 19;
+constexpr int kWalkWarp = 0, kMmaWarp0 = 1, kScaleWarp = 3;   // first: the schedulers seem to prefer older warps
+constexpr int kSoftWarp0 = 4;                                 // eight: TMEM lanes go by warp % 4
+constexpr int kConvWarp0 = 12, kConvWarps = 8;
 constexpr int kThreads = 20 * 32;
 // Registers of a thread, by warpgroup: the launch's (96, as the kernel's bounds
 // make it) are dealt anew.
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
   __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], note_full[2], note_empty[2], conv_meet;
   __shared__ __align__(8) uint64_t scale_raw[kScaleRing], scale_full[kScaleRing];
-  __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S];
+  __shared__ __align__(8) uint64_t kv_full[2][S], kv_empty[S];   // full: by stream
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
   __shared__ Join join;
@@ -239,7 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
     }
     mbar_init(&conv_meet, kConvWarps);
     for (int s = 0; s < S; ++s) {
-      mbar_init(&kv_full[s], kConvWarps / 2);
+      mbar_init(&kv_full[0][s], kConvWarps / 2);
+      mbar_init(&kv_full[1][s], kConvWarps / 2);
       mbar_init(&kv_empty[s], 2);   // both streams
     }
     mbar_init(&q_full, kConvWarps);
@@ -270,9 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
 
-  const bool converts = warp >= kConvWarp0 && warp < kWalkWarp;
-  const bool walks = warp < kConvWarp0 || (warp >= kWalkWarp && warp < kScaleWarp);   // has items of its own
-  Item* const items = s_items[!walks ? 0 : warp < kConvWarp0 ? warp : warp - kWalkWarp + kConvWarp0];   // written by lane 0
+  const bool converts = warp >= kConvWarp0;
+  const bool walks = !converts && warp != kScaleWarp;   // has items of its own
+  Item* const items = s_items[!walks ? 0 : warp < kSoftWarp0 ? warp : warp - 1];   // written by lane 0
   if (walks && lane < sizeof(Item) / 4) reinterpret_cast<int*>(items)[lane] = reinterpret_cast<const int*>(s_first)[lane];
   __syncwarp();
   const uint32_t progress_at = smem_u32(&s_progress), never_at = smem_u32(&s_never);
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   // a pair (both streams take every step) and 2 for an alternating tile
   // (stream s takes the steps of parity s).
 
-  if (warp >= kWalkWarp) {
+  if (warp < kSoftWarp0) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRestRegs));
     if (warp == kWalkWarp) {
       // ---------------- the walk over keys and values, and their copies ----------------
@@ -458,121 +460,167 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
     } else {
       // ---------------- products of one stream ----------------
       // As in paged_attn.cu: the warp goes through this as one, with one elected
-      // lane in front of the instructions.
+      // lane in front of the instructions. Each stream has its own barriers of
+      // halves that came, so that one with alternating steps need not follow the
+      // other's; a half's place is free when two products (or one, committed
+      // twice) have read it.
       const int s = warp_uniform(warp - kMmaWarp0);
       const bool one = elect_one();
       const uint32_t q_low = sdesc_low(smem_u32(smem)), ring_low = q_low + (C::kRingOff >> 4);
       const uint32_t vring_low = vdesc_low<D>(smem_u32(smem)) + (C::kRingOff >> 4);
-      const uint32_t full_at = smem_u32(kv_full), empty_at = smem_u32(kv_empty);
+      const uint32_t full_at = smem_u32(&kv_full[s][0]), empty_at = smem_u32(kv_empty);
       const uint32_t s_at = smem_u32(&s_full[0]) + s * 8, p_at = smem_u32(&p_full[0][0]) + s * 16;
       const uint32_t turn_at = smem_u32(&turn[0]) + s * 8, pass_at = smem_u32(&turn[0]) + (s ^ 1) * 8;
       const uint32_t tm = warp_uniform(tmem);
       const uint32_t s_col = tm + s * kStepKeys, o_col = tm + kOCol + s * D;
-      int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps with scores, items, P tiles, rounds of pairs
+      int c = 0, steps = 0, k = 0, np = 0, turns = 0;   // ring halves, steps, items, P tiles, rounds of pairs
+      uint32_t got = 0;                                 // by ring slot: parity of the halves that came for this stream
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
+        return ok;
+      };
+      auto scores = [&](uint32_t q_at, int slot) {   // S = Q K^T
+        const uint32_t k_at = ring_low + slot * (C::kHalf >> 4);
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
+            tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
+          }
+          bar_commit(s_at);
+          bar_commit(empty_at + slot * 8);
+        }
+      };
+      auto product = [&](int slot, uint32_t add) {   // O (+)= P V: the first page's weights while the second's are still made
+        const uint32_t v_at = vring_low + slot * (C::kHalf >> 4);
+        if (one) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, kk > 0 ? 1u : add);
+        }
+        __syncwarp();
+        if (!wait(p_at + 8, np & 1)) return;
+        tc_fence_after();
+        if (one) {
+#pragma unroll
+          for (int kk = 4; kk < 8; ++kk)
+            tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
+          bar_commit(empty_at + slot * 8);
+        }
       };
       while (true) {
         const Item& it = items[k & 1];
-        const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj), lead = pair ? 1 : 2;
+        const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj);
         if (nj <= 0) break;
         __syncwarp();
-        const uint32_t q_at = q_low + (pair ? s * (C::kQ1Off >> 4) : 0);
         wait(smem_u32(&q_full), k & 1);
         ++k;
         uint32_t add = 0;
-        uint32_t takes = 0;   // bit i: the stream takes step j + i
-#pragma unroll 1
-        for (int j = -lead; j < nj && ok; ++j) {
-          const int pv = j >= 0, more = j + lead < nj;
-          if (j == nj - lead) {   // the scores are all issued
+        if (!pair) {
+          // its steps s, s + 2, ...: the first's scores, then a step's product and
+          // the scores of the step after the next, in the order of the ring's halves
+          const int first = min(2, nj);   // keys before the first values
+          int j = s;
+          uint32_t next = j < nj ? c + j : 0;   // half with the keys of step j
+          while (ok && j < nj + 2) {
+            if (j < nj) {
+              const int slot = next % S;
+              if (!wait(full_at + slot * 8, got >> slot & 1)) break;
+              got ^= 1u << slot;
+              tc_fence_after();
+              scores(q_low, slot);
+              if (one) bar_commit(empty_at + slot * 8);
+            }
+            if (j >= nj - 2 && j < nj) {   // the last scores
+              if (one) bar_commit(smem_u32(&q_empty));
+              if (lane == 0) next_item(b, it, items[k & 1]);
+              __syncwarp();
+            }
+            const int jv = j;   // its weights are due
+            if (jv >= nj) break;
+            const int half = c + first + jv + min(jv, max(nj - 2, 0)), slot = half % S;
+            if (!wait(full_at + slot * 8, got >> slot & 1) || !wait(p_at, np & 1)) break;
+            got ^= 1u << slot;
+            tc_fence_after();
+            product(slot, add);
+            if (!ok) break;
+            if (one) bar_commit(empty_at + slot * 8);
+            add = 1;
+            ++np;
+            __syncwarp();
+            j += 2;
+            next = half + 1;
+          }
+          if (s >= nj) {   // no step of its own
+            if (one) bar_commit(smem_u32(&q_empty));
             if (lane == 0) next_item(b, it, items[k & 1]);
             __syncwarp();
           }
-          const int ck = c + pv, vslot = c % S, kslot = ck % S;
-          // One lane for each thing to wait for, so that the waits are one. Of a
-          // pair that is everything but the second page's weights, and its streams
-          // take turns; an alternating tile's values go back as soon as they can.
-          const bool weights = pair ? pv : takes & 1;   // the softmax has arrived, or will
-          uint32_t early = 0;
-          {
-            if (pair && more) early = note_early<kStepRing>(s_step, steps);
-            bool need = lane == 0 && pv;
-            uint32_t bar = full_at + vslot * 8, parity = c / S & 1;
-            if (lane == 1) need = pair && more, bar = full_at + kslot * 8, parity = ck / S & 1;
-            if (lane == 2) need = weights, bar = p_at, parity = np & 1;
-            if (lane == 3) need = pair && (s == 1 || turns > 0), bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
-            int polls = kWaitPolls, seen = 0;
-            while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
-              const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
-              if (progress != seen) polls = kWaitPolls;
-              seen = progress;
-              if (progress < 0 || --polls == 0) {
-                ok = false;
-                break;
+          c += 2 * nj;
+        } else {
+          // every step, in turns: in each round the product of the step's weights
+          // with its values and the scores of the next, where the stream takes them
+          const uint32_t q_at = q_low + s * (C::kQ1Off >> 4);
+          uint32_t takes = 0;   // bit 0: the stream takes step j, bit 1: the next
+#pragma unroll 1
+          for (int j = -1; j < nj && ok; ++j) {
+            const int pv = j >= 0, more = j + 1 < nj;
+            if (!more) {   // the scores are all issued
+              if (lane == 0) next_item(b, it, items[k & 1]);
+              __syncwarp();
+            }
+            const int ck = c + pv, vslot = c % S, kslot = ck % S;
+            // one lane for each thing to wait for, so that the waits are one
+            const uint32_t early = more ? note_early<kStepRing>(s_step, steps) : 0u;
+            {
+              bool need = lane == 0 && pv;
+              uint32_t bar = full_at + vslot * 8, parity = got >> vslot & 1;
+              if (lane == 1) need = more, bar = full_at + kslot * 8, parity = got >> kslot & 1;
+              if (lane == 2) need = pv, bar = p_at, parity = np & 1;
+              if (lane == 3) need = s == 1 || turns > 0, bar = turn_at, parity = (s == 1 ? turns : turns - 1) & 1;
+              int polls = kWaitPolls, seen = 0;
+              while (!__all_sync(0xffffffffu, !need || bar_test(bar, parity))) {
+                const int progress = warp_uniform(*const_cast<const volatile int*>(&s_progress));
+                if (progress != seen) polls = kWaitPolls;
+                seen = progress;
+                if (progress < 0 || --polls == 0) {
+                  ok = false;
+                  break;
+                }
               }
             }
-          }
-          turns += pair;
-          if (!ok) break;
-          uint32_t take = ((j + lead) & 1) == s && more;
-          if (pair && more) take = warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1);
-          tc_fence_after();
-          if (takes & 1) {   // O (+)= P V
-            const uint32_t v_at = vring_low + vslot * (C::kHalf >> 4);
-            // the first page's weights while the second's are still made
-            if (one) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, kk > 0 ? 1u : add);
-            }
-            __syncwarp();
-            wait(p_at + 8, np & 1);
+            ++turns;
             if (!ok) break;
+            if (pv) got ^= 1u << vslot;
+            if (more) got ^= 1u << kslot;
+            const uint32_t take = more ? warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1) : 0u;
             tc_fence_after();
-            if (one) {
-#pragma unroll
-              for (int kk = 4; kk < 8; ++kk)
-                tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
-              bar_commit(empty_at + vslot * 8);
+            if (takes & 1) {
+              product(vslot, add);
+              if (!ok) break;
+              add = 1;
+            } else if (pv) {
+              if (!wait(p_at + 8, np & 1)) break;
+              if (one) bar_arrive(empty_at + vslot * 8);
             }
-            add = 1;
-          } else if (pv) {
-            if (weights) wait(p_at + 8, np & 1);
-            if (one) bar_arrive(empty_at + vslot * 8);
-          }
-          np += weights;
-          __syncwarp();
-          if (!pair && more) {
-            wait(full_at + kslot * 8, ck / S & 1);
-            if (!ok) break;
-          }
-          if (pair && one) bar_arrive(pass_at);   // the other stream's waits pass under these products
-          if (take) {   // S = Q K^T
-            const uint32_t k_at = ring_low + kslot * (C::kHalf >> 4);
-            if (one) {
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * C::kBox + (kk & 3) * 32) >> 4;
-                tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
-              }
-              bar_commit(s_at);
-              bar_commit(empty_at + kslot * 8);
+            np += pv;
+            __syncwarp();
+            if (one) bar_arrive(pass_at);   // the other stream's waits pass under these products
+            if (take) {
+              scores(q_at, kslot);
+            } else if (more && one) {
+              bar_arrive(s_at);   // the softmax follows every step of a pair
+              bar_arrive(empty_at + kslot * 8);
             }
-            takes |= 1u << lead;
-          } else if (more && one) {
-            if (pair) bar_arrive(s_at);   // the softmax follows every step of a pair
-            bar_arrive(empty_at + kslot * 8);
+            if (one && j + 2 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
+            __syncwarp();
+            c = ck + more;
+            steps += more;
+            takes = take;
           }
-          if (one) {
-            if (more && j + lead + 1 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
-          }
-          __syncwarp();
-          c = ck + more;
-          steps += more;
-          takes >>= 1;
         }
+        if (!pair) steps += nj;
         if (!ok) {
           give_up();
           break;
@@ -659,7 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         __syncwarp();
         if (lane == 0) {
           bar_arrive(empty_at + place * 8);
-          bar_arrive(smem_u32(kv_full) + half % S * 8);
+          if (pair || !(j & 1)) bar_arrive(smem_u32(&kv_full[0][half % S]));
+          if (pair || (j & 1)) bar_arrive(smem_u32(&kv_full[1][half % S]));
         }
       }
       if (!ok) break;
@@ -669,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---------------- softmax and output ----------------
-    const int stream = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const int stream = (warp - kSoftWarp0) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t s_tmem = lane_tmem + stream * kStepKeys;
     const uint32_t o_tmem = lane_tmem + kOCol + stream * D;
@@ -709,6 +758,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         __syncwarp();
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&p_full[stream][u])), "r"(arrivals) : "memory");
       };
+      // Steps that begin at own_a .. own_b of sequence `alone` (if the warp's rows
+      // are of one), or up to pre_b of the prefix: every row sees all their keys.
+      int own_a, own_b, pre_b, alone;
+      {
+        const bool live = row.token >= 0;
+        alone = __reduce_min_sync(0xffffffffu, live ? row.seq : kNoEnd);
+        if (alone != __reduce_max_sync(0xffffffffu, live ? row.seq : -1)) alone = kNoEnd;
+        own_a = __reduce_max_sync(0xffffffffu, live ? row.lo : 0);
+        const int last = __reduce_min_sync(0xffffffffu, live ? row.hi : kNoEnd);
+        own_b = min(last, b.len[min(alone, b.n_seq - 1)] - 1) - (kStepKeys - 1);
+        pre_b = min(last + prefix_len, prefix_len - 1) - (kStepKeys - 1);
+      }
       if (quarter >= 4 - idle) {
         done = (nj + 1 - stream) / 2;
         ns += done;
@@ -726,39 +787,42 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           continue;
         }
         if (done == 0) cq = s_qc[(k - 1) & 1][(pair ? stream * kRows : 0) + r];
-        // columns [0, c_hi) less those in [c_sink, c_lo) are seen (rows of no
-        // token, which nobody reads, need no mask)
-        const bool dead = row.token < 0;
-        const RowSpan sp = dead || (w.s.seq >= 0 && w.s.seq != row.seq) ? RowSpan{0, -1, 0}
-                           : w.s.seq < 0 ? RowSpan{0, row.hi + prefix_len, 0} : RowSpan{row.lo, row.hi, sinks};
-        const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
-        const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
-        const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
-        if (__all_sync(0xffffffffu, none)) {
-          const uint32_t zero[16] = {};
+        const int gone = flags & 3;
+        bool none = false;
+        const bool masked = gone != 0 || (w.s.seq < 0 ? w.s.base > pre_b : w.s.seq != alone || w.s.base < own_a || w.s.base > own_b);
+        if (masked) {
+          // columns [0, c_hi) less those in [c_sink, c_lo) are seen
+          const RowSpan sp = row.token < 0 || (w.s.seq >= 0 && w.s.seq != row.seq) ? RowSpan{0, -1, 0}
+                             : w.s.seq < 0 ? RowSpan{0, row.hi + prefix_len, 0} : RowSpan{row.lo, row.hi, sinks};
+          const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
+          const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
+          none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
+          if (__all_sync(0xffffffffu, none)) {
+            const uint32_t zero[16] = {};
 #pragma unroll 1
-          for (int c0 = 0; c0 < kStepKeys / 2; c0 += 16) tmem_st_u16(s_tmem + c0, zero);
-          tmem_wait_st();
-          weights_there(0);
-          weights_there(1);
-        } else {
-          const int gone = flags & 3;
-          const bool masked = gone != 0 || !__all_sync(0xffffffffu, dead || (c_hi >= kStepKeys && (c_lo <= 0 || c_sink >= kStepKeys)));
-          if (gone != 0) report_gone(a.b.status, gone, c_lo, c_hi, c_sink);
-          if (masked) {
-            // scores of keys that the row does not see become -inf in place
-#pragma unroll 1
-            for (int c0 = 0; c0 < kStepKeys; c0 += 32) {
-              const unsigned long long seen = slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
-              const uint32_t vis = gone >> (c0 / kPage) & 1 ? 0u : static_cast<uint32_t>(seen);
-              float x[32];
-              tmem_ld32(s_tmem + c0, x);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) x[c] = vis >> c & 1 ? x[c] : -INFINITY;
-              tmem_st32(s_tmem + c0, x);
-            }
+            for (int c0 = 0; c0 < kStepKeys / 2; c0 += 16) tmem_st_u16(s_tmem + c0, zero);
             tmem_wait_st();
+            weights_there(0);
+            weights_there(1);
+            ++done;
+            ++ns;
+            continue;
           }
+          if (gone != 0) report_gone(a.b.status, gone, c_lo, c_hi, c_sink);
+          // scores of keys that the row does not see become -inf in place
+#pragma unroll 1
+          for (int c0 = 0; c0 < kStepKeys; c0 += 32) {
+            const unsigned long long seen = slot_bits(0, c_hi - c0) & (slot_bits(c_lo - c0, 64) | slot_bits(0, c_sink - c0));
+            const uint32_t vis = gone >> (c0 / kPage) & 1 ? 0u : static_cast<uint32_t>(seen);
+            float x[32];
+            tmem_ld32(s_tmem + c0, x);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = vis >> c & 1 ? x[c] : -INFINITY;
+            tmem_st32(s_tmem + c0, x);
+          }
+          tmem_wait_st();
+        }
+        {
           // the step's factor of dot products, with room for -inf at both ends
           const int2 un = s_unit[(step0 + j) % kScaleRing];
           const float cs = fminf(fmaxf(cq * pow2_of(un.x - 7), 0x1p-126f), 0x1p127f);
@@ -771,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           load(0);
           mx = fmaf(fmaxf(mx, row_max(sv)), cs, -kBias);
           // each row by itself, so that it does not depend on its neighbours
-          const int need = masked && none ? kNoUnit : un.y;
+          const int need = none ? kNoUnit : un.y;
           const bool grows = need > unit || mx > mref + kRescaleLog2;
           if (__any_sync(0xffffffffu, grows)) {
             const float nm = grows ? fmaxf(mref, mx) : mref;
