@@ -43,10 +43,11 @@ constexpr int kConvWarp0 = 12, kConvWarps = 8;
 constexpr int kThreads = 20 * 32;
 // Registers of a thread, by warpgroup: the launch's (96, as the kernel's bounds
 // make it) are dealt anew.
-constexpr int kLaunchRegs = 96, kSoftRegs = 136, kConvRegs = 64, kRestRegs = 80;
+constexpr int kLaunchRegs = 96, kSoftRegs = 144, kConvRegs = 64, kRestRegs = 64;
 static_assert(2 * kSoftRegs + 2 * kConvRegs + kRestRegs <= 5 * kLaunchRegs, "setmaxnreg waits for registers that the launch must have");
 static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs, "inc must go up and dec down");
 constexpr int kAhead = 16;       // steps that the walk looks up at a time
+constexpr int kScalesAhead = 2;  // steps that scales are ahead of their keys
 // The walk is ahead of the products by these and the halves of both rings (8
 // steps at most); scales are held of what is behind the first ring.
 constexpr int kStepRing = 32;
@@ -138,47 +139,60 @@ __device__ __forceinline__ uint32_t vdesc_low(uint32_t saddr) {
 // A row's power of two 2^(e - 126), e the biased exponent of its largest value.
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
+// An item's queries into shared memory as fp16, by the converting warps: a row
+// times the power of two that puts its largest finite value between 1/2 and 1
+// (its infinities and NaN stay what they are), and s_qc what its dot products are
+// multiplied by for that.
 template <int D, bool F16>
 __device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Notice& r, uint32_t q_at, float* s_qc, int ct) {
-  constexpr int kOf = D / 8, kPass = kConvWarps * 32 / kOf, kAtOnce = 4;
+  constexpr int kOf = D / 8, kPass = kConvWarps * 32 / kOf, kAtOnce = 4;   // lanes of a row, rows at a time
+  constexpr uint32_t kInf = F16 ? 0x7C00u : 0x7F80u;
   const int c = ct % kOf, G = a.b.group, stream_rows = a.stream_tokens * G;
   const int n = (r.pair ? 2 : 1) * stream_rows, end = r.t0 + r.ntok;
+  const int dt = kPass / G, dg = kPass - dt * G;
+  int token = r.t0 + ct / kOf / G, g = ct / kOf % G;   // a stream's tokens follow the other's
 #pragma unroll 1
-  for (int base = 0; base < n; base += kPass * kAtOnce) {
+  for (int i0 = ct / kOf; i0 - ct / kOf < n; i0 += kPass * kAtOnce) {
     uint4 w[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      const int i = base + u * kPass + ct / kOf, token = r.t0 + i / G;   // a stream's tokens follow the other's
       w[u] = make_uint4(0, 0, 0, 0);
-      if (i < n && token < end)
-        w[u] = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + static_cast<long long>(r.head * G + i % G) * D) + c);
+      if (i0 + u * kPass < n && token < end)
+        w[u] = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + static_cast<long long>(r.head * G + g) * D) + c);
+      token += dt;
+      g += dg;
+      if (g >= G) g -= G, ++token;
     }
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      const int i = base + u * kPass + ct / kOf;
-      float x[8];
-      uint32_t top = 0;
+      const int i = i0 + u * kPass;
+      uint32_t top = 0;   // magnitudes order as their bits
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = unpack2<F16>((&w[u].x)[e]);
-        x[2 * e] = f.x, x[2 * e + 1] = f.y;
-      }
+      for (int e = 0; e < 4; ++e) top = __vmaxu2(top, (&w[u].x)[e] & 0x7FFF7FFFu);
+      if (max(top & 0xFFFFu, top >> 16) >= kInf) {
+        top = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {   // of the finite ones: the others stay what they are
-        const uint32_t b = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-        top = b < 0x7F800000u ? max(top, b) : top;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t m = (&w[u].x)[e] & 0x7FFF7FFFu;
+          top = max(top, max((m & 0xFFFFu) < kInf ? m & 0xFFFFu : 0u, (m >> 16) < kInf ? m >> 16 : 0u));
+        }
       }
+      top = max(top & 0xFFFFu, top >> 16);
 #pragma unroll
       for (int o = kOf / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = static_cast<int>(top >> 23), up = 126 - e;   // times 2^up, in two factors: -128..126
-      const float f0 = pow2_of(up >> 1), f1 = pow2_of(up - (up >> 1));
+      // (of the largest bf16 values 2^-126 leaves 4)
+      const int up = max(126 - static_cast<int>(__float_as_uint(unpack2<F16>(top).x) >> 23), -126);
+      const float f = pow2_of(up);
       uint4 h;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) (&h.x)[k] = pack2<true>(x[2 * k] * f0 * f1, x[2 * k + 1] * f0 * f1);
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = unpack2<F16>((&w[u].x)[k]);
+        (&h.x)[k] = pack2<true>(x.x * f, x.y * f);
+      }
       if (i < n) {
         const int stream = i >= stream_rows, row = i - stream * stream_rows;
         store_shared16(q_at + stream * Cfg<D>::kQ1Off + (c >> 3) * Cfg<D>::kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4), h);
-        if (c == 0) s_qc[stream * kRows + row] = a.scale_log2 * pow2_of(-(up >> 1)) * pow2_of(-(up - (up >> 1)));
+        if (c == 0) s_qc[stream * kRows + row] = a.scale_log2 * pow2_of(-up);
       }
     }
   }
@@ -340,12 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         if (places > was) wait(smem_u32(&q_empty), (k - 1) & 1);
         if (at >= places) at = 0;
         if (!ok || !notice(Notice{nj, pair, head, it.t.t0, it.t.ntok, {}})) break;
-#pragma unroll 1
-        for (int i = 1 - 2 * lead; i < 2 * nj; ++i) {   // round i >> 1: values, then keys
-          const bool keys = i & 1;
-          const int j = (i >> 1) + (keys ? lead : 0);
-          if (j < 0 || j >= nj) continue;
-          if (keys && j % kAhead == 0) {
+        // Scales go kScalesAhead steps ahead of their keys: a warp has work with them.
+        auto bring_scales = [&](int j) {
+          if (j % kAhead == 0) {
             int4 f = found;
             if (lane < kAhead && j + lane < nj) {
               if (f.x < 0 || f.x >= a.b.n_pages) f.x = -1, f.w |= 1;
@@ -359,28 +370,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             if (lane < kAhead && of_j < of.nj) found = look_up(a, b, of, of_j);
             __syncwarp();
           }
+          const int4 f = s_steps[(steps + j) % kStepRing];
+          const int slot = (steps + j) % kScaleRing, page = lane ? f.y : f.x;
+          const bool has0 = f.x >= 0 && f.z > 0, has1 = f.y >= 0 && f.z > kPage;
+          const uint32_t bar = smem_u32(scale_raw) + slot * 8;
+          if (lane == 0)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((has0 ? 512 : 0) + (has1 ? 512 : 0)) : "memory");
+          __syncwarp();
+          if (lane < 2 && (lane ? has1 : has0))
+            bulk_copy(base_at + C::kScaleOff + slot * 1024 + lane * 512,
+                      pool + page * page_bytes + static_cast<long long>(head) * q8_block_bytes(D) + q8_key_scales_at(D), 512, bar);
+          ++keyed;
+        };
+#pragma unroll 1
+        for (int i = 1 - 2 * lead - 2 * kScalesAhead; i < 2 * nj; ++i) {   // round i >> 1: values, then scales and keys
+          const bool keys = i & 1;
+          const int j = (i >> 1) + (keys ? lead : 0);
+          if (keys && j + kScalesAhead < nj) bring_scales(j + kScalesAhead);
+          if (j < 0 || j >= nj) continue;
           if (!wait(empty_at + at * 8, (used >> at & 1) ^ 1)) break;
           const int4 f = s_steps[(steps + j) % kStepRing];
-          // lanes 0, 1: the codes of a page's keys that exist; 2, 3: with keys the scales of both kinds
+          // a lane for each page's keys that exist
           const int rows0 = f.x < 0 ? 0 : min(max(f.z, 0), kPage), rows1 = f.y < 0 ? 0 : min(max(f.z - kPage, 0), kPage);
-          const int u = lane & 1, rows = u ? rows1 : rows0;
-          const int slot = (steps + j) % kScaleRing;
-          const uint32_t bytes = rows == 0 ? 0 : lane < 2 ? rows * D : keys ? 512 : 0;
-          const uint32_t bar = full_at + at * 8, scale_bar = smem_u32(scale_raw) + slot * 8;
-          if (lane == 0) {
+          const int rows = lane ? rows1 : rows0;
+          const uint32_t bar = full_at + at * 8;
+          if (lane == 0)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"((rows0 + rows1) * D) : "memory");
-            if (keys)
-              asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(scale_bar),
-                           "r"((rows0 ? 512 : 0) + (rows1 ? 512 : 0))
-                           : "memory");
-          }
           __syncwarp();
-          if (lane < 4 && bytes > 0) {
-            const uint8_t* block = pool + (u ? f.y : f.x) * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
-            if (lane < 2) bulk_copy(base_at + C::raw_at(at) + u * kPage * D, block + (keys ? 0 : q8_values_at(D)), bytes, bar);
-            else bulk_copy(base_at + C::kScaleOff + slot * 1024 + u * 512, block + q8_key_scales_at(D), bytes, scale_bar);
-          }
-          keyed += keys;
+          if (lane < 2 && rows > 0)
+            bulk_copy(base_at + C::raw_at(at) + lane * kPage * D,
+                      pool + (lane ? f.y : f.x) * page_bytes + static_cast<long long>(head) * q8_block_bytes(D) + (keys ? 0 : q8_values_at(D)),
+                      rows * D, bar);
           sent |= 1u << at;
           go_on();
         }
