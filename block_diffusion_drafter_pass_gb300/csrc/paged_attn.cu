@@ -827,6 +827,14 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p,
   return e == cudaSuccess ? launch_combine(a, D, F16, p, s) : e;
 }
 
+// 8-bit pages: the rows of a tile for the kernel of few rows (16 or 32), or 0 for
+// the one of 128.
+int few_rows(const dflash_paged_batch& b, bool shared) {
+  const int group = b.n_heads / b.n_kv_heads;
+  const long long rows = static_cast<long long>(b.n_tokens) * group, tiles = shared ? 1 : b.n_seq;
+  return group <= 16 && rows <= 16 * tiles ? 16 : group <= 32 && rows <= 32 * tiles ? 32 : 0;
+}
+
 std::atomic<int> g_wait_tries{kWaitTries};
 
 dflash_status refuse(const char* why) {
@@ -854,7 +862,10 @@ dflash_status run(const dflash_paged_batch& b, PagedAttnArgs& a, void* workspace
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (b.dtype & DFLASH_POOL_Q8) {
-    cudaError_t e = launch_paged_attn_q8(a, b.head_dim, b.dtype & DFLASH_FP16, p.device, p.ctas, s);
+    const int rows = few_rows(b, a.shared);
+    if (rows > 0) a.stream_tokens = a.tile_tokens = rows / a.b.group;
+    cudaError_t e = rows > 0 ? launch_paged_attn_q8_few(a, b.head_dim, b.dtype & DFLASH_FP16, rows, p.device, p.ctas, s)
+                             : launch_paged_attn_q8(a, b.head_dim, b.dtype & DFLASH_FP16, p.device, p.ctas, s);
     if (e == cudaSuccess) e = launch_combine(a, b.head_dim, b.dtype & DFLASH_FP16, p, s);
     return e == cudaSuccess ? DFLASH_OK : fail_cuda("paged attention: kernel launch failed");
   }
