@@ -34,19 +34,23 @@ constexpr int kLeastE = -80, kNoUnit = -(1 << 20);   // smaller scales count as 
 
 template <int D, int MT>
 struct Few {
-  static constexpr int kWarps = MT == 1 ? 10 : 8;
+  static constexpr int kWarps = D * MT <= 128 ? 12 : 8;
+  static constexpr int kSlots = D * MT <= 128 && D == 128 ? 3 : 4;   // of a warp's ring
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRowsMax = 16 * MT;
-  // a unit: 32 key rows, 32 value rows, 32 key and 32 value scales; rows 16 bytes
-  // apart from a multiple of 128, so that neighbours lie in other banks
+  // a half of a unit: 32 key rows, then all 32 key and 32 value scales, or 32 value
+  // rows; rows 16 bytes apart from a multiple of 128, so that neighbours lie in other banks
   static constexpr int kRow = D + 16;
-  static constexpr int kValues = kUnit * kRow, kScales = 2 * kUnit * kRow, kStage = kScales + 8 * kUnit;
+  static constexpr int kScales = kUnit * kRow, kHalf = kScales + 8 * kUnit;
   static constexpr int kQBytes = kRowsMax * D * 2;
   static constexpr int kStageOff = kBatchBytes + kQBytes;
-  static constexpr int kJoinRow = D + 4;   // floats
-  static constexpr int kSmem = kStageOff + kWarps * 2 * kStage;
-  static_assert(kBatchBytes % 16 == 0 && kStage % 16 == 0, "16-byte copies");
-  static_assert(kWarps * kRowsMax * kJoinRow * 4 <= kWarps * 2 * kStage, "the join's rows lie over the units");
+  // The join's rows, in floats, and where four from d on lie in one: so that both
+  // the lanes that hold a row's columns and those that add them meet all banks.
+  static constexpr int kJoinRow = D == 128 ? D + 16 : D + 8;
+  static __device__ __forceinline__ int join_at(int d) { return d ^ (d >> 5 & (D / 32 - 1)) << 2; }
+  static constexpr int kSmem = kStageOff + kWarps * kSlots * kHalf;
+  static_assert(kBatchBytes % 16 == 0 && kHalf % 16 == 0, "16-byte copies");
+  static_assert(kWarps * kRowsMax * kJoinRow * 4 <= kWarps * kSlots * kHalf, "the join's rows lie over the units");
   static_assert(kSmem <= 220 * 1024, "static shared variables need the rest");
 };
 
@@ -85,7 +89,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
   Batch& b = *reinterpret_cast<Batch*>(smem);
   uint8_t* const s_q = smem + kBatchBytes;   // [D / 16][MT][32 lanes][4 words]
   __shared__ float s_qc[C::kRowsMax];
-  __shared__ float2 s_ml[W][C::kRowsMax];
+  __shared__ float2 s_ml[W][C::kRowsMax];   // maximum and sum
   __shared__ long long s_sum[kThreads / 32];
   __shared__ Item s_first[2], s_items[2];
 
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
   __syncthreads();
   if (tid < sizeof(Item) / 4) reinterpret_cast<int*>(s_items)[tid] = reinterpret_cast<const int*>(s_first)[tid];
   __syncthreads();
-  const uint32_t stage_at = smem_u32(smem) + C::kStageOff + warp * 2 * C::kStage;
+  const uint32_t ring_at = smem_u32(smem) + C::kStageOff + warp * C::kSlots * C::kHalf;
   const uint8_t* const pool = reinterpret_cast<const uint8_t*>(a.b.pool);
   const long long page_bytes = static_cast<long long>(a.b.n_kv) * q8_block_bytes(D);
   const int G = a.b.group;
@@ -189,29 +193,38 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
       return Unit{__shfl_sync(0xffffffffu, x.page, i & 31), __shfl_sync(0xffffffffu, x.base, i & 31),
                   __shfl_sync(0xffffffffu, x.seq, i & 31), __shfl_sync(0xffffffffu, x.end, i & 31)};
     };
-    auto bring = [&](const Unit& x, int stage) {   // a group of copies, whether there is something to copy or not
-      if (x.page >= 0) {
-        const uint8_t* block = pool + x.page * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
-        const int slot0 = x.base % kPage;
-        const uint32_t to = stage_at + stage * C::kStage;
+    auto bring = [&](int page, int base, bool keys, int slot) {   // a group of copies, whether there is something to copy or not
+      if (page >= 0) {
+        const uint8_t* block = pool + page * page_bytes + static_cast<long long>(head) * q8_block_bytes(D);
+        const int slot0 = base % kPage;
+        const uint32_t to = ring_at + slot * C::kHalf;
         constexpr int kOfRow = D / 16, kRowsAtOnce = 32 / kOfRow;
         const int r = lane / kOfRow, e = lane % kOfRow * 16;
-        const uint8_t* src = block + (slot0 + r) * D + e;
+        const uint8_t* src = block + (keys ? 0 : q8_values_at(D)) + (slot0 + r) * D + e;
 #pragma unroll
-        for (int i = 0; i < kUnit; i += kRowsAtOnce) {
-          copy_async16(to + (r + i) * C::kRow + e, src + i * D);
-          copy_async16(to + C::kValues + (r + i) * C::kRow + e, src + q8_values_at(D) + i * D);
-        }
-        if (lane < 16)   // 8 pieces of each kind
+        for (int i = 0; i < kUnit; i += kRowsAtOnce) copy_async16(to + (r + i) * C::kRow + e, src + i * D);
+        if (keys && lane < 16)   // 8 pieces of each kind
           copy_async16(to + C::kScales + lane * 16, block + q8_key_scales_at(D) + (lane >> 3) * 4 * kPage + slot0 * 4 + (lane & 7) * 16);
       }
       copy_async_commit();
     };
 
     const int units = (4 * nj - warp + W - 1) / W;   // of the warp
-    Unit looked = look_up(lane);
-    Unit next = unit_of(looked, 0);
-    if (units > 0) bring(next, 0);
+    // Halves in a ring, keys and values in turn: up to kSlots - 1 are under way. The
+    // lanes hold 32 units' pages, those of this unit and of what is to be brought.
+    Unit looked = look_up(lane), ahead = looked;
+    int brought = 0, to_slot = 0, slot = 0;   // halves; places to fill and to read
+    auto bring_next = [&]() {
+      const int i = brought >> 1;
+      const bool keys = !(brought & 1);
+      if (keys && i > 0 && (i & 31) == 0) ahead = look_up(i + lane);
+      const int page = __shfl_sync(0xffffffffu, ahead.page, i & 31), base = __shfl_sync(0xffffffffu, ahead.base, i & 31);
+      bring(page, base, keys, to_slot);
+      to_slot = to_slot + 1 < C::kSlots ? to_slot + 1 : 0;
+      ++brought;
+    };
+#pragma unroll
+    for (int h = 0; h < C::kSlots - 1; ++h) bring_next();
     __syncthreads();   // the queries are there, and the next item
     float o[MT][D / 8][4], mref[MT][2], l[MT][2];
     int unit[MT][2];
@@ -225,18 +238,14 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
     }
 #pragma unroll 1
     for (int i = 0; i < units; ++i) {
-      const Unit now = next;
-      if (i + 1 < units) {
-        if (((i + 1) & 31) == 0) looked = look_up(i + 1 + lane);
-        next = unit_of(looked, i + 1);
-        bring(next, (i + 1) & 1);
-        copy_async_wait<1>();
-      } else {
-        copy_async_wait<0>();
-      }
-      __syncwarp();
-      if (now.page == -2) continue;
-      if (now.page == -1) {   // a row that would see a key of the page says so
+      if (i > 0 && (i & 31) == 0) looked = ahead;
+      const Unit now = unit_of(looked, i);
+      bring_next();
+      if (now.page < 0) {   // both halves are empty
+        bring_next();
+        slot = slot + 2 < C::kSlots ? slot + 2 : slot + 2 - C::kSlots;
+        if (now.page == -2) continue;
+        // a row that would see a key of the page says so
         bool sees = false;
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -248,7 +257,10 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
         if (sees) latch_status(a.b.status, kDevBounds);
         continue;
       }
-      const uint32_t at = stage_at + (i & 1) * C::kStage;
+      copy_async_wait<C::kSlots - 1>();
+      __syncwarp();
+      const uint32_t at = ring_at + slot * C::kHalf;
+      slot = slot + 1 < C::kSlots ? slot + 1 : 0;
       // scales: those of slots past the end become 0, a value scale that is no
       // number the score of whoever sees the key; value scales in units of 2^(ev + 1)
       int ev;
@@ -371,6 +383,12 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
         }
       }
       // ---- output: two steps of 16 keys ----
+      __syncwarp();   // the keys' place is read
+      bring_next();
+      copy_async_wait<C::kSlots - 1>();
+      __syncwarp();
+      const uint32_t values_at = ring_at + slot * C::kHalf;
+      slot = slot + 1 < C::kSlots ? slot + 1 : 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         constexpr int kWords = D / 32;   // of a key's dims for this lane
@@ -378,7 +396,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = 16 * h + 8 * (e >> 1) + 2 * c + (e & 1);
-          const uint32_t from = at + C::kValues + key * C::kRow + g * (D / 8);
+          const uint32_t from = values_at + key * C::kRow + g * (D / 8);
           if constexpr (D == 128) asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v[e][0]), "=r"(v[e][1]), "=r"(v[e][2]), "=r"(v[e][3]) : "r"(from));
           else asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[e][0]), "=r"(v[e][1]) : "r"(from));
         }
@@ -402,6 +420,7 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
     }
 
     // ---- the warps' parts joined ----
+    copy_async_wait<0>();   // (of what is behind the item's end, nothing)
     __syncthreads();
     float* const s_o = reinterpret_cast<float*>(smem + C::kStageOff);   // [W][kRowsMax][kJoinRow]
 #pragma unroll
@@ -413,28 +432,32 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         const int r = m * 16 + u * 8 + g;
         if (c == 0) s_ml[warp][r] = make_float2(mref[m][u] + static_cast<float>(unit[m][u]), x);
-        float* to = s_o + (warp * C::kRowsMax + r) * C::kJoinRow + 2 * c * (D / 8);   // dims of columns 2 c, then 2 c + 1
+        float* to = s_o + (warp * C::kRowsMax + r) * C::kJoinRow;   // dims of columns 2 c, then 2 c + 1
+        if (units <= 0) continue;
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
-          to[t] = o[m][t][2 * u];
-          to[D / 8 + t] = o[m][t][2 * u + 1];
+        for (int t = 0; t < D / 8; t += 4) {
+          const int d = 2 * c * (D / 8) + t;
+          *reinterpret_cast<float4*>(to + C::join_at(d)) = make_float4(o[m][t][2 * u], o[m][t + 1][2 * u], o[m][t + 2][2 * u], o[m][t + 3][2 * u]);
+          *reinterpret_cast<float4*>(to + C::join_at(d + D / 8)) =
+              make_float4(o[m][t][2 * u + 1], o[m][t + 1][2 * u + 1], o[m][t + 2][2 * u + 1], o[m][t + 3][2 * u + 1]);
         }
       }
     }
     __syncthreads();
     const bool whole = nj == it.t.n;
+    const int parts = min(W, 4 * nj);   // warps that had units
 #pragma unroll 1
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float top = -INFINITY, sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[w][r].x);
+#pragma unroll 4
+      for (int w = 0; w < parts; ++w) top = fmaxf(top, s_ml[w][r].x);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
+#pragma unroll 4
+      for (int w = 0; w < parts; ++w) {
         const float2 ml = s_ml[w][r];
         const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * C::kRowsMax + r) * C::kJoinRow + d);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * C::kRowsMax + r) * C::kJoinRow + C::join_at(d));
         sum = fmaf(f, ml.y, sum);
         acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
       }
