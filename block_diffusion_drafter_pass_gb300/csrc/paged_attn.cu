@@ -786,14 +786,29 @@ const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_s
 
 // The tile's shape and the workspace's layout for a batch.
 struct Plan {
+  Q8Few few;
   int device, ctas, stream_tokens, tile_tokens, rows_cap;
   size_t piece_off, ml_off, o_off, bytes;   // the split records come first
 };
 
-bool make_plan(const dflash_paged_batch& b, Plan& p) {
+// Whether a batch over 8-bit pages is one for the kernel of few rows, and how.
+Q8Few few_rows(const dflash_paged_batch& b, bool shared) {
+  const int group = b.n_heads / b.n_kv_heads;
+  const long long rows = static_cast<long long>(b.n_tokens) * group, tiles = shared ? 1 : b.n_seq;
+  Q8Few few{0, 1};
+  if (!(b.dtype & DFLASH_POOL_Q8)) return few;
+  if (group <= 16 && rows <= 16 * tiles) few.rows = 16;
+  else if (group <= 32 && rows <= 32 * tiles) few.rows = 32;
+  if (few.rows == 32 || (few.rows == 16 && tiles * b.n_kv_heads > 8)) few.per_sm = 2;
+  return few;
+}
+
+bool make_plan(const dflash_paged_batch& b, bool shared, Plan& p) {
   if (cudaGetDevice(&p.device) != cudaSuccess ||
       cudaDeviceGetAttribute(&p.ctas, cudaDevAttrMultiProcessorCount, p.device) != cudaSuccess)
     return false;
+  p.few = few_rows(b, shared);
+  p.ctas *= p.few.per_sm;
   const int group = b.n_heads / b.n_kv_heads;
   p.stream_tokens = kRows / group;
   p.tile_tokens = 2 * p.stream_tokens;
@@ -827,14 +842,6 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p,
   return e == cudaSuccess ? launch_combine(a, D, F16, p, s) : e;
 }
 
-// 8-bit pages: the rows of a tile for the kernel of few rows (16 or 32), or 0 for
-// the one of 128.
-int few_rows(const dflash_paged_batch& b, bool shared) {
-  const int group = b.n_heads / b.n_kv_heads;
-  const long long rows = static_cast<long long>(b.n_tokens) * group, tiles = shared ? 1 : b.n_seq;
-  return group <= 16 && rows <= 16 * tiles ? 16 : group <= 32 && rows <= 32 * tiles ? 32 : 0;
-}
-
 std::atomic<int> g_wait_tries{kWaitTries};
 
 dflash_status refuse(const char* why) {
@@ -849,7 +856,7 @@ dflash_status fail_cuda(const char* why) {
 
 dflash_status run(const dflash_paged_batch& b, PagedAttnArgs& a, void* workspace, size_t workspace_bytes, void* stream) {
   Plan p;
-  if (!make_plan(b, p)) return fail_cuda("paged attention: no CUDA device");
+  if (!make_plan(b, a.shared, p)) return fail_cuda("paged attention: no CUDA device");
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) & 31 || workspace_bytes < p.bytes)
     return refuse("the workspace is null, not 32-byte aligned or smaller than dflash_paged_attn_workspace says");
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -862,11 +869,15 @@ dflash_status run(const dflash_paged_batch& b, PagedAttnArgs& a, void* workspace
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (b.dtype & DFLASH_POOL_Q8) {
-    const int rows = few_rows(b, a.shared);
-    if (rows > 0) a.stream_tokens = a.tile_tokens = rows / a.b.group;
-    cudaError_t e = rows > 0 ? launch_paged_attn_q8_few(a, b.head_dim, b.dtype & DFLASH_FP16, rows, p.device, p.ctas, s)
-                             : launch_paged_attn_q8(a, b.head_dim, b.dtype & DFLASH_FP16, p.device, p.ctas, s);
-    if (e == cudaSuccess) e = launch_combine(a, b.head_dim, b.dtype & DFLASH_FP16, p, s);
+    const bool f16 = b.dtype & DFLASH_FP16;
+    cudaError_t e;
+    if (p.few.rows > 0) {
+      a.stream_tokens = a.tile_tokens = p.few.rows / a.b.group;
+      e = launch_paged_attn_q8_few(a, b.head_dim, f16, p.few, p.device, p.ctas, s);
+    } else {
+      e = launch_paged_attn_q8(a, b.head_dim, f16, p.device, p.ctas, s);
+    }
+    if (e == cudaSuccess) e = launch_combine(a, b.head_dim, f16, p, s);
     return e == cudaSuccess ? DFLASH_OK : fail_cuda("paged attention: kernel launch failed");
   }
   const uint64_t d = b.head_dim, n_kv = b.n_kv_heads, pages = b.n_pages;
@@ -912,9 +923,9 @@ extern "C" dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b
   *bytes = 0;
   if (const char* why = paged_check(b)) return refuse(why);
   if (b->n_seq == 0 || b->n_tokens == 0) return DFLASH_OK;
-  Plan p;
-  if (!make_plan(*b, p)) return fail_cuda("paged attention: no CUDA device");
-  *bytes = p.bytes;
+  Plan own, shared;   // one workspace for either call
+  if (!make_plan(*b, false, own) || !make_plan(*b, true, shared)) return fail_cuda("paged attention: no CUDA device");
+  *bytes = std::max(own.bytes, shared.bytes);
   return DFLASH_OK;
 }
 

@@ -32,9 +32,9 @@ constexpr int kUnit = 32;        // keys
 constexpr float kBias = 7.f;
 constexpr int kLeastE = -80, kNoUnit = -(1 << 20);   // smaller scales count as 2^-80
 
-template <int D, int MT>
+template <int D, int MT, int PerSm>
 struct Few {
-  static constexpr int kWarps = D * MT <= 128 ? 12 : 8;
+  static constexpr int kWarps = (MT == 1 ? 12 : 8) / PerSm;
   static constexpr int kSlots = D * MT <= 128 && D == 128 ? 3 : 4;   // of a warp's ring
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kRowsMax = 16 * MT;
@@ -51,7 +51,7 @@ struct Few {
   static constexpr int kSmem = kStageOff + kWarps * kSlots * kHalf;
   static_assert(kBatchBytes % 16 == 0 && kHalf % 16 == 0, "16-byte copies");
   static_assert(kWarps * kRowsMax * kJoinRow * 4 <= kWarps * kSlots * kHalf, "the join's rows lie over the units");
-  static_assert(kSmem <= 220 * 1024, "static shared variables need the rest");
+  static_assert(kSmem <= 220 * 1024 / PerSm, "static shared variables need the rest");
 };
 
 // 2^e for e in -128..127 (the two below 2^-126 are no normal numbers).
@@ -81,9 +81,9 @@ struct Unit {
   int seq, end;  // as of its step
 };
 
-template <int D, bool F16, int MT>
-__global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_kernel(const __grid_constant__ PagedAttnArgs a) {
-  using C = Few<D, MT>;
+template <int D, bool F16, int MT, int PerSm>
+__global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn_q8_few_kernel(const __grid_constant__ PagedAttnArgs a) {
+  using C = Few<D, MT, PerSm>;
   constexpr int W = C::kWarps, kThreads = C::kThreads;
   extern __shared__ __align__(16) uint8_t smem[];
   Batch& b = *reinterpret_cast<Batch*>(smem);
@@ -482,28 +482,30 @@ __global__ void __launch_bounds__(Few<D, MT>::kThreads, 1) paged_attn_q8_few_ker
   if (tid == 0) a.split[blockIdx.x] = split;
 }
 
-template <int D, bool F16, int MT>
+template <int D, bool F16, int MT, int PerSm>
 cudaError_t launch(const PagedAttnArgs& a, int device, int ctas, cudaStream_t s) {
+  using C = Few<D, MT, PerSm>;
   // the shared-memory limit is set once per device (setting it again changes nothing)
   static std::atomic<uint64_t> set{0};
   if (device > 63 || !(set.load(std::memory_order_acquire) >> device & 1)) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_attn_q8_few_kernel<D, F16, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<D, MT>::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(paged_attn_q8_few_kernel<D, F16, MT, PerSm>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     if (device < 64) set.fetch_or(uint64_t(1) << device, std::memory_order_release);
   }
-  return launch_pdl(paged_attn_q8_few_kernel<D, F16, MT>, dim3(ctas), dim3(Few<D, MT>::kThreads), Few<D, MT>::kSmem, s, a);
+  return launch_pdl(paged_attn_q8_few_kernel<D, F16, MT, PerSm>, dim3(ctas), dim3(C::kThreads), C::kSmem, s, a);
 }
 
 template <int D, bool F16>
-cudaError_t pick(const PagedAttnArgs& a, int rows, int device, int ctas, cudaStream_t s) {
-  return rows <= 16 ? launch<D, F16, 1>(a, device, ctas, s) : launch<D, F16, 2>(a, device, ctas, s);
+cudaError_t pick(const PagedAttnArgs& a, const Q8Few& few, int device, int ctas, cudaStream_t s) {
+  if (few.rows > 16) return launch<D, F16, 2, 2>(a, device, ctas, s);
+  return few.per_sm == 2 ? launch<D, F16, 1, 2>(a, device, ctas, s) : launch<D, F16, 1, 1>(a, device, ctas, s);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attn_q8_few(const PagedAttnArgs& a, int head_dim, bool f16, int rows, int device, int ctas, cudaStream_t s) {
-  if (head_dim == 128) return f16 ? pick<128, true>(a, rows, device, ctas, s) : pick<128, false>(a, rows, device, ctas, s);
-  return f16 ? pick<64, true>(a, rows, device, ctas, s) : pick<64, false>(a, rows, device, ctas, s);
+cudaError_t launch_paged_attn_q8_few(const PagedAttnArgs& a, int head_dim, bool f16, const Q8Few& few, int device, int ctas, cudaStream_t s) {
+  if (head_dim == 128) return f16 ? pick<128, true>(a, few, device, ctas, s) : pick<128, false>(a, few, device, ctas, s);
+  return f16 ? pick<64, true>(a, few, device, ctas, s) : pick<64, false>(a, few, device, ctas, s);
 }
 
 }  // namespace dfl

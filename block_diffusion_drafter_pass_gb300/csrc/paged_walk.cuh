@@ -54,8 +54,12 @@ struct PagedAttnArgs {
 
 // The kernel over 8-bit pages (paged_attn_q8.cu); the partials are joined by the caller.
 cudaError_t launch_paged_attn_q8(const PagedAttnArgs& a, int head_dim, bool f16, int device, int ctas, cudaStream_t s);
-// The one for few rows (paged_attn_q8_few.cu): tiles of up to `rows` of them, 16 or 32, in one stream.
-cudaError_t launch_paged_attn_q8_few(const PagedAttnArgs& a, int head_dim, bool f16, int rows, int device, int ctas, cudaStream_t s);
+// The one for few rows (paged_attn_q8_few.cu): tiles of up to `rows` of them (16
+// or 32; 0: not for this batch) in one stream, and `per_sm` CTAs an SM.
+struct Q8Few {
+  int rows, per_sm;
+};
+cudaError_t launch_paged_attn_q8_few(const PagedAttnArgs& a, int head_dim, bool f16, const Q8Few& few, int device, int ctas, cudaStream_t s);
 
 namespace {
 
