@@ -34,6 +34,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxHeads = 8;   // heads one thread rotates with the same angles, at most
 constexpr int kAtOnce = 2;     // of them under way together (4 took registers, and 4% at 260 MB)
 constexpr int kVTokens = 64;   // tokens of a value block
+constexpr int kQ8Threads = 128, kQ8Ahead = 2;   // 8-bit pages
 
 struct AppendArgs {
   PagedView b;
@@ -189,32 +190,30 @@ __device__ __forceinline__ void write_q8(const float (&x)[16], uint8_t* codes, f
 // walk takes queries, keys and values, and a thread's 16 values of a row are
 // quantised where they are.
 template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kQ8Threads) kv_append_q8_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kOct = D / 16;                 // threads of a token: 8 pairs each
-  constexpr int kTokens = kThreads / kOct;
+  constexpr int kTokens = kQ8Threads / kOct;
   __shared__ int s_q[kPagedMaxSeqs + 1], s_len[kPagedMaxSeqs];
   grid_dep_wait();
   grid_dep_launch();
   const int tid = threadIdx.x, n_kv = a.b.n_kv;
-  for (int i = tid; i < a.b.n_seq; i += kThreads) s_len[i] = a.b.kv_len[i];
+  for (int i = tid; i < a.b.n_seq; i += kQ8Threads) s_len[i] = a.b.kv_len[i];
   const int tile = blockIdx.x / a.qk_groups, grp = blockIdx.x % a.qk_groups;
   const int t = tile * kTokens + tid / kOct, oct = tid % kOct;
   const unsigned group = ((1u << kOct) - 1u) << (tid & 31 & ~(kOct - 1));   // the lanes of the token
   const int n_q = a.q ? a.b.n_heads : 0;
   const int h0 = grp * a.heads, h1 = t < a.b.n_tokens ? min(n_q + 2 * n_kv, h0 + a.heads) : h0;
-  uint4 lo[kAtOnce], hi[kAtOnce];
-  auto read = [&](int h) {
-#pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
-      const int i = h + u - n_q;   // below 0: a query
-      if (h + u >= h1) continue;
-      const uint16_t* src = i < 0 ? a.q + t * a.q_stride + (h + u) * D
-                            : i < n_kv ? a.k + t * a.k_stride + i * D : a.v + t * a.v_stride + (i - n_kv) * D;
-      lo[u] = __ldg(reinterpret_cast<const uint4*>(src + oct * 8));
-      hi[u] = __ldg(reinterpret_cast<const uint4*>(src + D / 2 + oct * 8));
-    }
+  uint4 lo[kQ8Ahead], hi[kQ8Ahead];   // of the next heads, under way
+  auto read = [&](int h, int u) {
+    const int i = h - n_q;   // below 0: a query
+    if (h >= h1) return;
+    const uint16_t* src = i < 0 ? a.q + t * a.q_stride + h * D
+                          : i < n_kv ? a.k + t * a.k_stride + i * D : a.v + t * a.v_stride + (i - n_kv) * D;
+    lo[u] = __ldg(reinterpret_cast<const uint4*>(src + oct * 8));
+    hi[u] = __ldg(reinterpret_cast<const uint4*>(src + D / 2 + oct * 8));
   };
-  read(h0);
+#pragma unroll
+  for (int u = 0; u < kQ8Ahead; ++u) read(h0 + u, u);
   load_q_start(a.b, s_q);
   const Place p = place_of(a.b, s_q, s_len, t, static_cast<long long>(n_kv) * q8_block_bytes(D));
   if (p.pos < 0) return;
@@ -222,16 +221,18 @@ __global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const __grid_con
   if (a.rotate && h0 < n_q + n_kv) rotation(a, a.positions ? a.positions[t] : p.pos, oct, cs, sn);
   uint8_t* const page = reinterpret_cast<uint8_t*>(a.b.pool) + p.page;
 #pragma unroll 1
-  for (int h = h0; h < h1; h += kAtOnce) {
-    if (h > h0) read(h);
+  for (int h = h0; h < h1; h += kQ8Ahead) {
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) {
+    for (int u = 0; u < kQ8Ahead; ++u) {
       const int i = h + u - n_q;
-      if (h + u >= h1 || (i >= 0 && p.page < 0)) continue;
+      if (h + u >= h1) continue;
+      const uint4 wl = lo[u], wh = hi[u];
+      read(h + u + kQ8Ahead, u);
+      if (i >= 0 && p.page < 0) continue;
       float x[16];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float2 f = unpack2<F16>((&lo[u].x)[w]), g = unpack2<F16>((&hi[u].x)[w]);
+        const float2 f = unpack2<F16>((&wl.x)[w]), g = unpack2<F16>((&wh.x)[w]);
         x[2 * w] = f.x, x[2 * w + 1] = f.y, x[8 + 2 * w] = g.x, x[9 + 2 * w] = g.y;
       }
       if (a.rotate && i < n_kv) {
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_q8_kernel(const __grid_con
       }
       if (i < 0) {
         uint16_t* dst = a.q_out + t * a.out_stride + (h + u) * D;
-        uint4 ro = lo[u], rh = hi[u];
+        uint4 ro = wl, rh = wh;
         if (a.rotate) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -271,14 +272,14 @@ cudaError_t launch(AppendArgs& a, bool q8, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const long long enough = 2ll * sms;   // blocks that fill the device: few tokens are cut finer
-  const int tokens = kThreads / (D / 16);
+  const int threads = q8 ? kQ8Threads : kThreads, tokens = threads / (D / 16);
   const int heads = (a.q ? a.b.n_heads : 0) + (q8 ? 2 : 1) * a.b.n_kv;
   a.qk_tiles = (a.b.n_tokens + tokens - 1) / tokens;
   a.heads = static_cast<int>(std::min<long long>(kMaxHeads, std::max<long long>(1, heads * static_cast<long long>(a.qk_tiles) / enough)));
   a.qk_groups = (heads + a.heads - 1) / a.heads;
   if (q8) {
     const long long grid = static_cast<long long>(a.qk_tiles) * a.qk_groups;
-    return launch_pdl(kv_append_q8_kernel<D, F16>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, a);
+    return launch_pdl(kv_append_q8_kernel<D, F16>, dim3(static_cast<unsigned>(grid)), dim3(kQ8Threads), 0, s, a);
   }
   long long v_blocks = static_cast<long long>((a.b.n_tokens + kVTokens - 1) / kVTokens) * a.b.n_kv;
   a.v_split = v_blocks * 4 <= enough ? 4 : v_blocks * 2 <= enough ? 2 : 1;
