@@ -48,10 +48,9 @@ static_assert(2 * kSoftRegs + 2 * kConvRegs + kRestRegs <= 5 * kLaunchRegs, "set
 static_assert(kSoftRegs >= kLaunchRegs && kConvRegs <= kLaunchRegs && kRestRegs <= kLaunchRegs, "inc must go up and dec down");
 constexpr int kAhead = 16;       // steps that the walk looks up at a time
 constexpr int kScalesAhead = 2;  // steps that scales are ahead of their keys
-// The walk is ahead of the products by these and the halves of both rings (8
-// steps at most); scales are held of what is behind the first ring.
+// The walk is ahead of the softmax by these, the halves of both rings and the
+// scales' lead.
 constexpr int kStepRing = 32;
-constexpr int kScaleRing = 8;
 constexpr float kBias = 7.f;
 constexpr int kLeastE = -80, kNoUnit = -(1 << 20);   // smaller scales count as 2^-80
 
@@ -74,6 +73,12 @@ struct Cfg {
   static constexpr int kRawOff = kQ1Off + 2 * kRaw;         // of place 0; the last two before it
   static constexpr int kRingOff = kRawOff + kRawPair * kRaw;
   static constexpr int kIntOff = kRingOff + kSlots * kHalf;
+  // Steps whose scales are held: while the softmax is at step j, whose values the
+  // rings then begin with, kSlots + kRawSlots halves from there on may be in them,
+  // and the scales of kScalesAhead steps after the next half's.
+  static constexpr int kScaleRing = D == 128 ? 8 : 16;
+  static_assert((kSlots + kRawSlots - 1) / 2 + kScalesAhead + 3 <= kScaleRing, "scales that are still read");
+  static_assert((kSlots + kRawSlots - 1) / 2 + kScalesAhead + 3 + kAhead <= kStepRing, "pages that are still read");
   // A step's scales: per page those of its keys and of its values, as they come
   // (fp32), then as two fp16 each.
   static constexpr int kScaleOff = kIntOff + kBatchBytes;
@@ -214,7 +219,7 @@ struct NoRedo {
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid_constant__ PagedAttnArgs a) {
   using C = Cfg<D>;
-  constexpr int S = C::kSlots;
+  constexpr int S = C::kSlots, kScaleRing = C::kScaleRing;
   constexpr uint32_t kIdescS = idesc_f16_f32(kRows, kStepKeys);
   constexpr uint32_t kIdescO = idesc_f16_f32(kRows, D) | (1u << 16);   // B is MN-major
   extern __shared__ uint8_t smem_raw[];
