@@ -400,7 +400,7 @@ def dflash_kv_read(pool, n_tokens: int, q_start, kv_len, page_table, *, dtype=No
     return _run_on(torch, dev, stream, call)
 
 
-_workspace_bytes = {}   # by all that they depend on; above 128 tokens they no longer grow
+_workspace_bytes = {}   # by all that they depend on; above 128 tokens (of 8-bit pages 1024) they no longer grow
 
 
 def _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status, stream):
@@ -416,7 +416,8 @@ def _attend(torch, run, q, pool, q_start, kv_len, page_table, scale, out, status
     lib = _lib or load_library()
 
     def call(s):
-        key = (dev, n_heads, n_kv, d, min(T, 129))
+        q8 = pool.dtype == torch.uint8
+        key = (dev, n_heads, n_kv, d, q8, min(T, 1024 if q8 else 129))
         need = _workspace_bytes.get(key)
         if need is None:   # asked once: a library call between PyTorch's costs 3 us of cold code
             size = ctypes.c_size_t()

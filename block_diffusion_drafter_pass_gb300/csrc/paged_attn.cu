@@ -758,8 +758,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32) paged_combine_kernel(const
           }
         }
       }
-      const float f = l > 0.f || l != l ? 1.f / l : 0.f;
       const int j = i / G;
+      if (a.part == 1) {   // of the own caches: for the prefix's part
+        const size_t to = static_cast<size_t>(sp.x + j) * a.b.n_heads + sp.z * G + i - j * G;
+#pragma unroll
+        for (int e = 0; e < kPer; e += 2) *reinterpret_cast<float2*>(a.own_o + to * D + lane * kPer + e) = make_float2(acc[e], acc[e + 1]);
+        if (lane == 0) a.own_ml[to] = make_float2(top, l);
+        continue;
+      }
+      const float f = l > 0.f || l != l ? 1.f / l : 0.f;
       uint16_t* out = out_row(a, sp.x + j, sp.z, i - j * G, D) + lane * kPer;
 #pragma unroll
       for (int e = 0; e < kPer; e += 2)
@@ -788,7 +795,8 @@ const char* attn_check(const dflash_paged_batch* b, const void* q, long long q_s
 struct Plan {
   Q8Few few;
   int device, ctas, stream_tokens, tile_tokens, rows_cap;
-  size_t piece_off, ml_off, o_off, bytes;   // the split records come first
+  bool own;   // behind a prefix: the own caches apart (`few` is theirs then)
+  size_t piece_off, ml_off, o_off, own_ml_off, own_o_off, bytes;   // the split records come first
 };
 
 // Whether a batch over 8-bit pages is one for the kernel of few rows, and how.
@@ -803,26 +811,47 @@ Q8Few few_rows(const dflash_paged_batch& b, bool shared) {
   return few;
 }
 
+// Behind a prefix a tile of 128 rows meets the own cache of each of its sequences
+// with the rows of one. Of many short blocks with long own caches these steps are
+// most of the work, and are taken apart from the prefix, by the kernel of few rows.
+// The rule sees the page tables' width, not the lengths: single tokens behind 2048
+// take 108 us instead of 158 (64 sequences, own caches of 2048) and 159 instead of
+// 284 (128 of 2048), about the same at 1024 pages (98 and 100: 128 of 512), and
+// less would cost (71 instead of 65: 64 of 512; wide tables of short caches, 54
+// instead of 38: 64 of 64).
+constexpr int kOwnTokens = 1024;   // (the workspace holds their part in fp32)
+bool own_apart(const dflash_paged_batch& b) {
+  return b.n_seq >= 64 && b.n_tokens <= kOwnTokens && static_cast<long long>(b.n_seq) * b.table_pages > 1024 && few_rows(b, true).rows == 0 && few_rows(b, false).rows > 0;
+}
+
 bool make_plan(const dflash_paged_batch& b, bool shared, Plan& p) {
   if (cudaGetDevice(&p.device) != cudaSuccess ||
       cudaDeviceGetAttribute(&p.ctas, cudaDevAttrMultiProcessorCount, p.device) != cudaSuccess)
     return false;
-  p.few = few_rows(b, shared);
-  p.ctas *= p.few.per_sm;
   const int group = b.n_heads / b.n_kv_heads;
   p.stream_tokens = kRows / group;
   p.tile_tokens = 2 * p.stream_tokens;
   p.rows_cap = b.n_tokens > p.stream_tokens ? 2 * kRows : std::min(kRows, b.n_tokens * group);
+  p.own = shared && own_apart(b);
+  p.few = few_rows(b, shared && !p.own);
+  // the same for every batch of so many tokens: over 8-bit pages there may be two
+  // CTAs an SM, and own caches apart
+  const bool q8 = b.dtype & DFLASH_POOL_Q8;
+  const int ctas = q8 ? 2 * p.ctas : p.ctas;
+  const size_t own_rows = q8 ? static_cast<size_t>(std::min(b.n_tokens, kOwnTokens)) * b.n_heads : 0;
   auto up = [](size_t n) { return (n + 255) & ~size_t(255); };
-  p.piece_off = up(sizeof(int4) * p.ctas);
-  p.ml_off = p.piece_off + up(sizeof(int) * p.ctas);
-  p.o_off = p.ml_off + up(sizeof(float2) * 2 * p.ctas * p.rows_cap);
-  p.bytes = p.o_off + sizeof(float) * 2 * p.ctas * p.rows_cap * b.head_dim;
+  p.piece_off = up(sizeof(int4) * ctas);
+  p.ml_off = p.piece_off + up(sizeof(int) * ctas);
+  p.o_off = p.ml_off + up(sizeof(float2) * 2 * ctas * p.rows_cap);
+  p.bytes = p.o_off + sizeof(float) * 2 * ctas * p.rows_cap * b.head_dim;
+  p.own_ml_off = up(p.bytes);
+  p.own_o_off = p.own_ml_off + up(sizeof(float2) * own_rows);
+  if (own_rows) p.bytes = p.own_o_off + sizeof(float) * own_rows * b.head_dim;
   return true;
 }
 
-cudaError_t launch_combine(const PagedAttnArgs& a, int d, bool f16, const Plan& p, cudaStream_t s) {
-  const dim3 grid(p.ctas, std::min(kCombineBlocks, (p.rows_cap + kCombineWarps - 1) / kCombineWarps));
+cudaError_t launch_combine(const PagedAttnArgs& a, int d, bool f16, const Plan& p, int ctas, cudaStream_t s) {
+  const dim3 grid(ctas, std::min(kCombineBlocks, (p.rows_cap + kCombineWarps - 1) / kCombineWarps));
   auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(kCombineWarps * 32), 0, s, a); };
   if (d == 128) return f16 ? go(paged_combine_kernel<128, true>) : go(paged_combine_kernel<128, false>);
   return f16 ? go(paged_combine_kernel<64, true>) : go(paged_combine_kernel<64, false>);
@@ -839,7 +868,7 @@ cudaError_t launch(const PagedMaps& maps, const PagedAttnArgs& a, const Plan& p,
     if (p.device < 64) set.fetch_or(uint64_t(1) << p.device, std::memory_order_release);
   }
   e = launch_pdl(paged_attn_kernel<D, F16>, dim3(p.ctas), dim3(kThreads), Cfg<D>::kSmem, s, maps, a);
-  return e == cudaSuccess ? launch_combine(a, D, F16, p, s) : e;
+  return e == cudaSuccess ? launch_combine(a, D, F16, p, p.ctas, s) : e;
 }
 
 std::atomic<int> g_wait_tries{kWaitTries};
@@ -870,14 +899,27 @@ dflash_status run(const dflash_paged_batch& b, PagedAttnArgs& a, void* workspace
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (b.dtype & DFLASH_POOL_Q8) {
     const bool f16 = b.dtype & DFLASH_FP16;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
     if (p.few.rows > 0) {
-      a.stream_tokens = a.tile_tokens = p.few.rows / a.b.group;
-      e = launch_paged_attn_q8_few(a, b.head_dim, f16, p.few, p.device, p.ctas, s);
-    } else {
-      e = launch_paged_attn_q8(a, b.head_dim, f16, p.device, p.ctas, s);
+      PagedAttnArgs f = a;
+      f.stream_tokens = f.tile_tokens = p.few.rows / a.b.group;
+      if (p.own) {
+        f.shared = f.prefix_len = 0;
+        p.own = a.prefix_len > 0;   // else there is nothing but the own caches
+      }
+      if (p.own) {
+        f.part = 1;
+        f.own_ml = a.own_ml = reinterpret_cast<float2*>(ws + p.own_ml_off);
+        f.own_o = a.own_o = reinterpret_cast<float*>(ws + p.own_o_off);
+        a.part = 2;
+      }
+      e = launch_paged_attn_q8_few(f, b.head_dim, f16, p.few, p.device, p.few.per_sm * p.ctas, s);
+      if (e == cudaSuccess) e = launch_combine(f, b.head_dim, f16, p, p.few.per_sm * p.ctas, s);
     }
-    if (e == cudaSuccess) e = launch_combine(a, b.head_dim, f16, p, s);
+    if (e == cudaSuccess && (p.few.rows == 0 || p.own)) {
+      e = launch_paged_attn_q8(a, b.head_dim, f16, p.device, p.ctas, s);
+      if (e == cudaSuccess) e = launch_combine(a, b.head_dim, f16, p, p.ctas, s);
+    }
     return e == cudaSuccess ? DFLASH_OK : fail_cuda("paged attention: kernel launch failed");
   }
   const uint64_t d = b.head_dim, n_kv = b.n_kv_heads, pages = b.n_pages;
@@ -923,9 +965,9 @@ extern "C" dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b
   *bytes = 0;
   if (const char* why = paged_check(b)) return refuse(why);
   if (b->n_seq == 0 || b->n_tokens == 0) return DFLASH_OK;
-  Plan own, shared;   // one workspace for either call
-  if (!make_plan(*b, false, own) || !make_plan(*b, true, shared)) return fail_cuda("paged attention: no CUDA device");
-  *bytes = std::max(own.bytes, shared.bytes);
+  Plan p;
+  if (!make_plan(*b, false, p)) return fail_cuda("paged attention: no CUDA device");
+  *bytes = p.bytes;
   return DFLASH_OK;
 }
 

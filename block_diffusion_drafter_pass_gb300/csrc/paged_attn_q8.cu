@@ -918,8 +918,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       if (done > 0) warp_wait(&o_done[stream], outs++ & 1);
       if (!ok) break;
 
-      // what others join is the maximum in the unit's terms
-      ok = finish_item<D, F16, NoRedo>(a, b, it, join, stream, tmem, row.token, mref + static_cast<float>(unit), l, done > 0, nx & 1,
+      // what others join is the maximum in the unit's terms (the scales' 2^7 is in O and l)
+      ok = finish_item<D, F16, NoRedo>(a, b, it, join, stream, tmem, row.token, mref + static_cast<float>(unit - 7), l, done > 0, nx & 1,
                                        progress_at);
       nx += !it.pair;
       if (!ok) break;

@@ -461,7 +461,11 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         sum = fmaf(f, ml.y, sum);
         acc.x = fmaf(f, x.x, acc.x), acc.y = fmaf(f, x.y, acc.y), acc.z = fmaf(f, x.z, acc.z), acc.w = fmaf(f, x.w, acc.w);
       }
-      if (whole) {
+      if (whole && a.part == 1) {
+        const size_t at = static_cast<size_t>(it.t.t0 + r / G) * a.b.n_heads + head * G + r % G;
+        *reinterpret_cast<float4*>(a.own_o + at * D + d) = acc;
+        if (d == 0) a.own_ml[at] = make_float2(top, sum);
+      } else if (whole) {
         const float f = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         const int j = r / G;
         uint16_t* out = out_row(a, it.t.t0 + j, head, r - j * G, D) + d;

@@ -34,6 +34,12 @@ struct PagedAttnArgs {
   const int32_t* prefix_table;
   int prefix_len;
   int shared;                  // tiles span sequences, behind prefix_len shared tokens
+  // 8-bit pages: a batch behind a prefix may be taken in two parts, the sequences'
+  // own caches into own_o [token][head][d] and own_ml (maximum and sum), and then
+  // the prefix alone, which joins them
+  int part;                    // 0: all in one, 1: the own caches, 2: the prefix
+  float* own_o;
+  float2* own_ml;
   const uint16_t* q;
   long long q_stride;
   uint16_t* out;
@@ -110,7 +116,7 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 // called take it by reference, and a reference to registers or parameters
 // would put those into local memory.
 struct Batch {
-  int shared, causal, window, sinks, prefix_len;
+  int shared, causal, window, sinks, prefix_len, prefix_only;
   int stream_tokens, tile_tokens;
   int n_seq, n_kv, group;
   int q[kPagedMaxSeqs + 1];      // the bounds of the sequences' tokens (bent into range)
@@ -142,7 +148,7 @@ __device__ __forceinline__ Tile tile_at(const Batch& b, int tile) {
     r.window_step = 0;
     // the last sequence may go on behind the tile: its keys up to the tile's last row
     const int end = b.causal ? b.len[r.seq1] - (b.q[r.seq1 + 1] - 1 - last) : b.len[r.seq1];
-    r.n = max(1, r.head_steps + b.base[r.seq1] - b.base[r.seq0] + steps_of(end));
+    r.n = max(1, b.prefix_only ? r.head_steps : r.head_steps + b.base[r.seq1] - b.base[r.seq0] + steps_of(end));
     return r;
   }
   int lo = 0, hi = b.n_seq - 1;   // the last sequence whose tiles start at or before this one
@@ -447,6 +453,7 @@ __device__ __forceinline__ void set_batch(const PagedAttnArgs& a, Batch& b) {
   b.window = a.window;
   b.sinks = a.sinks;
   b.prefix_len = a.prefix_len;
+  b.prefix_only = a.part == 2;
   b.stream_tokens = a.stream_tokens;
   b.tile_tokens = a.tile_tokens;
   b.n_seq = a.b.n_seq;
@@ -587,10 +594,27 @@ __device__ DFL_WALK_CALL bool finish_item(const PagedAttnArgs& a, const Batch& b
     col = stream * (D / 2);
     col_end = col + D / 2;
   }
+  // what the row sees of its sequence's own cache, joined by the prefix's first piece
+  float w2 = 0.f;
+  const float* own = nullptr;
+  if constexpr (!Again::kOn) {
+    if (a.part == 2 && it.j == 0 && live) {
+      const size_t at = static_cast<size_t>(token) * a.b.n_heads + it.head * b.group + r % b.group;
+      const float2 m = __ldcg(a.own_ml + at);
+      const float both = fmaxf(top, m.x), f = top == -INFINITY ? 0.f : ex2(top - both);
+      w2 = m.x == -INFINITY ? 0.f : ex2(m.x - both);
+      top = both;
+      w0 *= f;
+      w1 *= f;
+      lj = fmaf(lj, f, m.y * w2);
+      own = a.own_o + at * D;
+    }
+  }
   if (whole) {
     const float f = lj > 0.f || lj != lj ? 1.f / lj : 0.f;
     w0 *= f;
     w1 *= f;
+    w2 *= f;
   }
   const bool any0 = __any_sync(0xffffffffu, use0), any1 = __any_sync(0xffffffffu, use1);
   float check = 0.f;   // NaN once a stored value is not finite
@@ -607,6 +631,12 @@ __device__ DFL_WALK_CALL bool finish_item(const PagedAttnArgs& a, const Batch& b
       tmem_ld16(lane_tmem + kOCol + D + col, o1);
 #pragma unroll
       for (int c = 0; c < 16; ++c) o[c] = use1 ? fmaf(o1[c], w1, o[c]) : o[c];
+    }
+#pragma unroll
+    for (int c = 0; c < 16 && !Again::kOn; c += 4) {
+      if (!own) continue;
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(own + col + c));
+      o[c] = fmaf(x.x, w2, o[c]), o[c + 1] = fmaf(x.y, w2, o[c + 1]), o[c + 2] = fmaf(x.z, w2, o[c + 2]), o[c + 3] = fmaf(x.w, w2, o[c + 3]);
     }
 #pragma unroll
     for (int c = 0; c < 16 && Again::kOn; ++c) check = fmaf(o[c], 0.f, check);

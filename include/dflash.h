@@ -488,8 +488,9 @@ dflash_status dflash_kv_read(const dflash_paged_batch* b, void* k_out, long long
                              long long v_stride, void* stream);
 
 /* Device bytes that the two attention calls below need as workspace for this
- * batch's shape (it depends on n_heads, n_kv_heads, head_dim, n_tokens and the
- * device only). Its contents need no preparation and mean nothing afterwards;
+ * batch's shape (it depends on whether the pages are 8-bit ones, n_heads,
+ * n_kv_heads, head_dim, n_tokens and the device only; of more than 128 tokens,
+ * with 8-bit pages 1024, it no longer grows). Its contents need no preparation and mean nothing afterwards;
  * calls that may run at the same time need one each. Errors: EINVAL, ECUDA. */
 dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b, size_t* bytes);
 

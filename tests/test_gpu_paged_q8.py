@@ -34,6 +34,8 @@ Tolerances, from the arithmetic, u = half a step of the tokens' type (bf16
    values by 2 2^-11 A. (That is what all of them on one side would give; found is
    0.0017 of the output's norm for bf16 and 0.0003 for fp16.)
 """
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -62,13 +64,20 @@ class Batch8(Batch):
         return p8.decode(self.pool.cpu().numpy(), self.d, bits)
 
     def oracle(self, bits="as run", **kw):
+        mixed = False
         if bits == "as run":
-            group = self.heads // self.n_kv
-            few = group <= 32 and self.T * group <= 32 * (1 if "prefix_len" in kw else len(self.kv_len))
-            bits = None if few else 11
+            group, n_seq = self.heads // self.n_kv, len(self.kv_len)
+            few = [group <= 32 and self.T * group <= 32 * n for n in (1, n_seq)]
+            mixed = "prefix_len" in kw and not few[0] and few[1] and n_seq >= 64 and n_seq * self.table.shape[1] > 1024
+            bits = None if few[0 if "prefix_len" in kw else 1] or mixed else 11
         scale = kw.pop("scale", self.d ** -0.5)
         ints = [t.cpu().numpy() for t in (self.q_start, self.kv_len, self.table)]
-        return pc.attention(f64(self.q), self.decoded(bits), *ints, scale, **kw)
+        pool = self.decoded(bits)
+        if mixed:   # the own caches by the kernel for few rows, the prefix by the other
+            pages = np.unique(kw["prefix_table"])
+            pages = pages[(pages >= 0) & (pages < len(pool))]
+            pool[pages] = self.decoded(11)[pages]
+        return pc.attention(f64(self.q), pool, *ints, scale, **kw)
 
 
 def check(b, got, ref, keys, scale=None, whole=False):
@@ -351,6 +360,25 @@ def test_shared_prefix(dfl, prefix, heads, n_kv, d, dtype):  # noqa: F811
         check_attn(dfl, Batch8(lens, heads, n_kv, d, dtype, prefix=prefix), shared=True)
 
 
+MANY = [(1, int(n)) for n in np.random.default_rng(5).integers(1, 1500, 64)]
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 300, 5000])
+@pytest.mark.parametrize("heads,n_kv,d,dtype", [(8, 2, 128, BF), (4, 4, 64, HF), (28, 4, 64, BF), (32, 1, 128, HF)])
+def test_many_short_blocks_behind_a_prefix(dfl, prefix, heads, n_kv, d, dtype):  # noqa: F811
+    """(Where the own caches are taken apart from the prefix; with 63 sequences they are not.)"""
+    check_attn(dfl, Batch8(MANY, heads, n_kv, d, dtype, prefix=prefix), shared=True)
+    check_attn(dfl, Batch8(MANY[:63], heads, n_kv, d, dtype, prefix=prefix), shared=True)
+    lens = MANY[:40] + [(0, 40), (0, 0), (3, 5), (2, 2), (1, 1), (1, 64), (1, 65), (0, 0), (1, 9000)] + MANY[40:]
+    b = Batch8(lens, heads, n_kv, d, dtype, prefix=prefix, pad=(2, 3))
+    out = torch.full((b.T, b.heads, d), 7.0, dtype=dtype, device=DEV)
+    got = f64(check_attn(dfl, b, shared=True, causal=False, out=out))
+    owned = np.zeros(b.T, dtype=bool)
+    for t, _, pos in pc.places(b.q_start.cpu().numpy(), b.kv_len.cpu().numpy()):
+        owned[t] = pos >= 0
+    assert (got[~owned] == 7.0).all() and (~owned).sum() == 5
+
+
 def test_strides_and_rows_of_no_sequence(dfl):  # noqa: F811
     b = Batch8([(5, 90), (130, 400)], 8, 2, 128, BF, pad=(3, 4), wide=8, prefix=65, extra_cols=5)
     whole = torch.full((b.T, 8 * 128 + 16), 9.0, dtype=BF, device=DEV)
@@ -601,6 +629,24 @@ def test_a_serving_step(dfl):  # noqa: F811
     one, two = b.attend(dfl, window=50, sinks=4), dfl.dflash_paged_attn(b.q, pool, b.q_start, b.kv_len, b.table, window=50, sinks=4)
     # every key is rounded to bf16: scores move by 2^-8 of their size (below 8 here), values by 2^-8
     assert (one.float() - two.float()).abs().max() < 0.1
+
+
+def test_the_workspace_depends_on_the_tokens_only(dfl):  # noqa: F811
+    """One buffer for all batches of so many tokens or fewer: for one sequence, many, with wide tables or narrow ones."""
+    lib = dfl.load_library()
+
+    def need(T, n_seq, table_pages, dtype=16):
+        pb = dfl.dflash_paged_batch(dtype, 32, 8, 128, n_seq, T, 1, table_pages, table_pages, *([1 << 20] * 4), None)
+        n = ctypes.c_size_t()
+        assert lib.dflash_paged_attn_workspace(ctypes.byref(pb), ctypes.byref(n)) == dfl.DFLASH_OK
+        return n.value
+
+    last = 0
+    for T in (1, 2, 8, 32, 33, 64, 128, 129, 1000, 1024, 1025, 100000):
+        sizes = {need(T, n_seq, pages) for n_seq in (1, 8, 64, 1024) for pages in (1, 16, 4096)}
+        assert len(sizes) == 1 and min(sizes) >= last and need(T, 8, 1, 0) == need(min(T, 129), 64, 16, 0)
+        last = min(sizes)
+    assert need(1024, 1, 1) == last
 
 
 def test_repeats_are_bit_identical(dfl):  # noqa: F811
