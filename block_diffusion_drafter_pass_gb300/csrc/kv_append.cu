@@ -188,7 +188,11 @@ __device__ __forceinline__ void write_q8(const float (&x)[16], uint8_t* codes, f
 
 // The same work for 8-bit pages. Keys and values alike lie in rows there, so one
 // walk takes queries, keys and values, and a thread's 16 values of a row are
-// quantised where they are.
+// quantised where they are. kQ8Ahead rows are under way while one is worked on:
+// 10.6 thousand tokens (32 + 8 + 8 heads of 128) take 45 us, 78% of the copy
+// bandwidth; with loads between the rows 56, and 52 in blocks of 128 then; 4 rows
+// ahead, 16 heads a thread and blocks of 256 or 64 are within 3 us of it. One token
+// of 32 sequences takes 3.4 us.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kQ8Threads) kv_append_q8_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kOct = D / 16;                 // threads of a token: 8 pairs each

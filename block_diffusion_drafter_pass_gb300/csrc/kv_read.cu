@@ -7,7 +7,9 @@
 // Bound: memory, the pages read once, the rows written once. A block takes 64
 // tokens of one kv head, whose rows lie together in a page: of 8-bit pages and
 // of 16-bit keys a thread has 16 bytes of a row at a time, 16-bit values, which
-// the pages hold transposed, are turned over in shared memory.
+// the pages hold transposed, are turned over in shared memory. Of 8-bit pages
+// 150 thousand tokens (8 heads of 128) take 149 us, 92% of the copy bandwidth for
+// codes and scales read and rows written; 300 tokens of 4 heads 2.7 us.
 #include <cstring>
 
 #include "paged.cuh"

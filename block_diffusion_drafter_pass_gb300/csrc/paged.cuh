@@ -31,7 +31,8 @@ constexpr int kPagedMaxTable = 1 << 20;  // pages of one sequence: positions sta
 // the products take them either way. One scale a row, not one for 32 values as in
 // the contexts' own 8-bit pages: codes are whole numbers of 8 bits, exact in
 // either 16-bit type, and a scale that belongs to the key can be multiplied into
-// its score or its weight in fp32, so nothing is rounded on the way to a product.
+// its score or its weight in fp32 (few rows: paged_attn_q8_few.cu), or into the
+// fp16 operands once for all rows (paged_attn_q8.cu).
 __host__ __device__ constexpr int q8_block_bytes(int d) { return kPage * (2 * d + 8); }
 __host__ __device__ constexpr int q8_values_at(int d) { return kPage * d; }
 __host__ __device__ constexpr int q8_key_scales_at(int d) { return 2 * kPage * d; }

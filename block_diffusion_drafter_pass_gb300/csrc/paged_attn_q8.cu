@@ -8,26 +8,46 @@
 // The products are of fp16 whatever the tokens' type. Queries are taken to it
 // behind a power of two that puts the row's largest value between 1/2 and 1
 // (values below 2^-13 of that are rounded in steps of 2^-24, all others of bf16
-// are exact). Keys and values are a code times its scale, which is
-// rounded to fp16 behind a power of two 2^(7 - e) that all 128 of a step share (its
-// largest scale comes to lie between 2^7 and 2^8), and the product once more: a
-// step of fp16 in all, an eighth of what rounding them to bf16 would cost. (Scales
-// multiplied onto scores and weights in fp32 instead are exact, but each row
-// then needs all 256 of a step: 364 us instead of @@ for 16 tokens of 32
-// sequences behind 32768.) Weights are rounded to fp16 for the product with the
+// are exact). Keys and values are a code times its scale, behind a power of two
+// 2^(7 - e) that all 128 of a step share (its largest scale comes to lie between 2^7
+// and 2^8), rounded to fp16 once, or for tokens of bf16, whose own steps are 8 times
+// as large, twice: the scale, too. Found over 2000 keys of scores of deviation 1.5:
+// 0.0005 of the output's norm in fp16 (0.0011 with a rounded scale; a plain fp32
+// computation rounded once at the end 0.0002), 0.0020 in bf16 (0.0017 with whole
+// scales; plain 0.0017), where whole scales take 287 us instead of 278 for 16
+// tokens of 32 sequences behind 32768. Scales 2^21 below their step's largest lose
+// bits. (Scales multiplied onto scores and weights in fp32 instead are exact, but
+// each row then needs all 256 of a step: 364 us instead of 322, then.)
+// Weights are rounded to fp16 for the product with the
 // values, in its best place: a row's weights are 2^(s - m - E + e) for a step of
 // value exponent e, m its reference maximum less 7 and E at least every e so far,
 // so that they stay below 2^15 and 2^-31 of the largest contribution still counts.
 // Sum and output share the unit, so it cancels.
 //
-// Per CTA: a warp walks the steps and writes down the pages of each half (128
-// keys, or their values); 8 warps take the halves from global memory
-// into registers, kAhead of them under way, and put them as fp16 into the ring
-// that the products read (and the queries of each item, scaled); two warps issue
-// the tcgen05.mma of a stream each and eight do the softmax, as in paged_attn.cu.
-// Values lie in rows of a token like keys; the product takes them as its
-// MN-major operand. Hidden or missing keys need no care in the products: every
-// code is finite, and weights of hidden keys are zero before their scale.
+// Per CTA: a warp walks the steps, looks up their pages and brings each half
+// (128 keys, or their values) and its scales by bulk copies; a warp turns scales
+// into fp16 pairs and exponents; 8 warps, in two teams that take every other half,
+// put codes as fp16 into the ring that the products read (and the queries of
+// each item, scaled); two warps issue the tcgen05.mma of a stream each and eight do
+// the softmax, as in paged_attn.cu. Values lie in rows of a token like keys; the
+// product takes them as its MN-major operand. Hidden or missing keys need no care
+// in the products: every code is finite, and weights of hidden keys are zero
+// before their scale. So no row has to be done again.
+//
+// What bounds it: shared memory and the warps beside it. A half goes through
+// shared memory three times (as codes, as fp16, to the products: the load/store
+// pipe is 70 to 87% busy), and a pair's step takes 2.4 us (4600 cycles for 2800 of
+// tensor work; with 16-bit pages 3400). 16 tokens of 32 sequences of 1024 to 8192
+// keys (32/8 heads of 128) take 118 us (floor 47.5), of one over 262144 keys 164
+// (3.4 TB/s), 8.7 thousand new tokens with a window of 2048 380, 16 of 32 sequences
+// behind 32768 278.
+// What was tried and is slower: halves in rounds of two with their scales, one wait
+// for each; codes by the converting warps' own loads from global memory, without
+// the first ring and with room for a fourth half of fp16 (130 us instead of 119, 190
+// instead of 168, 433 instead of 389, 338 instead of 281 in the four cases: with
+// registers for the loads in flight the softmax spills, without them the loads
+// do); one team of converting warps for every half (141 us instead of 137 and 380
+// instead of 364 in the first and last case, then).
 #include <algorithm>
 #include <atomic>
 
@@ -113,14 +133,24 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                : "memory");
 }
 
-// Four codes (bytes, + 128) times a scale (twice in a register), as fp16: behind
-// the byte 0x64 a byte is 1024 + itself.
+// Four codes (bytes, + 128) times a scale, as fp16: behind the byte 0x64 a byte
+// is 1024 + itself. The scale is its fp16 twice, or (kTwo) its fp16 and what that
+// leaves, so that only the product is rounded.
+template <bool kTwo>
 __device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 scale) {
   const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
   const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
-  const __half2 a = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&lo), off), scale);
-  const __half2 b = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&hi), off), scale);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&lo), off), y = __hsub2(*reinterpret_cast<const __half2*>(&hi), off);
+  const __half2 most = kTwo ? __low2half2(scale) : scale, rest = __high2half2(scale);
+  const __half2 a = kTwo ? __hfma2(x, most, __hmul2(x, rest)) : __hmul2(x, most);
+  const __half2 b = kTwo ? __hfma2(y, most, __hmul2(y, rest)) : __hmul2(y, most);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+template <bool kTwo>
+__device__ __forceinline__ uint32_t scale_of(float x) {
+  const float most = kTwo ? __half2float(__float2half_rn(x)) : x;
+  return pack2<true>(most, kTwo ? x - most : x);
 }
 
 // The exponent of the largest finite scale of a step, of which each lane has four.
@@ -473,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             const bool number = y[e] * 0.f == 0.f;
             const float kx = number ? x[e] * pow2_of(7 - ex) : __uint_as_float(0x7FC00000u), vx = number ? y[e] * pow2_of(7 - ey) : 0.f;
             const uint32_t to = at + (e >> 1) * 512 + (e & 1) * 128;
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(pack2<true>(kx, kx)) : "memory");
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 256), "r"(pack2<true>(vx, vx)) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(scale_of<F16>(kx)) : "memory");
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 256), "r"(scale_of<F16>(vx)) : "memory");
           }
           __syncwarp();
           if (lane == 0) bar_arrive(smem_u32(scale_full) + slot * 8);
@@ -723,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         for (int p = 0; p < P; ++p) {
           const uint4 w = code[p];
           const __half2 by = *reinterpret_cast<const __half2*>(&scale[p]);
-          const uint2 h0 = codes_to_f16(w.x, by), h1 = codes_to_f16(w.y, by);
-          const uint2 h2 = codes_to_f16(w.z, by), h3 = codes_to_f16(w.w, by);
+          const uint2 h0 = codes_to_f16<F16>(w.x, by), h1 = codes_to_f16<F16>(w.y, by);
+          const uint2 h2 = codes_to_f16<F16>(w.z, by), h3 = codes_to_f16<F16>(w.w, by);
           store_shared16(dst + p * kRowsOf * 128, make_uint4(h0.x, h0.y, h1.x, h1.y));
           store_shared16((dst ^ 16) + p * kRowsOf * 128, make_uint4(h2.x, h2.y, h3.x, h3.y));
         }

@@ -3,14 +3,16 @@
 //
 // The tensor cores' tile of 128 rows, and the fp16 copies of keys and values that
 // it reads from shared memory, are made for many rows: with few of them
-// the copies are what costs (paged_attn_q8.cu: shared memory is 80% busy). Here
-// every warp is by itself: it takes every W-th unit of 32 keys of its CTA's run,
-// has the next unit's codes under way into shared memory by asynchronous copies
+// the copies are what costs (paged_attn_q8.cu). Here every warp is by itself: it
+// takes every W-th unit of 32 keys of its CTA's run, has the next halves of units
+// (keys, or values) under way into a ring of its own by asynchronous copies
 // while it works, and multiplies by mma.sync, whose fragments are made in
-// registers: code * scale never exists, codes are exact in fp16, key scales go
-// onto scores and value scales onto weights in fp32 (which are then
-// rounded to fp16 as in paged_attn_q8.cu). At an item's end the warps' parts are
-// joined in shared memory.
+// registers. A product of code and scale never exists: codes are exact in fp16,
+// key scales go onto scores and value scales onto weights in fp32, which are then
+// rounded to fp16 for the product with the values, in units of 2^-E as in
+// paged_attn_q8.cu (weight times scale stays below 2^15 and counts down to 2^-31 of
+// that; E follows the largest value scale of each 32 keys). At an item's end
+// the warps' parts are joined in shared memory, in their order.
 //
 // Fragments. A product over dims (scores) or keys (output) may take them in any
 // order, as long as both operands do. Of a key row, lane (g, c) of the B operand
@@ -20,6 +22,15 @@
 // as weights that is where the A operand of the next product wants them; of the
 // values lane (g, c) loads dims 16 g .. (8 g .. of heads of 64) of the 4 keys that
 // a step of 16 gives it, and turns each 4 x 4 bytes over.
+//
+// What bounds it: up to 16 rows memory (one token of 64 sequences of 32768 keys,
+// 32/8 heads of 128: 685 us with one CTA an SM, 95% of the copy bandwidth, and 720
+// with two; one of 32 of 8192 100 us, start, joins and end included; by the kernel
+// for 128 rows 1191 and 171); of 17 to 32 rows the latency of 1200 instructions a
+// unit in 8 warps (8 tokens of 32 sequences of 8192 156 us instead of 175). Short
+// calls are chains of loads: one token over a window of 4096 keys 11.8 us (17.6).
+// 12 warps an SM (8 of 32 rows) are what registers allow; 10, unevenly on four
+// schedulers, take 801 us for the 685, 14, spilling, 832.
 #include <algorithm>
 #include <atomic>
 

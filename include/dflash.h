@@ -432,8 +432,13 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * as codes c = x * (127 / m) rounded to the nearest whole number (halves to the
  * even one), m = max |x|, each as the byte c + 128, and the scale m / 127; it
  * stands for c * scale. Rows with m below 2^-100 are held as zeros, and a row with
- * an infinity or a NaN stands for NaN throughout. Attention takes what the codes
- * stand for without rounding it. */
+ * an infinity or a NaN stands for NaN throughout. Attention takes codes and scales
+ * as they are where a sequence has up to 32 rows of a kv head on average (new
+ * tokens times n_heads / n_kv_heads; behind a prefix, of all sequences together).
+ * Above that, products of code and scale (with bf16 tokens the scales, too) are
+ * rounded to 11 bits, behind a power of two that 128 neighbouring keys share, whether
+ * a row sees them all or not: scales (of keys, or of values) 2^21 below the largest
+ * finite one of these lose bits, as do value scales below 2^-90. */
 enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1, DFLASH_POOL_Q8 = 16 };
 
 typedef struct {
@@ -506,10 +511,11 @@ dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b, size_t* b
  *  scale    in (0, 2^127]
  *  workspace  device, 32-byte aligned, at least dflash_paged_attn_workspace
  * A token that sees no key gets zeros. Keys and values it does not see have no
- * influence on it, infinities and NaN included. (Behind a length they cost
- * nothing. Those of cached keys that only some rows of a tile of 256 see, such as
+ * influence on it, infinities and NaN included (of 8-bit pages, but for the
+ * exponent that neighbouring keys share). (Behind a length, and in 8-bit pages, they
+ * cost nothing. Those of cached keys that only some rows of a tile of 256 see, such as
  * a later token of the block or another sequence behind the same prefix, make
- * the kernel compute the others again one by one: one sequence of NaN among 32
+ * the kernel compute the others of 16-bit pages again one by one: one sequence of NaN among 32
  * of 16 tokens behind 32768 shared ones, 46 ms instead of 0.2.)
  * A token whose visible scores are all -infinity gets zeros, too.
  * Errors: EINVAL (also a workspace that is too small), ECUDA. */

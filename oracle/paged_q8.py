@@ -42,14 +42,23 @@ def rounded(x, bits):
     return np.ldexp(np.rint(np.ldexp(m, bits)), e - bits)
 
 
-def decode(pool, d, bits=None):
+def decode(pool, d, bits=None, whole=False):
     """The pool [n_pages, 2, n_kv, 64 * d] in fp64 that the bytes stand for; with
-    `bits`, scales and products are rounded to so many significant bits."""
+    `bits`, scales and products are rounded to so many significant bits, or (whole)
+    products only, of a scale in two parts of that many (code * rest, rounded, is
+    added to code * most)."""
     kc, vc, ks, vs = parts(pool, d)
     n, h = ks.shape[:2]
-    to = (lambda x: x) if bits is None else (lambda x: rounded(x, bits))
+
+    def product(codes, scales):
+        scales = scales[..., None]
+        if bits is None:
+            return codes * scales
+        most = rounded(scales, bits)
+        rest = rounded(codes * rounded(scales - most, bits), bits) if whole else 0.0
+        return rounded(codes * most + rest, bits)
     with np.errstate(invalid="ignore"):
-        k, v = to(kc * to(ks)[..., None]), to(vc * to(vs)[..., None])
+        k, v = product(kc, ks), product(vc, vs)
     return np.stack([k.reshape(n, h, -1), v.transpose(0, 1, 3, 2).reshape(n, h, -1)], axis=1)
 
 

@@ -14,8 +14,9 @@ Tolerances, from the arithmetic, u = half a step of the tokens' type (bf16
    half a step of the smallest fp16 values.
  - attention, A = sum of w |v|, S = scale sum |q||k|. The products are of fp16:
    in batches of more than 32 rows of a kv head for each sequence (the kernel for
-   128 rows) what a key or value stands for is rounded twice to its 11 bits (the
-   scale, then its product with the code). The sharp check is against the definition
+   128 rows) what a key or value stands for is rounded to its 11 bits, twice (bf16
+   tokens: the scale, then its product with the code) or once (fp16 tokens: the scale
+   is taken in two parts of 11). The sharp check is against the definition
    over keys and values that are rounded so, for fewer rows over those that are not
    (codes are exact, scales stay in fp32); its tolerance is that for
    16-bit pages with these differences. Weights are rounded to fp16, whatever
@@ -30,9 +31,9 @@ Tolerances, from the arithmetic, u = half a step of the tokens' type (bf16
    the largest before it is rounded in steps of 2^-24 at least: of each of n terms at
    most 2^-25 2^-7 4 max |v| = 2^-30 max |v|.
    Against the definition itself the roundings of keys and values count in full:
-   a score is off by 2 2^-11 S more, a weight by twice that, and the sum of the
-   values by 2 2^-11 A. (That is what all of them on one side would give; found is
-   0.0017 of the output's norm for bf16 and 0.0003 for fp16.)
+   a score is off by 2 2^-11 S more (fp16 tokens 2^-11 S), a weight by twice that,
+   and the sum of the values by 2 2^-11 A (2^-11 A). (That is what all of them on one
+   side would give; found is 0.0020 of the output's norm for bf16 and 0.0005 for fp16.)
 """
 import ctypes
 
@@ -61,7 +62,7 @@ class Batch8(Batch):
         self.pool = torch.from_numpy(p8.encode(keys, values)).to(DEV)
 
     def decoded(self, bits=None):
-        return p8.decode(self.pool.cpu().numpy(), self.d, bits)
+        return p8.decode(self.pool.cpu().numpy(), self.d, bits, whole=self.dtype == HF)
 
     def oracle(self, bits="as run", **kw):
         mixed = False
@@ -93,7 +94,8 @@ def check(b, got, ref, keys, scale=None, whole=False):
     score = 2 * (d / 16 + 8) * 2.0 ** -23 * size + 2 * lost + 2.0 ** -21
     tol = u * np.abs(out) + (2.0 ** -11 + score + (keys / 16 + 64) * 2.0 ** -23) * mass + (keys * 2.0 ** -30 + 2.0 ** -31) * vmax
     if whole:
-        tol = tol + (2 * 2.0 ** -10 * size + 2.0 ** -10) * mass
+        once = 2.0 ** -11 * (2 if b.dtype == BF else 1)
+        tol = tol + (2 * once * size + once) * mass
     tol = tol + TINY[b.dtype]
     bad = np.abs(got - out) - tol
     bad[np.isnan(got) | np.isnan(out)] = np.inf
@@ -363,7 +365,7 @@ def test_shared_prefix(dfl, prefix, heads, n_kv, d, dtype):  # noqa: F811
 MANY = [(1, int(n)) for n in np.random.default_rng(5).integers(1, 1500, 64)]
 
 
-@pytest.mark.parametrize("prefix", [0, 1, 300, 5000])
+@pytest.mark.parametrize("prefix", [0, 1, 300, 1500])
 @pytest.mark.parametrize("heads,n_kv,d,dtype", [(8, 2, 128, BF), (4, 4, 64, HF), (28, 4, 64, BF), (32, 1, 128, HF)])
 def test_many_short_blocks_behind_a_prefix(dfl, prefix, heads, n_kv, d, dtype):  # noqa: F811
     """(Where the own caches are taken apart from the prefix; with 63 sequences they are not.)"""

@@ -1,0 +1,150 @@
+"""Edges of the attention over 8-bit pages on the GPU: which of its kernels takes
+a batch, waits that run out, streams by number, captured calls, pages in two tables.
+
+Tolerances are those of tests/test_gpu_paged_q8.py.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from tests.test_gpu_paged import BF, DEV, HF, dfl  # noqa: E402, F401
+from tests.test_gpu_paged_q8 import MANY, Batch8, check, check_attn  # noqa: E402
+
+
+# --- around the bounds between the kernels ---------------------------------------
+
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+@pytest.mark.parametrize("heads,n_kv", [(4, 4), (8, 2), (14, 2), (16, 1), (17, 1), (32, 1), (33, 1), (128, 1)])
+def test_rows_around_16_and_32(dfl, heads, n_kv, d, dtype):  # noqa: F811
+    """As many rows as the kernels for few rows take on average, one token less and
+    one more, in even and in uneven blocks."""
+    group = heads // n_kv
+    for rows in (16, 32):
+        for tokens in (rows // group - 1, rows // group, rows // group + 1):
+            if tokens < 1:
+                continue
+            check_attn(dfl, Batch8([(tokens, 70 + tokens)], heads, n_kv, d, dtype, prefix=90), shared=True)
+            check_attn(dfl, Batch8([(tokens, 300), (tokens, tokens)], heads, n_kv, d, dtype), window=100, sinks=3)
+            if tokens > 1:
+                check_attn(dfl, Batch8([(2 * tokens - 1, 200), (1, 129)], heads, n_kv, d, dtype))
+
+
+@pytest.mark.parametrize("heads,n_kv,d,dtype", [(32, 8, 128, BF), (14, 2, 64, HF)])
+def test_a_prompt_among_single_tokens(dfl, heads, n_kv, d, dtype):  # noqa: F811
+    """By its average the batch is one of few rows; the prompt is cut into many tiles."""
+    check_attn(dfl, Batch8([(1, 40 + 3 * i) for i in range(30)] + [(150, 700)] + [(1, 513)], heads, n_kv, d, dtype))
+
+
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+def test_single_tokens_over_many_units(dfl, d, dtype):  # noqa: F811
+    """More than 32 units of 32 keys a warp (page numbers are looked up that many at a time), and runs that end inside a tile."""
+    check_attn(dfl, Batch8([(1, 100000)], 4, 1, d, dtype))
+    check_attn(dfl, Batch8([(8, 66000), (1, 31), (7, 5000)], 4, 1, d, dtype), window=60001, sinks=1000)
+
+
+@pytest.mark.parametrize("heads,n_kv,d,dtype", [(8, 2, 128, BF), (4, 4, 64, HF)])
+def test_masks_of_few_rows(dfl, heads, n_kv, d, dtype):  # noqa: F811
+    """Windows and first tokens that begin and end around units of 32 keys and steps of 128."""
+    lens = [(1, 1000), (3, 161), (8, 129), (2, 2), (5, 4), (0, 7)]
+    b = Batch8(lens, heads, n_kv, d, dtype)
+    for window, sinks in ((1, 0), (1, 1), (31, 32), (32, 33), (33, 31), (128, 127), (129, 128), (1000, 5), (2 ** 31 - 1, 0)):
+        check_attn(dfl, b, window=window, sinks=sinks)
+        check_attn(dfl, b, window=window, sinks=sinks, causal=False)
+
+
+# --- waits that run out --------------------------------------------------------
+
+@pytest.mark.parametrize("lens,prefix,waits", [([(40, 3000)], 0, True), ([(300, 900), (2, 70)], 0, True),
+                                               ([(1, 90)] * 40, 700, True), (MANY, 700, True), ([(1, 3000)], 0, False)],
+                         ids=["block", "prompt", "shared", "apart", "few"])
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+def test_any_call_that_is_given_up_ends_and_says_so(dfl, lens, prefix, waits, d, dtype):  # noqa: F811
+    """(The kernel for few rows has no waits that could.)"""
+    b = Batch8(lens, 8, 2, d, dtype, prefix=prefix)
+    call = b.attend_shared if prefix else b.attend
+    clean = call(dfl)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dfl.dflash_debug_paged_wait_tries(0)
+    try:
+        call(dfl, status=status)
+        torch.cuda.synchronize()
+    finally:
+        dfl.dflash_debug_paged_wait_tries()
+    assert int(status) == int(waits)
+    status.zero_()
+    assert torch.equal(call(dfl, status=status), clean) and int(status) == 0
+
+
+# --- streams and graphs --------------------------------------------------------
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_stream_by_its_number(dfl, handle):  # noqa: F811
+    """The calls are ordered behind what that stream does before, also a slow fill."""
+    lens = [(1, 300), (5, 90), (64, 64)]
+    b, other = Batch8(lens, 8, 2, 64, BF, prefix=70), Batch8(lens, 8, 2, 64, BF, prefix=70, seed=1)
+    calls = lambda b, **kw: (b.attend(dfl, **kw), b.attend_shared(dfl, **kw),
+                             *dfl.dflash_kv_read(b.pool, b.T, b.q_start, b.kv_len, b.table, **kw))
+    ref = calls(other)
+    torch.cuda.synchronize()
+    slow = torch.empty(1 << 28, device=DEV)
+    for _ in range(10):
+        slow.fill_(1.0)
+    for x, y in ((b.pool, other.pool), (b.qkv, other.qkv), (b.table, other.table), (b.prefix_table, other.prefix_table)):
+        x.copy_(y)
+    got = calls(b, stream=handle)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, ref))
+
+
+def test_a_captured_decode_behind_a_prefix(dfl):  # noqa: F811
+    """64 growing caches, taken apart from their prefix: replays follow the lengths, and two graphs over one batch may run at once."""
+    b = Batch8(MANY, 8, 2, 128, BF, prefix=300)
+    b.attend_shared(dfl)
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(b.attend_shared(dfl))
+    full = b.kv_len.clone()
+    for less in (0, 1, 700):
+        b.kv_len.copy_((full - less).clamp(min=1))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        check(b, outs[0], b.oracle(prefix_table=b.prefix_np, prefix_len=300), 2000)
+        assert torch.equal(*outs)
+    kept, side = outs[0].clone(), torch.cuda.Stream()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], kept) and torch.equal(outs[1], kept)
+
+
+# --- pages -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("q", [1, 20])
+def test_pages_in_two_tables(dfl, q):  # noqa: F811
+    """Sequences that hold the same pages get the same results, also where a page comes up twice in one table."""
+    b = Batch8([(q, 500), (q, 500), (q, 900)], 8, 2, 128, BF)
+    b.table[1] = b.table[0]
+    b.table[2, 9] = b.table[2, 3]
+    b.q[q:2 * q] = b.q[:q]
+    got = check_attn(dfl, b)
+    assert torch.equal(got[:q], got[q:2 * q])
+
+
+@pytest.mark.parametrize("q", [1, 3, 20])
+def test_hidden_keys_that_are_larger(dfl, q):  # noqa: F811
+    """Keys that a row does not see share an exponent with those it does. Of finite
+    ones that is all they do: the tolerance counts the largest of the pool."""
+    b = Batch8([(q, 200)], 8, 2, 128, BF)
+    _, _, ks, vs = dfl.kv_pool_q8_views(b.pool, 128)
+    for s in (150, 170):      # before the window
+        p = int(b.table[0, s // 64])
+        ks[p][:, s % 64] *= 2.0 ** 10
+        vs[p][:, s % 64] *= 2.0 ** 10
+    check_attn(dfl, b, window=200 - 171 - q)
