@@ -3,6 +3,7 @@ a batch, waits that run out, streams by number, captured calls, pages in two tab
 
 Tolerances are those of tests/test_gpu_paged_q8.py.
 """
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -51,6 +52,70 @@ def test_masks_of_few_rows(dfl, heads, n_kv, d, dtype):  # noqa: F811
     for window, sinks in ((1, 0), (1, 1), (31, 32), (32, 33), (33, 31), (128, 127), (129, 128), (1000, 5), (2 ** 31 - 1, 0)):
         check_attn(dfl, b, window=window, sinks=sinks)
         check_attn(dfl, b, window=window, sinks=sinks, causal=False)
+
+
+def test_as_many_sequences_as_a_call_takes(dfl):  # noqa: F811
+    rng = np.random.default_rng(3)
+    lens = [(int(rng.integers(0, 3)), int(rng.integers(2, 150))) for _ in range(1024)]
+    check_attn(dfl, Batch8(lens, 4, 2, 64, HF))
+    check_attn(dfl, Batch8(lens, 4, 2, 64, HF, prefix=70), shared=True)
+
+
+# --- what must not matter to few rows ------------------------------------------
+
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+def test_hidden_keys_may_hold_anything(dfl, d, dtype):  # noqa: F811
+    """Keys that only some of the rows see: a later token's, and those before the window."""
+    b = Batch8([(6, 300)], 8, 2, d, dtype)
+    _, _, ks, vs = dfl.kv_pool_q8_views(b.pool, d)
+    first = 297 - 294     # the first new token that sees key 297
+    p, s = int(b.table[0, 297 // 64]), 297 % 64
+    for array in (ks, vs):
+        for value in (float("nan"), float("inf"), float("-inf")):
+            kept, clean = array[p][:, s].clone(), b.attend(dfl)
+            array[p][:, s] = value
+            got = b.attend(dfl)
+            assert torch.equal(got[:first], clean[:first])
+            if array is vs or value != value:
+                assert not got[first:].isfinite().any()
+            array[p][:, s] = kept
+    clean = b.attend(dfl, window=3, sinks=2)
+    p, s = int(b.table[0, 4]), 290 - 256
+    vs[p][:, s] = float("nan")
+    ks[p][:, s + 1] = float("inf")
+    assert torch.equal(b.attend(dfl, window=3, sinks=2), clean)
+
+
+def test_broken_rows_harm_themselves_only(dfl):  # noqa: F811
+    """A query of NaN or infinity, and a neighbour's cache of NaN, behind a prefix and alone."""
+    b = Batch8([(3, 300), (2, 90), (1, 33)], 8, 2, 128, BF, prefix=130)
+    clean = b.attend(dfl), b.attend_shared(dfl)
+    b.q = b.q.clone()
+    b.q[1, 3, 7], b.q[2, 1] = float("nan"), float("inf")
+    _, _, ks, _ = dfl.kv_pool_q8_views(b.pool, 128)
+    for p in b.table[1, :2].tolist():
+        ks[p] = float("nan")
+    for x, y in zip(clean, (b.attend(dfl), b.attend_shared(dfl))):
+        away = torch.ones(6, 8, dtype=torch.bool, device=DEV)
+        away[1, 3] = away[2, 1] = away[3:5] = False
+        assert torch.equal(x[away], y[away]) and y[1, 3].isnan().all() and y[3:5].isnan().all()
+
+
+def test_single_tokens_far_into_a_large_pool(dfl):  # noqa: F811
+    """Pages beyond 2^32 bytes, of which a batch of single tokens sees a few."""
+    b = Batch8([(1, 500), (1, 70), (1, 1), (4, 200)], 8, 2, 128, BF)
+    ref, n = b.attend(dfl), b.pool.shape[0]
+    big = torch.empty(160000, *b.pool.shape[1:], dtype=torch.uint8, device=DEV)
+    assert big.numel() > 5 * 2 ** 30
+    at = torch.linspace(123457, 159999, n, device=DEV).long()
+    big[at] = b.pool
+    table = torch.where(b.table < n, at.int()[b.table.clamp(max=n - 1).long()], b.table)
+    got = dfl.dflash_paged_attn(b.q, big, b.q_start, b.kv_len, table.contiguous())
+    assert torch.equal(got, ref)
+    q = b.q.clone()
+    dfl.dflash_kv_append(b.pool, b.k, b.v, b.q_start, b.kv_len, b.table, q=q, rope_base=1e4)
+    dfl.dflash_kv_append(big, b.k, b.v, b.q_start, b.kv_len, table.contiguous(), q=q, rope_base=1e4)
+    assert torch.equal(big[at], b.pool)
 
 
 # --- waits that run out --------------------------------------------------------
