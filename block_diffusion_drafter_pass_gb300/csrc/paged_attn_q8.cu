@@ -34,19 +34,22 @@
 // in the products: every code is finite, and weights of hidden keys are zero
 // before their scale. So no row has to be done again.
 //
-// What bounds it: shared memory and the warps beside it. A half goes through
-// shared memory three times (as codes, as fp16, to the products: the load/store
-// pipe is 70 to 87% busy), and a pair's step takes 2.4 us (4600 cycles for 2800 of
-// tensor work; with 16-bit pages 3400). 16 tokens of 32 sequences of 1024 to 8192
+// What bounds it: a step's chain (scores, weights, product, next scores), with
+// eight more warps on the softmax's schedulers than 16-bit pages need. A
+// pair's step takes 2.4 us, 4600 cycles of which the tensor pipe is active for 44%
+// (3300 and 57% there); issue slots are 54% taken, shared memory's load/store pipe
+// 36%. 16 tokens of 32 sequences of 1024 to 8192
 // keys (32/8 heads of 128) take 118 us (floor 47.5), of one over 262144 keys 164
-// (3.4 TB/s), 8.7 thousand new tokens with a window of 2048 380, 16 of 32 sequences
-// behind 32768 278.
+// (3.4 TB/s), 8.7 thousand new tokens with a window of 2048 377, 16 of 32 sequences
+// behind 32768 277.
 // What was tried and is slower: halves in rounds of two with their scales, one wait
 // for each; codes by the converting warps' own loads from global memory, without
 // the first ring and with room for a fourth half of fp16 (130 us instead of 119, 190
 // instead of 168, 433 instead of 389, 338 instead of 281 in the four cases: with
 // registers for the loads in flight the softmax spills, without them the loads
-// do); one team of converting warps for every half (141 us instead of 137 and 380
+// do); bytes as fp16's smallest numbers, times the scale and plus -128 times it in one
+// multiply-add, 4 instructions for 4 codes instead of 6 (121, 165, 379, 271 for 118,
+// 164, 377, 277, and scales lose bits at 2^12); one team of converting warps for every half (141 us instead of 137 and 380
 // instead of 364 in the first and last case, then).
 #include <algorithm>
 #include <atomic>
