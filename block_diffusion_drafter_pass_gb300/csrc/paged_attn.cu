@@ -802,7 +802,11 @@ struct Plan {
 // Whether a batch over 8-bit pages is one for the kernel of few rows (that many
 // of a kv head for each sequence on average: tiles hold no more, so longer blocks
 // are cut), and how. At 32 rows it takes 156 us instead of 175 (8 tokens of 32
-// sequences of 8192 keys, 4 heads a kv head); 64 would read the keys twice. Two
+// sequences of 8192 keys, 4 heads a kv head); 64 would read the keys twice. Short
+// caches of 17 to 32 rows are read twice by two tiles of 16, whose steps are
+// shorter chains (8 tokens over 4096 keys 13.8 us instead of 17.2, of 8 sequences
+// over 1024 21.9 instead of 23.5, of 16 over 2048 the same, of 48 over 1024 62
+// instead of 58; tables wider than the caches leave it at 32 rows). Two
 // CTAs an SM let one's ends pass under the other's work (uneven short blocks 23
 // us instead of 27, 128 tokens of 2048 keys 105 instead of 125, 64 of 32768 720
 // instead of 685); one for each, of all its warps, is better with few tiles (a
@@ -810,10 +814,11 @@ struct Plan {
 Q8Few few_rows(const dflash_paged_batch& b, bool shared) {
   const int group = b.n_heads / b.n_kv_heads;
   const long long rows = static_cast<long long>(b.n_tokens) * group, tiles = shared ? 1 : b.n_seq;
+  const long long keys = tiles * b.n_kv_heads * kPage * b.table_pages;   // at most, all heads together
   Q8Few few{0, 1};
   if (!(b.dtype & DFLASH_POOL_Q8)) return few;
   if (group <= 16 && rows <= 16 * tiles) few.rows = 16;
-  else if (group <= 32 && rows <= 32 * tiles) few.rows = 32;
+  else if (group <= 32 && rows <= 32 * tiles) few.rows = group <= 16 && !shared && keys <= 1 << 18 ? 16 : 32;
   if (few.rows == 32 || (few.rows == 16 && tiles * b.n_kv_heads > 8)) few.per_sm = 2;
   return few;
 }
