@@ -6,9 +6,9 @@
 // with codes d_j and scale b_j:
 //     s_j = q . (a_j c_j),   o = sum_j 2^(s_j - m) b_j d_j / sum_j 2^(s_j - m).
 // The products are of fp16 whatever the tokens' type. Queries are taken to it
-// as they are, or, where the row's largest value is below 1/2 or above 2^15, behind
-// a power of two that puts it between 1/2 and 1 (values below 2^-13 of that are
-// rounded in steps of 2^-24, all others of bf16 are exact). Keys and values are a code times its scale, behind a power of two
+// behind a power of two that puts the row's largest value between 1/2 and 1
+// (values below 2^-13 of that are rounded in steps of 2^-24, all others of bf16
+// are exact). Keys and values are a code times its scale, behind a power of two
 // 2^(7 - e) that all 128 of a step share (its largest scale comes to lie between 2^7
 // and 2^8), rounded to fp16 once, or for tokens of bf16, whose own steps are 8 times
 // as large, twice: the scale, too. Found over 2000 keys of scores of deviation 1.5:
@@ -40,8 +40,8 @@
 // (3300 and 57% there); issue slots are 54% taken, shared memory's load/store pipe
 // 36%. 16 tokens of 32 sequences of 1024 to 8192
 // keys (32/8 heads of 128) take 118 us (floor 47.5), of one over 262144 keys 164
-// (3.4 TB/s), 8.7 thousand new tokens with a window of 2048 365, 16 of 32 sequences
-// behind 32768 276.
+// (3.4 TB/s), 8.7 thousand new tokens with a window of 2048 377, 16 of 32 sequences
+// behind 32768 277.
 // What was tried and is slower: halves in rounds of two with their scales, one wait
 // for each; codes by the converting warps' own loads from global memory, without
 // the first ring and with room for a fourth half of fp16 (130 us instead of 119, 190
@@ -178,17 +178,13 @@ __device__ __forceinline__ uint32_t vdesc_low(uint32_t saddr) {
 __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127) << 23); }   // -126..127
 
 // An item's queries into shared memory as fp16, by the converting warps: a row
-// whose largest value lies from 1/2 to 2^15 (fp16's largest) as it is, others times the
-// power of two that puts their largest finite value between 1/2 and 1 (infinities
-// and NaN stay what they are), and s_qc what its dot products are
-// multiplied by for that. Only the last step before overlaps this: with each row's
-// maximum found by shuffles a prompt takes 377 us instead of 365, without any of
-// it 349.
+// times the power of two that puts its largest finite value between 1/2 and 1
+// (its infinities and NaN stay what they are), and s_qc what its dot products are
+// multiplied by for that.
 template <int D, bool F16>
 __device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Notice& r, uint32_t q_at, float* s_qc, int ct) {
   constexpr int kOf = D / 8, kPass = kConvWarps * 32 / kOf, kAtOnce = 4;   // lanes of a row, rows at a time
-  constexpr uint32_t kInf = F16 ? 0x7C00u : 0x7F80u, kLow = F16 ? 0x3800u : 0x3F00u, kHigh = F16 ? 0x7C00u : 0x4700u;   // 1/2, 2^15
-  constexpr uint32_t kOne = F16 ? 0x3C003C00u : 0x3F803F80u;
+  constexpr uint32_t kInf = F16 ? 0x7C00u : 0x7F80u;
   const int c = ct % kOf, G = a.b.group, stream_rows = a.stream_tokens * G;
   const int n = (r.pair ? 2 : 1) * stream_rows, end = r.t0 + r.ntok;
   const int dt = kPass / G, dg = kPass - dt * G;
@@ -198,7 +194,7 @@ __device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Noti
     uint4 w[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
-      w[u] = make_uint4(kOne, kOne, kOne, kOne);   // rows of no token
+      w[u] = make_uint4(0, 0, 0, 0);
       if (i0 + u * kPass < n && token < end)
         w[u] = __ldg(reinterpret_cast<const uint4*>(a.q + token * a.q_stride + static_cast<long long>(r.head * G + g) * D) + c);
       token += dt;
@@ -211,42 +207,30 @@ __device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Noti
       uint32_t top = 0;   // magnitudes order as their bits
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = __vmaxu2(top, (&w[u].x)[e] & 0x7FFF7FFFu);
+      if (max(top & 0xFFFFu, top >> 16) >= kInf) {
+        top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t m = (&w[u].x)[e] & 0x7FFF7FFFu;
+          top = max(top, max((m & 0xFFFFu) < kInf ? m & 0xFFFFu : 0u, (m >> 16) < kInf ? m >> 16 : 0u));
+        }
+      }
       top = max(top & 0xFFFFu, top >> 16);
-      const uint32_t of = (kOf == 32 ? 0u : 1u << kOf) - 1u, shift = threadIdx.x & 31 & ~(kOf - 1);
-      const bool held = (__ballot_sync(0xffffffffu, top >= kLow) >> shift & of) != 0 && (__ballot_sync(0xffffffffu, top >= kHigh) >> shift & of) == 0;
+#pragma unroll
+      for (int o = kOf / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // (of the largest bf16 values 2^-126 leaves 4)
+      const int up = max(126 - static_cast<int>(__float_as_uint(unpack2<F16>(top).x) >> 23), -126);
+      const float f = pow2_of(up);
       uint4 h;
-      float by = 1.f;
-      if (__all_sync(0xffffffffu, held)) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 x = unpack2<F16>((&w[u].x)[k]);
-          (&h.x)[k] = F16 ? (&w[u].x)[k] : pack2<true>(x.x, x.y);
-        }
-      } else {
-        if (top >= kInf) {   // of the finite ones
-          top = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t m = (&w[u].x)[e] & 0x7FFF7FFFu;
-            top = max(top, max((m & 0xFFFFu) < kInf ? m & 0xFFFFu : 0u, (m >> 16) < kInf ? m >> 16 : 0u));
-          }
-        }
-#pragma unroll
-        for (int o = kOf / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // (of the largest bf16 values 2^-126 leaves 4)
-        const int up = held ? 0 : max(126 - static_cast<int>(__float_as_uint(unpack2<F16>(top).x) >> 23), -126);
-        const float f = pow2_of(up);
-        by = pow2_of(-up);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 x = unpack2<F16>((&w[u].x)[k]);
-          (&h.x)[k] = pack2<true>(x.x * f, x.y * f);
-        }
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = unpack2<F16>((&w[u].x)[k]);
+        (&h.x)[k] = pack2<true>(x.x * f, x.y * f);
       }
       if (i < n) {
         const int stream = i >= stream_rows, row = i - stream * stream_rows;
         store_shared16(q_at + stream * Cfg<D>::kQ1Off + (c >> 3) * Cfg<D>::kBox + row * 128 + (((c & 7) ^ (row & 7)) << 4), h);
-        if (c == 0) s_qc[stream * kRows + row] = a.scale_log2 * by;
+        if (c == 0) s_qc[stream * kRows + row] = a.scale_log2 * pow2_of(-up);
       }
     }
   }

@@ -23,8 +23,8 @@ Tolerances, from the arithmetic, u = half a step of the tokens' type (bf16
    the tokens' type: 2^-11 A. Rounded keys and values are off by 127 times half a
    step of the smallest fp16 values more, where the step's largest scale is put at
    2^7 at least: 2^-25 / 2^7 of the largest row, 2^-32, for each of the two
-   roundings. The queries are taken to fp16 so (behind a power of two, if need be) that a
-   row's largest is 2^-1 at least, in steps of 2^-24 at least: off by 2^-24 max |q|
+   roundings. The queries are taken to fp16 behind a power of two that puts a row's
+   largest between 2^-1 and 1, in steps of 2^-24 at least: off by 2^-24 max |q|
    each. Three more factors are multiplied in in fp32: four more roundings of a score
    of size S. A weight, in the unit of the largest value exponent so far (4 times
    what the visible ones reach, at most: two powers of two), is scaled to 2^7 for
