@@ -118,6 +118,25 @@ def test_single_tokens_far_into_a_large_pool(dfl):  # noqa: F811
     assert torch.equal(big[at], b.pool)
 
 
+@pytest.mark.parametrize("heads,n_kv,d,dtype", [(8, 2, 128, BF), (4, 4, 64, HF), (8, 1, 128, HF)])
+def test_rows_of_very_different_size(dfl, heads, n_kv, d, dtype):  # noqa: F811
+    """Query rows far from 1 beside ordinary ones (of many rows, a row is scaled only where fp16 asks for it), and rows of zeros."""
+    for lens in ([(2, 200), (1, 90)], [(40, 200), (17, 150)]):
+        b = Batch8(lens, heads, n_kv, d, dtype, prefix=70)
+        power = torch.tensor([-30 if dtype == BF else -9, -12, -1, 0, 0, 0, 2, 3], device=DEV).float()
+        pick = torch.randint(0, 8, (b.T, heads, 1), generator=torch.Generator(device=DEV).manual_seed(1), device=DEV)
+        b.q = (b.q.float() * torch.exp2(power[pick])).to(dtype)
+        b.q[1, 0] = 0.0
+        clean = check_attn(dfl, b), check_attn(dfl, b, shared=True)
+        big = b.q.clone()
+        b.q[0, 1] = torch.finfo(dtype).max / 2    # nothing can be said of this row but that the others stay
+        away = torch.ones(b.T, heads, dtype=torch.bool, device=DEV)
+        away[0, 1] = False
+        for x, y in zip(clean, (b.attend(dfl), b.attend_shared(dfl))):
+            assert torch.equal(x[away], y[away])
+        b.q = big
+
+
 # --- waits that run out --------------------------------------------------------
 
 @pytest.mark.parametrize("lens,prefix,waits", [([(40, 3000)], 0, True), ([(300, 900), (2, 70)], 0, True),
@@ -213,3 +232,27 @@ def test_hidden_keys_that_are_larger(dfl, q):  # noqa: F811
         ks[p][:, s % 64] *= 2.0 ** 10
         vs[p][:, s % 64] *= 2.0 ** 10
     check_attn(dfl, b, window=200 - 171 - q)
+
+
+# --- many rows ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("d,dtype", [(64, HF), (64, BF), (128, HF), (128, BF)])
+def test_missing_pages_and_broken_rows_of_longer_blocks(dfl, d, dtype):  # noqa: F811
+    """As for few rows: pages that are not there are not seen and are told of, rows of NaN and infinity harm themselves only."""
+    b = Batch8([(40, 300), (50, 100)], 4, 2, d, dtype, prefix=130)
+    b.table[0, 1] = -7
+    b.table[1, 0] = b.pool.shape[0]
+    b.prefix_table[1] = 2 ** 30
+    b.prefix_np = b.prefix_table.cpu().numpy()
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    clean = []
+    for shared in (False, True):
+        status.zero_()
+        clean.append(check_attn(dfl, b, shared=shared, status=status))
+        assert int(status) == 2
+    b.q = b.q.clone()
+    b.q[4, 3, 7], b.q[60, 1] = float("nan"), float("inf")
+    away = torch.ones(90, 4, dtype=torch.bool, device=DEV)
+    away[4, 3] = away[60, 1] = False
+    for x, y in zip(clean, (b.attend(dfl), b.attend_shared(dfl))):
+        assert torch.equal(x[away], y[away]) and y[4, 3].isnan().all()
