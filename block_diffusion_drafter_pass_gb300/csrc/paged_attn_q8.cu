@@ -45,12 +45,13 @@
 // What was tried and is slower: halves in rounds of two with their scales, one wait
 // for each; codes by the converting warps' own loads from global memory, without
 // the first ring and with room for a fourth half of fp16 (130 us instead of 119, 190
-// instead of 168, 433 instead of 389, 338 instead of 281 in the four cases: with
+// instead of 168, 433 instead of 389, 338 instead of 281 in these four cases: with
 // registers for the loads in flight the softmax spills, without them the loads
 // do); bytes as fp16's smallest numbers, times the scale and plus -128 times it in one
 // multiply-add, 4 instructions for 4 codes instead of 6 (121, 165, 379, 271 for 118,
-// 164, 377, 277, and scales lose bits at 2^12); one team of converting warps for every half (141 us instead of 137 and 380
-// instead of 364 in the first and last case, then).
+// 164, 377, 277, and scales lose bits at 2^12); one team of converting warps for
+// every half (141 us instead of 137 and 380 instead of 364 in the first and last
+// case, then).
 #include <algorithm>
 #include <atomic>
 

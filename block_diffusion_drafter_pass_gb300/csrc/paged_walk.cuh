@@ -1,5 +1,6 @@
 // paged_walk.cuh - what the attention kernels over a caller's page pool share
-// (16-bit pages: paged_attn.cu, 8-bit pages: paged_attn_q8.cu): the batch in
+// (16-bit pages: paged_attn.cu, 8-bit pages: paged_attn_q8.cu, few rows of these:
+// paged_attn_q8_few.cu): the batch in
 // shared memory, its tiles and their steps of 128 keys, how they are dealt to
 // the CTAs, what a row sees, the waits, and an item's end. How the work is cut
 // is said at the head of paged_attn.cu.
