@@ -388,8 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         __syncwarp();
         const int was = places;
         places = pair ? C::kRawPair : C::kRawSlots;
-        // behind a pair's queries: their place is free when its last scores are
-        if (places > was) wait(smem_u32(&q_empty), (k - 1) & 1);
+        // Behind a pair's queries: their place is free when its last scores are done. A
+        // parity tells a phase from its neighbours only, and all of a pair of one step may
+        // be on its way before the scores of the item before it are done: then the pair's
+        // phase looks over. So first its queries must be in: who brings them has waited for those.
+        if (places > was) {
+          wait(smem_u32(note_empty) + ((k - 1) & 1) * 8, (k - 1) >> 1 & 1);
+          wait(smem_u32(&q_empty), (k - 1) & 1);
+        }
         if (at >= places) at = 0;
         if (!ok || !notice(Notice{nj, pair, head, it.t.t0, it.t.ntok, {}})) break;
         // Scales go kScalesAhead steps ahead of their keys: a warp has work with them.
