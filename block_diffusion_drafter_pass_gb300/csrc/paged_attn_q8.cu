@@ -57,6 +57,7 @@
 #include <atomic>
 
 #define DFL_WALK_CALL __forceinline__
+#include "paged_q8_rings.h"
 #include "paged_walk.cuh"
 
 namespace dfl {
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
   __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], note_full[2], note_empty[2], conv_meet;
   __shared__ __align__(8) uint64_t scale_raw[kScaleRing], scale_full[kScaleRing];
-  __shared__ __align__(8) uint64_t kv_full[2][S], kv_empty[S];   // full: by stream
+  __shared__ __align__(8) uint64_t kv_full[2][S], kv_empty[2 * S];   // full: by stream, empty: paged_q8_rings.h
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
   __shared__ Join join;
@@ -294,8 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
     for (int s = 0; s < S; ++s) {
       mbar_init(&kv_full[0][s], kConvWarps / 2);
       mbar_init(&kv_full[1][s], kConvWarps / 2);
-      mbar_init(&kv_empty[s], 2);   // both streams
     }
+    for (int s = 0; s < 2 * S; ++s) mbar_init(&kv_empty[s], 2);   // both streams
     mbar_init(&q_full, kConvWarps);
     mbar_init(&q_empty, 2);
     mbar_init(&mma_done, 2);
@@ -544,8 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         if (ok) ok = __all_sync(0xffffffffu, bar_wait(bar, parity, progress_at, wait_tries));
         return ok;
       };
-      auto scores = [&](uint32_t q_at, int slot) {   // S = Q K^T
-        const uint32_t k_at = ring_low + slot * (C::kHalf >> 4);
+      auto empty_of = [&](int half) { return empty_at + read_bar(half, S) * 8; };
+      auto scores = [&](uint32_t q_at, int half) {   // S = Q K^T
+        const uint32_t k_at = ring_low + half % S * (C::kHalf >> 4);
         if (one) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -553,11 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             tc_mma_bf16(s_col, sdesc_of(q_at + off), sdesc_of(k_at + off), kIdescS, kk > 0);
           }
           bar_commit(s_at);
-          bar_commit(empty_at + slot * 8);
+          bar_commit(empty_of(half));
         }
       };
-      auto product = [&](int slot, uint32_t add) {   // O (+)= P V: the first page's weights while the second's are still made
-        const uint32_t v_at = vring_low + slot * (C::kHalf >> 4);
+      auto product = [&](int half, uint32_t add) {   // O (+)= P V: the first page's weights while the second's are still made
+        const uint32_t v_at = vring_low + half % S * (C::kHalf >> 4);
         if (one) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
 #pragma unroll
           for (int kk = 4; kk < 8; ++kk)
             tc_mma_bf16_ts(o_col, s_col + kk * 8, sdesc_of(v_at + (kk * 2048 >> 4)), kIdescO, 1u);
-          bar_commit(empty_at + slot * 8);
+          bar_commit(empty_of(half));
         }
       };
       while (true) {
@@ -593,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
               if (!wait(full_at + slot * 8, got >> slot & 1)) break;
               got ^= 1u << slot;
               tc_fence_after();
-              scores(q_low, slot);
-              if (one) bar_commit(empty_at + slot * 8);
+              scores(q_low, next);
+              if (one) bar_commit(empty_of(next));
             }
             if (j >= nj - 2 && j < nj) {   // the last scores
               if (one) bar_commit(smem_u32(&q_empty));
@@ -607,9 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             if (!wait(full_at + slot * 8, got >> slot & 1) || !wait(p_at, np & 1)) break;
             got ^= 1u << slot;
             tc_fence_after();
-            product(slot, add);
+            product(half, add);
             if (!ok) break;
-            if (one) bar_commit(empty_at + slot * 8);
+            if (one) bar_commit(empty_of(half));
             add = 1;
             ++np;
             __syncwarp();
@@ -661,21 +663,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             const uint32_t take = more ? warp_uniform(note_of<kStepRing>(s_step, steps, early) >> (2 + s) & 1) : 0u;
             tc_fence_after();
             if (takes & 1) {
-              product(vslot, add);
+              product(c, add);
               if (!ok) break;
               add = 1;
             } else if (pv) {
               if (!wait(p_at + 8, np & 1)) break;
-              if (one) bar_arrive(empty_at + vslot * 8);
+              if (one) bar_arrive(empty_of(c));
             }
             np += pv;
             __syncwarp();
             if (one) bar_arrive(pass_at);   // the other stream's waits pass under these products
             if (take) {
-              scores(q_at, kslot);
+              scores(q_at, ck);
             } else if (more && one) {
               bar_arrive(s_at);   // the softmax follows every step of a pair
-              bar_arrive(empty_at + kslot * 8);
+              bar_arrive(empty_of(ck));
             }
             if (one && j + 2 == nj) bar_commit(smem_u32(&q_empty));   // the item's queries are not needed any more
             __syncwarp();
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           code[p] = load_shared_codes(src + p * kRowsOf * D);
           scale[p] = load_shared_u32(scales + (p * kRowsOf / kPage) * 512 + p * kRowsOf % kPage * 4);
         }
-        if (!wait(smem_u32(kv_empty) + half % S * 8, (half / S & 1) ^ 1)) break;
+        if (half >= S && !wait(smem_u32(kv_empty) + free_bar(half, S) * 8, free_parity(half, S))) break;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           const uint4 w = code[p];

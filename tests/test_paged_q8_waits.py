@@ -8,13 +8,31 @@ softmax, and products that end in the order of their issue, some time later. Wha
 checks is that nothing is written while it is still to be read: a place of the ring
 of fp16 halves, and the second stream's queries, which lie over the last raw places.
 """
+import ctypes
 import os
 import random
 import re
+import shutil
+import subprocess
 
 import pytest
 
 from block_diffusion_drafter_pass_gb300 import _build
+
+
+@pytest.fixture(scope="module")
+def rings(tmp_path_factory):
+    if not shutil.which("g++"):
+        pytest.skip("no g++")
+    d = tmp_path_factory.mktemp("rings")
+    src, lib = os.path.join(d, "rings.cpp"), os.path.join(d, "rings.so")
+    with open(src, "w") as f:
+        f.write('#include "paged_q8_rings.h"\nextern "C" {\n'
+                "int read_bar(int h, int s) { return dfl::read_bar(h, s); }\n"
+                "int free_bar(int h, int s) { return dfl::free_bar(h, s); }\n"
+                "int free_parity(int h, int s) { return dfl::free_parity(h, s); }\n}\n")
+    subprocess.run(["g++", "-std=c++17", "-shared", "-fPIC", "-I", _build.CSRC, src, "-o", lib], check=True)
+    return ctypes.CDLL(lib)
 
 
 class Bar:
@@ -246,8 +264,12 @@ def some_items(rng):
 
 
 def one_each(S):
-    """One barrier a slot: the phase by the half's turn in its slot."""
+    """One barrier a slot, as it was: the phase by the half's turn in its slot."""
     return (lambda h: h % S), (lambda h: (h % S, (h // S & 1) ^ 1))
+
+
+def of_header(rings, S):
+    return (lambda h: rings.read_bar(h, S)), (lambda h: (rings.free_bar(h, S), rings.free_parity(h, S)) if h >= S else None)
 
 
 SHAPES = {128: (3, 4, 2), 64: (6, 6, 4)}   # slots, raw places, those of a pair
@@ -266,9 +288,14 @@ def faults(make, n=400):
 
 
 @pytest.mark.parametrize("d", [64, 128])
-def test_queries_stay_until_their_scores_are_done(d):
-    make = lambda asks: faults(lambda rng, items: Model(rng, items, *SHAPES[d], one_each(SHAPES[d][0]), asks_note=asks))
-    assert "queries" not in make(True) and "queries" in make(False)
+def test_nothing_is_written_before_it_is_read(rings, d):
+    assert faults(lambda rng, items: Model(rng, items, *SHAPES[d], of_header(rings, SHAPES[d][0]))) == {}
+
+
+def test_the_model_finds_waits_that_pass_too_early(rings):
+    """What each of the two waits is there for."""
+    assert "queries" in faults(lambda rng, items: Model(rng, items, *SHAPES[128], of_header(rings, 3), asks_note=False))
+    assert "ring" in faults(lambda rng, items: Model(rng, items, *SHAPES[128], one_each(3)))
 
 
 def kernel():
@@ -288,3 +315,11 @@ def test_the_walk_asks_for_a_pairs_queries_first():
     assert m, "the walk's wait behind a pair"
     note, scores = m.group(1).find("note_empty"), m.group(1).find("q_empty")
     assert 0 <= note < scores and re.search(r"\(k - 1\) >> 1 & 1", m.group(1)[:scores])
+
+
+def test_the_ring_is_waited_for_as_modelled():
+    """Every arrival and the one wait for a half that was read go by the header's barriers."""
+    text = kernel()
+    assert "kv_empty[2 * S]" in text and "s < 2 * S; ++s) mbar_init(&kv_empty[s], 2)" in text
+    assert re.search(r"half >= S && !wait\(smem_u32\(kv_empty\) \+ free_bar\(half, S\) \* 8, free_parity\(half, S\)\)", text)
+    assert len(re.findall(r"bar_(?:commit|arrive)\(empty_of\(", text)) == 6 and "empty_at + slot" not in text
