@@ -516,6 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(scale_of<F16>(kx)) : "memory");
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 256), "r"(scale_of<F16>(vx)) : "memory");
           }
+          fence_proxy_async_smem();   // the next copies into this place are the async proxy's
           __syncwarp();
           if (lane == 0) bar_arrive(smem_u32(scale_full) + slot * 8);
         }

@@ -323,3 +323,13 @@ def test_the_ring_is_waited_for_as_modelled():
     assert "kv_empty[2 * S]" in text and "s < 2 * S; ++s) mbar_init(&kv_empty[s], 2)" in text
     assert re.search(r"half >= S && !wait\(smem_u32\(kv_empty\) \+ free_bar\(half, S\) \* 8, free_parity\(half, S\)\)", text)
     assert len(re.findall(r"bar_(?:commit|arrive)\(empty_of\(", text)) == 6 and "empty_at + slot" not in text
+
+
+def test_scales_are_fenced_before_their_place_is_copied_into_again():
+    """The scale warp's own accesses to a place lie before a proxy fence, and that before the arrival from
+    which, by way of the other roles, the next bulk copy into the place follows."""
+    text = kernel()
+    role = text[text.index("warp == kScaleWarp) {"):text.index("const int s = warp_uniform(warp - kMmaWarp0);")]
+    last = max(role.rindex("st.shared.b32"), role.rindex("load_shared_u32"))
+    fence, arrive = role.find("fence_proxy_async_smem()"), role.index("bar_arrive(smem_u32(scale_full)")
+    assert last < fence < arrive
