@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (done > 0) warp_wait(&o_done[stream], outs++ & 1);
       if (!ok) break;
 
-      ok = finish_item<D, F16, Redo<D, F16>>(a, b, it, join, stream, tmem, row.token, mref, l, done > 0, nx & 1, progress_at);
+      ok = finish_item<D, F16, Redo<D, F16>>(a, b, it, join, stream, tmem, row.token, mref, l, 1.f, done > 0, nx & 1, progress_at);
       nx += !it.pair;
       if (!ok) break;
     }

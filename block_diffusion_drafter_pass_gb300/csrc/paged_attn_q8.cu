@@ -78,7 +78,10 @@ constexpr int kScalesAhead = 2;  // steps that scales are ahead of their keys
 // scales' lead.
 constexpr int kStepRing = 32;
 constexpr float kBias = 7.f;
-constexpr int kLeastE = -80, kNoUnit = -(1 << 20);   // smaller scales count as 2^-80
+constexpr int kLeastE = -80;   // smaller scales count as 2^-80
+// A step whose largest contribution lies that far below the unit of O is summed by
+// itself: the exponentials of its weights in that unit would leave fp32.
+constexpr float kFar = 60.f;
 
 // Notice of an item's queries; nj = 0: the run's end.
 struct Notice {
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   __shared__ __align__(8) uint64_t kv_full[2][S], kv_empty[2 * S];   // full: by stream, empty: paged_q8_rings.h
   __shared__ __align__(8) uint64_t q_full, q_empty, mma_done;
   __shared__ __align__(8) uint64_t s_full[2], p_full[2][2], o_done[2], turn[2];   // p_full: by page of the step
-  __shared__ Join join;
+  __shared__ JoinUnits join;
   __shared__ __align__(16) int4 s_steps[kStepRing];
   __shared__ uint32_t s_step[kStepRing];
   __shared__ long long s_sum[kThreads / 32];
@@ -809,8 +812,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       if (lane == 0) next_item(b, it, items[++k & 1]);
       k = __shfl_sync(0xffffffffu, k, 0);
       const Row row = row_at(b, it.t, it.pair ? stream : 0, r);
-      float mref = -INFINITY, l = 0.f;   // the row's reference maximum (log2 units, less the bias), sum
-      int unit = kNoUnit;                // E: weights and sum are in units of 2^-E
+      // log2 units, whole numbers: the row's reference maximum (its sum is of 2^(s - mref)),
+      // and the unit of its products with the values (O is of 2^(s - top) values 2^7)
+      float mref = -INFINITY, l = 0.f, top = -INFINITY;
       float cq = 0.f;                    // of the row's dot products
       int done = 0;                      // steps of this item that this stream took
       StepWalk w;
@@ -855,7 +859,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         }
         if (done == 0) cq = s_qc[(k - 1) & 1][(pair ? stream * kRows : 0) + r];
         const int gone = flags & 3;
-        bool none = false;
         const bool masked = gone != 0 || (w.s.seq < 0 ? w.s.base > pre_b : w.s.seq != alone || w.s.base < own_a || w.s.base > own_b);
         if (masked) {
           // columns [0, c_hi) less those in [c_sink, c_lo) are seen
@@ -863,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
                              : w.s.seq < 0 ? RowSpan{0, row.hi + prefix_len, 0} : RowSpan{row.lo, row.hi, sinks};
           const int c_hi = min(sp.hi, w.s.end - 1) - w.s.base + 1;
           const int c_lo = sp.lo - w.s.base, c_sink = sp.sinks - w.s.base;
-          none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
+          const bool none = c_hi <= 0 || (c_lo >= min(c_hi, kStepKeys) && c_sink <= 0);
           if (__all_sync(0xffffffffu, none)) {
             const uint32_t zero[16] = {};
 #pragma unroll 1
@@ -900,17 +903,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           load(1);
           float mx = row_max(sv);
           load(0);
-          mx = fmaf(fmaxf(mx, row_max(sv)), cs, -kBias);
+          mx = fmaxf(mx, row_max(sv)) * cs;
           // each row by itself, so that it does not depend on its neighbours
-          const int need = none ? kNoUnit : un.y;
-          const bool grows = need > unit || mx > mref + kRescaleLog2;
-          if (__any_sync(0xffffffffu, grows)) {
-            const float nm = grows ? fmaxf(mref, mx) : mref;
-            const int nu = need > unit ? need + 1 : unit;
-            const float alpha = !grows || nm == -INFINITY ? 1.f : ex2(mref - nm + static_cast<float>(unit - nu));
-            l *= alpha;
+          const float need = ceilf(mx) + static_cast<float>(un.y);   // what the step adds to O, at most
+          const bool more = mx > mref + kRescaleLog2, grows = need > top + (kBias + kRescaleLog2);
+          if (more) {
+            const float nm = ceilf(mx);
+            l *= ex2(mref - nm);
             mref = nm;
-            unit = nu;
+          }
+          if (__any_sync(0xffffffffu, grows)) {
+            const float nt = grows ? need - kBias : top;
+            const float alpha = grows ? ex2(top - nt) : 1.f;
+            top = nt;
             if (done > 0) {
               // O holds the stream's products so far: they were issued before
               // the product whose scores these are, and end in that order
@@ -926,7 +931,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
               tmem_wait_st();
             }
           }
-          const float neg = mref == -INFINITY ? 0.f : -mref - static_cast<float>(unit - un.y);
+          // weights are 2^(s - ref), which times the step's values are in the unit of O
+          const float ref = top - static_cast<float>(un.y), neg = top == -INFINITY ? 0.f : -ref;
+          if (__any_sync(0xffffffffu, row.token >= 0 && need < top - kFar && need > -INFINITY)) {
+            // some row's step is far below its unit: sums by their own reference
+            const float by = ex2(fminf(mref - ref, 100.f)), own = mref == -INFINITY ? 0.f : -mref;
+            float part = 0.f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kStepKeys; c0 += 32) {   // P over scores that are read
+              float x[32];
+              uint32_t pk[16];
+              tmem_ld32(s_tmem + c0, x);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                x[c] = ex2_here(fmaf(x[c], cs, own));
+                part += x[c];
+              }
+#pragma unroll
+              for (int c = 0; c < 16; ++c) pk[c] = pack2<true>(x[2 * c] * by, x[2 * c + 1] * by);
+              tmem_st_u16(s_tmem + c0 / 2, pk);
+            }
+            tmem_wait_st();
+            weights_there(0);
+            weights_there(1);
+            l += part;
+            ++done;
+            ++ns;
+            continue;
+          }
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
           for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
@@ -949,7 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             tmem_wait_st();
             weights_there(u);
           }
-          l = fmaf((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y), pow2_of(7 - un.y), l);
+          // (ref - mref is at most kFar + kRescaleLog2 where there are weights)
+          l = fmaf((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y), ex2(fminf(ref - mref, 100.f)), l);
         }
         ++done;
         ++ns;
@@ -960,9 +993,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
       if (done > 0) warp_wait(&o_done[stream], outs++ & 1);
       if (!ok) break;
 
-      // what others join is the maximum in the unit's terms (the scales' 2^7 is in O and l)
-      ok = finish_item<D, F16, NoRedo>(a, b, it, join, stream, tmem, row.token, mref + static_cast<float>(unit - 7), l, done > 0, nx & 1,
-                                       progress_at);
+      const float2 whole = joined_form(mref, l);
+      const float unit = top == -INFINITY ? 0.f : ex2(top - 7.f - whole.x);
+      ok = finish_item<D, F16, NoRedo>(a, b, it, join, stream, tmem, row.token, whole.x, whole.y, unit, done > 0, nx & 1, progress_at);
       nx += !it.pair;
       if (!ok) break;
     }

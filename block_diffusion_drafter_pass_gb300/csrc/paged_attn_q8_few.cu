@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kUnit = 32;        // keys
 constexpr float kBias = 7.f;
-constexpr int kLeastE = -80, kNoUnit = -(1 << 20);   // smaller scales count as 2^-80
+constexpr int kLeastE = -80;   // smaller scales count as 2^-80
 
 template <int D, int MT, int PerSm>
 struct Few {
@@ -237,15 +237,15 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
 #pragma unroll
     for (int h = 0; h < C::kSlots - 1; ++h) bring_next();
     __syncthreads();   // the queries are there, and the next item
-    float o[MT][D / 8][4], mref[MT][2], l[MT][2];
-    int unit[MT][2];
+    // by row, log2 units, whole numbers: the reference maximum (its sum is of 2^(s - mref))
+    // and the unit of its products with the values (o is of 2^(s - top) values)
+    float o[MT][D / 8][4], mref[MT][2], l[MT][2], top[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int t = 0; t < D / 8; ++t) o[m][t][0] = o[m][t][1] = o[m][t][2] = o[m][t][3] = 0.f;
-      mref[m][0] = mref[m][1] = -INFINITY;
+      mref[m][0] = mref[m][1] = top[m][0] = top[m][1] = -INFINITY;
       l[m][0] = l[m][1] = 0.f;
-      unit[m][0] = unit[m][1] = kNoUnit;
     }
 #pragma unroll 1
     for (int i = 0; i < units; ++i) {
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
       const uint32_t at = ring_at + slot * C::kHalf;
       slot = slot + 1 < C::kSlots ? slot + 1 : 0;
       // scales: those of slots past the end become 0, a value scale that is no
-      // number the score of whoever sees the key; value scales in units of 2^(ev + 1)
+      // number the score of whoever sees the key; ev: the value scales are below 2^(ev + 1)
       int ev;
       {
         const bool there = now.base + lane < now.end;
@@ -285,7 +285,6 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         if (!there) kx = 0.f;
         if (!there || !number) vx = 0.f;
         ev = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(vx) & 0x7FFFFFFFu) >> 23) - 127, kLeastE);
-        vx *= pow2_of(-ev - 1);
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + C::kScales + lane * 4), "f"(kx) : "memory");
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + C::kScales + 4 * kUnit + lane * 4), "f"(vx) : "memory");
         __syncwarp();
@@ -333,7 +332,6 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         float mx[2] = {-INFINITY, -INFINITY};
-        bool none[2] = {false, false};
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -344,7 +342,6 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
           if (masked) {
             const RowSpan sp = span_of(b, mine[m][u], Step{now.seq, now.base, now.end});
             const uint32_t vis = sp.hi >= 0 ? static_cast<uint32_t>(row_sees(sp, now.base, now.end)) : 0u;
-            none[u] = vis == 0;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               s[m][t][2 * u] = vis >> (8 * t + 2 * c) & 1 ? s[m][t][2 * u] : -INFINITY;
@@ -361,15 +358,16 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           cq[u] = fminf(fmaxf(s_qc[m * 16 + u * 8 + g], 0x1p-126f), 0x1p127f);
-          mx[u] = fmaf(mx[u], cq[u], -kBias);
-          const int need = none[u] ? kNoUnit : ev + 1;
-          if (need > unit[m][u] || mx[u] > mref[m][u] + kRescaleLog2) {   // each row by itself
-            const float nm = fmaxf(mref[m][u], mx[u]);
-            const int nu = max(need + 1, unit[m][u]);
-            alpha[u] = nm == -INFINITY ? 1.f : ex2(mref[m][u] - nm + static_cast<float>(unit[m][u] - nu));
+          mx[u] *= cq[u];
+          if (mx[u] > mref[m][u] + kRescaleLog2) {   // each row by itself
+            const float nm = ceilf(mx[u]);
+            l[m][u] *= ex2(mref[m][u] - nm);
             mref[m][u] = nm;
-            unit[m][u] = nu;
-            l[m][u] *= alpha[u];
+          }
+          const float need = ceilf(mx[u]) + static_cast<float>(ev + 1);   // what the unit adds to o, at most
+          if (need > top[m][u] + (kBias + kRescaleLog2)) {
+            alpha[u] = ex2(top[m][u] - (need - kBias));
+            top[m][u] = need - kBias;
             grows = true;
           }
         }
@@ -382,15 +380,17 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float neg = mref[m][u] == -INFINITY ? 0.f : -mref[m][u] - static_cast<float>(unit[m][u] - ev - 1);
+          // (mref is at most 102 above top: no key counts for less than 2^-79 of its weight there)
+          const float neg = mref[m][u] == -INFINITY ? 0.f : -mref[m][u];
+          const float by = top[m][u] == -INFINITY ? 0.f : ex2(mref[m][u] - top[m][u]);
           float sum = 0.f;
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
             const float x = ex2(fmaf(s[m][t][2 * u], cq[u], neg)), y = ex2(fmaf(s[m][t][2 * u + 1], cq[u], neg));
             sum += x + y;
-            p[m][t][u] = pack2<true>(x * vs[t].x, y * vs[t].y);
+            p[m][t][u] = pack2<true>(x * by * vs[t].x, y * by * vs[t].y);
           }
-          l[m][u] = fmaf(sum, pow2_of(-ev - 1), l[m][u]);
+          l[m][u] += sum;
         }
       }
       // ---- output: two steps of 16 keys ----
@@ -442,15 +442,17 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         x += __shfl_xor_sync(0xffffffffu, x, 1);
         x += __shfl_xor_sync(0xffffffffu, x, 2);
         const int r = m * 16 + u * 8 + g;
-        if (c == 0) s_ml[warp][r] = make_float2(mref[m][u] + static_cast<float>(unit[m][u]), x);
+        const float2 whole = joined_form(mref[m][u], x);
+        const float f = top[m][u] == -INFINITY ? 0.f : ex2(top[m][u] - whole.x);   // o in its terms
+        if (c == 0) s_ml[warp][r] = whole;
         float* to = s_o + (warp * C::kRowsMax + r) * C::kJoinRow;   // dims of columns 2 c, then 2 c + 1
         if (units <= 0) continue;
 #pragma unroll
         for (int t = 0; t < D / 8; t += 4) {
           const int d = 2 * c * (D / 8) + t;
-          *reinterpret_cast<float4*>(to + C::join_at(d)) = make_float4(o[m][t][2 * u], o[m][t + 1][2 * u], o[m][t + 2][2 * u], o[m][t + 3][2 * u]);
+          *reinterpret_cast<float4*>(to + C::join_at(d)) = make_float4(o[m][t][2 * u] * f, o[m][t + 1][2 * u] * f, o[m][t + 2][2 * u] * f, o[m][t + 3][2 * u] * f);
           *reinterpret_cast<float4*>(to + C::join_at(d + D / 8)) =
-              make_float4(o[m][t][2 * u + 1], o[m][t + 1][2 * u + 1], o[m][t + 2][2 * u + 1], o[m][t + 3][2 * u + 1]);
+              make_float4(o[m][t][2 * u + 1] * f, o[m][t + 1][2 * u + 1] * f, o[m][t + 2][2 * u + 1] * f, o[m][t + 3][2 * u + 1] * f);
         }
       }
     }

@@ -548,14 +548,27 @@ struct Join {
   uint8_t bad[kRows];
 };
 
+// The same where O has a unit of its own.
+struct JoinUnits : Join {
+  float unit[2][kRows];
+};
+
+// A sum of weights and its reference, for others to join: the sum between 1 and 2,
+// so that a sum's product with a mean value stays in range where the value does.
+__device__ __forceinline__ float2 joined_form(float mref, float l) {
+  const int e = l > 0.f && l < INFINITY ? static_cast<int>(__float_as_uint(l) >> 23) - 127 : 0;
+  return make_float2(mref + static_cast<float>(e), l * __int_as_float((127 - e) << 23));
+}
+
 // A stream's part of an item's end: O out of tensor memory, joined with the
 // other stream's where both have the same rows, to `out` when the item is the
-// whole tile, else to the partials. False when a wait ran out. (A function of
-// its own so that its registers are not the softmax loop's.)
-template <int D, bool F16, class Again>
-__device__ DFL_WALK_CALL bool finish_item(const PagedAttnArgs& a, const Batch& b, const Item& it, Join& join, int stream,
-                                         uint32_t tmem, int token, float mref, float l, bool products, int parity,
-                                         uint32_t progress) {
+// whole tile, else to the partials. O times `unit` is in the terms of mref and l.
+// False when a wait ran out. (A function of its own so that its registers are not
+// the softmax loop's.)
+template <int D, bool F16, class Again, class J>
+__device__ DFL_WALK_CALL bool finish_item(const PagedAttnArgs& a, const Batch& b, const Item& it, J& join, int stream,
+                                         uint32_t tmem, int token, float mref, float l, float unit, bool products,
+                                         int parity, uint32_t progress) {
   const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, r = quarter * 32 + lane;
   const uint32_t lane_tmem = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   auto meet = [&](uint64_t* bar) {   // of the two groups' eight warps
@@ -577,18 +590,20 @@ __device__ DFL_WALK_CALL bool finish_item(const PagedAttnArgs& a, const Batch& b
   // A pair's stream has its rows' whole sums in its O. Of an alternating
   // tile both streams hold a part of every row's: the groups exchange
   // maxima and sums, and each joins half of the columns.
-  float w0 = 1.f, w1 = 0.f, top = mref, lj = l;   // out = w0 * O of stream s0 + w1 * O of stream 1
+  float w0 = Again::kOn ? 1.f : unit, w1 = 0.f, top = mref, lj = l;   // out = w0 * O of stream s0 + w1 * O of stream 1
   int col = 0, col_end = D, s0 = stream;
   bool use0 = products && l != 0.f, use1 = false;   // a stream without a visible key has no O to read
   if (!it.pair) {
     if (stream == 0) join.bad[r] = 0;
     join.ml[stream][r] = make_float2(mref, l);
+    if constexpr (!Again::kOn) join.unit[stream][r] = unit;
     if (!meet(&join.x_ml)) return false;
     const float2 m0 = join.ml[0][r], m1 = join.ml[1][r];
     top = fmaxf(m0.x, m1.x);
     w0 = m0.x == -INFINITY ? 0.f : ex2(m0.x - top);
     w1 = m1.x == -INFINITY ? 0.f : ex2(m1.x - top);
     lj = m0.y * w0 + m1.y * w1;
+    if constexpr (!Again::kOn) w0 *= join.unit[0][r], w1 *= join.unit[1][r];
     use0 = m0.y != 0.f;
     use1 = m1.y != 0.f;
     s0 = 0;
