@@ -79,6 +79,10 @@ constexpr int kScalesAhead = 2;  // steps that scales are ahead of their keys
 constexpr int kStepRing = 32;
 constexpr float kBias = 7.f;
 constexpr int kLeastE = -80;   // smaller scales count as 2^-80
+// In a wide step (kNear) each key has an exponent of its own, behind which its code *
+// scale is rounded just so; scores and weights are multiplied by the powers of two
+// then, each row's for what it sees. So one key's scale takes no bits from another's.
+constexpr int kLeastOwnE = -90, kWide = 1024;   // kWide stands for a wide step's value exponent, which is 0 then
 // A step whose largest contribution lies that far below the unit of O is summed by
 // itself: the exponentials of its weights in that unit would leave fp32.
 constexpr float kFar = 60.f;
@@ -111,7 +115,10 @@ struct Cfg {
   // A step's scales: per page those of its keys and of its values, as they come
   // (fp32), then as two fp16 each.
   static constexpr int kScaleOff = kIntOff + kBatchBytes;
-  static constexpr int kSmem = kScaleOff + kScaleRing * 1024 + 1024;
+  // Of a wide step, each key's exponents, a byte each: [128] of the key scales (less
+  // 32, + 127), [128] of the value scales (+ 127).
+  static constexpr int kExpOff = kScaleOff + kScaleRing * 1024;
+  static constexpr int kSmem = kExpOff + kScaleRing * 256 + 1024;
   static_assert(2 * kRaw >= kHalf && kRaw % 1024 == 0, "queries over raw places, halves in whole swizzle atoms");
   static_assert(kSmem <= 226 * 1024 - 5120, "static shared variables need the rest");
   static constexpr int kPieces = D / 16;                    // 16 bytes of a half for each converting thread
@@ -171,6 +178,27 @@ __device__ __forceinline__ int step_exponent(const float (&x)[4]) {
     top = mag < 0x7F800000u ? max(top, mag) : top;
   }
   return max(static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 23) - 127, kLeastE);
+}
+
+// The exponent of one scale, of a finite one in -90 .. 127.
+__device__ __forceinline__ int own_exponent(float x) {
+  return min(max(static_cast<int>(__float_as_uint(x) >> 23 & 255u) - 127, kLeastOwnE), 127);
+}
+
+__device__ __forceinline__ float own_log2(uint32_t byte) { return static_cast<float>(static_cast<int>(byte) - 127); }
+
+// A few columns of tensor memory at a time, for what is seldom done: its code shall be short.
+__device__ __forceinline__ void tmem_ld4(uint32_t at, float (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t at, const float (&v)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+}
+__device__ __forceinline__ void tmem_st2(uint32_t at, uint32_t x, uint32_t y) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
 
 // Descriptor of values as they lie in the ring, MN-major with 128-byte swizzle:
@@ -263,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Batch& b = *reinterpret_cast<Batch*>(smem + C::kIntOff);
   __shared__ __align__(16) Notice s_notice[2];
-  __shared__ __align__(8) int2 s_unit[kScaleRing];   // exponents of a step's key and value scales
+  __shared__ __align__(8) int2 s_unit[kScaleRing];   // exponents of a step's key and value scales, or (32, kWide)
   __shared__ float s_qc[2][2 * kRows];     // by item: what a row's dot products are multiplied by
   __shared__ __align__(8) uint64_t raw_full[C::kRawSlots], raw_empty[C::kRawSlots], note_full[2], note_empty[2], conv_meet;
   __shared__ __align__(8) uint64_t scale_raw[kScaleRing], scale_full[kScaleRing];
@@ -499,25 +527,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           if (!wait(smem_u32(scale_raw) + slot * 8, steps / kScaleRing & 1)) break;
           const int4 f = s_steps[steps % kStepRing];
           const uint32_t at = base_at + C::kScaleOff + slot * 1024 + lane * 4;   // of keys lane + 32 e
-          float x[4], y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          auto load = [&](int e, const int4& f, float& x, float& y) {
             const bool there = lane + 32 * e < f.z && !(f.w >> (e >> 1) & 1);
             const uint32_t from = at + (e >> 1) * 512 + (e & 1) * 128;
-            x[e] = there ? __uint_as_float(load_shared_u32(from)) : 0.f;
-            y[e] = there ? __uint_as_float(load_shared_u32(from + 256)) : 0.f;
-          }
-          const int ex = step_exponent(x), ey = step_exponent(y);
-          if (lane == 0) s_unit[slot] = make_int2(ex, ey);
+            x = there ? __uint_as_float(load_shared_u32(from)) : 0.f;
+            y = there ? __uint_as_float(load_shared_u32(from + 256)) : 0.f;
+          };
+          float x[4], y[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 4; ++e) load(e, f, x[e], y[e]);
+          const int ex = step_exponent(x), ey = step_exponent(y);
+          const bool wide_x = scales_are_wide(x, ex), wide = scales_are_wide(y, ey) || wide_x;
+          if (lane == 0) s_unit[slot] = wide ? make_int2(32, kWide) : make_int2(ex, ey);
+          auto put = [&](int e, float x, float y, int ek, int ev) {
             // A value scale that is no number becomes the score of whoever sees the
             // key: as a factor of a weight it would reach rows that do not.
-            const bool number = y[e] * 0.f == 0.f;
-            const float kx = number ? x[e] * pow2_of(7 - ex) : __uint_as_float(0x7FC00000u), vx = number ? y[e] * pow2_of(7 - ey) : 0.f;
+            const bool number = y * 0.f == 0.f;
+            const float kx = number ? x * pow2_of(7 - ek) : __uint_as_float(0x7FC00000u), vx = number ? y * pow2_of(7 - ev) : 0.f;
             const uint32_t to = at + (e >> 1) * 512 + (e & 1) * 128;
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(scale_of<F16>(kx)) : "memory");
             asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 256), "r"(scale_of<F16>(vx)) : "memory");
+          };
+          if (__builtin_expect(!wide, 1)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) put(e, x[e], y[e], ex, ey);
+          } else {
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {   // (read again: registers have no index)
+              float kx, vx;
+              load(e, f, kx, vx);
+              const int ek = own_exponent(kx), ev = own_exponent(vx);
+              uint8_t* const exps = smem + C::kExpOff + slot * 256 + lane + 32 * e;
+              exps[0] = static_cast<uint8_t>(ek + 95);   // (scores stay in range: these are 2^22 at most before)
+              exps[128] = static_cast<uint8_t>(ev + 127);
+              put(e, kx, vx, ek, ev);
+            }
           }
           fence_proxy_async_smem();   // the next copies into this place are the async proxy's
           __syncwarp();
@@ -584,6 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         const int pair = warp_uniform(it.pair), nj = warp_uniform(it.nj);
         if (nj <= 0) break;
         __syncwarp();
+        if (lane == 0) next_item(b, it, items[(k + 1) & 1]);   // while the queries come; in one place, since code costs where it lies
+        __syncwarp();
         wait(smem_u32(&q_full), k & 1);
         ++k;
         uint32_t add = 0;
@@ -604,7 +650,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             }
             if (j >= nj - 2 && j < nj) {   // the last scores
               if (one) bar_commit(smem_u32(&q_empty));
-              if (lane == 0) next_item(b, it, items[k & 1]);
               __syncwarp();
             }
             const int jv = j;   // its weights are due
@@ -624,7 +669,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           }
           if (s >= nj) {   // no step of its own
             if (one) bar_commit(smem_u32(&q_empty));
-            if (lane == 0) next_item(b, it, items[k & 1]);
             __syncwarp();
           }
           c += 2 * nj;
@@ -636,10 +680,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
 #pragma unroll 1
           for (int j = -1; j < nj && ok; ++j) {
             const int pv = j >= 0, more = j + 1 < nj;
-            if (!more) {   // the scores are all issued
-              if (lane == 0) next_item(b, it, items[k & 1]);
-              __syncwarp();
-            }
             const int ck = c + pv, vslot = c % S, kslot = ck % S;
             // one lane for each thing to wait for, so that the waits are one
             const uint32_t early = more ? note_early<kStepRing>(s_step, steps) : 0u;
@@ -829,6 +869,56 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
         __syncwarp();
         if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(&p_full[stream][u])), "r"(arrivals) : "memory");
       };
+      // The references for a step whose largest score is mx and that adds `need` to O
+      // at most (log2 units). Each row by itself, so that it does not depend on its neighbours.
+      auto raise = [&](float mx, float need) {
+        if (mx > mref + kRescaleLog2) {
+          const float nm = ceilf(mx);
+          l *= ex2(mref - nm);
+          mref = nm;
+        }
+        const bool grows = need > top + (kBias + kRescaleLog2);
+        const float nt = grows ? ceilf(need) - kBias : top;
+        const float alpha = grows ? ex2(top - nt) : 1.f;
+        top = nt;
+        if (done == 0 || !__any_sync(0xffffffffu, grows)) return;
+        // O holds the stream's products so far: they were issued before
+        // the product whose scores these are, and end in that order
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          float o[16];
+          uint32_t bits[16];
+          tmem_ld16(o_tmem + c0, o);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) bits[c] = __float_as_uint(o[c] * alpha);
+          tmem_st_u16(o_tmem + c0, bits);
+        }
+        tmem_wait_st();
+      };
+      // A step's weights 2^(s + neg), and their sum, for rows that are `alone` by the sum's own
+      // reference. exps: where a wide step's value exponents lie, which belong to the weights, or 0.
+      // Of the other rows sums are added in the order in which they are elsewhere.
+      auto weigh_apart = [&](float cs, float neg, bool alone, uint32_t exps) {
+        const float base = alone ? (mref == -INFINITY ? 0.f : -mref) : neg;
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int c0 = 0; c0 < kStepKeys; c0 += 4) {   // P over scores that are read
+          float x[4], w[4];
+          tmem_ld4(s_tmem + c0, x);
+          const uint32_t own = exps ? load_shared_u32(exps + c0) : 0x7F7F7F7Fu;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            part[e] += ex2_here(fmaf(x[e], cs, base));
+            w[e] = ex2_here(fmaf(x[e], cs, own_log2(own >> 8 * e & 255u) + neg));
+          }
+          tmem_st2(s_tmem + c0 / 2, pack2<true>(w[0], w[1]), pack2<true>(w[2], w[3]));
+        }
+        tmem_wait_st();
+        weights_there(0);
+        weights_there(1);
+        return (part[0] + part[2]) + (part[1] + part[3]);
+      };
+      auto exps_at = [&](int j) { return smem_u32(smem) + C::kExpOff + (step0 + j) % kScaleRing * 256; };
       // Steps that begin at own_a .. own_b of sequence `alone` (if the warp's rows
       // are of one), or up to pre_b of the prefix: every row sees all their keys.
       int own_a, own_b, pre_b, alone;
@@ -904,85 +994,63 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
           float mx = row_max(sv);
           load(0);
           mx = fmaxf(mx, row_max(sv)) * cs;
-          // each row by itself, so that it does not depend on its neighbours
-          const float need = ceilf(mx) + static_cast<float>(un.y);   // what the step adds to O, at most
-          const bool more = mx > mref + kRescaleLog2, grows = need > top + (kBias + kRescaleLog2);
-          if (more) {
-            const float nm = ceilf(mx);
-            l *= ex2(mref - nm);
-            mref = nm;
-          }
-          if (__any_sync(0xffffffffu, grows)) {
-            const float nt = grows ? need - kBias : top;
-            const float alpha = grows ? ex2(top - nt) : 1.f;
-            top = nt;
-            if (done > 0) {
-              // O holds the stream's products so far: they were issued before
-              // the product whose scores these are, and end in that order
+          // what the step adds to O, at most: its scales count as the largest of them
+          const float ey = static_cast<float>(un.y);
+          float need = mx + ey;
+          bool alone = row.token >= 0 && need < top - kFar && mx > -INFINITY;   // far below the unit
+          bool apart = false;
+          if (__any_sync(0xffffffffu, mx > mref + kRescaleLog2 || need > top + (kBias + kRescaleLog2) || alone || un.y == kWide)) {
+            if (un.y == kWide) {   // scores are multiplied by their keys' powers of two in place
+              need = mx = -INFINITY;   // the largest weight times value scale that the row sees, and score
+              alone = true;
 #pragma unroll 1
-              for (int c0 = 0; c0 < D; c0 += 16) {
-                float o[16];
-                uint32_t bits[16];
-                tmem_ld16(o_tmem + c0, o);
+              for (int c0 = 0; c0 < kStepKeys; c0 += 4) {
+                float x[4];
+                tmem_ld4(s_tmem + c0, x);
+                const uint32_t of_k = load_shared_u32(exps_at(j) + c0), of_v = load_shared_u32(exps_at(j) + 128 + c0);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) bits[c] = __float_as_uint(o[c] * alpha);
-                tmem_st_u16(o_tmem + c0, bits);
+                for (int e = 0; e < 4; ++e) {
+                  x[e] *= __uint_as_float((of_k >> 8 * e & 255u) << 23);
+                  mx = fmaxf(mx, x[e] * cs);
+                  need = fmaxf(need, fmaf(x[e], cs, own_log2(of_v >> 8 * e & 255u)));
+                }
+                tmem_st4(s_tmem + c0, x);
               }
               tmem_wait_st();
             }
+            raise(mx, need);
+            apart = __any_sync(0xffffffffu, alone);
           }
           // weights are 2^(s - ref), which times the step's values are in the unit of O
-          const float ref = top - static_cast<float>(un.y), neg = top == -INFINITY ? 0.f : -ref;
-          if (__any_sync(0xffffffffu, row.token >= 0 && need < top - kFar && need > -INFINITY)) {
-            // some row's step is far below its unit: sums by their own reference
-            const float by = ex2(fminf(mref - ref, 100.f)), own = mref == -INFINITY ? 0.f : -mref;
-            float part = 0.f;
+          const float ref = top - (un.y == kWide ? 0.f : ey), neg = top == -INFINITY ? 0.f : -ref;
+          if (__builtin_expect(apart, 0)) {
+            l = fmaf(weigh_apart(cs, neg, alone, un.y == kWide ? exps_at(j) + 128 : 0), alone ? 1.f : ex2(fminf(ref - mref, 100.f)), l);
+          } else {
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-            for (int c0 = 0; c0 < kStepKeys; c0 += 32) {   // P over scores that are read
-              float x[32];
-              uint32_t pk[16];
-              tmem_ld32(s_tmem + c0, x);
+            for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
+              if (u == 1) load(1);
 #pragma unroll
-              for (int c = 0; c < 32; ++c) {
-                x[c] = ex2_here(fmaf(x[c], cs, own));
-                part += x[c];
+              for (int h = 0; h < 64; h += 32) {
+                uint32_t pk[16];
+#pragma unroll
+                for (int c = h; c < h + 32; c += 2) {
+                  const float2 e = fma2(make_float2(sv[c], sv[c + 1]), make_float2(cs, cs), make_float2(neg, neg));
+                  sv[c] = ex2_here(e.x);
+                  sv[c + 1] = ex2_here(e.y);
+                }
+#pragma unroll
+                for (int c = 0; c < 16; ++c) pk[c] = pack2<true>(sv[h + 2 * c], sv[h + 2 * c + 1]);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) sum[c & 1] = add2(sum[c & 1], make_float2(sv[h + 2 * c], sv[h + 2 * c + 1]));
+                tmem_st_u16(s_tmem + u * (kPage / 2) + h / 2, pk);
               }
-#pragma unroll
-              for (int c = 0; c < 16; ++c) pk[c] = pack2<true>(x[2 * c] * by, x[2 * c + 1] * by);
-              tmem_st_u16(s_tmem + c0 / 2, pk);
+              tmem_wait_st();
+              weights_there(u);
             }
-            tmem_wait_st();
-            weights_there(0);
-            weights_there(1);
-            l += part;
-            ++done;
-            ++ns;
-            continue;
+            // (ref - mref is at most kFar + kRescaleLog2 where there are weights)
+            l = fmaf((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y), ex2(fminf(ref - mref, 100.f)), l);
           }
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-          for (int u = 0; u < 2; ++u) {   // P replaces scores that are in registers by then
-            if (u == 1) load(1);
-#pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int c = h; c < h + 32; c += 2) {
-                const float2 e = fma2(make_float2(sv[c], sv[c + 1]), make_float2(cs, cs), make_float2(neg, neg));
-                sv[c] = ex2_here(e.x);
-                sv[c + 1] = ex2_here(e.y);
-              }
-#pragma unroll
-              for (int c = 0; c < 16; ++c) pk[c] = pack2<true>(sv[h + 2 * c], sv[h + 2 * c + 1]);
-#pragma unroll
-              for (int c = 0; c < 16; ++c) sum[c & 1] = add2(sum[c & 1], make_float2(sv[h + 2 * c], sv[h + 2 * c + 1]));
-              tmem_st_u16(s_tmem + u * (kPage / 2) + h / 2, pk);
-            }
-            tmem_wait_st();
-            weights_there(u);
-          }
-          // (ref - mref is at most kFar + kRescaleLog2 where there are weights)
-          l = fmaf((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y), ex2(fminf(ref - mref, 100.f)), l);
         }
         ++done;
         ++ns;

@@ -275,6 +275,7 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
       // scales: those of slots past the end become 0, a value scale that is no
       // number the score of whoever sees the key; ev: the value scales are below 2^(ev + 1)
       int ev;
+      bool wide;
       {
         const bool there = now.base + lane < now.end;
         float kx, vx;
@@ -285,6 +286,8 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         if (!there) kx = 0.f;
         if (!there || !number) vx = 0.f;
         ev = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(vx) & 0x7FFFFFFFu) >> 23) - 127, kLeastE);
+        const float only[1] = {vx};
+        wide = scales_are_wide(only, ev);
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + C::kScales + lane * 4), "f"(kx) : "memory");
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + C::kScales + 4 * kUnit + lane * 4), "f"(vx) : "memory");
         __syncwarp();
@@ -353,21 +356,37 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
           mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
           mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
         }
-        float alpha[2] = {1.f, 1.f}, cq[2];
+        float alpha[2] = {1.f, 1.f}, cq[2], most[2];
         bool grows = false;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           cq[u] = fminf(fmaxf(s_qc[m * 16 + u * 8 + g], 0x1p-126f), 0x1p127f);
           mx[u] *= cq[u];
+          most[u] = mx[u] + static_cast<float>(ev + 1);   // the row's largest weight times value scale, at most
+        }
+        if (wide) {   // of what it sees, key by key
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            most[u] = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              most[u] = max3(most[u], fmaf(s[m][t][2 * u], cq[u], scale_log2_bound(vs[t].x)),
+                             fmaf(s[m][t][2 * u + 1], cq[u], scale_log2_bound(vs[t].y)));
+            most[u] = fmaxf(most[u], __shfl_xor_sync(0xffffffffu, most[u], 1));
+            most[u] = fmaxf(most[u], __shfl_xor_sync(0xffffffffu, most[u], 2));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
           if (mx[u] > mref[m][u] + kRescaleLog2) {   // each row by itself
             const float nm = ceilf(mx[u]);
             l[m][u] *= ex2(mref[m][u] - nm);
             mref[m][u] = nm;
           }
-          const float need = ceilf(mx[u]) + static_cast<float>(ev + 1);   // what the unit adds to o, at most
-          if (need > top[m][u] + (kBias + kRescaleLog2)) {
-            alpha[u] = ex2(top[m][u] - (need - kBias));
-            top[m][u] = need - kBias;
+          if (most[u] > top[m][u] + (kBias + kRescaleLog2)) {
+            const float nt = ceilf(most[u]) - kBias;
+            alpha[u] = ex2(top[m][u] - nt);
+            top[m][u] = nt;
             grows = true;
           }
         }
@@ -380,7 +399,7 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          // (mref is at most 102 above top: no key counts for less than 2^-79 of its weight there)
+          // (mref is at most 106 above top, since no key counts for less than 2^-90 of its weight there)
           const float neg = mref[m][u] == -INFINITY ? 0.f : -mref[m][u];
           const float by = top[m][u] == -INFINITY ? 0.f : ex2(mref[m][u] - top[m][u]);
           float sum = 0.f;

@@ -553,6 +553,27 @@ struct JoinUnits : Join {
   float unit[2][kRows];
 };
 
+// log2 of a value scale's size from its bits, at least and by less than 0.09 too
+// much; of smaller scales than 2^-90, and of zeros, -90.
+__device__ __forceinline__ float scale_log2_bound(float scale) {
+  return fmaxf(fmaf(static_cast<float>(__float_as_uint(scale) & 0x7FFFFFFFu), 0x1p-23f, -126.9138f), -90.f);
+}
+
+// Scales (of 128 keys, or of 32) that lie further apart than this many powers of two,
+// zeros apart, are wide: each counts by itself there, for the rows that see its key.
+constexpr int kNear = 10;
+// Whether those of the warp's lanes are, with the largest's exponent.
+template <int N>
+__device__ __forceinline__ bool scales_are_wide(const float (&x)[N], int exponent) {
+  uint32_t low = 0x7F800000u;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const uint32_t mag = __float_as_uint(x[e]) & 0x7FFFFFFFu;
+    low = mag != 0 ? min(low, mag) : low;
+  }
+  return static_cast<int>(__reduce_min_sync(0xffffffffu, low) >> 23) - 127 < exponent - kNear;
+}
+
 // A sum of weights and its reference, for others to join: the sum between 1 and 2,
 // so that a sum's product with a mean value stays in range where the value does.
 __device__ __forceinline__ float2 joined_form(float mref, float l) {

@@ -1,15 +1,96 @@
 """What the scales of other keys may do to a row of the attention over 8-bit pages on
-the GPU: those of keys whose values are zero.
+the GPU: those of keys that it does not see or that have no weight in it, and
+those of keys whose values are zero.
 
-Tolerances: those of tests/test_gpu_paged_q8.py.
+Tolerances: those of tests/test_gpu_paged_q8.py against the definition, with the
+largest value that has a weight in the row (max |v| there) in place of the pool's, and the
+size of the scores of such keys. The weights' rounding counts for values 2^10 larger:
+scales that lie closer together than that count as the largest of their step of 128
+keys (of few rows, of their 32), whichever key has it; of others each is its key's alone.
 """
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
-from tests.test_gpu_paged import BF, DEV, dfl  # noqa: E402, F401
-from tests.test_gpu_paged_q8 import Batch8, check_attn  # noqa: E402
+from tests.test_gpu_paged import BF, DEV, HF, dfl  # noqa: E402, F401
+from tests.test_gpu_paged_q8 import Batch8, check, check_attn  # noqa: E402
+
+KINDS = [(1, 8, 2, 128, BF), (3, 8, 2, 64, HF), (8, 8, 2, 128, BF), (20, 8, 2, 128, BF), (40, 4, 2, 64, HF), (90, 8, 2, 128, HF)]
+POWERS = (9, 14, 31, 60)   # an outlier's scale beside ordinary ones
+
+
+def compare(b, got, ref, keys):
+    """`check` against the definition, the term of the weights' rounding 2^10 times as large (by way of the
+    mass, which 2^-11 is multiplied to)."""
+    out, mass, size, owned = ref
+    more = keys * 2.0 ** -30 * np.abs(b.decoded()[:, 1]).max() * 2.0 ** 10
+    check(b, got, (out, mass + 2.0 ** 11 * more, size, owned), keys, whole=True)
+
+
+def put(b, dfl, seq, at, keys=None, values=None):  # noqa: F811
+    """Multiplies the scales of the key at a position of a sequence."""
+    _, _, ks, vs = dfl.kv_pool_q8_views(b.pool, b.d)
+    p = int(b.table[seq, at // 64])
+    if keys is not None:
+        ks[p][:, at % 64] *= keys
+    if values is not None:
+        vs[p][:, at % 64] *= values
+
+
+@pytest.mark.parametrize("q,heads,n_kv,d,dtype", KINDS)
+def test_scales_in_front_of_the_window(dfl, q, heads, n_kv, d, dtype):  # noqa: F811
+    """Keys that no row sees, in steps that rows see: the definition over an ordinary cache."""
+    b = Batch8([(q, 300)], heads, n_kv, d, dtype)
+    window = 300 - q - 170
+    ref = b.oracle(bits=None, window=window)
+    for at in (150, 100, 169):      # in the window's first units of 32 and steps of 128
+        for power in POWERS:
+            for kw in (dict(values=2.0 ** power), dict(keys=2.0 ** power), dict(keys=2.0 ** power, values=2.0 ** power)):
+                clean = b.pool.clone()
+                put(b, dfl, 0, at, **kw)
+                got = b.attend(dfl, window=window)
+                b.pool.copy_(clean)
+                compare(b, got, ref, 300)
+
+
+@pytest.mark.parametrize("q,heads,n_kv,d,dtype", KINDS[1:])
+def test_scales_of_later_tokens(dfl, q, heads, n_kv, d, dtype):  # noqa: F811
+    """Rows before a token do not see its key, which other rows of their tile do."""
+    b = Batch8([(q, 300), (q, 129)], heads, n_kv, d, dtype, prefix=70)
+    refs = b.oracle(bits=None), b.oracle(bits=None, prefix_table=b.prefix_np, prefix_len=70)
+    sees = q - 1                    # only the last token of sequence 0
+    rows = np.ones(2 * q, dtype=bool)
+    rows[sees] = False
+    for power in POWERS:
+        for kw in (dict(values=2.0 ** power), dict(keys=2.0 ** power)):
+            clean = b.pool.clone()
+            put(b, dfl, 0, 299, **kw)
+            got = b.attend(dfl), b.attend_shared(dfl)
+            b.pool.copy_(clean)
+            for g, (out, mass, size, owned) in zip(got, refs):
+                compare(b, g, (out, mass, size, owned & rows), 370)
+
+
+@pytest.mark.parametrize("q,heads,n_kv,d,dtype", KINDS)
+def test_scales_of_keys_without_weight(dfl, q, heads, n_kv, d, dtype):  # noqa: F811
+    """A key far below the others in every row (by 70 or more, so that its weight is below 2^-90)
+    with larger values: it has no part in the output, and takes none from the others."""
+    b = Batch8([(q, 300)], heads, n_kv, d, dtype)
+    b.q = b.q.abs() + 0.5
+    kc, _, ks, _ = dfl.kv_pool_q8_views(b.pool, d)
+    _, mass, size, owned = b.oracle(bits=None)
+    lowest = float((b.q.double().sum(dim=-1) * d ** -0.5 * 127).min())
+    for at in (0, 130, 200):
+        for power in POWERS:
+            clean = b.pool.clone()
+            p = int(b.table[0, at // 64])
+            kc[p][:, at % 64], ks[p][:, at % 64] = 1, 75.0 / lowest     # code -126
+            put(b, dfl, 0, at, values=2.0 ** power)
+            got, out = b.attend(dfl), b.oracle(bits=None)[0]
+            b.pool.copy_(clean)
+            compare(b, got, (out, mass, size, owned), 300)
 
 
 @pytest.mark.parametrize("power", [0, 30, 50, 60, 100])
