@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         const bool number = vx * 0.f == 0.f;
         if (there && !number) kx = __uint_as_float(0x7FC00000u);
         if (!there) kx = 0.f;
+        kx *= 0x1p-16f;   // a score before cq: dot products with codes come to 2^14, scales of bf16 keys to 2^121
         if (!there || !number) vx = 0.f;
         ev = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(vx) & 0x7FFFFFFFu) >> 23) - 127, kLeastE);
         const float only[1] = {vx};
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         bool grows = false;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          cq[u] = fminf(fmaxf(s_qc[m * 16 + u * 8 + g], 0x1p-126f), 0x1p127f);
+          cq[u] = fminf(fmaxf(s_qc[m * 16 + u * 8 + g] * 0x1p16f, 0x1p-126f), 0x1p127f);
           mx[u] *= cq[u];
           most[u] = mx[u] + static_cast<float>(ev + 1);   // the row's largest weight times value scale, at most
         }

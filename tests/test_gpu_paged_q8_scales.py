@@ -128,3 +128,16 @@ def test_zero_values_behind_a_prefix_of_larger_ones(dfl, power, lens):  # noqa: 
             vs[zero] = 0.0
             vs[~zero] *= 2.0 ** power
             check_attn(dfl, b, shared=True)
+
+
+@pytest.mark.parametrize("q", [1, 8, 20, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_as_large_as_the_type_holds(dfl, q, d):  # noqa: F811
+    """bf16 keys near 2^127 and queries near 2^-106, and the other way round: the scores are ordinary."""
+    for power in (-106, -60, 60, 100):
+        b = Batch8([(q, 200)], 8, 2, d, BF)
+        _, _, ks, _ = dfl.kv_pool_q8_views(b.pool, d)
+        ks *= 2.0 ** min(-power + 20, 125)
+        b.q = (b.q.float() * 2.0 ** power).to(BF)
+        back = 2.0 ** (-power - min(-power + 20, 125))
+        check_attn(dfl, b, scale=back * d ** -0.5)
