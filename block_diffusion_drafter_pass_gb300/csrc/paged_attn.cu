@@ -801,16 +801,23 @@ struct Plan {
 
 // Whether a batch over 8-bit pages is one for the kernel of few rows (that many
 // of a kv head for each sequence on average: tiles hold no more, so longer blocks
-// are cut), and how. At 32 rows it takes 156 us instead of 175 (8 tokens of 32
+// are cut), and how. At 32 rows it takes 166 us instead of 177 (8 tokens of 32
 // sequences of 8192 keys, 4 heads a kv head); 64 would read the keys twice. Short
 // caches of 17 to 32 rows are read twice by two tiles of 16, whose steps are
-// shorter chains (8 tokens over 4096 keys 13.8 us instead of 17.2, of 8 sequences
-// over 1024 21.9 instead of 23.5, of 16 over 2048 the same, of 48 over 1024 62
+// shorter chains (8 tokens over 4096 keys 14.2 us instead of 17.7, of 8 sequences
+// over 1024 22.4 instead of 24.3, of 16 over 2048 the same, of 48 over 1024 62
 // instead of 58; tables wider than the caches leave it at 32 rows). Two
-// CTAs an SM let one's ends pass under the other's work (uneven short blocks 23
-// us instead of 27, 128 tokens of 2048 keys 105 instead of 125, 64 of 32768 720
-// instead of 685); one for each, of all its warps, is better with few tiles (a
-// token over 4096 keys 11.8 us instead of 12.9; with 16 tiles 16.9 instead of 16.2).
+// CTAs an SM let one's ends pass under the other's work (8 tokens of 16 sequences of
+// 2048 keys 40 us instead of 43, 128 single ones of 2048 109 instead of 129; but 64 of
+// 32768 720 instead of 670, 8 tokens of 8 of 256 16.3 instead of 12.5); one for
+// each, of all its warps, is better with few tiles (a token over 4096 keys 12.2 us
+// instead of 13.2; with 16 tiles 14.2 instead of 13.7).
+// What the average hides: a long block among single tokens or empty entries is cut
+// into tiles of so many rows, which each read its whole cache, at most as often as the
+// batch has sequences. 160 single tokens and a block of 1024, all over 8192 keys, take
+// 1300 us (446 and 158 in two calls; over 16-bit pages 1178), 63 and a block of 200
+// 420 (191 and 62; 470), a block of 4096 among 1023 empty entries 2046 (alone 424; 329).
+// The lengths that tell are on the device; the caller can give such a block its own call.
 Q8Few few_rows(const dflash_paged_batch& b, bool shared) {
   const int group = b.n_heads / b.n_kv_heads;
   const long long rows = static_cast<long long>(b.n_tokens) * group, tiles = shared ? 1 : b.n_seq;
@@ -827,10 +834,11 @@ Q8Few few_rows(const dflash_paged_batch& b, bool shared) {
 // with the rows of one. Of many short blocks with long own caches these steps are
 // most of the work, and are taken apart from the prefix, by the kernel of few rows.
 // The rule sees the page tables' width, not the lengths: single tokens behind 2048
-// take 108 us instead of 158 (64 sequences, own caches of 2048) and 159 instead of
-// 284 (128 of 2048), about the same at 1024 pages (98 and 100: 128 of 512), and
-// less would cost (71 instead of 65: 64 of 512; wide tables of short caches, 54
-// instead of 38: 64 of 64).
+// take 110 us instead of 158 (64 sequences, own caches of 2048) and 163 instead of
+// 285 (128 of 2048), about the same at 1024 pages (98 and 101: 128 of 512), and
+// less would cost (67 instead of 65: 64 of 512; wide tables of short caches, 56
+// instead of 39: 64 of 64). Below 64 sequences it is never done, also where it would
+// pay (139 us instead of 208: 32 of 8192; 50 instead of 46: 16 of 2048).
 constexpr int kOwnTokens = 1024;   // (the workspace holds their part in fp32)
 bool own_apart(const dflash_paged_batch& b) {
   return b.n_seq >= 64 && b.n_tokens <= kOwnTokens && static_cast<long long>(b.n_seq) * b.table_pages > 1024 && few_rows(b, true).rows == 0 && few_rows(b, false).rows > 0;

@@ -14,16 +14,22 @@
 // as large, twice: the scale, too. Found over 2000 keys of scores of deviation 1.5:
 // 0.0005 of the output's norm in fp16 (0.0011 with a rounded scale; a plain fp32
 // computation rounded once at the end 0.0002), 0.0020 in bf16 (0.0017 with whole
-// scales; plain 0.0017), where whole scales take 287 us instead of 278 for 16
+// scales; plain 0.0017), where whole scales took 287 us instead of 278 for 16
 // tokens of 32 sequences behind 32768; quantising the same keys and values moves the
-// output by 0.013. Scales 2^21 below their step's largest lose
-// bits. (Scales multiplied onto scores and weights in fp32 instead are exact, but
+// output by 0.013. (Scales multiplied onto scores and weights in fp32 instead are exact, but
 // each row then needs all 256 of a step: 364 us instead of 322, then.)
-// Weights are rounded to fp16 for the product with the
-// values, in its best place: a row's weights are 2^(s - m - E + e) for a step of
-// value exponent e, m its reference maximum less 7 and E at least every e so far,
-// so that they stay below 2^15 and 2^-31 of the largest contribution still counts.
-// Sum and output share the unit, so it cancels.
+// The step's scales must lie within 2^10 of each other for that (zeros apart). In a
+// step of wider ones each key has a power of two of its own, and the softmax
+// multiplies the row's scores and weights by these, in a second pass over the
+// scores: no key's scale takes bits from another's.
+// Weights are rounded to fp16 for the product with the values, in its best place:
+// as 2^(s - T + e) for a value exponent e, T (`top`) at least the row's largest s + e
+// less 15 so far, of which s is its largest score in a step and e the step's exponent
+// (in a wide step s + e is of one key that the row sees). So they stay below 2^15, and
+// 2^-21 of the row's largest weight times value scale still counts, 2^-31 where
+// scales are alike. Their sum is in fp32 by a reference m of its own, since keys of
+// small or no values count there, too. m and T are whole numbers, and what is left of an
+// item is given on by m: the sum between 1 and 2, and O 2^(T - m).
 //
 // Per CTA: a warp walks the steps, looks up their pages and brings each half
 // (128 keys, or their values) and its scales by bulk copies; a warp turns scales
@@ -37,12 +43,17 @@
 //
 // What bounds it: a step's chain (scores, weights, product, next scores), with
 // eight more warps on the softmax's schedulers than 16-bit pages need. A
-// pair's step takes 2.4 us, 4600 cycles of which the tensor pipe is active for 44%
+// pair's step took 2.4 us, 4600 cycles of which the tensor pipe is active for 44%
 // (3300 and 57% there); issue slots are 54% taken, shared memory's load/store pipe
 // 36%. 16 tokens of 32 sequences of 1024 to 8192
-// keys (32/8 heads of 128) take 118 us (floor 47.5), of one over 262144 keys 164
-// (3.4 TB/s), 8.7 thousand new tokens with a window of 2048 377, 16 of 32 sequences
-// behind 32768 277.
+// keys (32/8 heads of 128) take 120 us (floor 47.5), of one over 262144 keys 165
+// (3.4 TB/s), 8.7 thousand new tokens with a window of 2048 398, 16 of 32 sequences
+// behind 32768 284. Instruction fetch is part of it: with five roles at work a warp is
+// held up by it for every instruction issued (1.0 of 11 stalled warps, ncu), so the
+// same rare code (wide steps, an item's successor) costs from nothing to 14% of these
+// times by its length and by how often it is laid out: prompts 386 us without it, 438
+// unrolled and in line, 400 as short loops with the products' warps' three copies of
+// the item's successor made one.
 // What was tried and is slower: halves in rounds of two with their scales, one wait
 // for each; codes by the converting warps' own loads from global memory, without
 // the first ring and with room for a fourth half of fp16 (130 us instead of 119, 190
@@ -215,8 +226,10 @@ __device__ __forceinline__ float pow2_of(int e) { return __int_as_float((e + 127
 // times the power of two that puts its largest finite value between 1/2 and 1
 // (its infinities and NaN stay what they are), and s_qc what its dot products are
 // multiplied by for that. No branch depends on the values: rows that fp16 holds
-// taken as they are, behind a vote, made prompts 3% faster, and then an illegal
-// instruction of batches whose rows differ (which reading did not explain).
+// taken as they are, behind votes and shuffles in a branch, made prompts 3% faster,
+// and then an illegal instruction of batches whose rows differ, in calls whose CTAs
+// had one step each (so no ring was gone round) and with the same addresses, barriers
+// and dealt registers as here. Reading found no cause.
 template <int D, bool F16>
 __device__ __forceinline__ void bring_queries(const PagedAttnArgs& a, const Notice& r, uint32_t q_at, float* s_qc, int ct) {
   constexpr int kOf = D / 8, kPass = kConvWarps * 32 / kOf, kAtOnce = 4;   // lanes of a row, rows at a time

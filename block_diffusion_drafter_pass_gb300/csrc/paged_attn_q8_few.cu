@@ -9,9 +9,11 @@
 // while it works, and multiplies by mma.sync, whose fragments are made in
 // registers. A product of code and scale never exists: codes are exact in fp16,
 // key scales go onto scores and value scales onto weights in fp32, which are then
-// rounded to fp16 for the product with the values, in units of 2^-E as in
-// paged_attn_q8.cu (weight times scale stays below 2^15 and counts down to 2^-31 of
-// that; E follows the largest value scale of each 32 keys). At an item's end
+// rounded to fp16 for the product with the values, in the unit of `top` as in
+// paged_attn_q8.cu: it follows the row's largest weight times value scale, of each
+// 32 keys its largest weight times their largest scale where scales lie within
+// 2^10, and else the largest over the keys that it sees. So 2^-21 of that still
+// counts. The sum has its own reference. At an item's end
 // the warps' parts are joined in shared memory, in their order.
 //
 // Fragments. A product over dims (scores) or keys (output) may take them in any
@@ -24,13 +26,14 @@
 // a step of 16 gives it, and turns each 4 x 4 bytes over.
 //
 // What bounds it: up to 16 rows memory (one token of 64 sequences of 32768 keys,
-// 32/8 heads of 128: 685 us with one CTA an SM, 95% of the copy bandwidth, and 720
-// with two; one of 32 of 8192 100 us, start, joins and end included; by the kernel
-// for 128 rows 1191 and 171); of 17 to 32 rows the latency of 1200 instructions a
-// unit in 8 warps (8 tokens of 32 sequences of 8192 156 us instead of 175). Short
-// calls are chains of loads: one token over a window of 4096 keys 11.8 us (17.6).
+// 32/8 heads of 128: 720 us, 91% of the copy bandwidth, with two CTAs an SM, as the rule
+// has it, and 670 with one; one of 32 of 8192 104 us, start, joins and end included; by
+// the kernel for 128 rows 1194 and 172); of 17 to 32 rows the latency of 1300 instructions a
+// unit in 8 warps (8 tokens of 32 sequences of 8192 166 us instead of 177; 156 before
+// sum and unit were apart). Short
+// calls are chains of loads: one token over a window of 4096 keys 12.6 us (18.8).
 // 12 warps an SM (8 of 32 rows) are what registers allow; 10, unevenly on four
-// schedulers, take 801 us for the 685, 14, spilling, 832.
+// schedulers, took 801 us for 685 then, 14, spilling, 832.
 #include <algorithm>
 #include <atomic>
 

@@ -436,9 +436,16 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * as they are where a sequence has up to 32 rows of a kv head on average (new
  * tokens times n_heads / n_kv_heads; behind a prefix, of all sequences together).
  * Above that, products of code and scale (with bf16 tokens the scales, too) are
- * rounded to 11 bits, behind a power of two that 128 neighbouring keys share, whether
- * a row sees them all or not: scales (of keys, or of values) 2^21 below the largest
- * finite one of these lose bits, as do value scales below 2^-90. */
+ * rounded to 11 bits. Before it is multiplied with the value's codes, a row's weight
+ * (with up to 32 rows: times the value scale) is rounded to 11 bits, or in steps of
+ * 2^-21 of the row's largest weight times value scale, if that is more. Sums of
+ * weights are not rounded. Other keys' scales have no further part in a row than
+ * that: keys that it does not see, or of no weight, may have scales of any size.
+ * Weights below 2^-126 of the row's largest count as zero; value scales below 2^-90
+ * lose bits, above 32 rows key scales, too.
+ * The number of rows decides on the kernel as an average: one long block among many
+ * short or empty ones is read in their manner, its cache as often as the block has
+ * 16 or 32 rows, and is better given a call of its own. */
 enum { DFLASH_BF16 = 0, DFLASH_FP16 = 1, DFLASH_POOL_Q8 = 16 };
 
 typedef struct {
@@ -512,7 +519,7 @@ dflash_status dflash_paged_attn_workspace(const dflash_paged_batch* b, size_t* b
  *  workspace  device, 32-byte aligned, at least dflash_paged_attn_workspace
  * A token that sees no key gets zeros. Keys and values it does not see have no
  * influence on it, infinities and NaN included (of 8-bit pages, but for the
- * exponent that neighbouring keys share). (Behind a length, and in 8-bit pages, they
+ * rounding said above). (Behind a length, and in 8-bit pages, they
  * cost nothing. Those of cached keys that only some rows of a tile of 256 see, such as
  * a later token of the block or another sequence behind the same prefix, make
  * the kernel compute the others of 16-bit pages again one by one: one sequence of NaN among 32
