@@ -18,10 +18,11 @@
 // tokens of 32 sequences behind 32768; quantising the same keys and values moves the
 // output by 0.013. (Scales multiplied onto scores and weights in fp32 instead are exact, but
 // each row then needs all 256 of a step: 364 us instead of 322, then.)
-// The step's scales must lie within 2^10 of each other for that (zeros apart). In a
-// step of wider ones each key has a power of two of its own, and the softmax
-// multiplies the row's scores and weights by these, in a second pass over the
-// scores: no key's scale takes bits from another's.
+// The step's scales must lie within 2^10 of each other for that (a key scale of zero
+// apart, but not a value scale of zero beside others). In a step of wider ones each key
+// has a power of two of its own, and the softmax multiplies the row's scores and
+// weights by these, in a second pass over the scores: no key's scale takes bits from
+// another's.
 // Weights are rounded to fp16 for the product with the values, in its best place:
 // as 2^(s - T + e) for a value exponent e, T (`top`) at least the row's largest s + e
 // less 15 so far, of which s is its largest score in a step and e the step's exponent
@@ -180,15 +181,17 @@ __device__ __forceinline__ uint32_t scale_of(float x) {
   return pack2<true>(most, kTwo ? x - most : x);
 }
 
-// The exponent of the largest finite scale of a step, of which each lane has four.
-__device__ __forceinline__ int step_exponent(const float (&x)[4]) {
-  uint32_t top = 0;
+// Of a step's scales, of which each lane has four: their finite ones' spread. Zeros
+// count where the mask has a bit (there, a key of all the weight may have no values).
+__device__ __forceinline__ Spread step_spread(const float (&x)[4], uint32_t zeros) {
+  uint32_t top = 0, low = 0x7F800000u;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint32_t mag = __float_as_uint(x[e]) & 0x7FFFFFFFu;
     top = mag < 0x7F800000u ? max(top, mag) : top;
+    low = mag != 0 || (zeros >> e & 1) ? min(low, mag) : low;
   }
-  return max(static_cast<int>(__reduce_max_sync(0xffffffffu, top) >> 23) - 127, kLeastE);
+  return spread_of(__reduce_max_sync(0xffffffffu, top), __reduce_min_sync(0xffffffffu, low), kLeastE);
 }
 
 // The exponent of one scale, of a finite one in -90 .. 127.
@@ -545,12 +548,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_q8_kernel(const __grid
             const uint32_t from = at + (e >> 1) * 512 + (e & 1) * 128;
             x = there ? __uint_as_float(load_shared_u32(from)) : 0.f;
             y = there ? __uint_as_float(load_shared_u32(from + 256)) : 0.f;
+            return there ? 1u << e : 0u;
           };
           float x[4], y[4];
+          uint32_t there = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) load(e, f, x[e], y[e]);
-          const int ex = step_exponent(x), ey = step_exponent(y);
-          const bool wide_x = scales_are_wide(x, ex), wide = scales_are_wide(y, ey) || wide_x;
+          for (int e = 0; e < 4; ++e) there |= load(e, f, x[e], y[e]);
+          const Spread sx = step_spread(x, 0), sy = step_spread(y, there);
+          const int ex = sx.exponent, ey = sy.exponent;
+          const bool wide = sx.wide || sy.wide;
           if (lane == 0) s_unit[slot] = wide ? make_int2(32, kWide) : make_int2(ex, ey);
           auto put = [&](int e, float x, float y, int ek, int ev) {
             // A value scale that is no number becomes the score of whoever sees the

@@ -289,9 +289,11 @@ __global__ void __launch_bounds__(Few<D, MT, PerSm>::kThreads, PerSm) paged_attn
         if (!there) kx = 0.f;
         kx *= 0x1p-16f;   // a score before cq: dot products with codes come to 2^14, scales of bf16 keys to 2^121
         if (!there || !number) vx = 0.f;
-        ev = max(static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(vx) & 0x7FFFFFFFu) >> 23) - 127, kLeastE);
-        const float only[1] = {vx};
-        wide = scales_are_wide(only, ev);
+        // (a zero counts as the smallest: a key of all the weight may have no values)
+        const uint32_t mag = __float_as_uint(vx) & 0x7FFFFFFFu;
+        const Spread sv = spread_of(__reduce_max_sync(0xffffffffu, mag), __reduce_min_sync(0xffffffffu, there && number ? mag : 0x7F800000u), kLeastE);
+        ev = sv.exponent;
+        wide = sv.wide;
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + C::kScales + lane * 4), "f"(kx) : "memory");
         asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + C::kScales + 4 * kUnit + lane * 4), "f"(vx) : "memory");
         __syncwarp();

@@ -559,19 +559,21 @@ __device__ __forceinline__ float scale_log2_bound(float scale) {
   return fmaxf(fmaf(static_cast<float>(__float_as_uint(scale) & 0x7FFFFFFFu), 0x1p-23f, -126.9138f), -90.f);
 }
 
-// Scales (of 128 keys, or of 32) that lie further apart than this many powers of two,
-// zeros apart, are wide: each counts by itself there, for the rows that see its key.
+// Scales (of 128 keys, or of 32) are wide when they lie further apart than this many
+// powers of two: each counts by itself then, for the rows that see its key.
 constexpr int kNear = 10;
-// Whether those of the warp's lanes are, with the largest's exponent.
-template <int N>
-__device__ __forceinline__ bool scales_are_wide(const float (&x)[N], int exponent) {
-  uint32_t low = 0x7F800000u;
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const uint32_t mag = __float_as_uint(x[e]) & 0x7FFFFFFFu;
-    low = mag != 0 ? min(low, mag) : low;
-  }
-  return static_cast<int>(__reduce_min_sync(0xffffffffu, low) >> 23) - 127 < exponent - kNear;
+// Of the largest and the smallest of finite magnitudes, as bits (0x7F800000: there is no
+// smallest), the largest's exponent, at least `least`, and whether they are wide. Scales
+// that are all zero are not.
+struct Spread {
+  int exponent;
+  bool wide;
+};
+__device__ __forceinline__ Spread spread_of(uint32_t top, uint32_t low, int least) {
+  Spread r;
+  r.exponent = max(static_cast<int>(top >> 23) - 127, least);
+  r.wide = top != 0 && static_cast<int>(low >> 23) - 127 < r.exponent - kNear;
+  return r;
 }
 
 // A sum of weights and its reference, for others to join: the sum between 1 and 2,

@@ -441,8 +441,8 @@ dflash_status dflash_set_conv(dflash_ctx* ctx, const dflash_conv_site* sites, in
  * 2^-21 of the row's largest weight times value scale, if that is more. Sums of
  * weights are not rounded. Other keys' scales have no further part in a row than
  * that: keys that it does not see, or of no weight, may have scales of any size.
- * Weights below 2^-126 of the row's largest count as zero; value scales below 2^-90
- * lose bits, above 32 rows key scales, too.
+ * Weights below 2^-126 of the row's largest count as zero, and weights times value
+ * scales below 2^-80 of it lose bits, as do, above 32 rows, key scales below 2^-90.
  * The number of rows decides on the kernel as an average: one long block among many
  * short or empty ones is read in their manner, its cache as often as the block has
  * 16 or 32 rows, and is better given a call of its own. */

@@ -141,3 +141,25 @@ def test_keys_as_large_as_the_type_holds(dfl, q, d):  # noqa: F811
         b.q = (b.q.float() * 2.0 ** power).to(BF)
         back = 2.0 ** (-power - min(-power + 20, 125))
         check_attn(dfl, b, scale=back * d ** -0.5)
+
+
+@pytest.mark.parametrize("q,heads,n_kv,d", [(1, 8, 2, 128), (3, 8, 2, 64), (8, 8, 2, 128), (20, 8, 2, 128), (40, 4, 2, 64), (90, 8, 2, 128)])
+def test_a_key_of_all_the_weight_without_values(dfl, q, heads, n_kv, d):  # noqa: F811
+    """A key 20 or more above the others (in units of e) whose values are zeros: what is left of the
+    others is small, and as precise as without it. Compared behind the factor between the two, by
+    which the score's own error counts (its size is that key's)."""
+    b = Batch8([(q, 300)], heads, n_kv, d, BF)
+    b.q = b.q.abs() + 0.5
+    kc, _, ks, vs = dfl.kv_pool_q8_views(b.pool, d)
+    lowest = float((b.q.double().sum(dim=-1) * d ** -0.5 * 127).min())
+    for at in (0, 130, 200):
+        clean = b.pool.clone()
+        p = int(b.table[0, at // 64])
+        kc[p][:, at % 64], ks[p][:, at % 64], vs[p][:, at % 64] = 1, 75.0 / lowest, 0.0   # out of it all
+        out, mass, _, owned = b.oracle(bits=None)
+        kc[p][:, at % 64], ks[p][:, at % 64] = 255, 25.0 / lowest
+        got, (_, less, size, _) = b.attend(dfl), b.oracle(bits=None)
+        b.pool.copy_(clean)
+        back = (mass.max(axis=-1) / less.max(axis=-1))[..., None]
+        assert back.min() > 2.0 ** 20
+        compare(b, got.double() * torch.from_numpy(back).to(DEV), (out, mass, size, owned), 300)
